@@ -528,6 +528,156 @@ rf_status rf_fp8_gemm(const uint8_t *a, const float *sa, const uint8_t *w, const
                       void *c, int M, int N, int K, rf_stream stream);
 
 /*
+ * Serving over a paged key/value cache. The cache is a pool of pages of `page`
+ * tokens; sequence b's token j lives in row j % page of page
+ * table[b * table_stride + j / page]. The keys of token row r of page P and
+ * key head h are the d elements at k_cache + P * k_page_stride +
+ * r * k_token_stride + h * k_head_stride (strides in elements; the same for
+ * v), so both [pages, page, Hkv, d] and [pages, Hkv, page, d] pools fit. A
+ * step's new tokens are ragged: sequence b has the rows cu_q[b] ..
+ * cu_q[b + 1] - 1 of T packed rows, and kv_len[b] cached tokens that include
+ * them (they are the last ones). Rows outside every sequence (a padded batch)
+ * are neither read nor written.
+ *
+ * rf_paged_slots writes, for each of the T rows, its position
+ * (kv_len[b] - n_b + i; 0 for a row outside every sequence or before the
+ * cache's first token) and its slot (page id * page + row in the page; -1 when
+ * it has none): the inputs of rf_kv_append_paged, computed once a step.
+ *  cu_q int32 [B + 1], kv_len int32 [B], table int32 [B, max_pages] (rows
+ *  table_stride apart), pos int32 [T], slots int64 [T]; all device.
+ * A table entry outside [0, num_pages) that a row needs gives slot -1 and is
+ * reported through rf_device_status. B, T >= 0; page, max_pages, num_pages
+ * >= 1; page * max_pages and page * num_pages <= 2^31 - 1. Errors:
+ * RF_ERR_INVALID (sizes, NULL or misaligned pointers).
+ */
+rf_status rf_paged_slots(const int32_t *cu_q, const int32_t *kv_len, const int32_t *table,
+                         int64_t table_stride, int B, int T, int max_pages, int page,
+                         int num_pages, int32_t *pos, int64_t *slots, rf_stream stream);
+
+/*
+ * Append a step's keys and values to a paged cache, with the queries' and
+ * keys' head norm and position rotation on the way: per (token, head) row x of
+ * q and k, in float32,
+ *   x <- x / sqrt(mean(x^2) + eps) * weight          (q_weight / k_weight given)
+ *   (x_i, x_j) <- (x_i c - x_j s, x_j c + x_i s)      (rot > 0, rot / 2 pairs)
+ * then q goes to q_out [T, H, d] and k to the token's slot; v goes there
+ * unchanged. Each value is rounded once, when it is stored.
+ *  q [T, H, d], k, v [T, Hkv, d]: dtype dt (RF_F32 or RF_BF16), a token's
+ *      heads back to back, tokens q_stride / k_stride / v_stride elements
+ *      apart (views of one fused projection fit). q NULL: only the cache is
+ *      written (q_out, q_weight, q_stride are ignored). q_out may be q itself
+ *      when q_stride == H * d.
+ *  slots int64 [T]: the token's slot in the pool; negative: the token is
+ *      skipped (q_out's row too). Slots must differ; of two tokens with one
+ *      slot, either one's bytes may stay.
+ *  pos int32 [T], cos_sin float32 [max_pos, rot]: rot / 2 cosines, then
+ *      rot / 2 sines of a position's angles. pair i is elements (i, i + rot/2),
+ *      or (2i, 2i + 1) with interleaved = 1; elements from rot on pass
+ *      through. rot = 0: no rotation, pos and cos_sin are ignored.
+ *  q_weight, k_weight: dtype dt [d], each may be NULL (no norm).
+ * d and rot multiples of 16, d <= 256 (RF_ERR_UNSUPPORTED otherwise), rot <= d.
+ * Pointers and strides in bytes 16-byte aligned (slots 8, pos 4). A slot or
+ * position out of range skips the token and is reported through
+ * rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED, RF_ERR_CUDA.
+ */
+rf_status rf_kv_append_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, void *q_out, void *k_cache,
+                             int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             void *v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                             int64_t v_head_stride, int T, int H, int Hkv, int d, int page,
+                             int num_pages, const int64_t *slots, const int32_t *pos,
+                             const float *cos_sin, int max_pos, int rot, int interleaved,
+                             const void *q_weight, const void *k_weight, float eps, rf_dtype dt,
+                             rf_stream stream);
+
+/*
+ * The division of a step's paged attention among the SMs, computed on the
+ * device from the lengths (rf_attn_paged reads it; one plan serves the
+ * attention of every layer of the step, and holds its own copy of the
+ * lengths). Each CTA gets a contiguous span of the step's key tiles of about
+ * equal cost; a query tile that a cut falls into is computed in parts and
+ * merged by log-sum-exp (RedFuser, section 3, multi-segment strategy).
+ *  cu_q int32 [B + 1], kv_len int32 [B]: device, lengths as above;
+ *  causal 1: token i of sequence b sees keys j <= kv_len[b] - n_b + i, 0: all;
+ *  plan: device, 256-byte aligned, plan_bytes >= rf_paged_plan_bytes(B).
+ * Lengths must be consistent (cu_q ascending within [0, T], 0 <= kv_len <=
+ * max_pages * page); otherwise the plan is empty (the attention computes
+ * nothing) and RF_ERR_INVALID is left in the device status word. A sequence
+ * may have no new tokens, or more than cached ones (its first rows then see
+ * no key). B, T >= 0, H % Hkv == 0. Errors: RF_ERR_INVALID; RF_ERR_UNSUPPORTED
+ * for H / Hkv > 128; RF_ERR_CUDA.
+ */
+size_t rf_paged_plan_bytes(int B);
+rf_status rf_paged_plan(const int32_t *cu_q, const int32_t *kv_len, int B, int T, int H, int Hkv,
+                        int page, int max_pages, int causal, void *plan, size_t plan_bytes,
+                        rf_stream stream);
+
+/*
+ * Attention of a step's new tokens over a paged cache: a decode step (one
+ * token a sequence), drafted tokens, a chunk of a long prompt, or a mix.
+ *  q   : bf16 [T, H, d], a token's heads back to back, tokens q_stride
+ *        elements apart;
+ *  o   : bf16 [T, H, d]; lse: float [T, H] or NULL (natural log; a row that
+ *        sees no key gets O = 0 and lse = -inf);
+ *  plan: as rf_paged_plan left it for the same B, T, H, Hkv, page, max_pages
+ *        (another plan computes nothing and is reported through
+ *        rf_device_status);
+ *  ws  : device workspace, 256-byte aligned, ws_bytes >=
+ *        rf_attn_paged_workspace_bytes(d): partial states of query tiles that
+ *        several CTAs share; calls that may overlap need one each.
+ * d in {64, 128}, page a multiple of 8, dt RF_BF16 (RF_ERR_UNSUPPORTED
+ * otherwise); H % Hkv == 0, H / Hkv <= 128; scale > 0 and finite. q, k_cache,
+ * v_cache and o 16-byte aligned, strides multiples of 8 elements. Cache rows
+ * past kv_len may hold anything; rows of visible or later tokens of the
+ * sequence must be finite. A table entry outside [0, num_pages) reads as zeros
+ * and is reported through rf_device_status. Errors: RF_ERR_INVALID,
+ * RF_ERR_UNSUPPORTED, RF_ERR_CUDA.
+ */
+size_t rf_attn_paged_workspace_bytes(int d);
+rf_status rf_attn_paged(const void *q, int64_t q_stride, const void *k_cache,
+                        int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        const void *v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, int page, int num_pages, const int32_t *table,
+                        int64_t table_stride, int max_pages, const void *plan, int B, int T, int H,
+                        int Hkv, int d, float scale, void *o, float *lse, float *ws,
+                        size_t ws_bytes, rf_dtype dt, rf_stream stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given random numbers. Per sequence b with n = n_draft[b] drafts, p_i and q_i
+ * the softmax of its target and draft logits over temperature[b]: draft x_i is
+ * accepted while u[b, i] * q_i(x_i) < p_i(x_i); the first refused position
+ * draws a token from max(p - q, 0), and when all are accepted one more token
+ * is drawn from p_n. A draw is argmax_j w_j / expo[b, j] (lowest index on a
+ * tie): with independent exponential variates that is j with probability
+ * w_j / sum w, so the emitted tokens follow the target's distribution. If
+ * nothing remains of max(p - q, 0) in float32, p itself is drawn from.
+ *  target : [B, S + 1, V] logits, dtype dt (RF_F32 or RF_BF16): row i judges
+ *           draft i, row n gives the extra token; -inf entries have no
+ *           probability;
+ *  draft  : [B, S, V] logits of the same dtype, or NULL: drafts with
+ *           certainty (copied ones): q_i is 1 at x_i;
+ *  tokens : int32 [B, S]; u: float [B, S] in [0, 1); expo: float [B, V] > 0;
+ *  n_draft: int32 [B] in [0, S], or NULL (all S);
+ *  temperature: float [B], or NULL (1); 0: greedy (draft i is accepted when it
+ *           is the target's largest logit, lowest index first);
+ *  out    : int32 [B, S + 1]: the accepted drafts, the drawn token, then -1;
+ *  n_accepted: int32 [B].
+ *  ws     : device workspace, 16-byte aligned, ws_bytes >=
+ *           rf_draft_verify_workspace_bytes(B, S).
+ * B >= 0, 1 <= S <= 64, V >= 1. A token outside [0, V) is refused, and a row
+ * with nothing to draw from (all -inf, NaN) yields -1; both are reported
+ * through rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED
+ * (S > 64), RF_ERR_CUDA.
+ */
+size_t rf_draft_verify_workspace_bytes(int B, int S);
+rf_status rf_draft_verify(const void *target, const void *draft, const int32_t *tokens,
+                          const float *u, const float *expo, const int32_t *n_draft,
+                          const float *temperature, int B, int S, int V, int32_t *out,
+                          int32_t *n_accepted, void *ws, size_t ws_bytes, rf_dtype dt,
+                          rf_stream stream);
+
+/*
  * Test aid: when visited is non-NULL, every later rf_attn_fwd on this host
  * thread sets visited[((b*H + h) * nqt + qt) * nkt + kt] = 1 for each
  * 128 x 128 tile (qt, kt) whose scores it computes. The caller zeroes the

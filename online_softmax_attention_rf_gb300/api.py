@@ -79,6 +79,17 @@ SIGNATURES = {
     "rf_rowquant_e4m3": (_I, [_P, _I64, _I64, _P, _P, _I, _P]),
     "rf_mla_decode_workspace_bytes": (_SZ, [_I, _I]),
     "rf_mla_decode": (_I, [_P, _P, _P, _P, _I, _I, _F, _I, _P, _SZ, _P]),
+    "rf_paged_slots": (_I, [_P, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "rf_kv_append_paged": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64,
+                                _I64, _I64, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P,
+                                _P, _F, _I, _P]),
+    "rf_paged_plan_bytes": (_SZ, [_I]),
+    "rf_paged_plan": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "rf_attn_paged_workspace_bytes": (_SZ, [_I]),
+    "rf_attn_paged": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I, _P, _I64,
+                           _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _I, _P]),
+    "rf_draft_verify_workspace_bytes": (_SZ, [_I, _I]),
+    "rf_draft_verify": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _SZ, _I, _P]),
     "rf_fp8_gemm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "rf_debug_set_visited": (_I, [_P, _I64]),
     "rf_debug_inject_fault": (_I, [_I]),
@@ -550,6 +561,229 @@ def splitk_merge(o_part, lse_part, out_dtype=torch.bfloat16):
             _ptr(o_part), _ptr(lse_part), _ptr(o), _ptr(lse), rows, nsplit, d, o_part.stride(1),
             o_part.stride(0), lse_part.stride(1), lse_part.stride(0), out_dt, _stream()))
     return o, lse
+
+
+def _same_device(*ts):
+    """The one CUDA device of the tensors that are given."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must live on one device")
+    return dev
+
+
+def _expect(t, name, dtype, shape, optional=False):
+    """A contiguous tensor of this dtype and shape (None where that is allowed)."""
+    if t is None and optional:
+        return
+    if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s"
+                         % (name, dtype, tuple(shape)))
+
+
+def _pool(cache, name, Hkv, d, dtype):
+    """Strides (page, token, head) of a [pages, page, Hkv, d] pool (any strided view
+    whose last dimension is contiguous)."""
+    if cache.dim() != 4 or tuple(cache.shape[2:]) != (Hkv, d) or cache.dtype != dtype:
+        raise ValueError("%s must be a %s pool [pages, page, %d, %d]" % (name, dtype, Hkv, d))
+    if cache.stride(3) != 1:
+        raise ValueError("%s's last dimension must be contiguous" % name)
+    return cache.stride(0), cache.stride(1), cache.stride(2)
+
+
+def _rows(x, name, T, heads, d, dtype):
+    """Token stride of [T, heads, d] rows whose heads are back to back."""
+    if x.dim() != 3 or tuple(x.shape) != (T, heads, d) or x.dtype != dtype:
+        raise ValueError("%s must be a %s tensor [%d, %d, %d]" % (name, dtype, T, heads, d))
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+        raise ValueError("%s: a token's heads must lie back to back" % name)
+    return x.stride(0) if T > 1 else heads * d
+
+
+def paged_slots(cu_q, kv_len, block_table, page_size, num_pages, total_q):
+    """rf_paged_slots: where a step's new tokens go -> (pos int32 [T], slots int64
+    [T]). cu_q int32 [B + 1], kv_len int32 [B] (with the new tokens),
+    block_table int32 [B, max_pages] (rows may be strided)."""
+    dev = _same_device(cu_q, kv_len, block_table)
+    B = kv_len.shape[0]
+    _expect(cu_q, "cu_q", torch.int32, (B + 1,))
+    _expect(kv_len, "kv_len", torch.int32, (B,))
+    stride, width = _table(block_table, B)
+    pos = torch.empty(total_q, dtype=torch.int32, device=dev)
+    slots = torch.empty(total_q, dtype=torch.int64, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().rf_paged_slots(_ptr(cu_q), _ptr(kv_len), _ptr(block_table), stride, B,
+                                    int(total_q), width, int(page_size), int(num_pages),
+                                    _ptr(pos), _ptr(slots), _stream()))
+    return pos, slots
+
+
+def _table(block_table, B):
+    if block_table.dim() != 2 or block_table.shape[0] != B or \
+            block_table.dtype != torch.int32 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages] with contiguous rows")
+    width = block_table.shape[1]
+    return (block_table.stride(0) if B > 1 else width), width
+
+
+def kv_append_paged(q, k, v, k_cache, v_cache, slots, pos=None, cos_sin=None, q_weight=None,
+                    k_weight=None, eps=1e-6, interleaved=False, q_out=None):
+    """rf_kv_append_paged: write a step's keys and values into their pages, with
+    the head norm (q_weight, k_weight [d]) and the rotation (cos_sin float32
+    [max_pos, rot], pos int32 [T]) of queries and keys on the way.
+
+    q [T, H, d] (or None), k, v [T, Hkv, d] (views of a fused projection fit),
+    k_cache, v_cache [pages, page, Hkv, d] (any strides with d contiguous),
+    slots int64 [T] (negative: skipped) -> q_out [T, H, d], or None without q.
+    q_out may be q itself when q is contiguous."""
+    dev = _same_device(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight, k_weight, q_out)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, d]")
+    T, Hkv, d = k.shape
+    ks, vs = _rows(k, "k", T, Hkv, d, k.dtype), _rows(v, "v", T, Hkv, d, k.dtype)
+    H, qs = 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, H, d]")
+        H = q.shape[1]
+        qs = _rows(q, "q", T, H, d, k.dtype)
+        if q_out is None:
+            q_out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+        _expect(q_out, "q_out", k.dtype, (T, H, d))
+    kst = _pool(k_cache, "k_cache", Hkv, d, k.dtype)
+    vst = _pool(v_cache, "v_cache", Hkv, d, k.dtype)
+    if v_cache.shape[:2] != k_cache.shape[:2]:
+        raise ValueError("k_cache and v_cache must have the same pages")
+    _expect(slots, "slots", torch.int64, (T,))
+    _expect(q_weight, "q_weight", k.dtype, (d,), optional=True)
+    _expect(k_weight, "k_weight", k.dtype, (d,), optional=True)
+    rot, max_pos = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 tensor [max_pos, rot]")
+        max_pos, rot = cos_sin.shape
+        _expect(pos, "pos", torch.int32, (T,))
+    with torch.cuda.device(dev):
+        _check(lib().rf_kv_append_paged(
+            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_out if q is not None else None),
+            _ptr(k_cache), *kst, _ptr(v_cache), *vst, T, H, Hkv, d, k_cache.shape[1],
+            k_cache.shape[0], _ptr(slots), _ptr(pos), _ptr(cos_sin), max_pos, rot,
+            1 if interleaved else 0, _ptr(q_weight), _ptr(k_weight), float(eps), _dt(k),
+            _stream()))
+    return q_out if q is not None else None
+
+
+class PagedPlan:
+    """rf_paged_plan: a step's paged attention divided among the SMs, on the device.
+
+    Made once a step from cu_q int32 [B + 1] and kv_len int32 [B] (with the new
+    tokens) and read by the ``attn_paged`` of every layer; it keeps its own
+    copy of the lengths. ``update`` makes it again in place, for a captured
+    step whose lengths change."""
+
+    def __init__(self, cu_q, kv_len, total_q, H, Hkv, page_size, max_pages, causal=True):
+        self.B, self.T, self.H, self.Hkv = kv_len.shape[0], int(total_q), int(H), int(Hkv)
+        self.page, self.max_pages, self.causal = int(page_size), int(max_pages), bool(causal)
+        dev = _same_device(cu_q, kv_len)
+        self.buf = torch.empty(int(lib().rf_paged_plan_bytes(self.B)), dtype=torch.uint8,
+                               device=dev)
+        self.update(cu_q, kv_len)
+
+    def update(self, cu_q, kv_len):
+        """The plan for new lengths of the same batch size."""
+        _same_device(cu_q, kv_len, self.buf)
+        _expect(cu_q, "cu_q", torch.int32, (self.B + 1,))
+        _expect(kv_len, "kv_len", torch.int32, (self.B,))
+        with torch.cuda.device(self.buf.device):
+            _check(lib().rf_paged_plan(_ptr(cu_q), _ptr(kv_len), self.B, self.T, self.H, self.Hkv,
+                                       self.page, self.max_pages, 1 if self.causal else 0,
+                                       _ptr(self.buf), self.buf.numel(), _stream()))
+        return self
+
+
+def attn_paged_workspace(d, device="cuda"):
+    """A workspace for ``attn_paged`` with head dimension d (calls that may
+    overlap need one each)."""
+    n = int(lib().rf_attn_paged_workspace_bytes(int(d)))
+    return torch.empty(max(1, n // 4), dtype=torch.float32, device=device)
+
+
+def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse=None,
+               with_lse=True, workspace=None):
+    """rf_attn_paged: q [T, H, d] bf16 (a strided view of a fused projection
+    fits), k_cache, v_cache [pages, page, Hkv, d] (any strides with d
+    contiguous), block_table int32 [B, max_pages], plan a ``PagedPlan`` of the
+    step -> (o [T, H, d], lse float32 [T, H] or None)."""
+    dev = _same_device(q, k_cache, v_cache, block_table, plan.buf, out, lse, workspace)
+    if q.dim() != 3 or q.shape[:2] != (plan.T, plan.H):
+        raise ValueError("q must be [%d, %d, d], as the plan was made for" % (plan.T, plan.H))
+    T, H, d = q.shape
+    qs = _rows(q, "q", T, H, d, q.dtype)
+    kst = _pool(k_cache, "k_cache", plan.Hkv, d, q.dtype)
+    vst = _pool(v_cache, "v_cache", plan.Hkv, d, q.dtype)
+    if v_cache.shape[:2] != k_cache.shape[:2] or k_cache.shape[1] != plan.page:
+        raise ValueError("k_cache and v_cache must have the same pages, of the plan's size")
+    stride, width = _table(block_table, plan.B)
+    if width != plan.max_pages:
+        raise ValueError("block_table must be as wide as the plan's max_pages")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty((T, H, d), dtype=q.dtype, device=dev) if out is None else out
+    _expect(o, "out", q.dtype, (T, H, d))
+    if lse is None and with_lse:
+        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    _expect(lse, "lse", torch.float32, (T, H), optional=True)
+    ws = attn_paged_workspace(d, dev) if workspace is None else workspace
+    _cuda(ws)
+    with torch.cuda.device(dev):
+        _check(lib().rf_attn_paged(
+            _ptr(q), qs, _ptr(k_cache), *kst, _ptr(v_cache), *vst, plan.page, k_cache.shape[0],
+            _ptr(block_table), stride, width, _ptr(plan.buf), plan.B, T, H, plan.Hkv, d,
+            float(scale), _ptr(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _dt(q),
+            _stream()))
+    return o, lse
+
+
+def draft_verify_workspace(B, S, device="cuda"):
+    """A workspace for ``draft_verify`` of B sequences and up to S drafts."""
+    n = int(lib().rf_draft_verify_workspace_bytes(int(B), int(S)))
+    return torch.empty(max(1, n), dtype=torch.uint8, device=device)
+
+
+def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None, workspace=None):
+    """rf_draft_verify: target logits [B, S + 1, V], draft logits [B, S, V] (or
+    None: drafts with certainty), tokens int32 [B, S], u float32 [B, S] in
+    [0, 1), expo float32 [B, V] exponential variates, n_draft int32 [B],
+    temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1], n_accepted
+    int32 [B])."""
+    dev = _same_device(target, draft, tokens, u, expo, n_draft, temperature, workspace)
+    if target.dim() != 3 or target.shape[1] < 2:
+        raise ValueError("target must be [B, S + 1, V] with S >= 1")
+    B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    _expect(target, "target", target.dtype, (B, S + 1, V))
+    _expect(draft, "draft", target.dtype, (B, S, V), optional=True)
+    _expect(tokens, "tokens", torch.int32, (B, S))
+    _expect(u, "u", torch.float32, (B, S))
+    _expect(expo, "expo", torch.float32, (B, V))
+    _expect(n_draft, "n_draft", torch.int32, (B,), optional=True)
+    _expect(temperature, "temperature", torch.float32, (B,), optional=True)
+    out = torch.empty(B, S + 1, dtype=torch.int32, device=dev)
+    n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    ws = draft_verify_workspace(B, S, dev) if workspace is None else workspace
+    _cuda(ws)
+    with torch.cuda.device(dev):
+        _check(lib().rf_draft_verify(
+            _ptr(target), _ptr(draft), _ptr(tokens), _ptr(u), _ptr(expo), _ptr(n_draft),
+            _ptr(temperature), B, S, V, _ptr(out), _ptr(n_accepted), _ptr(ws),
+            ws.numel() * ws.element_size(), _dt(target), _stream()))
+    return out, n_accepted
 
 
 def set_debug_visited(buf):

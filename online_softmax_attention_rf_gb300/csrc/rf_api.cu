@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include "paged_plan.h"
 #include "rf_internal.h"
 
 namespace {
@@ -221,6 +222,25 @@ rf_status attn_prepare(const char* fn, const void* q, const void* k, const void*
   a.visited = visited;
   a.status = st;
   return ok();
+}
+
+// Sizes shared by the paged-cache entry points.
+rf_status check_pool(const char* fn, int B, int T, int page, int num_pages, int max_pages) {
+  if (B < 0 || T < 0 || page < 1 || num_pages < 1 || max_pages < 1)
+    return fail(RF_ERR_INVALID, "%s: bad sizes B=%d T=%d page=%d num_pages=%d max_pages=%d", fn, B,
+                T, page, num_pages, max_pages);
+  if (B > (1 << 20) || T > (1 << 28))
+    return fail(RF_ERR_INVALID, "%s: need B <= 2^20 and T <= 2^28", fn);
+  if (int64_t(page) * num_pages > INT32_MAX || int64_t(page) * max_pages > INT32_MAX)
+    return fail(RF_ERR_INVALID, "%s: more than 2^31-1 cached tokens", fn);
+  return RF_OK;
+}
+
+rf_status check_heads(const char* fn, int H, int Hkv) {
+  if (H < 1 || Hkv < 1 || H % Hkv != 0)
+    return fail(RF_ERR_INVALID, "%s: bad head counts H=%d Hkv=%d", fn, H, Hkv);
+  if (H / Hkv > 128) return fail(RF_ERR_UNSUPPORTED, "%s: H/Hkv > 128", fn);
+  return RF_OK;
 }
 
 }  // namespace
@@ -650,6 +670,229 @@ rf_status rf_mla_decode(const void* q, const void* kv, void* o, float* lse, int 
   if (e != cudaSuccess) return cuda_fail(e, "rf_mla_decode: partials launch");
   e = rf::launch_splitk_merge(o_part, lse_part, o, lse, int64_t(B) * 128, nsplit, 512, RF_BF16, s);
   if (e != cudaSuccess) return cuda_fail(e, "rf_mla_decode: merge launch");
+  return ok();
+}
+
+rf_status rf_paged_slots(const int32_t* cu_q, const int32_t* kv_len, const int32_t* table,
+                         int64_t table_stride, int B, int T, int max_pages, int page,
+                         int num_pages, int32_t* pos, int64_t* slots, rf_stream stream) {
+  const char* fn = "rf_paged_slots";
+  const rf_status chk = check_pool(fn, B, T, page, num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  if (T == 0) return ok();
+  if (cu_q == nullptr || pos == nullptr || slots == nullptr ||
+      (B > 0 && (kv_len == nullptr || table == nullptr)))
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(table, 4) || !aligned(pos, 4) ||
+      !aligned(slots, 8))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  if (table_stride < max_pages && B > 1)
+    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  cudaError_t e = rf::launch_paged_slots(cu_q, kv_len, table, table_stride, B, T, max_pages, page,
+                                         num_pages, pos, slots,
+                                         reinterpret_cast<cudaStream_t>(stream), st);
+  if (e != cudaSuccess) return cuda_fail(e, "rf_paged_slots: launch");
+  return ok();
+}
+
+rf_status rf_kv_append_paged(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, void* q_out, void* k_cache,
+                             int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             void* v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                             int64_t v_head_stride, int T, int H, int Hkv, int d, int page,
+                             int num_pages, const int64_t* slots, const int32_t* pos,
+                             const float* cos_sin, int max_pos, int rot, int interleaved,
+                             const void* q_weight, const void* k_weight, float eps, rf_dtype dt,
+                             rf_stream stream) {
+  const char* fn = "rf_kv_append_paged";
+  const rf_status chk = check_pool(fn, 0, T, page, num_pages, 1);
+  if (chk != RF_OK) return chk;
+  if (Hkv < 1 || d < 1 || rot < 0 || rot > d || (q != nullptr && H < 1))
+    return fail(RF_ERR_INVALID, "%s: bad sizes H=%d Hkv=%d d=%d rot=%d", fn, H, Hkv, d, rot);
+  if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
+  if (d % 16 != 0 || d > 256 || rot % 16 != 0)
+    return fail(RF_ERR_UNSUPPORTED, "%s: d and rot must be multiples of 16, d <= 256", fn);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(RF_ERR_INVALID, "%s: interleaved must be 0/1", fn);
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(RF_ERR_INVALID, "%s: eps must be finite and >= 0", fn);
+  if (q == nullptr) { H = 0; q_out = nullptr; q_weight = nullptr; q_stride = 0; }
+  if (int64_t(H) + 2 * int64_t(Hkv) > (1 << 20))
+    return fail(RF_ERR_INVALID, "%s: more than 2^20 heads", fn);
+  if (T == 0) return ok();
+  if (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr ||
+      slots == nullptr || (q != nullptr && q_out == nullptr) ||
+      (rot > 0 && (pos == nullptr || cos_sin == nullptr)))
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (rot > 0 && max_pos < 1) return fail(RF_ERR_INVALID, "%s: max_pos must be >= 1", fn);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16) || !aligned(slots, 8) ||
+      (rot > 0 && (!aligned(pos, 4) || !aligned(cos_sin, 16))))
+    return fail(RF_ERR_INVALID, "%s: tensors must be 16-byte aligned (slots 8, pos 4)", fn);
+  const int64_t unit = dt == RF_F32 ? 4 : 8;  // elements in 16 bytes
+  const int64_t strides[] = {q_stride, k_stride, v_stride, k_page_stride, k_token_stride,
+                             k_head_stride, v_page_stride, v_token_stride, v_head_stride};
+  for (int64_t x : strides)
+    if (x < 0 || x % unit != 0)
+      return fail(RF_ERR_INVALID, "%s: strides must be multiples of 16 bytes", fn);
+  if ((q != nullptr && T > 1 && q_stride < int64_t(H) * d) ||
+      (T > 1 && (k_stride < int64_t(Hkv) * d || v_stride < int64_t(Hkv) * d)))
+    return fail(RF_ERR_INVALID, "%s: a token's heads overlap the next token's", fn);
+  if (q != nullptr && q_out == q && T > 1 && q_stride != int64_t(H) * d)
+    return fail(RF_ERR_INVALID, "%s: q_out may be q only when q_stride == H * d", fn);
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::KvAppendArgs a{};
+  a.q = q; a.k = k; a.v = v; a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.T = T; a.H = H; a.Hkv = Hkv; a.d = d; a.page = page; a.num_pages = num_pages;
+  a.slots = slots; a.pos = pos; a.cos_sin = cos_sin; a.max_pos = max_pos; a.rot = rot;
+  a.interleaved = interleaved;
+  a.q_weight = q_weight; a.k_weight = k_weight;
+  a.norm = q_weight != nullptr || k_weight != nullptr;
+  a.eps = eps;
+  a.status = st;
+  cudaError_t e = rf::launch_kv_append(a, dt, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_kv_append_paged: launch");
+  return ok();
+}
+
+size_t rf_paged_plan_bytes(int B) { return B < 0 ? 0 : rf::plan_bytes(B); }
+
+rf_status rf_paged_plan(const int32_t* cu_q, const int32_t* kv_len, int B, int T, int H, int Hkv,
+                        int page, int max_pages, int causal, void* plan, size_t plan_bytes,
+                        rf_stream stream) {
+  const char* fn = "rf_paged_plan";
+  rf_status chk = check_pool(fn, B, T, page, 1, max_pages);
+  if (chk != RF_OK) return chk;
+  chk = check_heads(fn, H, Hkv);
+  if (chk != RF_OK) return chk;
+  if (causal != 0 && causal != 1) return fail(RF_ERR_INVALID, "%s: causal must be 0/1", fn);
+  if (cu_q == nullptr || (B > 0 && kv_len == nullptr) || plan == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(plan, 256))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer (plan: 256 bytes)", fn);
+  if (plan_bytes < rf::plan_bytes(B))
+    return fail(RF_ERR_INVALID, "%s: plan too small (%zu < %zu)", fn, plan_bytes,
+                rf::plan_bytes(B));
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::PagedPlanArgs a{};
+  a.cu_q = cu_q; a.kv_len = kv_len;
+  a.B = B; a.T = T; a.H = H; a.Hkv = Hkv; a.page = page; a.max_pages = max_pages;
+  a.causal = causal; a.plan = plan; a.status = st;
+  cudaError_t e = rf::launch_paged_plan(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_paged_plan: launch");
+  return ok();
+}
+
+size_t rf_attn_paged_workspace_bytes(int d) {
+  if (d != 64 && d != 128) return 0;
+  // two partial query tiles pairs per CTA: d accumulators and a log-sum-exp a row
+  return size_t(2) * rf::kPlanCtas * rf::kPlanRows * (size_t(d) + 1) * sizeof(float);
+}
+
+rf_status rf_attn_paged(const void* q, int64_t q_stride, const void* k_cache,
+                        int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        const void* v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, int page, int num_pages, const int32_t* table,
+                        int64_t table_stride, int max_pages, const void* plan, int B, int T, int H,
+                        int Hkv, int d, float scale, void* o, float* lse, float* ws,
+                        size_t ws_bytes, rf_dtype dt, rf_stream stream) {
+  const char* fn = "rf_attn_paged";
+  rf_status chk = check_pool(fn, B, T, page, num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  chk = check_heads(fn, H, Hkv);
+  if (chk != RF_OK) return chk;
+  if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
+  if (dt != RF_BF16 || (d != 64 && d != 128))
+    return fail(RF_ERR_UNSUPPORTED, "%s: bf16 with d in {64,128} only", fn);
+  if (page % 8 != 0) return fail(RF_ERR_UNSUPPORTED, "%s: page must be a multiple of 8", fn);
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(RF_ERR_INVALID, "%s: scale must be finite and > 0", fn);
+  if (T == 0 || B == 0) return ok();
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || table == nullptr ||
+      plan == nullptr || o == nullptr || ws == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
+    return fail(RF_ERR_INVALID, "%s: q, k_cache, v_cache and o must be 16-byte aligned", fn);
+  if (!aligned(table, 4) || !aligned(lse, 4) || !aligned(plan, 256) || !aligned(ws, 256))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer (plan, ws: 256 bytes)", fn);
+  const int64_t strides[] = {q_stride,      k_page_stride, k_token_stride, k_head_stride,
+                             v_page_stride, v_token_stride, v_head_stride};
+  for (int64_t x : strides)
+    if (x <= 0 || x % 8 != 0 || x >= (int64_t(1) << 38))
+      return fail(RF_ERR_INVALID, "%s: strides must be positive multiples of 8 elements", fn);
+  if (q_stride < int64_t(H) * d && T > 1)
+    return fail(RF_ERR_INVALID, "%s: q_stride < H * d", fn);
+  if (table_stride < max_pages && B > 1)
+    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
+  if (ws_bytes < rf_attn_paged_workspace_bytes(d))
+    return fail(RF_ERR_INVALID, "%s: workspace too small (%zu < %zu)", fn, ws_bytes,
+                rf_attn_paged_workspace_bytes(d));
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::PagedAttnArgs a{};
+  a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.page = page; a.num_pages = num_pages; a.table = table; a.table_stride = table_stride;
+  a.max_pages = max_pages; a.plan = plan;
+  a.B = B; a.T = T; a.H = H; a.Hkv = Hkv; a.d = d; a.scale = scale;
+  a.o = o; a.lse = lse; a.ws = ws; a.status = st;
+  const char* why = nullptr;
+  cudaError_t e = rf::launch_attn_paged(a, reinterpret_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why != nullptr)
+    return fail(RF_ERR_CUDA, "%s: %s: %s", fn, why, cudaGetErrorString(e));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_attn_paged: launch");
+  return ok();
+}
+
+size_t rf_draft_verify_workspace_bytes(int B, int S) {
+  if (B < 1 || S < 1 || S > rf::kMaxDrafts) return 0;
+  return static_cast<size_t>((rf::draft_verify_stats(B, S) + 255) / 256 * 256);
+}
+
+rf_status rf_draft_verify(const void* target, const void* draft, const int32_t* tokens,
+                          const float* u, const float* expo, const int32_t* n_draft,
+                          const float* temperature, int B, int S, int V, int32_t* out,
+                          int32_t* n_accepted, void* ws, size_t ws_bytes, rf_dtype dt,
+                          rf_stream stream) {
+  const char* fn = "rf_draft_verify";
+  if (B < 0 || S < 1 || V < 1)
+    return fail(RF_ERR_INVALID, "%s: bad sizes B=%d S=%d V=%d", fn, B, S, V);
+  if (S > rf::kMaxDrafts) return fail(RF_ERR_UNSUPPORTED, "%s: S > %d", fn, rf::kMaxDrafts);
+  if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
+  if (B == 0) return ok();
+  if (B > (1 << 20)) return fail(RF_ERR_INVALID, "%s: B > 2^20", fn);
+  if (target == nullptr || tokens == nullptr || u == nullptr || expo == nullptr ||
+      out == nullptr || n_accepted == nullptr || ws == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  const uintptr_t es = dt == RF_F32 ? 4 : 2;
+  if (!aligned(target, es) || !aligned(draft, es) || !aligned(tokens, 4) || !aligned(u, 4) ||
+      !aligned(expo, 4) || !aligned(n_draft, 4) || !aligned(temperature, 4) || !aligned(out, 4) ||
+      !aligned(n_accepted, 4) || !aligned(ws, 16))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  if (ws_bytes < rf_draft_verify_workspace_bytes(B, S))
+    return fail(RF_ERR_INVALID, "%s: workspace too small (%zu < %zu)", fn, ws_bytes,
+                rf_draft_verify_workspace_bytes(B, S));
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::VerifyArgs a{};
+  a.target = target; a.draft = draft; a.tokens = tokens; a.u = u; a.expo = expo;
+  a.n_draft = n_draft; a.temperature = temperature;
+  a.B = B; a.S = S; a.V = V; a.out = out; a.n_accepted = n_accepted; a.status = st;
+  cudaError_t e = rf::launch_draft_verify(a, dt, ws, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_draft_verify: launch");
   return ok();
 }
 

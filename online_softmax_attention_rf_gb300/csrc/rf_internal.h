@@ -27,7 +27,10 @@ enum DevKernel : int {
   kKerMerge = 5,
   kKerBlockmask = 6,
   kKerFp8 = 7,
-  kKerMla = 8
+  kKerMla = 8,
+  kKerAppend = 9,
+  kKerVerify = 10,
+  kKerPaged = 11
 };
 
 __host__ __device__ constexpr int dev_code(int kind, int kernel, int site) {
@@ -91,6 +94,77 @@ struct AttnArgs {
   int* status;
 };
 
+// Arguments of one paged-cache append (validated on the host). Strides are in
+// elements; rows of q, k and v hold their heads back to back.
+struct KvAppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  int64_t q_stride, k_stride, v_stride;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int T, H, Hkv, d, page, num_pages;
+  const int64_t* slots;
+  const int32_t* pos;
+  const float* cos_sin;  // [max_pos, rot]: rot / 2 cosines, then rot / 2 sines
+  int max_pos, rot, interleaved;
+  const void* q_weight;
+  const void* k_weight;
+  int norm;  // either weight is given
+  float eps;
+  int* status;
+};
+
+// Arguments of one draft verification (validated on the host).
+constexpr int kMaxDrafts = 64;
+struct VerifyArgs {
+  const void* target;
+  const void* draft;
+  const int32_t* tokens;
+  const float* u;
+  const float* expo;
+  const int32_t* n_draft;
+  const float* temperature;
+  int B, S, V;
+  int32_t* out;
+  int32_t* n_accepted;
+  int* status;
+};
+
+// The step's division of work for rf_attn_paged, as rf_paged_plan leaves it in
+// device memory (paged_plan.h has the layout).
+struct PagedPlanArgs {
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int B, T, H, Hkv, page, max_pages, causal;
+  void* plan;
+  int* status;
+};
+
+// Arguments of one attention over a paged cache (validated on the host).
+struct PagedAttnArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k_cache;
+  const void* v_cache;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int page, num_pages;
+  const int32_t* table;
+  int64_t table_stride;
+  int max_pages;
+  const void* plan;
+  int B, T, H, Hkv, d;
+  float scale;
+  void* o;
+  float* lse;
+  float* ws;
+  int* status;
+};
+
 // Each launcher validates nothing (the entry points do) and returns the
 // launch error, if any.
 // skip_first_copy: fault injection (rf_debug_inject_fault site 1).
@@ -130,6 +204,15 @@ cudaError_t launch_moment_of_inertia(const float* points, const float* masses, i
                                      cudaStream_t s);
 cudaError_t launch_row_moments(const void* x, int64_t rows, int64_t cols, float eps, float* mean,
                                float* var, void* y, rf_dtype dt, cudaStream_t s);
+cudaError_t launch_kv_append(const KvAppendArgs& a, rf_dtype dt, cudaStream_t s);
+cudaError_t launch_paged_slots(const int32_t* cu_q, const int32_t* kv_len, const int32_t* table,
+                               int64_t table_stride, int B, int T, int max_pages, int page,
+                               int num_pages, int32_t* pos, int64_t* slots, cudaStream_t s,
+                               int* status);
+cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s);
+cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t s, const char** why);
+int64_t draft_verify_stats(int B, int S);  // bytes of the row statistics
+cudaError_t launch_draft_verify(const VerifyArgs& a, rf_dtype dt, void* ws, cudaStream_t s);
 // order[c] for c < items: the double items whose listed tiles exceed twice
 // the mean first, then the others, both ascending (one CTA).
 cudaError_t launch_cta_order(const int32_t* row_ptr, int per_head, int nqt, int BH, int32_t* order,

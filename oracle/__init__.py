@@ -28,9 +28,12 @@ Modules
                  inertia of point sets about their centre of mass, and
                  per-row FP8 (E4M3) absmax quantisation with the GEMM over
                  the quantised values.
+``paged``        serving over a paged key/value cache: slots, append with head
+                 norm and rotation, attention of new tokens over pages, and
+                 the verification of drafted tokens.
 
 Every function here is pinned by the ``-m "not gpu"`` tests in
-``tests/test_oracle_pins.py`` against brute force, closed forms, invariants
+``tests/test_oracle_pins.py`` (``paged``: ``test_oracle_paged.py``) against brute force, closed forms, invariants
 and library routines; none is "parity unpinned".
 """
 
