@@ -1,90 +1,971 @@
 // attn_paged.cu -- attention of a ragged batch's new tokens over a paged
-// key/value cache. Simple form: one warp per (token, head).
+// key/value cache, on the tcgen05 tensor cores.
+//
+// The cascade max -> sum exp -> normalised P.V in the incremental form of
+// attn_tc.cu (RedFuser: An Automatic Operator Fusion Framework for Cascaded
+// Reductions on AI Accelerators, section 2), with the multi-segment strategy
+// of section 3 across CTAs. Differences that the paged cache and the ragged
+// batch ask for:
+//  - Query rows are packed: the G query heads of one key head at one token are
+//    G neighbouring rows, so that a tile of 128 rows holds floor(128 / G)
+//    tokens and the keys of a group are read once for all its heads. A decode
+//    step is a tile with G live rows, drafted tokens one with a few times G.
+//  - Work is dealt by the step's plan (paged_plan.h): one persistent CTA per
+//    span of key tiles. A whole item is written by the CTA itself; a part goes
+//    to the workspace and attn_paged_merge joins the parts by log-sum-exp.
+//  - A key tile of 128 keys comes in boxes of R = gcd(page, 128) rows, one TMA
+//    copy per box and 64 columns, each lane of the producer warp looking up
+//    one box's page. Boxes that start past the cache's end are not copied; the
+//    rows of V between the end and the tile's edge are zeroed in shared memory
+//    before P.V (their weights are 0, but 0 * NaN is not).
+//  - An item of one tile (up to 128 packed rows) is worked on by both softmax
+//    groups: they take alternate key tiles and join their states at the end.
+//    With one group the chain Q K^T -> softmax -> P.V of a tile would not keep
+//    up with memory; with two it runs at twice the rate.
+//
+// Roles of the 352 threads, tensor memory, the lock and the reuse of S by P
+// are those of attn_tc.cu: warps 0-3 and 4-7 softmax groups, warp 8 producer,
+// warps 9 and 10 MMA issuers of the two groups. Every wait is bounded; on
+// expiry the kernel records a status code and the CTA unwinds.
+//
+// P is rounded to bf16 for the tensor cores (scores, maxima, sums and
+// accumulators stay in float32): half a step, 2^-8, of each weight. The row
+// sum takes the unrounded weights.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "paged_plan.h"
 #include "rf_device.cuh"
 
 namespace rf {
 namespace {
 
-__device__ __forceinline__ bool plan_matches(const PlanHeader* h, const PagedAttnArgs& a) {
-  return h->magic == kPlanMagic && h->B == a.B && h->T == a.T && h->H == a.H && h->Hkv == a.Hkv &&
-         h->page == a.page && h->max_pages == a.max_pages;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale when the max grows > 256x
+constexpr int kBM = kPlanTile;             // packed query rows per tile
+constexpr int kBN = kPlanTile;             // keys per tile
+constexpr int kThreads = 352;
+constexpr int kWarpLoad = 8;
+constexpr int kWarpIssue = 9;
+constexpr int kChunk = 16384;              // one 128-row x 64-column bf16 swizzle block
+
+template <int D>
+struct Layout {
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int kStages = (D == 128) ? 5 : 8;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = kOffQ + 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
+  static constexpr int kBarBytes = 256;
+  static constexpr int kOffXch = kOffBar + kBarBytes;  // group 1's m and l for group 0
+  static constexpr int kXchBytes = 2 * kBM * 4;
+  static constexpr int kBytes = kOffXch + kXchBytes + 1024;  // + alignment slack
+  static constexpr uint32_t kTmemS = 0;
+  static constexpr uint32_t kTmemO = 2 * kBN;
+  __host__ __device__ static constexpr uint32_t tmem_p(int t) {
+    return D == 128 ? kTmemS + t * kBN : kTmemO + 2 * D + t * 64;
+  }
+};
+
+struct Bars {
+  uint64_t kv_full[8];
+  uint64_t kv_empty[8];
+  uint64_t q_full[2];
+  uint64_t q_empty[2];
+  uint64_t s_full[2];
+  uint64_t o_done[2];
+  uint64_t mma_idle[2];
+  uint64_t split_ready;
+  uint64_t split_read;
+  uint32_t tmem_base;
+  int abort_flag;
+  int issue_lock;
+};
+static_assert(sizeof(Bars) <= Layout<64>::kBarBytes && sizeof(Bars) <= Layout<128>::kBarBytes,
+              "barrier block overflows its shared-memory slot");
+static_assert(Layout<64>::kBytes <= 227 * 1024 && Layout<128>::kBytes <= 227 * 1024,
+              "attention shared memory exceeds a CTA's limit");
+
+struct Params {
+  const PlanHeader* plan;
+  const int32_t* table;
+  int64_t table_stride;
+  int B, T, H, Hkv, page, max_pages, num_pages;
+  int G, tt;            // heads of a group, tokens of a tile
+  int box;              // rows of one copied box
+  int k_token_first, v_token_first;  // the map's dimension 1 is the token (else the head)
+  float scale_log2;
+  __nv_bfloat16* o;
+  float* lse;
+  float* o_part;    // [2 * kPlanCtas][kPlanRows][D]
+  float* lse_part;  // [2 * kPlanCtas][kPlanRows]
+  int* status;
+};
+
+__device__ __forceinline__ bool plan_matches(const PlanHeader* h, const Params& p) {
+  return h->magic == kPlanMagic && h->B == p.B && h->T == p.T && h->H == p.H && h->Hkv == p.Hkv &&
+         h->page == p.page && h->max_pages == p.max_pages;
+}
+
+__device__ __forceinline__ bool same_item(const PlanStart& a, const PlanStart& b) {
+  return a.seq == b.seq && a.head == b.head && a.pair == b.pair;
+}
+
+// One CTA's part of one item: steps [kb, ke) of the item's `steps`.
+struct Seg {
+  int seq, head;
+  int row0;        // the item's first token among the packed tokens
+  int tok0, ntok;  // the same within the sequence; tokens of the item
+  int n, kv;       // new and cached tokens of the sequence
+  int kb, ke, steps;
+  bool split;      // one tile, shared by both groups
+  int slot;        // partial slot, -1: the whole item
+};
+
+// Walks a CTA's span. Every role computes the same sequence of segments.
+struct Span {
+  PlanStart cur, end;
+  const int32_t* cu;
+  const int32_t* kvl;
+  int B, Hkv, tt, causal;
+
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (cur.seq >= B || (same_item(cur, end) && cur.step == end.step)) return false;
+    s.seq = cur.seq;
+    s.head = cur.head;
+    const int t0 = cu[cur.seq];
+    s.n = cu[cur.seq + 1] - t0;
+    s.kv = kvl[cur.seq];
+    s.tok0 = cur.pair * 2 * tt;
+    s.ntok = min(2 * tt, s.n - s.tok0);
+    s.row0 = t0 + s.tok0;
+    s.split = s.ntok <= tt;
+    s.steps = (plan_visible(s.tok0 + s.ntok - 1, s.n, s.kv, causal) + kBN - 1) / kBN;
+    s.kb = cur.step;
+    const int cta = static_cast<int>(blockIdx.x);
+    if (same_item(cur, end)) {
+      s.ke = min(s.steps, end.step);
+      cur = end;
+    } else {
+      s.ke = s.steps;
+      cur.step = 0;
+      if (s.tok0 + s.ntok < s.n) {
+        ++cur.pair;
+      } else {
+        cur.pair = 0;
+        if (++cur.head == Hkv) {
+          cur.head = 0;
+          do ++cur.seq;
+          while (cur.seq < B && cu[cur.seq + 1] == cu[cur.seq]);
+        }
+      }
+    }
+    s.slot = s.kb > 0 ? 2 * cta : s.ke < s.steps ? 2 * cta + 1 : -1;
+    return true;
+  }
+  // Steps that tile t of an item could need, of all its steps.
+  __device__ __forceinline__ int tile_steps(const Seg& s, int t) const {
+    if (s.split) return s.steps;
+    const int last = min(s.ntok, (t + 1) * tt) - 1;
+    return (plan_visible(s.tok0 + last, s.n, s.kv, causal) + kBN - 1) / kBN;
+  }
+  // Steps that group t takes in a segment.
+  __device__ __forceinline__ int group_steps(const Seg& s, int t) const {
+    if (s.split) return (s.ke - s.kb - t + 1) / 2;
+    return max(0, min(s.ke, tile_steps(s, t)) - s.kb);
+  }
+};
+
+__device__ __forceinline__ Span make_span(const Params& p) {
+  Span sp;
+  sp.cur = p.plan->start[blockIdx.x];
+  sp.end = p.plan->start[blockIdx.x + 1];
+  sp.cu = plan_cu_q(p.plan);
+  sp.kvl = plan_kv_len(p.plan, p.B);
+  sp.B = p.B;
+  sp.Hkv = p.Hkv;
+  sp.tt = p.tt;
+  sp.causal = p.plan->causal;
+  return sp;
+}
+
+// Named barrier of one group -- its four softmax warps and its issuer warp --
+// that also ORs a predicate over the group.
+__device__ __forceinline__ bool group_sync_or(int t, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 160, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(1 + t)
+      : "memory");
+  return r != 0;
+}
+
+// The MMA issue lock (attn_tc.cu): a block of MMAs reaches the pipe whole.
+__device__ __forceinline__ bool issue_lock(int* lk, int* status, int code,
+                                           volatile int* abort_flag) {
+  if (atomicCAS(lk, 0, 1) == 0) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    __nanosleep(32);
+    if (atomicCAS(lk, 0, 1) == 0) return true;
+    if (*abort_flag || globaltimer_ns() - t0 > RF_WAIT_LIMIT_NS) {
+      record_status(status, code);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void issue_unlock(int* lk) { atomicExch(lk, 0); }
+
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tm_s, uint64_t q_desc, uint64_t k_desc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunk + (kk & 3) * 32) >> 4);
+    mma_bf16(tm_s, q_desc + off, k_desc + off, idesc, kk > 0 ? 1u : 0u);
+  }
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) attn_paged_simple(const PagedAttnArgs a) {
-  constexpr int E = D / 32;
-  const PlanHeader* h = static_cast<const PlanHeader*>(a.plan);
-  if (!plan_matches(h, a)) {
-    record_status(a.status, dev_code(kDevBadList, kKerPaged, 2));
+__device__ __forceinline__ void issue_pv(uint32_t tm_o, uint32_t tm_p, uint64_t v_desc,
+                                         bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kBM, D, 1);
+#pragma unroll
+  for (int kk = 0; kk < kBN / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>((kk * 16 * 128) >> 4);
+    mma_bf16_ts(tm_o, tm_p + kk * 8, v_desc + off, idesc, (kk > 0 || accumulate) ? 1u : 0u);
+  }
+}
+
+// Where a packed row's result goes: O and LSE of the call, or the row of a
+// partial slot.
+template <int D>
+struct RowOut {
+  __nv_bfloat16* o;
+  float* part;
+  float* lse;
+};
+
+template <int D>
+__device__ __forceinline__ RowOut<D> row_out(const Params& p, const Seg& s, int t, int r) {
+  RowOut<D> w{nullptr, nullptr, nullptr};
+  if (s.slot >= 0) {
+    const int64_t row = int64_t(s.slot) * kPlanRows + t * kBM + r;
+    w.part = p.o_part + row * D;
+    w.lse = p.lse_part + row;
+  } else {
+    const int64_t row = int64_t(s.row0 + t * p.tt + r / p.G) * p.H + s.head * p.G + r % p.G;
+    w.o = p.o + row * D;
+    w.lse = p.lse != nullptr ? p.lse + row : nullptr;
+  }
+  return w;
+}
+
+// 32 columns of a finished row from column c on.
+template <int D>
+__device__ __forceinline__ void put32(const RowOut<D>& w, int c, const float (&v)[32]) {
+  if (w.part != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<float4*>(w.part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      uint4 x;
+      x.x = pack_bf16x2(v[e], v[e + 1]);
+      x.y = pack_bf16x2(v[e + 2], v[e + 3]);
+      x.z = pack_bf16x2(v[e + 4], v[e + 5]);
+      x.w = pack_bf16x2(v[e + 6], v[e + 7]);
+      *reinterpret_cast<uint4*>(w.o + c + e) = x;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using L = Layout<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(smem + L::kOffBar);
+  const uint32_t s_base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (!plan_matches(p.plan, p)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+      record_status(p.status, dev_code(kDevBadList, kKerPaged, 2));
     return;
   }
-  if (h->ctas == 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= int64_t(a.T) * a.H) return;
-  const int t = static_cast<int>(row / a.H), hd = static_cast<int>(row % a.H);
-  const int32_t* cu = plan_cu_q(a.plan);
-  const int32_t* kvl = plan_kv_len(a.plan, a.B);
-  int lo = 0, hi = a.B;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
-  }
-  if (lo >= a.B || cu[lo] > t) return;
-  const int n = cu[lo + 1] - cu[lo], kv = kvl[lo];
-  const int lim = plan_visible(t - cu[lo], n, kv, h->causal);
-  const int hk = hd / (a.H / a.Hkv);
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride + hd * D + lane * E;
-  float qv[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __bfloat162float(q[e]) * a.scale * kLog2e;
-    acc[e] = 0.f;
-  }
-  float m = kNegInf, l = 0.f;
-  for (int j = 0; j < lim; ++j) {
-    const int id = a.table[lo * a.table_stride + j / a.page];
-    if (id < 0 || id >= a.num_pages) {
-      record_status(a.status, dev_code(kDevBadList, kKerPaged, 3));
-      return;
+  if (static_cast<int>(blockIdx.x) >= p.plan->ctas) return;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bar.kv_full[i], 1);
+      mbar_init(&bar.kv_empty[i], 2);  // one release per softmax group
     }
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k_cache) + id * a.k_page_stride +
-                             (j % a.page) * a.k_token_stride + hk * a.k_head_stride + lane * E;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) + id * a.v_page_stride +
-                             (j % a.page) * a.v_token_stride + hk * a.v_head_stride + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += qv[e] * __bfloat162float(k[e]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s);
-    const float al = m == kNegInf ? 0.f : ex2_approx(m - mn);
-    const float p = s == kNegInf ? 0.f : ex2_approx(s - mn);
-    m = mn;
-    l = l * al + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + p * __bfloat162float(v[e]);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar.q_full[t], 1);
+      mbar_init(&bar.q_empty[t], 1);
+      mbar_init(&bar.s_full[t], 1);
+      mbar_init(&bar.o_done[t], 1);
+      mbar_init(&bar.mma_idle[t], 1);
+    }
+    mbar_init(&bar.split_ready, 4);
+    mbar_init(&bar.split_read, 4);
+    bar.abort_flag = 0;
+    bar.issue_lock = 0;
+    fence_barrier_init();
   }
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + row * D + lane * E;
+  if (warp == kWarpLoad) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bar.tmem_base;
+  volatile int* abort_flag = &bar.abort_flag;
+  Span span = make_span(p);
+
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ producer
+    // Per segment: the first K/V pair, then Q0 and Q1 (each once the previous
+    // segment's last QK on it has completed), then the remaining K/V pairs.
+    // Lane l copies box l % boxes, columns 64 (l / boxes) .. + 63, of a tile.
+    if (lane == 0) {
+      prefetch_tensormap(&tm_q);
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
+    const int boxes = kBN / p.box;
+    const int my_box = lane % boxes, my_chunk = lane / boxes;
+    int seq = 0;
+    int q_loads[2] = {0, 0};
+    bool ok = true;
+    Seg s;
+    while (ok && span.next(s)) {
+      const int32_t* row = p.table + int64_t(s.seq) * p.table_stride;
+      // this lane's page of tile u and the box's first row in it
+      auto page_of = [&](int u, int& in_page) -> int {
+        const int key = u * kBN + my_box * p.box;
+        in_page = 0;
+        if (my_chunk >= D / 64 || key >= s.kv) return -1;
+        const int pi = key / p.page;
+        in_page = key - pi * p.page;
+        return row[pi];
+      };
+      int in_page = 0, in_next = 0;
+      int id = s.kb < s.ke ? page_of(s.kb, in_page) : -1;
+      for (int u = s.kb; ok && u < s.ke; ++u) {
+        const int id_next = u + 1 < s.ke ? page_of(u + 1, in_next) : -1;
+        const int key = u * kBN + my_box * p.box;
+        const bool mine = my_chunk < D / 64 && key < s.kv;
+        if (mine && (id < 0 || id >= p.num_pages)) {
+          record_status(p.status, dev_code(kDevBadList, kKerPaged, 3));
+          id = p.num_pages;  // past the pool: the copy fills with zeros
+        }
+        const int n_box = min(boxes, (s.kv - u * kBN + p.box - 1) / p.box);
+        for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
+          const int slot = seq % NS;
+          if (lane == 0) {
+            ok = mbar_wait(&bar.kv_empty[slot], ((seq / NS) & 1) ^ 1, p.status,
+                           dev_code(kDevTimeout, kKerPaged, 10), abort_flag);
+            if (ok) mbar_arrive_expect_tx(&bar.kv_full[slot], n_box * p.box * D * 2);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (mine) {
+            unsigned char* dst = smem + L::kOffKV + slot * L::kTileBytes + my_chunk * kChunk +
+                                 my_box * p.box * 128;
+            const bool first = kv == 0 ? p.k_token_first : p.v_token_first;
+            tma_load_4d(dst, kv == 0 ? &tm_k : &tm_v, &bar.kv_full[slot], my_chunk * 64,
+                        first ? in_page : s.head, first ? s.head : in_page, id);
+          }
+        }
+        if (u == s.kb && ok && lane == 0) {
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (span.group_steps(s, t) == 0) continue;
+            if (q_loads[t] > 0)
+              ok = mbar_wait(&bar.q_empty[t], (q_loads[t] - 1) & 1, p.status,
+                             dev_code(kDevTimeout, kKerPaged, 12), abort_flag);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bar.q_full[t], p.G * p.tt * D * 2);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(smem + L::kOffQ + t * L::kTileBytes + c * kChunk, &tm_q, &bar.q_full[t],
+                          c * 64, 0, s.head, s.row0 + (s.split ? 0 : t * p.tt));
+            ++q_loads[t];
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        id = id_next;
+        in_page = in_next;
+      }
+    }
+    // never leave with copies in flight: the last load into each slot
+    if (lane == 0) {
+      for (int sq = max(0, seq - NS); sq < seq; ++sq)
+        mbar_wait(&bar.kv_full[sq % NS], (sq / NS) & 1, p.status,
+                  dev_code(kDevTimeout, kKerPaged, 11), nullptr);
+      for (int t = 0; t < 2; ++t)
+        if (q_loads[t] > 0)
+          mbar_wait(&bar.q_full[t], (q_loads[t] - 1) & 1, p.status,
+                    dev_code(kDevTimeout, kKerPaged, 13), nullptr);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpIssue) {
+    // ------------------------------------------------------------ MMA issuers
+    const int t = warp - kWarpIssue;
+    bool ok = true;
+    const uint64_t q_desc = sdesc_sw128(s_base + L::kOffQ + t * L::kTileBytes, 16, 1024);
+    const uint64_t k_desc0 = sdesc_sw128(s_base + L::kOffKV, 16, 1024);
+    const uint64_t v_desc0 = sdesc_sw128(s_base + L::kOffKV, kChunk, 1024);
+    const uint32_t mm_s = tmem + L::kTmemS + t * kBN;
+    const uint32_t mm_o = tmem + L::kTmemO + t * D;
+    const uint32_t mm_p = tmem + L::tmem_p(t);
+    int seq = 0;              // K/V sequence number of the next step
+    int vseq = 0;             // V tile of the step whose QK was issued last
+    int nq = 0;               // segments whose Q_t was waited for
+    int n_iss = 0, n_seg = 0; // steps of the started segment issued so far, and all of them
+    int started = -1;         // last segment whose first QK was issued
+    bool issued_any = false;
+    Span ahead = span;        // the segment being started (lane 0)
+    Seg a{};
+    int u_next = 0, a_end = 0;  // its next step, and this group's bound in a pair
+#define RF_WAIT(b, par, site)                                                         \
+  mbar_wait(&bar.b, (par), p.status, dev_code(kDevTimeout, kKerPaged, site), abort_flag)
+#define RF_SLOT(sq) (static_cast<uint64_t>((((sq) % NS) * L::kTileBytes) >> 4))
+#define RF_LOCK() issue_lock(&bar.issue_lock, p.status, dev_code(kDevTimeout, kKerPaged, 23), abort_flag)
+    auto needs = [&](int u) { return a.split ? ((u - a.kb) & 1) == t : u < a_end; };
+    // The next step this group takes; steps that only the other group takes are
+    // released (both slots) once they have landed. False at the segment's end.
+    auto advance = [&](int& kseq) -> bool {
+      while (u_next < a.ke) {
+        const int u = u_next++;
+        const int ks = seq;
+        seq += 2;
+        if (needs(u)) {
+          kseq = ks;
+          return true;
+        }
+        for (int e = 0; e < 2; ++e) {
+          if (!(ok = RF_WAIT(kv_full[(ks + e) % NS], ((ks + e) / NS) & 1, 20))) return false;
+          mbar_arrive(&bar.kv_empty[(ks + e) % NS]);
+        }
+      }
+      return false;
+    };
+    auto next_k = [&](int& kseq) -> bool {
+      if (!advance(kseq)) return false;
+      return (ok = RF_WAIT(kv_full[kseq % NS], (kseq / NS) & 1, 21));
+    };
+    auto qk_commits = [&](int kseq) {
+      mma_commit(&bar.s_full[t]);
+      mma_commit(&bar.kv_empty[kseq % NS]);
+      if (++n_iss == n_seg) mma_commit(&bar.q_empty[t]);  // the segment's last read of Q_t
+      vseq = kseq + 1;
+    };
+    auto start_segment = [&](int k) {
+      started = k;
+      if (!ahead.next(a)) return;
+      u_next = a.kb;
+      a_end = a.split ? a.ke : ahead.tile_steps(a, t);
+      n_iss = 0;
+      n_seg = ahead.group_steps(a, t);
+      int kseq;
+      if (n_seg == 0) {
+        advance(kseq);  // releases every step; returns false
+        return;
+      }
+      if (!(ok = RF_WAIT(q_full[t], nq & 1, 22))) return;
+      ++nq;
+      if (next_k(kseq) && (ok = RF_LOCK())) {
+        tc_fence_after_sync();
+        issue_qk<D>(mm_s, q_desc, k_desc0 + RF_SLOT(kseq));
+        issue_unlock(&bar.issue_lock);
+        issued_any = true;
+        qk_commits(kseq);
+      }
+    };
+
+    Seg s;
+    for (int item = 0; span.next(s); ++item) {
+      const int n = span.group_steps(s, t);
+      if (lane == 0 && started < item) start_segment(item);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int jj = 0; jj < n; ++jj) {
+        // While the softmax runs: wait for V_u, zero its rows past the cache's
+        // end, and, when the next step is this group's, wait for its K tile.
+        // Waiting for that tile before this step's P.V is safe: the slot it is
+        // loaded into was freed by releases committed in earlier blocks.
+        const bool last = jj + 1 == n;
+        const int u = s.kb + (s.split ? 2 * jj + t : jj);
+        int k2 = 0;
+        bool fast = false;
+        if (lane == 0 && ok) ok = RF_WAIT(kv_full[vseq % NS], (vseq / NS) & 1, 24);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        const int rows = s.kv - u * kBN;
+        if (ok && rows < kBN) {
+          const int vs = __shfl_sync(0xffffffffu, vseq, 0) % NS;
+          unsigned char* v = smem + L::kOffKV + vs * L::kTileBytes;
+          for (int i = rows * 8 + lane; i < kBN * 8; i += 32)
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = __float2bfloat16(l > 0.f ? acc[e] / l : 0.f);
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+            for (int c = 0; c < D / 64; ++c)
+              *reinterpret_cast<uint4*>(v + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0 && ok && !last) fast = next_k(k2);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        // P_t is in tensor memory
+        if (group_sync_or(t, !ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0 && (ok = RF_LOCK())) {
+          tc_fence_after_sync();
+          issue_pv<D>(mm_o, mm_p, v_desc0 + RF_SLOT(vseq), jj > 0);
+          if (fast) issue_qk<D>(mm_s, q_desc, k_desc0 + RF_SLOT(k2));
+          issue_unlock(&bar.issue_lock);
+          const int v_done = vseq;
+          if (fast) qk_commits(k2);
+          mma_commit(&bar.kv_empty[v_done % NS]);
+          if (last) mma_commit(&bar.o_done[t]);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      if (group_sync_or(t, !ok)) {  // after the segment's steps
+        ok = false;
+        break;
+      }
+      // while the softmax warps write this segment's output: release the steps
+      // after this group's last, and start the next segment
+      if (lane == 0 && n > 0) {
+        int k2;
+        advance(k2);
+        if (ok) start_segment(item + 1);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (group_sync_or(t, !ok)) {  // after the segment's epilogue
+        ok = false;
+        break;
+      }
+    }
+#undef RF_WAIT
+#undef RF_SLOT
+#undef RF_LOCK
+    // never leave with MMAs in flight (their operands live in this CTA)
+    if (lane == 0 && issued_any) {
+      mma_commit(&bar.mma_idle[t]);
+      mbar_wait(&bar.mma_idle[t], 0, p.status, dev_code(kDevTimeout, kKerPaged, 28), nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax groups
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;     // row within the tile == TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + L::kTmemS + t * kBN + lane_off;
+    const uint32_t tm_o = tmem + L::kTmemO + t * D + lane_off;
+    const uint32_t tm_p = tmem + L::tmem_p(t) + lane_off;
+    const int row_tok = r / p.G;
+    int j = 0;                           // S tiles consumed (all segments)
+    int o_segs = 0;                      // segments whose final P.V was waited for
+    int n_split = 0;                     // split segments so far
+    bool ok = true;
+    Seg s;
+    while (span.next(s)) {
+      const int tile = s.split ? 0 : t;              // the group's query tile
+      const int tok = tile * p.tt + row_tok;         // token within the item
+      const bool row_ok = row_tok < p.tt && tok < s.ntok;
+      // a warp without live rows leaves the softmax to the others
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+      const int n = span.group_steps(s, t);
+      // keys this row sees, and the fewest any row of the tile sees; a row that
+      // holds no token computes on whatever is there and is not written
+      const int row_lim = row_ok ? plan_visible(s.tok0 + tok, s.n, s.kv, span.causal) : s.kv;
+      const int first_lim = plan_visible(s.tok0 + tile * p.tt, s.n, s.kv, span.causal);
+      float m_run = kNegInf, l_run = 0.f;
+      for (int jj = 0; jj < n; ++jj, ++j) {
+        const int u = s.kb + (s.split ? 2 * jj + t : jj);
+        if (ok && warp_ok)
+          ok = mbar_wait_warp(&bar.s_full[t], j & 1, p.status,
+                              dev_code(kDevTimeout, kKerPaged, 30), abort_flag);
+        if (ok && warp_ok) {
+          tc_fence_after_sync();
+          const int k0 = u * kBN;
+          const int lim = (k0 + kBN > first_lim) ? max(0, min(kBN, row_lim - k0)) : kBN;
+          float mx;
+          {
+            uint32_t sr[128];
+            tmem_ld128_wait(tm_s, sr);
+            if (lim < kBN) {
+#pragma unroll
+              for (int c = 0; c < kBN; ++c)
+                if (c >= lim) sr[c] = __float_as_uint(kNegInf);
+            }
+            float m8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m8[i] = kNegInf;
+#pragma unroll
+            for (int c = 0; c < kBN; c += 2)
+              m8[(c >> 1) & 7] = fmax3(m8[(c >> 1) & 7], __uint_as_float(sr[c]),
+                                       __uint_as_float(sr[c + 1]));
+            mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                       fmaxf(m8[6], m8[7]));
+          }
+          const float m_new = (mx == kNegInf) ? m_run : fmaxf(m_run, mx * p.scale_log2);
+          const bool resc = m_new > m_run + kRescaleThreshold;
+          const float m_use = resc ? m_new : m_run;
+          const float alpha = resc ? ex2_approx(m_run - m_new) : 1.f;
+          const float sh = (m_use == kNegInf) ? 0.f : m_use;
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+          const float2 nsh2 = make_float2(-sh, -sh);
+          float2 s4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s4[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t sh1[64];
+            tmem_ld64_wait(tm_s + 64 * h, sh1);
+            if (lim < kBN) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (64 * h + c >= lim) sh1[c] = __float_as_uint(kNegInf);
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float2 x = ffma2(
+                  make_float2(__uint_as_float(sh1[c]), __uint_as_float(sh1[c + 1])), sc2, nsh2);
+              const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              s4[(c >> 1) & 3] = fadd2(s4[(c >> 1) & 3], pp);
+              sh1[c >> 1] = pack_bf16x2(pp.x, pp.y);
+            }
+            tmem_st32(tm_p + 32 * h, *reinterpret_cast<const uint32_t(*)[32]>(&sh1[0]));
+          }
+          tmem_wait_st();
+          const float2 st = fadd2(fadd2(s4[0], s4[1]), fadd2(s4[2], s4[3]));
+          l_run = l_run * alpha + (st.x + st.y);
+          m_run = m_use;
+          if (jj > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t ov[32];
+              tmem_ld32_wait(tm_o + c, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st32_wait(tm_o + c, ov);
+            }
+          }
+          tc_fence_before_sync();
+        }
+        if (group_sync_or(t, !ok)) {
+          ok = false;
+          break;
+        }
+      }
+      // the issuer has committed the segment's last P.V (or given up)
+      if (group_sync_or(t, !ok)) {
+        ok = false;
+        break;
+      }
+      // epilogue: O = acc / l, LSE = (m + log2 l) ln 2
+      if (n > 0) {
+        ok = mbar_wait_warp(&bar.o_done[t], o_segs & 1, p.status,
+                            dev_code(kDevTimeout, kKerPaged, 32), abort_flag);
+        ++o_segs;
+      }
+      if (s.split) {
+        // Group 1's state over the odd steps goes to group 0 (m and l through
+        // shared memory, O_1 read from tensor memory in the same lanes), which
+        // joins it with its own and writes the rows. Group 1 then waits until
+        // group 0 has read them before its next segment can overwrite O_1.
+        float* xm = reinterpret_cast<float*>(smem + L::kOffXch);
+        float* xl = xm + kBM;
+        const uint32_t sp = n_split & 1;
+        ++n_split;
+        if (t == 1) {
+          if (ok) {
+            tc_fence_after_sync();
+            xm[r] = m_run;
+            xl[r] = l_run;
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.split_ready);
+            ok = mbar_wait_warp(&bar.split_read, sp, p.status,
+                                dev_code(kDevTimeout, kKerPaged, 34), abort_flag);
+          }
+        } else {
+          if (ok)
+            ok = mbar_wait_warp(&bar.split_ready, sp, p.status,
+                                dev_code(kDevTimeout, kKerPaged, 35), abort_flag);
+          if (ok) {
+            tc_fence_after_sync();
+            if (warp_ok) {
+              const float m1 = xm[r], l1 = xl[r];
+              const float m = fmaxf(m_run, m1);
+              const float a0 = m_run == kNegInf ? 0.f : ex2_approx(m_run - m);
+              const float a1 = m1 == kNegInf ? 0.f : ex2_approx(m1 - m);
+              const float l = a0 * l_run + a1 * l1;
+              const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+              // a group without steps leaves its O columns unwritten: its
+              // weight is 0 and its values are never used
+              const float w0 = a0 * inv, w1 = a1 * inv;
+              const uint32_t tm_o1 = tmem + L::kTmemO + D + lane_off;
+              const RowOut<D> out = row_out<D>(p, s, 0, r);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o0[32], o1[32];
+                tmem_ld32_wait(tm_o + c, o0);
+                tmem_ld32_wait(tm_o1 + c, o1);
+                if (row_ok) {
+                  float v[32];
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    v[e] = (w0 != 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) +
+                           (w1 != 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
+                  put32<D>(out, c, v);
+                }
+              }
+              if (row_ok && out.lse != nullptr)
+                *out.lse = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.split_read);
+          }
+        }
+      } else if (ok && warp_ok) {
+        const RowOut<D> out = row_out<D>(p, s, t, r);
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // NaN stays NaN
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t ov[32];
+          if (n > 0) tmem_ld32_wait(tm_o + c, ov);
+          if (row_ok) {
+            float v[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              v[e] = inv != 0.f && n > 0 ? __uint_as_float(ov[e]) * inv : 0.f;
+            put32<D>(out, c, v);
+          }
+        }
+        tc_fence_before_sync();
+        if (row_ok && out.lse != nullptr)
+          *out.lse = l_run == 0.f ? kNegInf : (m_run + log2f(l_run)) * kLn2;
+      }
+      if (group_sync_or(t, !ok)) {
+        ok = false;
+        break;
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpLoad) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that several CTAs share: one warp per packed
+// row, LSE = log sum_s exp(lse_s), O = sum_s exp(lse_s - LSE) O_s, parts in
+// the order of their keys.
+template <int D>
+__global__ void __launch_bounds__(128) attn_paged_merge(const Params p) {
+  constexpr int E = D / 32;  // columns per lane
+  constexpr int kBatch = 8;  // parts in flight
+  const PlanHeader* h = p.plan;
+  if (!plan_matches(h, p)) return;
+  const int lane = threadIdx.x & 31;
+  const int n_merge = h->n_merge, rows = h->merge_rows;
+  const int32_t* cu = plan_cu_q(h);
+  for (int w = blockIdx.x * 4 + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4) {
+    // the entry whose rows hold w: the last one with row0 <= w
+    int e = -1;
+    for (int i = lane; i < n_merge; i += 32)
+      if (h->merge[i].row0 <= w) e = i;
+    e = __reduce_max_sync(0xffffffffu, e);
+    const PlanMerge g = h->merge[e];
+    const int local = w - g.row0;  // token * G + head of the item
+    const int tok = local / p.G, hd = local - tok * p.G;
+    const int tile = tok / p.tt;
+    const int slot_row = tile * kBM + (tok - tile * p.tt) * p.G + hd;
+    float M = kNegInf;
+    for (int i = lane; i < g.parts; i += 32) {
+      const int cta = g.cta + i;
+      const PlanStart a = h->start[cta], b = h->start[cta + 1];
+      const bool has = i == 0 || !same_item(a, b) || a.step != b.step;
+      if (has) M = fmaxf(M, p.lse_part[int64_t(i == 0 ? 2 * cta + 1 : 2 * cta) * kPlanRows + slot_row]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[E], tot = 0.f;
+#pragma unroll
+    for (int c = 0; c < E; ++c) acc[c] = 0.f;
+    for (int i0 = 0; i0 < g.parts; i0 += 32) {
+      const int i = i0 + lane;
+      float wt = 0.f;
+      if (i < g.parts) {
+        const int cta = g.cta + i;
+        const PlanStart a = h->start[cta], b = h->start[cta + 1];
+        const bool has = i == 0 || !same_item(a, b) || a.step != b.step;
+        if (has) {
+          const float ls = p.lse_part[int64_t(i == 0 ? 2 * cta + 1 : 2 * cta) * kPlanRows + slot_row];
+          wt = ls == kNegInf ? 0.f : expf(ls - M);
+        }
+      }
+      tot += wt;
+      unsigned live = __ballot_sync(0xffffffffu, wt != 0.f);
+      while (live != 0u) {
+        float v[kBatch][E], f[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int src = live != 0u ? __ffs(live) - 1 : -1;
+          live &= live - 1u;
+          f[k] = __shfl_sync(0xffffffffu, wt, src < 0 ? 0 : src);
+          if (src < 0) f[k] = 0.f;
+#pragma unroll
+          for (int c = 0; c < E; ++c) v[k][c] = 0.f;
+          if (src >= 0) {
+            const int cta = g.cta + i0 + src;
+            const float* from =
+                p.o_part + (int64_t(i0 + src == 0 ? 2 * cta + 1 : 2 * cta) * kPlanRows + slot_row) * D +
+                lane * E;
+            if constexpr (E == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(from);
+              v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(from);
+              v[k][0] = x.x; v[k][1] = x.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+          for (int c = 0; c < E; ++c) acc[c] = fmaf(f[k], v[k][c], acc[c]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    const int64_t row =
+        int64_t(cu[g.seq] + g.pair * 2 * p.tt + tok) * p.H + g.head * p.G + hd;
+    __nv_bfloat16* o = p.o + row * D + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = tot == 0.f ? kNegInf : M + logf(tot);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, []() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A 4-D bf16 map, 128-byte swizzle; extents, strides and box of dimensions
+// 1..3 in elements (dimension 0: D contiguous elements, boxes of 64).
+bool make_map(CUtensorMap* m, const void* base, int D, const int64_t (&ext)[3],
+              const int64_t (&stride)[3], const int (&box)[3]) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(ext[0]),
+                              static_cast<cuuint64_t>(ext[1]), static_cast<cuuint64_t>(ext[2])};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[0]) * 2,
+                                 static_cast<cuuint64_t>(stride[1]) * 2,
+                                 static_cast<cuuint64_t>(stride[2]) * 2};
+  const cuuint32_t b[4] = {64, static_cast<cuuint32_t>(box[0]), static_cast<cuuint32_t>(box[1]),
+                           static_cast<cuuint32_t>(box[2])};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, b, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One cache's map: dimensions (token, head) in the order of their strides,
+// then the page; *token_first tells which.
+bool make_cache_map(CUtensorMap* m, const void* base, const PagedAttnArgs& a, int64_t page_stride,
+                    int64_t token_stride, int64_t head_stride, int box, int* token_first) {
+  *token_first = token_stride <= head_stride ? 1 : 0;
+  if (*token_first)
+    return make_map(m, base, a.d, {a.page, a.Hkv, a.num_pages},
+                    {token_stride, head_stride, page_stride}, {box, 1, 1});
+  return make_map(m, base, a.d, {a.Hkv, a.page, a.num_pages},
+                  {head_stride, token_stride, page_stride}, {1, box, 1});
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+template <int D>
+cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
+  Params p{};
+  p.plan = static_cast<const PlanHeader*>(a.plan);
+  p.table = a.table;
+  p.table_stride = a.table_stride;
+  p.B = a.B; p.T = a.T; p.H = a.H; p.Hkv = a.Hkv;
+  p.page = a.page; p.max_pages = a.max_pages; p.num_pages = a.num_pages;
+  p.G = a.H / a.Hkv;
+  p.tt = plan_tile_tokens(p.G);
+  p.box = gcd(a.page, kBN);
+  p.scale_log2 = a.scale * kLog2e;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.o_part = a.ws;
+  p.lse_part = a.ws + size_t(2) * kPlanCtas * kPlanRows * D;
+  p.status = a.status;
+  CUtensorMap mq, mk, mv;
+  // query rows packed (head in group, key head, token): strides ascend
+  if (!make_map(&mq, a.q, D, {p.G, a.Hkv, a.T}, {D, int64_t(p.G) * D, a.q_stride},
+                {p.G, 1, p.tt}) ||
+      !make_cache_map(&mk, a.k_cache, a, a.k_page_stride, a.k_token_stride, a.k_head_stride, p.box,
+                      &p.k_token_first) ||
+      !make_cache_map(&mv, a.v_cache, a, a.v_page_stride, a.v_token_stride, a.v_head_stride, p.box,
+                      &p.v_token_first)) {
+    *why = "tensor map encoding failed";
+    return cudaErrorInvalidValue;
+  }
+  constexpr int smem = Layout<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) {
+    *why = "shared memory attribute";
+    return e;
+  }
+  attn_paged_kernel<D><<<kPlanCtas, kThreads, smem, s>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  attn_paged_merge<D><<<kPlanCtas * 4, 128, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
-  const int64_t grid = (int64_t(a.T) * a.H + 3) / 4;
-  if (grid > 0x7fffffffLL) {
-    *why = "too many rows";
-    return cudaErrorInvalidConfiguration;
-  }
-  if (a.d == 128)
-    attn_paged_simple<128><<<static_cast<unsigned>(grid), 128, 0, s>>>(a);
-  else
-    attn_paged_simple<64><<<static_cast<unsigned>(grid), 128, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.d == 128 ? launch_d<128>(a, s, why) : launch_d<64>(a, s, why);
 }
 
 }  // namespace rf

@@ -166,6 +166,86 @@ def test_kv_append_paged_reports_places_out_of_range(cuda_device):
         assert (kc[0, :2] == 1).all()
 
 
+# ---------------------------------------------------------------- plan
+
+def _spans(plan, cu, kv, H, Hkv, causal):
+    """The plan's spans as lists of (seq, head, pair, first step, end step, steps)
+    and its merge entries, decoded from device memory."""
+    w = plan.buf.cpu().numpy().view(np.int32)
+    ctas, n_merge, merge_rows = w[8], w[9], w[10]
+    start = w[16:16 + 153 * 4].reshape(153, 4)
+    merge = w[16 + 153 * 4:16 + 153 * 4 + 152 * 8].reshape(152, 8)[:n_merge]
+    tt = 128 // (H // Hkv)
+    items = []
+    for b in range(len(kv)):
+        n = cu[b + 1] - cu[b]
+        for h in range(Hkv):
+            for p in range(-(-n // (2 * tt))):
+                i1 = min(n, (p + 1) * 2 * tt)
+                seen = max(0, kv[b] - n + i1) if causal else kv[b]
+                items.append((b, h, p, -(-seen // 128), (i1 - p * 2 * tt) * (H // Hkv)))
+    where = {it[:3]: i for i, it in enumerate(items)}
+    where[(len(kv), 0, 0)] = len(items)
+    spans = []
+    for c in range(ctas):
+        a, b = start[c], start[c + 1]
+        i, j = where[tuple(a[:3])], where[tuple(b[:3])]
+        assert (i, a[3]) <= (j, b[3])
+        span, k0 = [], int(a[3])
+        while i < j:
+            span.append((i, k0, items[i][3]))
+            i, k0 = i + 1, 0
+        if k0 < b[3]:
+            span.append((i, k0, int(b[3])))
+        spans.append(span)
+    assert ctas == 0 or (tuple(start[0]) == items[0][:3] + (0,)
+                         and tuple(start[ctas]) == (len(kv), 0, 0, 0))
+    return items, spans, merge, merge_rows
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,H,Hkv", [
+    ([(1, 1)], 1, 1), ([(1, 100000)], 8, 8), ([(1, 5000)] * 3, 32, 8), ([(2048, 32768)], 64, 8),
+    ([(0, 5), (3, 1), (0, 0), (700, 900), (1, 4000), (0, 9)], 28, 4),
+    ([(1 + i % 5, 40 * i + 6) for i in range(1100)], 8, 2), ([(130, 130)] * 7, 128, 1),
+    ([(0, 3)], 4, 4), ([(9000, 9000), (1, 60000)], 4, 4),
+])
+def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal):
+    cu = [0]
+    for n, _ in lengths:
+        cu.append(cu[-1] + n)
+    kv = [m for _, m in lengths]
+    plan = api.PagedPlan(_i32(cu), _i32(kv), cu[-1] + 3, H, Hkv, 16, 6250, causal)
+    assert api.device_status() == 0
+    items, spans, merge, merge_rows = _spans(plan, cu, kv, H, Hkv, causal)
+    parts = {}
+    for cta, span in enumerate(spans):
+        for i, k0, k1 in span:
+            parts.setdefault(i, []).append((cta, k0, k1))
+    assert sorted(parts) == list(range(len(items)))
+    cut = {}
+    for i, pieces in parts.items():
+        # contiguous steps from 0 to the item's end, one piece a CTA
+        assert pieces[0][1] == 0 and pieces[-1][2] == items[i][3]
+        assert all(x[2] == y[1] for x, y in zip(pieces, pieces[1:]))
+        if len(pieces) > 1:
+            cut[i] = pieces
+    where = {it[:3]: i for i, it in enumerate(items)}
+    assert sorted(where[tuple(m[:3])] for m in merge) == sorted(cut)
+    row0 = 0
+    for m in merge:
+        i = where[tuple(m[:3])]
+        live = [c for c, _, _ in cut[i]]
+        assert live[0] == m[3] and set(live) <= set(range(m[3], m[3] + m[4]))
+        assert m[5] == items[i][4] and m[6] == row0
+        row0 += m[5]
+    assert row0 == merge_rows
+    if len(spans) > 1:     # and the spans are even, up to a step and an item's fixed cost
+        cost = [sum(2 + (k1 - k0) * (3 if items[i][4] > 128 // (H // Hkv) * (H // Hkv) else 2)
+                    for i, k0, k1 in span) for span in spans]
+        assert max(cost) <= sum(cost) / len(cost) + 12
+
+
 # ---------------------------------------------------------------- attention
 
 def _attention_case(lengths, H, Hkv, d, page, seed=0, causal=True, head_major=False, pad=0, amp=1.0,
@@ -305,6 +385,20 @@ def test_attn_paged_ignores_what_lies_past_the_cache(cuda_device, page, value):
     assert torch.equal(o, o_ref) and torch.equal(lse, lse_ref)
 
 
+@pytest.mark.parametrize("lengths", [[(1, 33)], [(1, 640)], [(1, 9000)], [(40, 700)], [(200, 300)]])
+def test_attn_paged_a_visible_nan_shows(cuda_device, lengths):
+    # in a key that every row sees: that key head's rows are NaN, the others' not
+    # touched, whether the item is whole or in parts
+    c = _attention_case(lengths, 8, 2, 128, 16, seed=16)
+    for at in (0, 31):
+        bad = dict(c, kc=c["kc"].clone())
+        bad["kc"][c["rows"][0][at // 16], at % 16, 1, 5] = float("nan")
+        o, lse = _attend(bad)
+        o_ref, lse_ref = _attend(c)
+        assert torch.equal(o[:, :4], o_ref[:, :4]) and torch.equal(lse[:, :4], lse_ref[:, :4])
+        assert o[:, 4:].isnan().all() and lse[:, 4:].isnan().all()
+
+
 def test_attn_paged_many_sequences(cuda_device):
     # more items than CTAs, every length of a tile's neighbourhood
     lengths = [(1 + (i % 3), 1 + (i * 37) % 400 + 3) for i in range(300)]
@@ -403,7 +497,7 @@ def test_attn_paged_captured_step_follows_its_lengths(cuda_device):
     table = torch.randperm(pages, generator=gen)[:B * width].view(B, width)
     kc = _pool(pages, page, Hkv, d, False, torch.bfloat16, gen)
     vc = _pool(pages, page, Hkv, d, False, torch.bfloat16, gen)
-    qkv = torch.empty(B, H + 2 * Hkv, d, dtype=torch.bfloat16, device="cuda")
+    qkv = torch.zeros(B, H + 2 * Hkv, d, dtype=torch.bfloat16, device="cuda")
     kv_len, cu = _i32([1] * B), _i32(range(B + 1))
     tab = table.int().cuda()
     cs = torch.cat([torch.ones(1000, 64), torch.zeros(1000, 64)], 1).cuda()
