@@ -466,6 +466,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!advance(kseq)) return false;
       return (ok = RF_WAIT(kv_full[kseq % NS], (kseq / NS) & 1, 21));
     };
+    // Whether everything up to the K tile of this group's next step has landed.
+    // Between this group's steps lies at most one of the other's (an item shared
+    // by both groups), so each barrier tested is at most one phase behind.
+    auto landed = [&]() -> bool {
+      int sq = seq;
+      for (int u = u_next; u < a.ke; ++u, sq += 2) {
+        const bool k_in = mbar_test_wait(&bar.kv_full[sq % NS], (sq / NS) & 1);
+        if (!k_in || needs(u)) return k_in;
+        if (!mbar_test_wait(&bar.kv_full[(sq + 1) % NS], ((sq + 1) / NS) & 1)) return false;
+      }
+      return false;
+    };
     auto qk_commits = [&](int kseq) {
       mma_commit(&bar.s_full[t]);
       mma_commit(&bar.kv_empty[kseq % NS]);
@@ -502,9 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int jj = 0; jj < n; ++jj) {
         // While the softmax runs: wait for V_u, zero its rows past the cache's
-        // end, and, when the next step is this group's, wait for its K tile.
-        // Waiting for that tile before this step's P.V is safe: the slot it is
-        // loaded into was freed by releases committed in earlier blocks.
+        // end, and see whether the next step's K tile is there. If it is, its
+        // Q K^T goes out in one block with this step's P.V. If it is not (memory
+        // bounds a decode step), P.V goes first: it frees V_u's slot, without
+        // which the ring of five slots could not run ahead of the two groups.
         const bool last = jj + 1 == n;
         const int u = s.kb + (s.split ? 2 * jj + t : jj);
         int k2 = 0;
@@ -522,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0 && ok && !last) fast = next_k(k2);
+        if (lane == 0 && ok && !last && landed()) fast = next_k(k2);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         // P_t is in tensor memory
         if (group_sync_or(t, !ok)) {
@@ -537,7 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int v_done = vseq;
           if (fast) qk_commits(k2);
           mma_commit(&bar.kv_empty[v_done % NS]);
-          if (last) mma_commit(&bar.o_done[t]);
+          if (last) {
+            mma_commit(&bar.o_done[t]);
+          } else if (!fast && next_k(k2) && (ok = RF_LOCK())) {
+            tc_fence_after_sync();
+            issue_qk<D>(mm_s, q_desc, k_desc0 + RF_SLOT(k2));
+            issue_unlock(&bar.issue_lock);
+            qk_commits(k2);
+          }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
