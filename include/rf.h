@@ -666,8 +666,8 @@ rf_status rf_attn_paged(const void *q, int64_t q_stride, const void *k_cache,
  *  ws     : device workspace, 16-byte aligned, ws_bytes >=
  *           rf_draft_verify_workspace_bytes(B, S).
  * B >= 0, 1 <= S <= 64, V >= 1. A token outside [0, V) is refused, and a row
- * with nothing to draw from (all -inf, NaN) yields -1; both are reported
- * through rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED
+ * that gives no probabilities (all -inf, or a NaN or +inf in it) refuses its
+ * draft and draws -1; both are reported through rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED
  * (S > 64), RF_ERR_CUDA.
  */
 size_t rf_draft_verify_workspace_bytes(int B, int S);

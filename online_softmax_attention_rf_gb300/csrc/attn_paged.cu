@@ -97,8 +97,13 @@ struct Params {
   float scale_log2;
   __nv_bfloat16* o;
   float* lse;
-  float* o_part;    // [2 * kPlanCtas][kPlanRows][D]
-  float* lse_part;  // [2 * kPlanCtas][kPlanRows]
+  int o_wide;       // o is 32-byte aligned
+  // Partial states. A slot holds two tiles; O of a tile is stored by groups of
+  // four columns, [D / 4][128 rows][4], so that the warp that owns 32 rows
+  // writes 512 contiguous bytes at a time (a row-major tile would take 32
+  // half-written sectors a store: 8 us a pair of tiles).
+  float* o_part;    // [2 * kPlanCtas][2][D / 4][128][4]
+  float* lse_part;  // [2 * kPlanCtas][2][128]
   int* status;
 };
 
@@ -242,22 +247,20 @@ __device__ __forceinline__ void issue_pv(uint32_t tm_o, uint32_t tm_p, uint64_t 
   }
 }
 
-// Where a packed row's result goes: O and LSE of the call, or the row of a
-// partial slot.
-template <int D>
+// Where a packed row's result goes: O and LSE of the call, or a partial slot.
 struct RowOut {
   __nv_bfloat16* o;
-  float* part;
+  float* part;  // the row's first four columns; the next four are 4 * kBM floats on
   float* lse;
 };
 
 template <int D>
-__device__ __forceinline__ RowOut<D> row_out(const Params& p, const Seg& s, int t, int r) {
-  RowOut<D> w{nullptr, nullptr, nullptr};
+__device__ __forceinline__ RowOut row_out(const Params& p, const Seg& s, int t, int r) {
+  RowOut w{nullptr, nullptr, nullptr};
   if (s.slot >= 0) {
-    const int64_t row = int64_t(s.slot) * kPlanRows + t * kBM + r;
-    w.part = p.o_part + row * D;
-    w.lse = p.lse_part + row;
+    const int64_t tile = int64_t(s.slot) * 2 + t;
+    w.part = p.o_part + (tile * (D / 4) * kBM + r) * 4;
+    w.lse = p.lse_part + tile * kBM + r;
   } else {
     const int64_t row = int64_t(s.row0 + t * p.tt + r / p.G) * p.H + s.head * p.G + r % p.G;
     w.o = p.o + row * D;
@@ -266,23 +269,29 @@ __device__ __forceinline__ RowOut<D> row_out(const Params& p, const Seg& s, int 
   return w;
 }
 
+// 16 columns of a row of O.
+__device__ __forceinline__ void put_bf16x16(__nv_bfloat16* o, const float* v, int wide) {
+  uint32_t x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  if (wide) {
+    st_global_v8(o, x);
+  } else {
+    *reinterpret_cast<uint4*>(o) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(o + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // 32 columns of a finished row from column c on.
-template <int D>
-__device__ __forceinline__ void put32(const RowOut<D>& w, int c, const float (&v)[32]) {
+__device__ __forceinline__ void put32(const RowOut& w, int c, const float (&v)[32], int wide) {
   if (w.part != nullptr) {
 #pragma unroll
     for (int e = 0; e < 32; e += 4)
-      *reinterpret_cast<float4*>(w.part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      *reinterpret_cast<float4*>(w.part + (c + e) * kBM) =
+          make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
   } else {
-#pragma unroll
-    for (int e = 0; e < 32; e += 8) {
-      uint4 x;
-      x.x = pack_bf16x2(v[e], v[e + 1]);
-      x.y = pack_bf16x2(v[e + 2], v[e + 3]);
-      x.z = pack_bf16x2(v[e + 4], v[e + 5]);
-      x.w = pack_bf16x2(v[e + 6], v[e + 7]);
-      *reinterpret_cast<uint4*>(w.o + c + e) = x;
-    }
+    put_bf16x16(w.o + c, v, wide);
+    put_bf16x16(w.o + c + 16, v + 16, wide);
   }
 }
 
@@ -299,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t s_base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  pdl_wait();
+  pdl_trigger();
   if (!plan_matches(p.plan, p)) {
     if (blockIdx.x == 0 && threadIdx.x == 0)
       record_status(p.status, dev_code(kDevBadList, kKerPaged, 2));
@@ -740,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // weight is 0 and its values are never used
               const float w0 = a0 * inv, w1 = a1 * inv;
               const uint32_t tm_o1 = tmem + L::kTmemO + D + lane_off;
-              const RowOut<D> out = row_out<D>(p, s, 0, r);
+              const RowOut out = row_out<D>(p, s, 0, r);
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o0[32], o1[32];
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int e = 0; e < 32; ++e)
                     v[e] = (w0 != 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) +
                            (w1 != 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
-                  put32<D>(out, c, v);
+                  put32(out, c, v, p.o_wide);
                 }
               }
               if (row_ok && out.lse != nullptr)
@@ -764,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (ok && warp_ok) {
-        const RowOut<D> out = row_out<D>(p, s, t, r);
+        const RowOut out = row_out<D>(p, s, t, r);
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // NaN stays NaN
         tc_fence_after_sync();
 #pragma unroll 1
@@ -776,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               v[e] = inv != 0.f && n > 0 ? __uint_as_float(ov[e]) * inv : 0.f;
-            put32<D>(out, c, v);
+            put32(out, c, v, p.o_wide);
           }
         }
         tc_fence_before_sync();
@@ -799,97 +810,122 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the items that several CTAs share: one warp per packed
-// row, LSE = log sum_s exp(lse_s), O = sum_s exp(lse_s - LSE) O_s, parts in
-// the order of their keys.
+// Running softmax state of a row over parts: m, l and 16 columns.
+struct MergeState {
+  float m, l, acc[16];
+};
+
+__device__ __forceinline__ void merge_add(MergeState& st, float ls, float weight,
+                                          const float (&v)[16]) {
+  // a part without keys (-inf) adds nothing; NaN passes through
+  const float mn = fmaxf(st.m, ls);
+  const float a = st.m == kNegInf ? 0.f : expf(st.m - mn);
+  const float b = ls == kNegInf ? 0.f : weight * expf(ls - mn);
+  st.l = st.l * a + b;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) st.acc[e] = st.acc[e] * a + (b != 0.f ? b * v[e] : 0.f);
+  st.m = mn;
+}
+
+// Joins the parts of the items that several CTAs share: LSE = log sum_s
+// exp(lse_s), O = sum_s exp(lse_s - LSE) O_s, parts in a fixed order. A block
+// takes 32 rows (a lane each) and 64 columns of an item: with few parts a warp
+// joins all of them for 16 columns, with many the four warps take every fourth
+// part and join their states through shared memory.
+constexpr int kMergeShare = 8;  // parts from which the warps share them
+
 template <int D>
 __global__ void __launch_bounds__(128) attn_paged_merge(const Params p) {
-  constexpr int E = D / 32;  // columns per lane
-  constexpr int kBatch = 8;  // parts in flight
+  __shared__ float xs[4][18][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PlanHeader* h = p.plan;
+  pdl_wait();
   if (!plan_matches(h, p)) return;
-  const int lane = threadIdx.x & 31;
-  const int n_merge = h->n_merge, rows = h->merge_rows;
+  const int n_merge = h->n_merge;
+  const int tasks = h->merge_units * (D / 64);
   const int32_t* cu = plan_cu_q(h);
-  for (int w = blockIdx.x * 4 + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4) {
-    // the entry whose rows hold w: the last one with row0 <= w
-    int e = -1;
+  for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int unit = task / (D / 64), c64 = task % (D / 64) * 64;
+    int e = -1;  // the item: the last one with unit0 <= unit
     for (int i = lane; i < n_merge; i += 32)
-      if (h->merge[i].row0 <= w) e = i;
+      if (h->merge[i].unit0 <= unit) e = i;
     e = __reduce_max_sync(0xffffffffu, e);
     const PlanMerge g = h->merge[e];
-    const int local = w - g.row0;  // token * G + head of the item
-    const int tok = local / p.G, hd = local - tok * p.G;
-    const int tile = tok / p.tt;
-    const int slot_row = tile * kBM + (tok - tile * p.tt) * p.G + hd;
-    float M = kNegInf;
-    for (int i = lane; i < g.parts; i += 32) {
-      const int cta = g.cta + i;
-      const PlanStart a = h->start[cta], b = h->start[cta + 1];
-      const bool has = i == 0 || !same_item(a, b) || a.step != b.step;
-      if (has) M = fmaxf(M, p.lse_part[int64_t(i == 0 ? 2 * cta + 1 : 2 * cta) * kPlanRows + slot_row]);
-    }
+    const int ntok = g.rows / p.G;
+    const int u0 = plan_units(ntok, 0, p.G);
+    const int tile = unit - g.unit0 >= u0 ? 1 : 0;
+    const int r = (unit - g.unit0 - tile * u0) * 32 + lane;
+    const int tok = tile * p.tt + r / p.G;
+    const bool row_ok = r < p.G * p.tt && tok < ntok;
+    const bool share = g.parts >= kMergeShare;
+    const int64_t row =
+        int64_t(cu[g.seq] + g.pair * 2 * p.tt + tok) * p.H + g.head * p.G + r % p.G;
+    MergeState st;
+    for (int k = 0; k < (share ? 4 : 1); ++k) {
+      const int c = c64 + (share ? k : warp) * 16;
+      st.m = kNegInf;
+      st.l = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float acc[E], tot = 0.f;
-#pragma unroll
-    for (int c = 0; c < E; ++c) acc[c] = 0.f;
-    for (int i0 = 0; i0 < g.parts; i0 += 32) {
-      const int i = i0 + lane;
-      float wt = 0.f;
-      if (i < g.parts) {
+      for (int i = 0; i < 16; ++i) st.acc[i] = 0.f;
+#pragma unroll 4
+      for (int i = share ? warp : 0; i < g.parts; i += share ? 4 : 1) {
         const int cta = g.cta + i;
-        const PlanStart a = h->start[cta], b = h->start[cta + 1];
-        const bool has = i == 0 || !same_item(a, b) || a.step != b.step;
-        if (has) {
-          const float ls = p.lse_part[int64_t(i == 0 ? 2 * cta + 1 : 2 * cta) * kPlanRows + slot_row];
-          wt = ls == kNegInf ? 0.f : expf(ls - M);
+        const int64_t at = int64_t(i == 0 ? 2 * cta + 1 : 2 * cta) * 2 + tile;
+        if (row_ok) {
+          const float ls = p.lse_part[at * kBM + r];
+          const float* from = p.o_part + (at * (D / 4) * kBM + r) * 4 + c * kBM;
+          float v[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(from + q * 4 * kBM);
+            v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+          }
+          merge_add(st, ls, 1.f, v);
         }
       }
-      tot += wt;
-      unsigned live = __ballot_sync(0xffffffffu, wt != 0.f);
-      while (live != 0u) {
-        float v[kBatch][E], f[kBatch];
+      if (share) {
+        // the four warps' states of these columns; warp k joins them
+        __syncthreads();
+        xs[warp][0][lane] = st.m;
+        xs[warp][1][lane] = st.l;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int src = live != 0u ? __ffs(live) - 1 : -1;
-          live &= live - 1u;
-          f[k] = __shfl_sync(0xffffffffu, wt, src < 0 ? 0 : src);
-          if (src < 0) f[k] = 0.f;
+        for (int i = 0; i < 16; ++i) xs[warp][2 + i][lane] = st.acc[i];
+        __syncthreads();
+        if (warp == k) {
+          st.m = kNegInf;
+          st.l = 0.f;
 #pragma unroll
-          for (int c = 0; c < E; ++c) v[k][c] = 0.f;
-          if (src >= 0) {
-            const int cta = g.cta + i0 + src;
-            const float* from =
-                p.o_part + (int64_t(i0 + src == 0 ? 2 * cta + 1 : 2 * cta) * kPlanRows + slot_row) * D +
-                lane * E;
-            if constexpr (E == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(from);
-              v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-            } else {
-              const float2 x = *reinterpret_cast<const float2*>(from);
-              v[k][0] = x.x; v[k][1] = x.y;
-            }
+          for (int i = 0; i < 16; ++i) st.acc[i] = 0.f;
+          for (int w = 0; w < 4; ++w) {
+            // a warp's state is (m, l, acc): its mean acc / l, with weight l
+            const float m2 = xs[w][0][lane], l2 = xs[w][1][lane];
+            const float mn = fmaxf(st.m, m2);
+            const float a = st.m == kNegInf ? 0.f : expf(st.m - mn);
+            const float b = m2 == kNegInf ? 0.f : expf(m2 - mn);
+            st.l = st.l * a + (l2 == 0.f ? 0.f : l2 * b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              st.acc[i] = st.acc[i] * a + (l2 == 0.f ? 0.f : xs[w][2 + i][lane] * b);
+            st.m = mn;
+          }
+          if (row_ok) {
+            const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) st.acc[i] *= inv;
+            put_bf16x16(p.o + row * D + c, st.acc, p.o_wide);
+            if (c == 0 && p.lse != nullptr) p.lse[row] = st.l == 0.f ? kNegInf : st.m + logf(st.l);
           }
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-          for (int c = 0; c < E; ++c) acc[c] = fmaf(f[k], v[k][c], acc[c]);
       }
     }
+    if (!share && row_ok) {
+      const int c = c64 + warp * 16;
+      const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    const float inv = tot == 0.f ? 0.f : 1.f / tot;
-    const int64_t row =
-        int64_t(cu[g.seq] + g.pair * 2 * p.tt + tok) * p.H + g.head * p.G + hd;
-    __nv_bfloat16* o = p.o + row * D + lane * E;
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse != nullptr) p.lse[row] = tot == 0.f ? kNegInf : M + logf(tot);
+      for (int i = 0; i < 16; ++i) st.acc[i] *= inv;
+      put_bf16x16(p.o + row * D + c, st.acc, p.o_wide);
+      if (c == 0 && p.lse != nullptr) p.lse[row] = st.l == 0.f ? kNegInf : st.m + logf(st.l);
+    }
   }
 }
 
@@ -954,6 +990,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
   p.scale_log2 = a.scale * kLog2e;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
+  p.o_wide = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
   p.o_part = a.ws;
   p.lse_part = a.ws + size_t(2) * kPlanCtas * kPlanRows * D;
   p.status = a.status;
@@ -975,11 +1012,9 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
     *why = "shared memory attribute";
     return e;
   }
-  attn_paged_kernel<D><<<kPlanCtas, kThreads, smem, s>>>(mq, mk, mv, p);
-  e = cudaGetLastError();
+  e = launch_pdl(attn_paged_kernel<D>, dim3(kPlanCtas), dim3(kThreads), smem, s, mq, mk, mv, p);
   if (e != cudaSuccess) return e;
-  attn_paged_merge<D><<<kPlanCtas * 4, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(attn_paged_merge<D>, dim3(kPlanCtas * 6), dim3(128), 0, s, p);
 }
 
 }  // namespace

@@ -14,7 +14,8 @@
 // by a third reduction that needs both: stats_kernel takes (max, sum) of every
 // logit row in one pass, split over CTAs; choose_kernel joins the pieces,
 // walks the acceptance chain and takes the third reduction over the one row
-// per sequence that needs it, with a cluster of CTAs per sequence.
+// per sequence that needs it, with a cluster of CTAs per sequence (most of
+// that row's logits are in L2 by then).
 #include <cooperative_groups.h>
 
 #include "rf_device.cuh"
@@ -24,7 +25,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
+constexpr int kStatThreads = 256;
+constexpr int kStatWarps = kStatThreads / 32;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSplits = 32;
 constexpr int kCluster = 8;
@@ -56,21 +59,93 @@ __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int b) {
 
 __device__ __forceinline__ void merge(float& m, float& l, float m2, float l2, float c) {
   const float mn = fmaxf(m, m2);
-  // an empty side (m = -inf) has weight 0; its exponent would be inf - inf
-  l = (m == kNegInf ? 0.f : l * weight(m, mn, c)) + (m2 == kNegInf ? 0.f : l2 * weight(m2, mn, c));
+  // an empty side (m = -inf) has l = 0, or NaN where it met one; its weight
+  // would be inf - inf
+  l = (m == kNegInf ? l : l * weight(m, mn, c)) + (m2 == kNegInf ? l2 : l2 * weight(m2, mn, c));
   m = mn;
 }
 
-// One CTA: piece `split` of one logit row. Rows of sequence b: its S + 1
-// target rows, then its S draft rows.
+// Where a row's numbers come from: 16 bytes at a time.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) stats_kernel(const VerifyArgs a, Stat* stats, int nsplit,
-                                                         int piece) {
+struct Vec16;
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+
+// A thread's running state over the numbers it reads.
+struct Running {
+  float m = kNegInf, l = 0.f;
+  int arg = kNone;
+};
+
+// n numbers x of consecutive indices from v0 on. Probabilities: the maximum of
+// the batch first, so that the state is rescaled at most once a batch. Greedy
+// rows: the lowest index of the maximum.
+template <int n>
+__device__ __forceinline__ void take_batch(Running& st, const float* x, float c) {
+  float mx = x[0];
+#pragma unroll
+  for (int i = 1; i < n; ++i) mx = fmaxf(mx, x[i]);
+  if (mx > st.m) {
+    if (st.m != kNegInf) st.l *= weight(st.m, mx, c);
+    st.m = mx;
+  }
+  // all of the thread's numbers so far -inf: a finite stand-in keeps their
+  // weights 0 rather than NaN
+  const float m = st.m == kNegInf ? 0.f : st.m;
+  const float2 nm = make_float2(-m, -m), cc = make_float2(c, c);
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i + 1 < n; i += 2) {
+    const float2 d = __fmul2_rn(fadd2(make_float2(x[i], x[i + 1]), nm), cc);
+    s = fadd2(s, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
+  }
+  if (n & 1) s.x += weight(x[n - 1], m, c);
+  st.l += s.x + s.y;
+}
+
+__device__ __forceinline__ void take_greedy(Running& st, float x, int v) {
+  if (x > st.m || (x == st.m && v < st.arg)) {
+    st.m = x;
+    st.arg = v;
+  }
+}
+
+// One CTA: piece `split` of one logit row. Rows of sequence b: its S + 1
+// target rows, then its S draft rows. Bound by memory (each logit is read
+// once) with about 70 % of the issue slots: 16-byte loads, four in flight a
+// thread, packed float32 arithmetic; rows of any alignment (a row of an odd
+// vocabulary starts anywhere) by single numbers up to the first 16-byte
+// boundary and after the last.
+template <typename T>
+__global__ void __launch_bounds__(kStatThreads) stats_kernel(const VerifyArgs a, Stat* stats,
+                                                             int nsplit, int piece) {
+  using V = Vec16<T>;
+  constexpr int N = V::N, U = 4;
   const int per = a.draft != nullptr ? 2 * a.S + 1 : a.S + 1;
   const int row = blockIdx.x / nsplit, split = blockIdx.x % nsplit;
   const int b = row / per, r = row % per;
   const bool is_draft = r > a.S;
   const int i = is_draft ? r - a.S - 1 : r;
+  pdl_wait();
+  pdl_trigger();
   bool greedy;
   const float c = log2e_over(a.temperature, b, &greedy);
   const int nd = drafts_of(a, b);
@@ -78,18 +153,52 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const VerifyArgs a, Sta
   const T* x = is_draft ? static_cast<const T*>(a.draft) + (int64_t(b) * a.S + i) * a.V
                         : static_cast<const T*>(a.target) + (int64_t(b) * (a.S + 1) + i) * a.V;
   const int v0 = min(a.V, split * piece), v1 = min(a.V, v0 + piece);
-  float m = kNegInf, l = 0.f;
-  int arg = kNone;
-  for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-    const float xv = to_f32(x[v]);
-    if (xv > m) {
-      l = m == kNegInf ? 0.f : l * weight(m, xv, c);
-      m = xv;
-      arg = v;
+  const int tid = threadIdx.x;
+  // [v0, h) single, [h, h + N * nv) by 16 bytes, [.., v1) single
+  const int lead = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x + v0) & 15)) & 15) /
+                   static_cast<int>(sizeof(T));
+  const int h = min(v1, v0 + lead);
+  const int nv = (v1 - h) / N;
+  const int tail = h + nv * N;
+  const uint4* xv = reinterpret_cast<const uint4*>(x + h);
+  Running st;
+  if (!greedy) {
+    int k = tid;
+    for (; k + (U - 1) * kStatThreads < nv; k += U * kStatThreads) {
+      uint4 w[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) w[j] = xv[k + j * kStatThreads];
+      float y[U * N];
+#pragma unroll
+      for (int j = 0; j < U; ++j) V::unpack(w[j], y + j * N);
+      take_batch<U * N>(st, y, c);
     }
-    if (xv != kNegInf) l += weight(xv, m, c);
+    for (; k < nv; k += kStatThreads) {
+      float y[N];
+      V::unpack(xv[k], y);
+      take_batch<N>(st, y, c);
+    }
+    for (int v = v0 + tid; v < h; v += kStatThreads) {
+      const float y = to_f32(x[v]);
+      take_batch<1>(st, &y, c);
+    }
+    for (int v = tail + tid; v < v1; v += kStatThreads) {
+      const float y = to_f32(x[v]);
+      take_batch<1>(st, &y, c);
+    }
+  } else {
+    for (int k = tid; k < nv; k += kStatThreads) {
+      float y[N];
+      V::unpack(xv[k], y);
+#pragma unroll
+      for (int j = 0; j < N; ++j) take_greedy(st, y[j], h + k * N + j);
+    }
+    for (int v = v0 + tid; v < h; v += kStatThreads) take_greedy(st, to_f32(x[v]), v);
+    for (int v = tail + tid; v < v1; v += kStatThreads) take_greedy(st, to_f32(x[v]), v);
   }
-  __shared__ Stat part[kWarps];
+  float m = st.m, l = st.l;
+  int arg = st.arg;
+  __shared__ Stat part[kStatWarps];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
@@ -97,10 +206,10 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const VerifyArgs a, Sta
     arg = m2 > m ? a2 : m2 == m ? min(arg, a2) : arg;
     merge(m, l, m2, l2, c);
   }
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = Stat{m, l, arg, 0};
+  if ((tid & 31) == 0) part[tid >> 5] = Stat{m, l, arg, 0};
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) {
+  if (tid == 0) {
+    for (int w = 1; w < kStatWarps; ++w) {
       const Stat s = part[w];
       arg = s.m > m ? s.arg : s.m == m ? min(arg, s.arg) : arg;
       merge(m, l, s.m, s.l, c);
@@ -117,24 +226,54 @@ __device__ __forceinline__ void take(Best& a, float score, int idx) {
   if (score > a.score || (score == a.score && idx < a.idx)) a = Best{score, idx};
 }
 
-// One cluster per sequence.
-template <typename T>
+// Four consecutive numbers.
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+// One cluster per sequence. kVec: every row starts on a boundary of four
+// numbers (V a multiple of 4 and aligned tensors): loads of four numbers,
+// otherwise of one.
+template <typename T, bool kVec>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     choose_kernel(const VerifyArgs a, const Stat* __restrict__ stats, int nsplit) {
   __shared__ float rm[2 * kMaxDrafts + 1], rl[2 * kMaxDrafts + 1];
   __shared__ int rarg[2 * kMaxDrafts + 1];
   __shared__ uint8_t accept[kMaxDrafts];
-  __shared__ Best wbest[2][kWarps];
+  __shared__ Best wbest[kWarps];
   __shared__ Best cbest[2][kCluster];
+  __shared__ int chosen_pass[2];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int b = blockIdx.x / kCluster;
-  cluster.barrier_arrive();  // waited for before rank 0's memory is written
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = a.draft != nullptr ? 2 * a.S + 1 : a.S + 1;
+  cluster.barrier_arrive();  // waited for before any CTA's memory is written by another
+  const T* target = static_cast<const T*>(a.target) + int64_t(b) * (a.S + 1) * a.V;
+  const T* draft = static_cast<const T*>(a.draft) + (a.draft != nullptr ? int64_t(b) * a.S * a.V : 0);
+  pdl_wait();
   bool greedy;
   const float c = log2e_over(a.temperature, b, &greedy);
   const int nd = drafts_of(a, b);
+  // the drafted tokens' logits, on their way while the statistics are joined
+  int x = 0;
+  bool in_range = false;
+  float xt = 0.f, xd = 0.f, xu = 0.f;
+  if (tid < nd) {
+    x = a.tokens[int64_t(b) * a.S + tid];
+    xu = a.u[int64_t(b) * a.S + tid];
+    in_range = x >= 0 && x < a.V;
+    if (in_range && !greedy) {
+      xt = to_f32(target[int64_t(tid) * a.V + x]);
+      if (a.draft != nullptr) xd = to_f32(draft[int64_t(tid) * a.V + x]);
+    }
+  }
   // the row statistics, joined from their pieces in a fixed order
   for (int r = warp; r < per; r += kWarps) {
     const bool is_draft = r > a.S;
@@ -162,33 +301,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  const T* target = static_cast<const T*>(a.target) + int64_t(b) * (a.S + 1) * a.V;
-  const T* draft = static_cast<const T*>(a.draft) + (a.draft != nullptr ? int64_t(b) * a.S * a.V : 0);
-  for (int i = threadIdx.x; i < nd; i += kThreads) {
-    const int x = a.tokens[int64_t(b) * a.S + i];
+  if (tid < nd) {
     bool acc = false;
-    if (x < 0 || x >= a.V) {
+    if (!in_range) {
       record_status(a.status, dev_code(kDevBadList, kKerVerify, 1));
     } else if (greedy) {
-      acc = x == rarg[i];
+      acc = x == rarg[tid];
     } else {
-      const float p = weight(to_f32(target[int64_t(i) * a.V + x]), rm[i], c) / rl[i];
-      float q = 1.f;
-      if (a.draft != nullptr) {
-        const int rd = a.S + 1 + i;
-        q = weight(to_f32(draft[int64_t(i) * a.V + x]), rm[rd], c) / rl[rd];
-      }
-      acc = a.u[int64_t(b) * a.S + i] * q < p;
+      const float p = weight(xt, rm[tid], c) / rl[tid];
+      const int rd = a.S + 1 + tid;
+      const float q = a.draft != nullptr ? weight(xd, rm[rd], c) / rl[rd] : 1.f;
+      acc = xu * q < p;
     }
-    accept[i] = acc;
+    accept[tid] = acc;
   }
   __syncthreads();
   int at = 0;
   while (at < nd && accept[at]) ++at;  // nd <= kMaxDrafts, shared memory broadcast
   // the choice at position `at`
   int chosen;
+  cluster.barrier_wait();
   if (greedy) {
-    cluster.barrier_wait();
     chosen = rarg[at] == kNone ? -1 : rarg[at];
   } else {
     const bool refused = at < nd;
@@ -198,51 +331,67 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const float* e = a.expo + int64_t(b) * a.V;
     const float pm = rm[at], pl = 1.f / rl[at];
     const float qm = has_q ? rm[a.S + 1 + at] : 0.f, ql = has_q ? 1.f / rl[a.S + 1 + at] : 0.f;
-    const int xd = refused && a.draft == nullptr ? a.tokens[int64_t(b) * a.S + at] : -1;
-    // best over the remainder max(p - q, 0), and over p itself for the case
-    // that rounding leaves nothing of the remainder
-    Best rest{0.f, kNone}, full{0.f, kNone};
-    for (int v = rank * kThreads + threadIdx.x; v < a.V; v += kCluster * kThreads) {
-      const float p = weight(to_f32(pt[v]), pm, c) * pl;
-      float w = p;
-      if (has_q) w = p - weight(to_f32(qt[v]), qm, c) * ql;
-      if (v == xd) w = 0.f;
-      const float ev = e[v];
-      take(rest, w > 0.f ? w / ev : 0.f, v);
-      take(full, p / ev, v);
-    }
-    Best two[2] = {rest, full};
+    const int out_of_race = refused && !has_q ? a.tokens[int64_t(b) * a.S + at] : -1;
+    chosen = -1;
+    // pass 0: the remainder max(p - q, 0) (p itself when everything was
+    // accepted); pass 1, only when rounding leaves nothing of the remainder: p
+    for (int pass = 0; pass < (refused ? 2 : 1); ++pass) {
+      Best best{0.f, kNone};
+      const bool minus_q = has_q && pass == 0;
+      const int skip = pass == 0 ? out_of_race : -1;
+      auto one = [&](float xp, float xq, float ev, int v) {
+        float w = weight(xp, pm, c) * pl;
+        if (minus_q) w -= weight(xq, qm, c) * ql;
+        // the quotient's error is two steps: below what the weights carry
+        if (w > 0.f && v != skip) take(best, __fdividef(w, ev), v);
+      };
+      if constexpr (kVec) {
+#pragma unroll 2
+        for (int v = (rank * kThreads + tid) * 4; v < a.V; v += kCluster * kThreads * 4) {
+          float xp[4], xq[4] = {0.f, 0.f, 0.f, 0.f}, ev[4];
+          load4(pt + v, xp);
+          load4(e + v, ev);
+          if (minus_q) load4(qt + v, xq);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+          for (int i = 0; i < 4; ++i) one(xp[i], xq[i], ev[i], v + i);
+        }
+      } else {
+#pragma unroll 4
+        for (int v = rank * kThreads + tid; v < a.V; v += kCluster * kThreads)
+          one(to_f32(pt[v]), minus_q ? to_f32(qt[v]) : 0.f, e[v], v);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
-        take(two[k], __shfl_xor_sync(0xffffffffu, two[k].score, o),
-             __shfl_xor_sync(0xffffffffu, two[k].idx, o));
-      if (lane == 0) wbest[k][warp] = two[k];
+        take(best, __shfl_xor_sync(0xffffffffu, best.score, o),
+             __shfl_xor_sync(0xffffffffu, best.idx, o));
+      if (lane == 0) wbest[warp] = best;
+      __syncthreads();
+      if (warp == 0) {
+        best = lane < kWarps ? wbest[lane] : Best{0.f, kNone};
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          take(best, __shfl_xor_sync(0xffffffffu, best.score, o),
+               __shfl_xor_sync(0xffffffffu, best.idx, o));
+        if (lane < kCluster) *cluster.map_shared_rank(&cbest[pass][rank], lane) = best;
+      }
+      cluster.sync();
+      // every CTA joins the cluster's bests, so that all agree on a second pass
+      if (tid == 0) {
+        Best all = cbest[pass][0];
+        for (int k = 1; k < kCluster; ++k) take(all, cbest[pass][k].score, cbest[pass][k].idx);
+        chosen_pass[pass] = all.score > 0.f ? all.idx : -1;
+      }
+      __syncthreads();
+      chosen = chosen_pass[pass];
+      if (chosen >= 0) break;
     }
-    __syncthreads();
-    cluster.barrier_wait();
-    if (threadIdx.x < 2) {
-      Best best = wbest[threadIdx.x][0];
-      for (int w = 1; w < kWarps; ++w) take(best, wbest[threadIdx.x][w].score, wbest[threadIdx.x][w].idx);
-      *cluster.map_shared_rank(&cbest[threadIdx.x][rank], 0) = best;
-    }
-    cluster.sync();
-    if (rank != 0) return;
-    Best r = cbest[0][0], f = cbest[1][0];
-    for (int k = 1; k < kCluster; ++k) {
-      take(r, cbest[0][k].score, cbest[0][k].idx);
-      take(f, cbest[1][k].score, cbest[1][k].idx);
-    }
-    const Best best = r.score > 0.f ? r : f;
-    chosen = best.score > 0.f ? best.idx : -1;
   }
   if (rank != 0) return;
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     if (chosen < 0) record_status(a.status, dev_code(kDevBadList, kKerVerify, 2));
     a.n_accepted[b] = at;
   }
-  for (int i = threadIdx.x; i <= a.S; i += kThreads)
+  for (int i = tid; i <= a.S; i += kThreads)
     a.out[int64_t(b) * (a.S + 1) + i] =
         i < at ? a.tokens[int64_t(b) * a.S + i] : i == at ? chosen : -1;
 }
@@ -255,16 +404,20 @@ cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
   // at least 2048 logits
   int64_t nsplit = (152 * 8 + rows - 1) / rows;
   nsplit = min64(min64(nsplit, kMaxSplits), (int64_t(a.V) + 2047) / 2048);
-  const int piece = static_cast<int>((a.V + nsplit - 1) / nsplit);
+  // pieces of whole 16-byte groups
+  const int piece = static_cast<int>(((a.V + nsplit - 1) / nsplit + 7) / 8 * 8);
   if (rows * nsplit > 0x7fffffffLL || int64_t(a.B) * kCluster > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
-  stats_kernel<T><<<static_cast<unsigned>(rows * nsplit), kThreads, 0, s>>>(
-      a, stats, static_cast<int>(nsplit), piece);
-  cudaError_t e = cudaGetLastError();
+  const int ns = static_cast<int>(nsplit);
+  cudaError_t e = launch_pdl(stats_kernel<T>, dim3(static_cast<unsigned>(rows * nsplit)),
+                             dim3(kStatThreads), 0, s, a, stats, ns, piece);
   if (e != cudaSuccess) return e;
-  choose_kernel<T><<<static_cast<unsigned>(a.B) * kCluster, kThreads, 0, s>>>(
-      a, stats, static_cast<int>(nsplit));
-  return cudaGetLastError();
+  const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  const bool vec = a.V % 4 == 0 && at(a.target) % (4 * sizeof(T)) == 0 &&
+                   at(a.draft) % (4 * sizeof(T)) == 0 && at(a.expo) % 16 == 0;
+  const dim3 grid(static_cast<unsigned>(a.B) * kCluster);
+  return launch_pdl(vec ? choose_kernel<T, true> : choose_kernel<T, false>, grid, dim3(kThreads), 0,
+                    s, a, static_cast<const Stat*>(stats), ns);
 }
 
 }  // namespace

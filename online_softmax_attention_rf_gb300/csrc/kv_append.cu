@@ -27,9 +27,9 @@ struct Piece;  // 16 bytes of a row
 template <>
 struct Piece<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const float* p, float (&x)[N]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[N]) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   }
   static __device__ __forceinline__ void store(float* p, const float (&x)[N]) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -39,8 +39,7 @@ struct Piece<float> {
 template <>
 struct Piece<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[N]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[N]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -58,113 +57,133 @@ struct Piece<__nv_bfloat16> {
   }
 };
 
-// L lanes per row (a power of two >= pieces / 2).
+template <typename T>
+__device__ __forceinline__ uint4 raw(const T* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+// L lanes per row (a power of two >= pieces / 2), kThreads / L rows at a time.
+// A block takes one token: its slot, position, angles and norm weights are
+// read once and stay in registers while the token's rows pass, kRows of them
+// in flight per lane (the loads of all are issued before the first is used).
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a, int64_t rows) {
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a) {
   using P = Piece<T>;
   constexpr int N = P::N;
-  const int lane = threadIdx.x & (L - 1);
-  const int64_t row = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / L;
-  // rows run token-major: H query heads (when q is given), then Hkv key heads
-  // and Hkv value heads
+  constexpr int kRows = 3;
+  constexpr int kStep = kThreads / L;
+  const int lane = threadIdx.x & (L - 1), first = threadIdx.x / L;
+  const int t = blockIdx.x;
+  // rows of a token: H query heads (when q is given), then Hkv key heads and
+  // Hkv value heads
   const int heads = a.H + 2 * a.Hkv;
-  const bool live = row < rows;
-  const int64_t t = live ? row / heads : 0;
-  const int h = static_cast<int>(row - t * heads);
-  const int64_t slot = live ? a.slots[t] : -1;
-  bool ok = live && slot >= 0;
-  if (ok && slot >= int64_t(a.num_pages) * a.page) {
-    record_status(a.status, dev_code(kDevBadList, kKerAppend, 1));
-    ok = false;
-  }
-  int pos = 0;
-  if (ok && a.rot > 0) {
-    pos = a.pos[t];
-    if (pos < 0 || pos >= a.max_pos) {
-      record_status(a.status, dev_code(kDevBadList, kKerAppend, 2));
-      ok = false;
-    }
-  }
-  const bool is_q = h < a.H, is_v = h >= a.H + a.Hkv;
-  const int hk = is_q ? h : is_v ? h - a.H - a.Hkv : h - a.H;
-  const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) +
-                 t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + int64_t(hk) * a.d;
-  T* dst;
-  if (is_q) {
-    dst = static_cast<T*>(a.q_out) + (t * a.H + hk) * a.d;
-  } else {
-    const int s = ok ? static_cast<int>(slot) : 0;
-    dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) +
-          (s / a.page) * (is_v ? a.v_page_stride : a.k_page_stride) +
-          (s % a.page) * (is_v ? a.v_token_stride : a.k_token_stride) +
-          hk * (is_v ? a.v_head_stride : a.k_head_stride);
-  }
-  // this lane's pieces c0, c1 and the first angle of each
+  const bool mine = lane < a.d / (2 * N);
+  // this lane's pieces c0 and c1 of a row that is rotated, and of one that is not
   const int half = a.rot / 2;
   const int rot_lanes = a.rot / (2 * N);
-  const bool mine = ok && lane < a.d / (2 * N);
-  const bool split = !a.interleaved && lane < rot_lanes;
+  const bool rotates = lane < rot_lanes;
+  const bool split = !a.interleaved && rotates;
   const int c0 = split ? lane * N : 2 * lane * N;
   const int c1 = split ? c0 + half : c0 + N;
-  float x0[N], x1[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) x0[i] = x1[i] = 0.f;
-  if (mine) {
-    P::load(src + c0, x0);
-    P::load(src + c1, x1);
+  pdl_wait();
+  pdl_trigger();
+  const int64_t slot = a.slots[t];
+  if (slot < 0) return;
+  const int pos = a.rot > 0 ? a.pos[t] : 0;
+  const bool bad_slot = slot >= int64_t(a.num_pages) * a.page;
+  if (bad_slot || (a.rot > 0 && (pos < 0 || pos >= a.max_pos))) {
+    if (threadIdx.x == 0)
+      record_status(a.status, dev_code(kDevBadList, kKerAppend, bad_slot ? 1 : 2));
+    return;
   }
-  const T* w = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
-  if (a.norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (mine && !is_v && w != nullptr) {
-      const float r = 1.f / sqrtf(ss / a.d + a.eps);
-      float w0[N], w1[N];
-      P::load(w + c0, w0);
-      P::load(w + c1, w1);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x0[i] = x0[i] * r * w0[i];
-        x1[i] = x1[i] * r * w1[i];
-      }
-    }
-  }
-  if (!mine) return;
-  if (!is_v && lane < rot_lanes) {
-    const float* cs = a.cos_sin + int64_t(pos) * a.rot;
-    float c[N], s[N];
-    const int a0 = split ? c0 : c0 / 2;  // N angles from here on
+  const int page = static_cast<int>(slot) / a.page, in_page = static_cast<int>(slot) - page * a.page;
+  const T* q_row = static_cast<const T*>(a.q) + t * a.q_stride;
+  const T* k_row = static_cast<const T*>(a.k) + t * a.k_stride;
+  const T* v_row = static_cast<const T*>(a.v) + t * a.v_stride;
+  T* q_to = static_cast<T*>(a.q_out) + int64_t(t) * a.H * a.d;
+  T* k_to = static_cast<T*>(a.k_cache) + page * a.k_page_stride + in_page * a.k_token_stride;
+  T* v_to = static_cast<T*>(a.v_cache) + page * a.v_page_stride + in_page * a.v_token_stride;
+  float c[N], s[N];
+  if (rotates) {
+    const float* cs = a.cos_sin + int64_t(pos) * a.rot + (split ? c0 : c0 / 2);  // N angles
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const float4 cv = *reinterpret_cast<const float4*>(cs + a0 + i);
-      const float4 sv = *reinterpret_cast<const float4*>(cs + half + a0 + i);
+      const float4 cv = *reinterpret_cast<const float4*>(cs + i);
+      const float4 sv = *reinterpret_cast<const float4*>(cs + half + i);
       c[i] = cv.x; c[i + 1] = cv.y; c[i + 2] = cv.z; c[i + 3] = cv.w;
       s[i] = sv.x; s[i + 1] = sv.y; s[i + 2] = sv.z; s[i + 3] = sv.w;
     }
-    if (split) {
+  }
+  // every lane runs every round: the norm's sum is taken by whole warps
+  for (int h0 = first; h0 - first < heads; h0 += kRows * kStep) {
+    uint4 raw0[kRows], raw1[kRows];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float u = x0[i], v = x1[i];
-        x0[i] = u * c[i] - v * s[i];
-        x1[i] = v * c[i] + u * s[i];
+    for (int j = 0; j < kRows; ++j) {
+      const int h = h0 + j * kStep;
+      const T* src = h < a.H ? q_row + h * a.d
+                             : h < a.H + a.Hkv ? k_row + (h - a.H) * a.d
+                                               : v_row + (h - a.H - a.Hkv) * a.d;
+      raw0[j] = raw1[j] = make_uint4(0, 0, 0, 0);
+      if (mine && h < heads) {
+        raw0[j] = raw(src + c0);
+        raw1[j] = raw(src + c1);
       }
-    } else {
+    }
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float u = x0[2 * i], v = x0[2 * i + 1];
-        x0[2 * i] = u * c[i] - v * s[i];
-        x0[2 * i + 1] = v * c[i] + u * s[i];
-        const float y = x1[2 * i], z = x1[2 * i + 1];
-        x1[2 * i] = y * c[N / 2 + i] - z * s[N / 2 + i];
-        x1[2 * i + 1] = z * c[N / 2 + i] + y * s[N / 2 + i];
+    for (int j = 0; j < kRows; ++j) {
+      const int h = h0 + j * kStep;
+      const bool is_q = h < a.H, is_v = h >= a.H + a.Hkv;
+      const T* w = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
+      float x0[N], x1[N];
+      P::unpack(raw0[j], x0);
+      P::unpack(raw1[j], x1);
+      if (a.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (mine && !is_v && w != nullptr) {
+          const float r = 1.f / sqrtf(ss / a.d + a.eps);
+          float w0[N], w1[N];
+          P::unpack(raw(w + c0), w0);
+          P::unpack(raw(w + c1), w1);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            x0[i] = x0[i] * r * w0[i];
+            x1[i] = x1[i] * r * w1[i];
+          }
+        }
+      }
+      if (!is_v && rotates) {
+        if (split) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float u = x0[i], v = x1[i];
+            x0[i] = u * c[i] - v * s[i];
+            x1[i] = v * c[i] + u * s[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            const float u = x0[2 * i], v = x0[2 * i + 1];
+            x0[2 * i] = u * c[i] - v * s[i];
+            x0[2 * i + 1] = v * c[i] + u * s[i];
+            const float y = x1[2 * i], z = x1[2 * i + 1];
+            x1[2 * i] = y * c[N / 2 + i] - z * s[N / 2 + i];
+            x1[2 * i + 1] = z * c[N / 2 + i] + y * s[N / 2 + i];
+          }
+        }
+      }
+      if (mine && h < heads) {
+        T* dst = is_q ? q_to + h * a.d
+                      : is_v ? v_to + (h - a.H - a.Hkv) * a.v_head_stride
+                             : k_to + (h - a.H) * a.k_head_stride;
+        P::store(dst + c0, x0);
+        P::store(dst + c1, x1);
       }
     }
   }
-  P::store(dst + c0, x0);
-  P::store(dst + c1, x1);
 }
 
 __global__ void paged_slots_kernel(const int32_t* __restrict__ cu_q,
@@ -202,11 +221,8 @@ __global__ void paged_slots_kernel(const int32_t* __restrict__ cu_q,
 
 template <typename T, int L>
 cudaError_t launch_l(const KvAppendArgs& a, cudaStream_t s) {
-  const int64_t rows = int64_t(a.T) * (a.H + 2 * a.Hkv);
-  const int64_t grid = (rows * L + kThreads - 1) / kThreads;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kv_append_kernel<T, L><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, rows);
-  return cudaGetLastError();
+  return launch_pdl(kv_append_kernel<T, L>, dim3(static_cast<unsigned>(a.T)), dim3(kThreads), 0, s,
+                    a);
 }
 
 template <typename T>

@@ -17,8 +17,10 @@ constexpr int kItemCost = 2;
 constexpr int kPairCost = 3;
 constexpr int kSingleCost = 2;
 // A span is worth at least this much, so that a short step is not cut into
-// more parts than merging them pays for.
+// more parts than merging them pays for. Two cuts of one item are then more
+// than a step apart: no CTA inside an item is left without steps.
 constexpr int kMinSpan = 8;
+static_assert(kMinSpan / 2 >= kPairCost && kPairCost >= kSingleCost, "cuts may coincide");
 
 struct Item {
   int rows, steps, cost;
@@ -80,7 +82,7 @@ __device__ __forceinline__ bool same_item(const PlanStart& a, const PlanStart& b
 
 __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArgs a) {
   __shared__ PlanStart start[kPlanCtas + 1];
-  __shared__ int flag[kPlanCtas + 1], nrows[kPlanCtas + 1], nparts[kPlanCtas + 1];
+  __shared__ int flag[kPlanCtas + 1], units[kPlanCtas + 1];
   __shared__ int64_t wsum[32];
   __shared__ int64_t carry;
   PlanHeader* h = static_cast<PlanHeader*>(a.plan);
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
   if (__syncthreads_or(bad)) {
     // lengths that contradict themselves or the table: nothing is computed
     if (tid == 0) {
-      h->ctas = h->n_merge = h->merge_rows = 0;
+      h->ctas = h->n_merge = h->merge_units = 0;
       record_status(a.status, dev_code(kDevBadList, kKerPaged, 1));
     }
     return;
@@ -159,41 +161,38 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
   if (tid <= ctas) start[tid] = locate(ctas > 0 ? total * tid / ctas : 0, cost, cu, kvl, a);
   __syncthreads();
   // items that a cut falls into: found by the first cut inside each
+  PlanMerge m{};
+  bool first = false;
   if (tid <= ctas) {
     const PlanStart s = start[tid];
-    bool first = false;
-    int parts = 0, rows = 0;
     if (tid > 0 && tid < ctas && s.step > 0) {
       const PlanStart p = start[tid - 1];
       first = !same_item(p, s) || p.step == 0;
       if (first) {
-        parts = 1;
+        int parts = 1;
         while (tid + parts <= ctas && start[tid + parts - 1].step > 0 &&
                same_item(start[tid + parts - 1], s))
           ++parts;
-        rows = item_of(s.pair, cu[s.seq + 1] - cu[s.seq], kvl[s.seq], a.causal, G).rows;
+        const int rows = item_of(s.pair, cu[s.seq + 1] - cu[s.seq], kvl[s.seq], a.causal, G).rows;
+        m = PlanMerge{s.seq, s.head, s.pair, tid - 1, parts, rows, 0, 0};
       }
     }
     flag[tid] = first;
-    nrows[tid] = rows;
-    nparts[tid] = parts;
+    units[tid] = first ? plan_units(m.rows / G, 0, G) + plan_units(m.rows / G, 1, G) : 0;
     h->start[tid] = s;
   }
   __syncthreads();
   if (tid <= ctas) {
-    int idx = 0, row0 = 0;
+    int idx = 0;
     for (int c = 0; c < tid; ++c) {
       idx += flag[c];
-      row0 += nrows[c];
+      m.unit0 += units[c];
     }
-    if (flag[tid]) {
-      const PlanStart s = start[tid];
-      h->merge[idx] = PlanMerge{s.seq, s.head, s.pair, tid - 1, nparts[tid], nrows[tid], row0, 0};
-    }
+    if (first) h->merge[idx] = m;
     if (tid == ctas) {
       h->ctas = ctas;
       h->n_merge = idx;
-      h->merge_rows = row0;
+      h->merge_units = m.unit0;
     }
   }
 }

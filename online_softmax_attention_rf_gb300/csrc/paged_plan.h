@@ -30,17 +30,17 @@ struct PlanStart {
   int seq, head, pair, step;
 };
 
-// An item computed by the CTAs [cta, cta + parts); its rows are the rows
-// [row0, row0 + rows) of the merge.
+// An item computed by the CTAs [cta, cta + parts), with `rows` packed rows. The
+// merge takes each of its tiles in units of 32 rows, numbered from unit0 on.
 struct PlanMerge {
-  int seq, head, pair, cta, parts, rows, row0, pad;
+  int seq, head, pair, cta, parts, rows, unit0, pad;
 };
 
 struct PlanHeader {
   int magic, B, T, H, Hkv, page, max_pages, causal;
   int ctas;         // spans in use
   int n_merge;      // items in parts
-  int merge_rows;   // their rows
+  int merge_units;  // their units of 32 rows
   int pad[5];
   PlanStart start[kPlanCtas + 1];
   PlanMerge merge[kPlanCtas];
@@ -65,6 +65,13 @@ __host__ __device__ inline size_t plan_bytes(int B) {
 
 // Tokens per 128-row tile.
 __host__ __device__ inline int plan_tile_tokens(int G) { return kPlanTile / G; }
+
+// Units of 32 rows in tile `tile` of an item of ntok tokens.
+__host__ __device__ inline int plan_units(int ntok, int tile, int G) {
+  const int tt = plan_tile_tokens(G);
+  const int tok = ntok - tile * tt < tt ? ntok - tile * tt : tt;
+  return tok > 0 ? (tok * G + 31) / 32 : 0;
+}
 
 // Keys that token i of n new ones sees, of kv cached ones.
 __host__ __device__ inline int plan_visible(int i, int n, int kv, int causal) {

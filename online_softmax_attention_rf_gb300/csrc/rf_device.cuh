@@ -232,6 +232,22 @@ __device__ __forceinline__ void st_global_policy(uint4* a, uint4 v, uint64_t pol
                : "memory");
 }
 
+// 32-byte global store (a full sector per lane). a 32-byte aligned.
+__device__ __forceinline__ void st_global_v8(void* a, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Programmatic dependent launch: a kernel launched so may start before the
+// ones ahead of it in the stream are done; it touches global memory only after
+// pdl_wait, which returns when they are done and their writes visible.
+// pdl_trigger lets the next such kernel start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 
 // Allocate `ncols` TMEM columns (power of two >= 32) for this CTA; the base

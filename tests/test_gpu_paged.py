@@ -172,7 +172,7 @@ def _spans(plan, cu, kv, H, Hkv, causal):
     """The plan's spans as lists of (seq, head, pair, first step, end step, steps)
     and its merge entries, decoded from device memory."""
     w = plan.buf.cpu().numpy().view(np.int32)
-    ctas, n_merge, merge_rows = w[8], w[9], w[10]
+    ctas, n_merge, units = w[8], w[9], w[10]
     start = w[16:16 + 153 * 4].reshape(153, 4)
     merge = w[16 + 153 * 4:16 + 153 * 4 + 152 * 8].reshape(152, 8)[:n_merge]
     tt = 128 // (H // Hkv)
@@ -200,7 +200,7 @@ def _spans(plan, cu, kv, H, Hkv, causal):
         spans.append(span)
     assert ctas == 0 or (tuple(start[0]) == items[0][:3] + (0,)
                          and tuple(start[ctas]) == (len(kv), 0, 0, 0))
-    return items, spans, merge, merge_rows
+    return items, spans, merge, units
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -217,7 +217,7 @@ def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal)
     kv = [m for _, m in lengths]
     plan = api.PagedPlan(_i32(cu), _i32(kv), cu[-1] + 3, H, Hkv, 16, 6250, causal)
     assert api.device_status() == 0
-    items, spans, merge, merge_rows = _spans(plan, cu, kv, H, Hkv, causal)
+    items, spans, merge, units = _spans(plan, cu, kv, H, Hkv, causal)
     parts = {}
     for cta, span in enumerate(spans):
         for i, k0, k1 in span:
@@ -232,14 +232,14 @@ def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal)
             cut[i] = pieces
     where = {it[:3]: i for i, it in enumerate(items)}
     assert sorted(where[tuple(m[:3])] for m in merge) == sorted(cut)
-    row0 = 0
+    unit0, G = 0, H // Hkv
     for m in merge:
         i = where[tuple(m[:3])]
-        live = [c for c, _, _ in cut[i]]
-        assert live[0] == m[3] and set(live) <= set(range(m[3], m[3] + m[4]))
-        assert m[5] == items[i][4] and m[6] == row0
-        row0 += m[5]
-    assert row0 == merge_rows
+        assert [c for c, _, _ in cut[i]] == list(range(m[3], m[3] + m[4]))
+        assert m[5] == items[i][4] and m[6] == unit0
+        first = min(m[5], 128 // G * G)        # rows of the first tile, in units of 32
+        unit0 += -(-first // 32) + -(-(m[5] - first) // 32)
+    assert unit0 == units
     if len(spans) > 1:     # and the spans are even, up to a step and an item's fixed cost
         cost = [sum(2 + (k1 - k0) * (3 if items[i][4] > 128 // (H // Hkv) * (H // Hkv) else 2)
                     for i, k0, k1 in span) for span in spans]
