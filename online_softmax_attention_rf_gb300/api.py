@@ -563,6 +563,25 @@ def splitk_merge(o_part, lse_part, out_dtype=torch.bfloat16):
     return o, lse
 
 
+# The paged serving calls run once a layer or once a token, where the host's
+# share of a call shows: each checks what it is given in one expression and
+# leaves naming the fault to a function of its own.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(index, fn, *args):
+    """fn(*args, the current stream of device `index`), with that device current."""
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != RF_OK:
+        _check(status)
+
+
 def _same_device(*ts):
     """The one CUDA device of the tensors that are given."""
     dev = None
@@ -587,23 +606,28 @@ def _expect(t, name, dtype, shape, optional=False):
                          % (name, dtype, tuple(shape)))
 
 
-def _pool(cache, name, Hkv, d, dtype):
-    """Strides (page, token, head) of a [pages, page, Hkv, d] pool (any strided view
-    whose last dimension is contiguous)."""
+def _fits(t, dtype, shape, index):
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
+
+
+def _expect_pool(cache, name, Hkv, d, dtype):
     if cache.dim() != 4 or tuple(cache.shape[2:]) != (Hkv, d) or cache.dtype != dtype:
         raise ValueError("%s must be a %s pool [pages, page, %d, %d]" % (name, dtype, Hkv, d))
     if cache.stride(3) != 1:
         raise ValueError("%s's last dimension must be contiguous" % name)
-    return cache.stride(0), cache.stride(1), cache.stride(2)
 
 
-def _rows(x, name, T, heads, d, dtype):
-    """Token stride of [T, heads, d] rows whose heads are back to back."""
+def _expect_rows(x, name, T, heads, d, dtype):
     if x.dim() != 3 or tuple(x.shape) != (T, heads, d) or x.dtype != dtype:
         raise ValueError("%s must be a %s tensor [%d, %d, %d]" % (name, dtype, T, heads, d))
     if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
         raise ValueError("%s: a token's heads must lie back to back" % name)
-    return x.stride(0) if T > 1 else heads * d
+
+
+def _expect_table(block_table, B):
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages] with contiguous rows")
 
 
 def paged_slots(cu_q, kv_len, block_table, page_size, num_pages, total_q):
@@ -614,23 +638,40 @@ def paged_slots(cu_q, kv_len, block_table, page_size, num_pages, total_q):
     B = kv_len.shape[0]
     _expect(cu_q, "cu_q", torch.int32, (B + 1,))
     _expect(kv_len, "kv_len", torch.int32, (B,))
-    stride, width = _table(block_table, B)
+    _expect_table(block_table, B)
+    width = block_table.shape[1]
     pos = torch.empty(total_q, dtype=torch.int32, device=dev)
     slots = torch.empty(total_q, dtype=torch.int64, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().rf_paged_slots(_ptr(cu_q), _ptr(kv_len), _ptr(block_table), stride, B,
-                                    int(total_q), width, int(page_size), int(num_pages),
-                                    _ptr(pos), _ptr(slots), _stream()))
+    _launch(dev.index, lib().rf_paged_slots, cu_q.data_ptr(), kv_len.data_ptr(),
+            block_table.data_ptr(), block_table.stride(0) if B > 1 else width, B, int(total_q),
+            width, int(page_size), int(num_pages), pos.data_ptr(), slots.data_ptr())
     return pos, slots
 
 
-def _table(block_table, B):
-    if block_table.dim() != 2 or block_table.shape[0] != B or \
-            block_table.dtype != torch.int32 or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [B, max_pages] with contiguous rows")
-    width = block_table.shape[1]
-    return (block_table.stride(0) if B > 1 else width), width
+def _refuse_append(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight, k_weight, q_out):
+    _same_device(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight, k_weight, q_out)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, d]")
+    T, Hkv, d = k.shape
+    _expect_rows(k, "k", T, Hkv, d, k.dtype)
+    _expect_rows(v, "v", T, Hkv, d, k.dtype)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, H, d]")
+        _expect_rows(q, "q", T, q.shape[1], d, k.dtype)
+        _expect(q_out, "q_out", k.dtype, (T, q.shape[1], d), optional=True)
+    _expect_pool(k_cache, "k_cache", Hkv, d, k.dtype)
+    _expect_pool(v_cache, "v_cache", Hkv, d, k.dtype)
+    if v_cache.shape[:2] != k_cache.shape[:2]:
+        raise ValueError("k_cache and v_cache must have the same pages")
+    _expect(slots, "slots", torch.int64, (T,))
+    _expect(q_weight, "q_weight", k.dtype, (d,), optional=True)
+    _expect(k_weight, "k_weight", k.dtype, (d,), optional=True)
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 tensor [max_pos, rot]")
+        _expect(pos, "pos", torch.int32, (T,))
+    raise ValueError("kv_append_paged: unsupported tensors")
 
 
 def kv_append_paged(q, k, v, k_cache, v_cache, slots, pos=None, cos_sin=None, q_weight=None,
@@ -643,41 +684,45 @@ def kv_append_paged(q, k, v, k_cache, v_cache, slots, pos=None, cos_sin=None, q_
     k_cache, v_cache [pages, page, Hkv, d] (any strides with d contiguous),
     slots int64 [T] (negative: skipped) -> q_out [T, H, d], or None without q.
     q_out may be q itself when q is contiguous."""
-    dev = _same_device(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight, k_weight, q_out)
-    if k.dim() != 3:
-        raise ValueError("k must be [T, Hkv, d]")
-    T, Hkv, d = k.shape
-    ks, vs = _rows(k, "k", T, Hkv, d, k.dtype), _rows(v, "v", T, Hkv, d, k.dtype)
-    H, qs = 0, 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [T, H, d]")
-        H = q.shape[1]
-        qs = _rows(q, "q", T, H, d, k.dtype)
-        if q_out is None:
-            q_out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
-        _expect(q_out, "q_out", k.dtype, (T, H, d))
-    kst = _pool(k_cache, "k_cache", Hkv, d, k.dtype)
-    vst = _pool(v_cache, "v_cache", Hkv, d, k.dtype)
-    if v_cache.shape[:2] != k_cache.shape[:2]:
-        raise ValueError("k_cache and v_cache must have the same pages")
-    _expect(slots, "slots", torch.int64, (T,))
-    _expect(q_weight, "q_weight", k.dtype, (d,), optional=True)
-    _expect(k_weight, "k_weight", k.dtype, (d,), optional=True)
-    rot, max_pos = 0, 0
-    if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 tensor [max_pos, rot]")
-        max_pos, rot = cos_sin.shape
-        _expect(pos, "pos", torch.int32, (T,))
-    with torch.cuda.device(dev):
-        _check(lib().rf_kv_append_paged(
-            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_out if q is not None else None),
-            _ptr(k_cache), *kst, _ptr(v_cache), *vst, T, H, Hkv, d, k_cache.shape[1],
-            k_cache.shape[0], _ptr(slots), _ptr(pos), _ptr(cos_sin), max_pos, rot,
-            1 if interleaved else 0, _ptr(q_weight), _ptr(k_weight), float(eps), _dt(k),
-            _stream()))
-    return q_out if q is not None else None
+    index, dtype, shape = k.get_device(), k.dtype, k.shape
+    kst, vst, kc, vc = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+    pool = k_cache.shape
+    ok = (index >= 0 and len(shape) == 3 and v.shape == shape and v.dtype is dtype
+          and v.get_device() == index and kst[2] == 1 == vst[2]
+          and (shape[1] == 1 or kst[1] == shape[2] == vst[1])
+          and len(pool) == 4 and pool[2:] == shape[1:] and v_cache.shape == pool
+          and kc[3] == 1 == vc[3] and k_cache.dtype is dtype and v_cache.dtype is dtype
+          and k_cache.get_device() == index and v_cache.get_device() == index
+          and _fits(slots, torch.int64, shape[:1], index)
+          and (q_weight is None or _fits(q_weight, dtype, shape[2:], index))
+          and (k_weight is None or _fits(k_weight, dtype, shape[2:], index))
+          and (cos_sin is None or (cos_sin.dim() == 2 and cos_sin.is_contiguous()
+                                   and cos_sin.dtype is torch.float32
+                                   and cos_sin.get_device() == index and pos is not None
+                                   and _fits(pos, torch.int32, shape[:1], index))))
+    H = qs = 0
+    if ok and q is not None:
+        qshape, qst = q.shape, q.stride()
+        ok = (len(qshape) == 3 and qshape[0] == shape[0] and qshape[2] == shape[2]
+              and q.dtype is dtype and q.get_device() == index and qst[2] == 1
+              and (qshape[1] == 1 or qst[1] == shape[2])
+              and (q_out is None or _fits(q_out, dtype, qshape, index)))
+        H = qshape[1]
+        qs = qst[0] if qshape[0] > 1 else H * shape[2]
+    if not ok:
+        _refuse_append(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight, k_weight, q_out)
+    T, Hkv, d = shape
+    if q is not None and q_out is None:
+        q_out = torch.empty(qshape, dtype=dtype, device=q.device)
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    _launch(index, lib().rf_kv_append_paged, None if q is None else q.data_ptr(), qs, k.data_ptr(),
+            kst[0] if T > 1 else Hkv * d, v.data_ptr(), vst[0] if T > 1 else Hkv * d, None if q is None else q_out.data_ptr(),
+            k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2], T, H,
+            Hkv, d, pool[1], pool[0], slots.data_ptr(), None if pos is None else pos.data_ptr(),
+            None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot, 1 if interleaved else 0,
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), eps, _dt(k))
+    return None if q is None else q_out
 
 
 class PagedPlan:
@@ -698,13 +743,12 @@ class PagedPlan:
 
     def update(self, cu_q, kv_len):
         """The plan for new lengths of the same batch size."""
-        _same_device(cu_q, kv_len, self.buf)
+        dev = _same_device(cu_q, kv_len, self.buf)
         _expect(cu_q, "cu_q", torch.int32, (self.B + 1,))
         _expect(kv_len, "kv_len", torch.int32, (self.B,))
-        with torch.cuda.device(self.buf.device):
-            _check(lib().rf_paged_plan(_ptr(cu_q), _ptr(kv_len), self.B, self.T, self.H, self.Hkv,
-                                       self.page, self.max_pages, 1 if self.causal else 0,
-                                       _ptr(self.buf), self.buf.numel(), _stream()))
+        _launch(dev.index, lib().rf_paged_plan, cu_q.data_ptr(), kv_len.data_ptr(), self.B, self.T,
+                self.H, self.Hkv, self.page, self.max_pages, 1 if self.causal else 0,
+                self.buf.data_ptr(), self.buf.numel())
         return self
 
 
@@ -715,39 +759,60 @@ def attn_paged_workspace(d, device="cuda"):
     return torch.empty(max(1, n // 4), dtype=torch.float32, device=device)
 
 
+def _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace):
+    _same_device(q, k_cache, v_cache, block_table, plan.buf, out, lse, workspace)
+    if q.dim() != 3 or q.shape[:2] != (plan.T, plan.H):
+        raise ValueError("q must be [%d, %d, d], as the plan was made for" % (plan.T, plan.H))
+    T, H, d = q.shape
+    _expect_rows(q, "q", T, H, d, q.dtype)
+    _expect_pool(k_cache, "k_cache", plan.Hkv, d, q.dtype)
+    _expect_pool(v_cache, "v_cache", plan.Hkv, d, q.dtype)
+    if v_cache.shape[:2] != k_cache.shape[:2] or k_cache.shape[1] != plan.page:
+        raise ValueError("k_cache and v_cache must have the same pages, of the plan's size")
+    _expect_table(block_table, plan.B)
+    if block_table.shape[1] != plan.max_pages:
+        raise ValueError("block_table must be as wide as the plan's max_pages")
+    _expect(out, "out", q.dtype, (T, H, d), optional=True)
+    _expect(lse, "lse", torch.float32, (T, H), optional=True)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    raise ValueError("attn_paged: unsupported tensors")
+
+
 def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse=None,
                with_lse=True, workspace=None):
     """rf_attn_paged: q [T, H, d] bf16 (a strided view of a fused projection
     fits), k_cache, v_cache [pages, page, Hkv, d] (any strides with d
     contiguous), block_table int32 [B, max_pages], plan a ``PagedPlan`` of the
     step -> (o [T, H, d], lse float32 [T, H] or None)."""
-    dev = _same_device(q, k_cache, v_cache, block_table, plan.buf, out, lse, workspace)
-    if q.dim() != 3 or q.shape[:2] != (plan.T, plan.H):
-        raise ValueError("q must be [%d, %d, d], as the plan was made for" % (plan.T, plan.H))
-    T, H, d = q.shape
-    qs = _rows(q, "q", T, H, d, q.dtype)
-    kst = _pool(k_cache, "k_cache", plan.Hkv, d, q.dtype)
-    vst = _pool(v_cache, "v_cache", plan.Hkv, d, q.dtype)
-    if v_cache.shape[:2] != k_cache.shape[:2] or k_cache.shape[1] != plan.page:
-        raise ValueError("k_cache and v_cache must have the same pages, of the plan's size")
-    stride, width = _table(block_table, plan.B)
-    if width != plan.max_pages:
-        raise ValueError("block_table must be as wide as the plan's max_pages")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    o = torch.empty((T, H, d), dtype=q.dtype, device=dev) if out is None else out
-    _expect(o, "out", q.dtype, (T, H, d))
+    index, dtype, shape, pool = q.get_device(), q.dtype, q.shape, k_cache.shape
+    qs, kc, vc, tb = q.stride(), k_cache.stride(), v_cache.stride(), block_table.stride()
+    d = shape[-1]
+    ok = (index >= 0 and shape == (plan.T, plan.H, d) and qs[-1] == 1
+          and (plan.H == 1 or qs[1] == d)
+          and pool[1:] == (plan.page, plan.Hkv, d) and v_cache.shape == pool
+          and kc[-1] == 1 == vc[-1] and k_cache.dtype is dtype and v_cache.dtype is dtype
+          and block_table.dtype is torch.int32 and tb[-1] == 1
+          and block_table.shape == (plan.B, plan.max_pages)
+          and k_cache.get_device() == index and v_cache.get_device() == index
+          and block_table.get_device() == index and plan.buf.get_device() == index
+          and (out is None or _fits(out, dtype, shape, index))
+          and (lse is None or _fits(lse, torch.float32, shape[:2], index))
+          and (workspace is None or (workspace.is_contiguous()
+                                     and workspace.get_device() == index)))
+    if not ok:
+        _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace)
+    dev = q.device
+    o = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
     if lse is None and with_lse:
-        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-    _expect(lse, "lse", torch.float32, (T, H), optional=True)
-    ws = attn_paged_workspace(d, dev) if workspace is None else workspace
-    _cuda(ws)
-    with torch.cuda.device(dev):
-        _check(lib().rf_attn_paged(
-            _ptr(q), qs, _ptr(k_cache), *kst, _ptr(v_cache), *vst, plan.page, k_cache.shape[0],
-            _ptr(block_table), stride, width, _ptr(plan.buf), plan.B, T, H, plan.Hkv, d,
-            float(scale), _ptr(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _dt(q),
-            _stream()))
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = attn_paged_workspace(d, dev)
+    _launch(index, lib().rf_attn_paged, q.data_ptr(), qs[0] if plan.T > 1 else plan.H * d, k_cache.data_ptr(), kc[0], kc[1],
+            kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2], plan.page, pool[0],
+            block_table.data_ptr(), tb[0], plan.max_pages, plan.buf.data_ptr(), plan.B, plan.T,
+            plan.H, plan.Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, o.data_ptr(),
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _dt(q))
     return o, lse
 
 
@@ -757,13 +822,8 @@ def draft_verify_workspace(B, S, device="cuda"):
     return torch.empty(max(1, n), dtype=torch.uint8, device=device)
 
 
-def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None, workspace=None):
-    """rf_draft_verify: target logits [B, S + 1, V], draft logits [B, S, V] (or
-    None: drafts with certainty), tokens int32 [B, S], u float32 [B, S] in
-    [0, 1), expo float32 [B, V] exponential variates, n_draft int32 [B],
-    temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1], n_accepted
-    int32 [B])."""
-    dev = _same_device(target, draft, tokens, u, expo, n_draft, temperature, workspace)
+def _refuse_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace):
+    _same_device(target, draft, tokens, u, expo, n_draft, temperature, workspace)
     if target.dim() != 3 or target.shape[1] < 2:
         raise ValueError("target must be [B, S + 1, V] with S >= 1")
     B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
@@ -774,15 +834,41 @@ def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None,
     _expect(expo, "expo", torch.float32, (B, V))
     _expect(n_draft, "n_draft", torch.int32, (B,), optional=True)
     _expect(temperature, "temperature", torch.float32, (B,), optional=True)
-    out = torch.empty(B, S + 1, dtype=torch.int32, device=dev)
-    n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
-    ws = draft_verify_workspace(B, S, dev) if workspace is None else workspace
-    _cuda(ws)
-    with torch.cuda.device(dev):
-        _check(lib().rf_draft_verify(
-            _ptr(target), _ptr(draft), _ptr(tokens), _ptr(u), _ptr(expo), _ptr(n_draft),
-            _ptr(temperature), B, S, V, _ptr(out), _ptr(n_accepted), _ptr(ws),
-            ws.numel() * ws.element_size(), _dt(target), _stream()))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    raise ValueError("draft_verify: unsupported tensors")
+
+
+def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None, workspace=None):
+    """rf_draft_verify: target logits [B, S + 1, V], draft logits [B, S, V] (or
+    None: drafts with certainty), tokens int32 [B, S], u float32 [B, S] in
+    [0, 1), expo float32 [B, V] exponential variates, n_draft int32 [B],
+    temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1], n_accepted
+    int32 [B])."""
+    index, dtype, shape = target.get_device(), target.dtype, target.shape
+    ok = index >= 0 and len(shape) == 3 and shape[1] > 1 and target.is_contiguous()
+    if ok:
+        B, S, V = shape[0], shape[1] - 1, shape[2]
+        ok = ((draft is None or _fits(draft, dtype, (B, S, V), index))
+              and _fits(tokens, torch.int32, (B, S), index)
+              and _fits(u, torch.float32, (B, S), index)
+              and _fits(expo, torch.float32, (B, V), index)
+              and (n_draft is None or _fits(n_draft, torch.int32, (B,), index))
+              and (temperature is None or _fits(temperature, torch.float32, (B,), index))
+              and (workspace is None or (workspace.is_contiguous()
+                                         and workspace.get_device() == index)))
+    if not ok:
+        _refuse_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
+    dev = target.device
+    out = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
+    n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = draft_verify_workspace(B, S, dev)
+    _launch(index, lib().rf_draft_verify, target.data_ptr(),
+            None if draft is None else draft.data_ptr(), tokens.data_ptr(), u.data_ptr(),
+            expo.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
+            None if temperature is None else temperature.data_ptr(), B, S, V, out.data_ptr(),
+            n_accepted.data_ptr(), workspace.data_ptr(), workspace.nbytes, _dt(target))
     return out, n_accepted
 
 

@@ -14,19 +14,24 @@
 //    span of key tiles. A whole item is written by the CTA itself; a part goes
 //    to the workspace and attn_paged_merge joins the parts by log-sum-exp.
 //  - A key tile of 128 keys comes in boxes of R = gcd(page, 128) rows, one TMA
-//    copy per box and 64 columns, each lane of the producer warp looking up
-//    one box's page. Boxes that start past the cache's end are not copied; the
-//    rows of V between the end and the tile's edge are zeroed in shared memory
-//    before P.V (their weights are 0, but 0 * NaN is not).
-//  - An item of one tile (up to 128 packed rows) is worked on by both softmax
-//    groups: they take alternate key tiles and join their states at the end.
-//    With one group the chain Q K^T -> softmax -> P.V of a tile would not keep
-//    up with memory; with two it runs at twice the rate.
+//    copy per box and 64 columns, each lane of a producer warp looking up one
+//    box's page. A page of 16 takes 32 copies a step; one warp's issue of them
+//    would bound a decode step at 5.5 TB/s, so K and V have a producer each.
+//    Boxes that start past the cache's end are not copied; the rows of V between
+//    the end and the tile's edge are zeroed in shared memory before P.V (their
+//    weights are 0, but 0 * NaN is not).
+//  - An item of one tile (up to 128 packed rows) is either split: both softmax
+//    groups take alternate key tiles and join their states at the end (with one
+//    group the chain Q K^T -> softmax -> P.V of a tile would not keep up with
+//    memory); or, when it is short, solo: the groups take whole items in turn,
+//    and one's epilogue runs under the other's softmax.
 //
-// Roles of the 352 threads, tensor memory, the lock and the reuse of S by P
-// are those of attn_tc.cu: warps 0-3 and 4-7 softmax groups, warp 8 producer,
-// warps 9 and 10 MMA issuers of the two groups. Every wait is bounded; on
-// expiry the kernel records a status code and the CTA unwinds.
+// Roles of the 384 threads: warps 0-3 and 4-7 softmax groups, warp 8 walks the
+// span, publishes a descriptor of each segment (an item or a part of one) and
+// copies Q and K, warp 11 copies V, warps 9 and 10 issue the two groups' MMAs.
+// Tensor memory, the lock and the reuse of S by P are those of attn_tc.cu.
+// Every wait is bounded; on expiry the kernel records a status code and the CTA
+// unwinds, the five warps of a group together at a reducing named barrier.
 //
 // P is rounded to bf16 for the tensor cores (scores, maxima, sums and
 // accumulators stay in float32): half a step, 2^-8, of each weight. The row
@@ -44,9 +49,12 @@ namespace {
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale when the max grows > 256x
 constexpr int kBM = kPlanTile;             // packed query rows per tile
 constexpr int kBN = kPlanTile;             // keys per tile
-constexpr int kThreads = 352;
-constexpr int kWarpLoad = 8;
-constexpr int kWarpIssue = 9;
+constexpr int kThreads = 384;
+constexpr int kWarpK = 8;                  // spans, Q, K; TMEM allocator
+constexpr int kWarpIssue = 9;              // warps 9 and 10
+constexpr int kWarpV = 11;
+constexpr int kSegs = 4;                   // segment descriptors in flight
+constexpr int kSoloSteps = 4;              // a one-tile segment up to this long is solo
 constexpr int kChunk = 16384;              // one 128-row x 64-column bf16 swizzle block
 
 template <int D>
@@ -56,7 +64,7 @@ struct Layout {
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kOffQ + 2 * kTileBytes;
   static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
-  static constexpr int kBarBytes = 256;
+  static constexpr int kBarBytes = 640;
   static constexpr int kOffXch = kOffBar + kBarBytes;  // group 1's m and l for group 0
   static constexpr int kXchBytes = 2 * kBM * 4;
   static constexpr int kBytes = kOffXch + kXchBytes + 1024;  // + alignment slack
@@ -67,7 +75,29 @@ struct Layout {
   }
 };
 
+// One CTA's part of one item: steps [kb, ke). Group t's query tile is t in a
+// pair and 0 otherwise; its steps are the first n[t] (pair), every second one
+// from kb + t on (split), or all or none (solo).
+enum SegMode : int { kPair = 0, kSplit = 1, kSolo0 = 2, kSolo1 = 3 };
+struct Seg {
+  int seq;         // -1: the span's end
+  int head;
+  int row0, ntok;  // the item's first token among the packed tokens, and its tokens
+  int kv;          // cached tokens of the sequence
+  int lim0;        // keys that the item's first token sees (may be below 0; kv when not causal)
+  int kb, ke;
+  int n[2];
+  int slot;        // partial slot, -1: the whole item
+  int mode;
+  int q;           // Q ring number of the first tile
+  int pad[3];
+};
+static_assert(sizeof(Seg) == 64, "descriptor size");
+
 struct Bars {
+  Seg seg[kSegs];
+  uint64_t seg_full[kSegs];
+  uint64_t seg_empty[kSegs];
   uint64_t kv_full[8];
   uint64_t kv_empty[8];
   uint64_t q_full[2];
@@ -116,83 +146,105 @@ __device__ __forceinline__ bool same_item(const PlanStart& a, const PlanStart& b
   return a.seq == b.seq && a.head == b.head && a.pair == b.pair;
 }
 
-// One CTA's part of one item: steps [kb, ke) of the item's `steps`.
-struct Seg {
-  int seq, head;
-  int row0;        // the item's first token among the packed tokens
-  int tok0, ntok;  // the same within the sequence; tokens of the item
-  int n, kv;       // new and cached tokens of the sequence
-  int kb, ke, steps;
-  bool split;      // one tile, shared by both groups
-  int slot;        // partial slot, -1: the whole item
-};
-
-// Walks a CTA's span. Every role computes the same sequence of segments.
+// Walks a CTA's span (the K producer warp, all lanes alike). The next
+// sequence's lengths are on their way while the current one is worked on.
 struct Span {
   PlanStart cur, end;
   const int32_t* cu;
   const int32_t* kvl;
   int B, Hkv, tt, causal;
+  int t0, t1, kv, t2, kv1;  // cu[seq], cu[seq + 1], kvl[seq], and the next ones
+  int q, solo;              // Q ring numbers and solo segments handed out
 
+  __device__ __forceinline__ void fetch() {
+    t2 = cu[min(cur.seq + 2, B)];
+    kv1 = kvl[min(cur.seq + 1, B - 1)];
+  }
+  __device__ __forceinline__ void init(const Params& p) {
+    cur = p.plan->start[blockIdx.x];
+    end = p.plan->start[blockIdx.x + 1];
+    cu = plan_cu_q(p.plan);
+    kvl = plan_kv_len(p.plan, p.B);
+    B = p.B;
+    Hkv = p.Hkv;
+    tt = p.tt;
+    causal = p.plan->causal;
+    q = solo = 0;
+    if (cur.seq < B) {
+      t0 = cu[cur.seq];
+      t1 = cu[cur.seq + 1];
+      kv = kvl[cur.seq];
+      fetch();
+    }
+  }
   __device__ __forceinline__ bool next(Seg& s) {
-    if (cur.seq >= B || (same_item(cur, end) && cur.step == end.step)) return false;
+    if (cur.seq >= B || (same_item(cur, end) && cur.step == end.step)) {
+      s = Seg{};
+      s.seq = -1;
+      return false;
+    }
+    const int n = t1 - t0, tok0 = cur.pair * 2 * tt;
     s.seq = cur.seq;
     s.head = cur.head;
-    const int t0 = cu[cur.seq];
-    s.n = cu[cur.seq + 1] - t0;
-    s.kv = kvl[cur.seq];
-    s.tok0 = cur.pair * 2 * tt;
-    s.ntok = min(2 * tt, s.n - s.tok0);
-    s.row0 = t0 + s.tok0;
-    s.split = s.ntok <= tt;
-    s.steps = (plan_visible(s.tok0 + s.ntok - 1, s.n, s.kv, causal) + kBN - 1) / kBN;
+    s.ntok = min(2 * tt, n - tok0);
+    s.row0 = t0 + tok0;
+    s.kv = kv;
+    s.lim0 = causal ? kv - n + tok0 + 1 : kv;
+    const int steps = steps_of(s.ntok - 1, s);
     s.kb = cur.step;
     const int cta = static_cast<int>(blockIdx.x);
     if (same_item(cur, end)) {
-      s.ke = min(s.steps, end.step);
+      s.ke = min(steps, end.step);
       cur = end;
     } else {
-      s.ke = s.steps;
+      s.ke = steps;
       cur.step = 0;
-      if (s.tok0 + s.ntok < s.n) {
+      if (tok0 + s.ntok < n) {
         ++cur.pair;
       } else {
         cur.pair = 0;
         if (++cur.head == Hkv) {
           cur.head = 0;
-          do ++cur.seq;
-          while (cur.seq < B && cu[cur.seq + 1] == cu[cur.seq]);
+          do {
+            ++cur.seq;
+            t0 = t1;
+            t1 = t2;
+            kv = kv1;
+            if (cur.seq < B) fetch();
+          } while (cur.seq < B && t1 == t0);
         }
       }
     }
-    s.slot = s.kb > 0 ? 2 * cta : s.ke < s.steps ? 2 * cta + 1 : -1;
+    s.slot = s.kb > 0 ? 2 * cta : s.ke < steps ? 2 * cta + 1 : -1;
+    const int len = s.ke - s.kb;
+    const bool last = cur.seq >= B || (same_item(cur, end) && cur.step == end.step);
+    s.q = q;
+    if (s.ntok > tt) {
+      s.mode = kPair;
+      s.n[0] = max(0, min(s.ke, steps_of(tt - 1, s)) - s.kb);
+      s.n[1] = len;
+      q += len > 0 ? 2 : 0;
+    } else {
+      if (len > kSoloSteps || last) {
+        s.mode = kSplit;
+        s.n[0] = (len + 1) / 2;
+        s.n[1] = len / 2;
+      } else {
+        const int t = solo++ & 1;
+        s.mode = kSolo0 + t;
+        s.n[0] = t == 0 ? len : 0;
+        s.n[1] = t == 1 ? len : 0;
+      }
+      q += len > 0 ? 1 : 0;
+    }
     return true;
   }
-  // Steps that tile t of an item could need, of all its steps.
-  __device__ __forceinline__ int tile_steps(const Seg& s, int t) const {
-    if (s.split) return s.steps;
-    const int last = min(s.ntok, (t + 1) * tt) - 1;
-    return (plan_visible(s.tok0 + last, s.n, s.kv, causal) + kBN - 1) / kBN;
-  }
-  // Steps that group t takes in a segment.
-  __device__ __forceinline__ int group_steps(const Seg& s, int t) const {
-    if (s.split) return (s.ke - s.kb - t + 1) / 2;
-    return max(0, min(s.ke, tile_steps(s, t)) - s.kb);
+  // Steps that the item's token i needs.
+  __device__ __forceinline__ int steps_of(int i, const Seg& s) const {
+    const int lim = causal ? max(0, s.lim0 + i) : s.kv;
+    return (lim + kBN - 1) / kBN;
   }
 };
-
-__device__ __forceinline__ Span make_span(const Params& p) {
-  Span sp;
-  sp.cur = p.plan->start[blockIdx.x];
-  sp.end = p.plan->start[blockIdx.x + 1];
-  sp.cu = plan_cu_q(p.plan);
-  sp.kvl = plan_kv_len(p.plan, p.B);
-  sp.B = p.B;
-  sp.Hkv = p.Hkv;
-  sp.tt = p.tt;
-  sp.causal = p.plan->causal;
-  return sp;
-}
 
 // Named barrier of one group -- its four softmax warps and its issuer warp --
 // that also ORs a predicate over the group.
@@ -255,14 +307,15 @@ struct RowOut {
 };
 
 template <int D>
-__device__ __forceinline__ RowOut row_out(const Params& p, const Seg& s, int t, int r) {
+__device__ __forceinline__ RowOut row_out(const Params& p, const Seg& s, int t, int r, int row_tok,
+                                          int row_head) {
   RowOut w{nullptr, nullptr, nullptr};
   if (s.slot >= 0) {
     const int64_t tile = int64_t(s.slot) * 2 + t;
     w.part = p.o_part + (tile * (D / 4) * kBM + r) * 4;
     w.lse = p.lse_part + tile * kBM + r;
   } else {
-    const int64_t row = int64_t(s.row0 + t * p.tt + r / p.G) * p.H + s.head * p.G + r % p.G;
+    const int64_t row = int64_t(s.row0 + t * p.tt + row_tok) * p.H + (s.head * p.G + row_head);
     w.o = p.o + row * D;
     w.lse = p.lse != nullptr ? p.lse + row : nullptr;
   }
@@ -318,13 +371,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (static_cast<int>(blockIdx.x) >= p.plan->ctas) return;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bar.seg_full[i], 1);
+      mbar_init(&bar.seg_empty[i], 11);  // softmax and issuer warps, V producer
+    }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bar.kv_full[i], 1);
       mbar_init(&bar.kv_empty[i], 2);  // one release per softmax group
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar.q_full[t], 1);
-      mbar_init(&bar.q_empty[t], 1);
+      mbar_init(&bar.q_empty[t], 2);   // one release per softmax group
       mbar_init(&bar.s_full[t], 1);
       mbar_init(&bar.o_done[t], 1);
       mbar_init(&bar.mma_idle[t], 1);
@@ -335,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar.issue_lock = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpLoad) {
+  if (warp == kWarpK) {
     tmem_alloc(&bar.tmem_base, 512);
     tmem_relinquish();
   }
@@ -344,98 +401,141 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = bar.tmem_base;
   volatile int* abort_flag = &bar.abort_flag;
-  Span span = make_span(p);
+#define RF_WAIT(b, par, site)                                                         \
+  mbar_wait(&bar.b, (par), p.status, dev_code(kDevTimeout, kKerPaged, site), abort_flag)
+#define RF_WAIT_WARP(b, par, site)                                                    \
+  mbar_wait_warp(&bar.b, (par), p.status, dev_code(kDevTimeout, kKerPaged, site), abort_flag)
 
-  if (warp == kWarpLoad) {
-    // ------------------------------------------------------------ producer
-    // Per segment: the first K/V pair, then Q0 and Q1 (each once the previous
-    // segment's last QK on it has completed), then the remaining K/V pairs.
-    // Lane l copies box l % boxes, columns 64 (l / boxes) .. + 63, of a tile.
+  if (warp == kWarpK || warp == kWarpV) {
+    // ------------------------------------------------------------ producers
+    // K producer, per segment: the first K tile, then Q (once the Q ring has
+    // room: after the second K tile at the latest), then the other K tiles. It
+    // publishes each segment while it works on the one before. Lane l copies
+    // box l % boxes, columns 64 (l / boxes) .. + 63, of a tile.
+    const bool is_k = warp == kWarpK;
+    const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+    const bool token_first = is_k ? p.k_token_first : p.v_token_first;
     if (lane == 0) {
-      prefetch_tensormap(&tm_q);
-      prefetch_tensormap(&tm_k);
-      prefetch_tensormap(&tm_v);
+      prefetch_tensormap(map);
+      if (is_k) prefetch_tensormap(&tm_q);
     }
     const int boxes = kBN / p.box;
-    const int my_box = lane % boxes, my_chunk = lane / boxes;
-    int seq = 0;
-    int q_loads[2] = {0, 0};
+    const int my_key = lane % boxes * p.box, my_chunk = lane / boxes;
+    const bool has_box = my_chunk < D / 64;
+    unsigned char* const my_dst = smem + L::kOffKV + my_chunk * kChunk + my_key * 128;
+    int seq = is_k ? 0 : 1;     // K/V sequence number of the next copy
+    int q_loads = 0;
     bool ok = true;
-    Seg s;
-    while (ok && span.next(s)) {
-      const int32_t* row = p.table + int64_t(s.seq) * p.table_stride;
-      // this lane's page of tile u and the box's first row in it
-      auto page_of = [&](int u, int& in_page) -> int {
-        const int key = u * kBN + my_box * p.box;
-        in_page = 0;
-        if (my_chunk >= D / 64 || key >= s.kv) return -1;
-        const int pi = key / p.page;
-        in_page = key - pi * p.page;
-        return row[pi];
-      };
-      int in_page = 0, in_next = 0;
-      int id = s.kb < s.ke ? page_of(s.kb, in_page) : -1;
-      for (int u = s.kb; ok && u < s.ke; ++u) {
-        const int id_next = u + 1 < s.ke ? page_of(u + 1, in_next) : -1;
-        const int key = u * kBN + my_box * p.box;
-        const bool mine = my_chunk < D / 64 && key < s.kv;
+    // this lane's page of step u of a segment and the box's first row in it
+    auto page_of = [&](const Seg& s, int u, int& in_page) -> int {
+      const int key = u * kBN + my_key;
+      in_page = 0;
+      if (u >= s.ke || !has_box || key >= s.kv) return -1;
+      const int pi = key / p.page;
+      in_page = key - pi * p.page;
+      return p.table[int64_t(s.seq) * p.table_stride + pi];
+    };
+    Span span;
+    Seg s, nxt;
+    int id = -1, in_page = 0;
+    auto publish = [&](int k, const Seg& d) {
+      if (lane == 0) {
+        ok = RF_WAIT(seg_empty[k % kSegs], ((k / kSegs) & 1) ^ 1, 14);
+        if (ok) {
+          bar.seg[k % kSegs] = d;
+          mbar_arrive(&bar.seg_full[k % kSegs]);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    };
+    if (is_k) {
+      span.init(p);
+      span.next(s);
+      publish(0, s);
+      if (s.seq >= 0) id = page_of(s, s.kb, in_page);
+    }
+    for (int k = 0; ok; ++k) {
+      int id_seg = -1, in_seg = 0;  // the next segment's first page
+      if (is_k) {
+        if (s.seq < 0) break;
+        span.next(nxt);
+        publish(k + 1, nxt);
+        if (!ok) break;
+        if (nxt.seq >= 0) id_seg = page_of(nxt, nxt.kb, in_seg);
+      } else {
+        ok = RF_WAIT_WARP(seg_full[k % kSegs], (k / kSegs) & 1, 15);
+        if (!ok) break;
+        s = bar.seg[k % kSegs];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.seg_empty[k % kSegs]);
+        if (s.seq < 0) break;
+        id = page_of(s, s.kb, in_page);
+      }
+      bool q_due = is_k && s.ke > s.kb;
+      for (int u = s.kb; ok && u < s.ke; ++u, seq += 2) {
+        int in_next = 0;
+        const int id_next = page_of(s, u + 1, in_next);
+        const bool mine = has_box && u * kBN + my_key < s.kv;
         if (mine && (id < 0 || id >= p.num_pages)) {
           record_status(p.status, dev_code(kDevBadList, kKerPaged, 3));
           id = p.num_pages;  // past the pool: the copy fills with zeros
         }
-        const int n_box = min(boxes, (s.kv - u * kBN + p.box - 1) / p.box);
-        for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
-          const int slot = seq % NS;
-          if (lane == 0) {
-            ok = mbar_wait(&bar.kv_empty[slot], ((seq / NS) & 1) ^ 1, p.status,
-                           dev_code(kDevTimeout, kKerPaged, 10), abort_flag);
-            if (ok) mbar_arrive_expect_tx(&bar.kv_full[slot], n_box * p.box * D * 2);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          if (mine) {
-            unsigned char* dst = smem + L::kOffKV + slot * L::kTileBytes + my_chunk * kChunk +
-                                 my_box * p.box * 128;
-            const bool first = kv == 0 ? p.k_token_first : p.v_token_first;
-            tma_load_4d(dst, kv == 0 ? &tm_k : &tm_v, &bar.kv_full[slot], my_chunk * 64,
-                        first ? in_page : s.head, first ? s.head : in_page, id);
-          }
+        const int slot = seq % NS;
+        if (lane == 0) {
+          const int n_box = min(boxes, (s.kv - u * kBN + p.box - 1) / p.box);
+          ok = RF_WAIT(kv_empty[slot], ((seq / NS) & 1) ^ 1, 10);
+          if (ok) mbar_arrive_expect_tx(&bar.kv_full[slot], n_box * p.box * D * 2);
         }
-        if (u == s.kb && ok && lane == 0) {
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (span.group_steps(s, t) == 0) continue;
-            if (q_loads[t] > 0)
-              ok = mbar_wait(&bar.q_empty[t], (q_loads[t] - 1) & 1, p.status,
-                             dev_code(kDevTimeout, kKerPaged, 12), abort_flag);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&bar.q_full[t], p.G * p.tt * D * 2);
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(smem + L::kOffQ + t * L::kTileBytes + c * kChunk, &tm_q, &bar.q_full[t],
-                          c * 64, 0, s.head, s.row0 + (s.split ? 0 : t * p.tt));
-            ++q_loads[t];
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (mine)
+          tma_load_4d(my_dst + slot * L::kTileBytes, map, &bar.kv_full[slot], my_chunk * 64,
+                      token_first ? in_page : s.head, token_first ? s.head : in_page, id);
+        if (q_due && lane == 0) {
+          const int tiles = s.mode == kPair ? 2 : 1;
+          // the ring has two tiles: the last number's release is the later one
+          const int lq = s.q + tiles - 1;
+          const bool must = u > s.kb || u + 1 == s.ke;
+          if (must || mbar_test_wait(&bar.q_empty[lq & 1], ((lq >> 1) & 1) ^ 1)) {
+            for (int i = 0; i < tiles && ok; ++i) {
+              const int qs = s.q + i, b = qs & 1;
+              ok = RF_WAIT(q_empty[b], ((qs >> 1) & 1) ^ 1, 12);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&bar.q_full[b], p.G * p.tt * D * 2);
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(smem + L::kOffQ + b * L::kTileBytes + c * kChunk, &tm_q,
+                            &bar.q_full[b], c * 64, 0, s.head, s.row0 + i * p.tt);
+              q_loads = qs + 1;
+            }
+            q_due = false;
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         id = id_next;
         in_page = in_next;
       }
+      if (is_k) {
+        s = nxt;
+        id = id_seg;
+        in_page = in_seg;
+      }
     }
-    // never leave with copies in flight: the last load into each slot
+    // never leave with copies in flight: this warp's last copies, one per slot
     if (lane == 0) {
-      for (int sq = max(0, seq - NS); sq < seq; ++sq)
+      const int end = is_k ? seq : seq - 1;  // the last copy into each slot: from end - NS on
+      for (int sq = seq - 2; sq >= 0 && sq >= end - NS; sq -= 2)
         mbar_wait(&bar.kv_full[sq % NS], (sq / NS) & 1, p.status,
                   dev_code(kDevTimeout, kKerPaged, 11), nullptr);
-      for (int t = 0; t < 2; ++t)
-        if (q_loads[t] > 0)
-          mbar_wait(&bar.q_full[t], (q_loads[t] - 1) & 1, p.status,
-                    dev_code(kDevTimeout, kKerPaged, 13), nullptr);
+      for (int qs = max(0, q_loads - 2); qs < q_loads; ++qs)
+        mbar_wait(&bar.q_full[qs & 1], (qs >> 1) & 1, p.status,
+                  dev_code(kDevTimeout, kKerPaged, 13), nullptr);
     }
     __syncwarp();
   } else if (warp >= kWarpIssue) {
     // ------------------------------------------------------------ MMA issuers
     const int t = warp - kWarpIssue;
     bool ok = true;
-    const uint64_t q_desc = sdesc_sw128(s_base + L::kOffQ + t * L::kTileBytes, 16, 1024);
+    const uint64_t q_desc0 = sdesc_sw128(s_base + L::kOffQ, 16, 1024);
     const uint64_t k_desc0 = sdesc_sw128(s_base + L::kOffKV, 16, 1024);
     const uint64_t v_desc0 = sdesc_sw128(s_base + L::kOffKV, kChunk, 1024);
     const uint32_t mm_s = tmem + L::kTmemS + t * kBN;
@@ -443,22 +543,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t mm_p = tmem + L::tmem_p(t);
     int seq = 0;              // K/V sequence number of the next step
     int vseq = 0;             // V tile of the step whose QK was issued last
-    int nq = 0;               // segments whose Q_t was waited for
     int n_iss = 0, n_seg = 0; // steps of the started segment issued so far, and all of them
-    int started = -1;         // last segment whose first QK was issued
+    int started = -1;         // last segment whose Q was waited for
     bool issued_any = false;
-    Span ahead = span;        // the segment being started (lane 0)
-    Seg a{};
-    int u_next = 0, a_end = 0;  // its next step, and this group's bound in a pair
-#define RF_WAIT(b, par, site)                                                         \
-  mbar_wait(&bar.b, (par), p.status, dev_code(kDevTimeout, kKerPaged, site), abort_flag)
+    // the segment being started (lane 0), this group's Q tile in it
+    int a_kb = 0, a_ke = 0, a_mode = 0, u_next = 0, q_slot = 0;
 #define RF_SLOT(sq) (static_cast<uint64_t>((((sq) % NS) * L::kTileBytes) >> 4))
 #define RF_LOCK() issue_lock(&bar.issue_lock, p.status, dev_code(kDevTimeout, kKerPaged, 23), abort_flag)
-    auto needs = [&](int u) { return a.split ? ((u - a.kb) & 1) == t : u < a_end; };
+    auto needs = [&](int u) {
+      if (a_mode == kPair) return u < a_kb + n_seg;
+      if (a_mode == kSplit) return ((u - a_kb) & 1) == t;
+      return n_seg > 0;
+    };
     // The next step this group takes; steps that only the other group takes are
     // released (both slots) once they have landed. False at the segment's end.
     auto advance = [&](int& kseq) -> bool {
-      while (u_next < a.ke) {
+      while (u_next < a_ke) {
         const int u = u_next++;
         const int ks = seq;
         seq += 2;
@@ -478,11 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       return (ok = RF_WAIT(kv_full[kseq % NS], (kseq / NS) & 1, 21));
     };
     // Whether everything up to the K tile of this group's next step has landed.
-    // Between this group's steps lies at most one of the other's (an item shared
-    // by both groups), so each barrier tested is at most one phase behind.
+    // Between this group's steps lies at most one of the other's (a split
+    // item), so each barrier tested is at most one phase behind.
     auto landed = [&]() -> bool {
       int sq = seq;
-      for (int u = u_next; u < a.ke; ++u, sq += 2) {
+      for (int u = u_next; u < a_ke; ++u, sq += 2) {
         const bool k_in = mbar_test_wait(&bar.kv_full[sq % NS], (sq / NS) & 1);
         if (!k_in || needs(u)) return k_in;
         if (!mbar_test_wait(&bar.kv_full[(sq + 1) % NS], ((sq + 1) / NS) & 1)) return false;
@@ -492,37 +592,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto qk_commits = [&](int kseq) {
       mma_commit(&bar.s_full[t]);
       mma_commit(&bar.kv_empty[kseq % NS]);
-      if (++n_iss == n_seg) mma_commit(&bar.q_empty[t]);  // the segment's last read of Q_t
+      if (++n_iss == n_seg) mma_commit(&bar.q_empty[q_slot]);  // the segment's last read of Q
       vseq = kseq + 1;
     };
+    auto issue_s = [&](int kseq) {
+      issue_qk<D>(mm_s, q_desc0 + static_cast<uint64_t>((q_slot * L::kTileBytes) >> 4),
+                  k_desc0 + RF_SLOT(kseq));
+    };
+    // Segment k (lane 0): wait for its Q tiles, release the ones this group does
+    // not read, and issue the first QK; without steps of its own, release all.
+    // Every phase of every barrier is observed, in order, by both groups.
     auto start_segment = [&](int k) {
       started = k;
-      if (!ahead.next(a)) return;
-      u_next = a.kb;
-      a_end = a.split ? a.ke : ahead.tile_steps(a, t);
-      n_iss = 0;
-      n_seg = ahead.group_steps(a, t);
+      n_seg = n_iss = 0;
+      if (!(ok = RF_WAIT(seg_full[k % kSegs], (k / kSegs) & 1, 25))) return;
+      const Seg& a = bar.seg[k % kSegs];
+      if (a.seq < 0 || a.kb == a.ke) return;
+      a_kb = u_next = a.kb;
+      a_ke = a.ke;
+      a_mode = a.mode;
+      n_seg = a.n[t];
+      const int q0 = a.q, tiles = a.mode == kPair ? 2 : 1;
+      for (int i = 0; i < tiles; ++i) {
+        const int qs = q0 + i, b = qs & 1;
+        if (!(ok = RF_WAIT(q_full[b], (qs >> 1) & 1, 22))) return;
+        if (n_seg > 0 && (tiles == 1 || i == t))
+          q_slot = b;
+        else
+          mbar_arrive(&bar.q_empty[b]);
+      }
       int kseq;
       if (n_seg == 0) {
         advance(kseq);  // releases every step; returns false
         return;
       }
-      if (!(ok = RF_WAIT(q_full[t], nq & 1, 22))) return;
-      ++nq;
       if (next_k(kseq) && (ok = RF_LOCK())) {
         tc_fence_after_sync();
-        issue_qk<D>(mm_s, q_desc, k_desc0 + RF_SLOT(kseq));
+        issue_s(kseq);
         issue_unlock(&bar.issue_lock);
         issued_any = true;
         qk_commits(kseq);
       }
     };
 
-    Seg s;
-    for (int item = 0; span.next(s); ++item) {
-      const int n = span.group_steps(s, t);
-      if (lane == 0 && started < item) start_segment(item);
+    for (int k = 0;; ++k) {
+      // the five warps of a group take up a segment together, or unwind together
+      if (ok) ok = RF_WAIT_WARP(seg_full[k % kSegs], (k / kSegs) & 1, 26);
+      if (group_sync_or(t, !ok)) {
+        ok = false;
+        break;
+      }
+      const Seg& d = bar.seg[k % kSegs];
+      const int n = d.n[t], kb = d.kb, kv = d.kv, mode = d.mode;
+      const bool end = d.seq < 0;
+      if (lane == 0 && !end && started < k) start_segment(k);
       ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (lane == 0) mbar_arrive(&bar.seg_empty[k % kSegs]);
+      if (end) break;
+      if (mode >= kSolo0 && mode != kSolo0 + t) continue;  // the other group's
       for (int jj = 0; jj < n; ++jj) {
         // While the softmax runs: wait for V_u, zero its rows past the cache's
         // end, and see whether the next step's K tile is there. If it is, its
@@ -530,12 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bounds a decode step), P.V goes first: it frees V_u's slot, without
         // which the ring of five slots could not run ahead of the two groups.
         const bool last = jj + 1 == n;
-        const int u = s.kb + (s.split ? 2 * jj + t : jj);
+        const int u = kb + (mode == kSplit ? 2 * jj + t : jj);
         int k2 = 0;
         bool fast = false;
         if (lane == 0 && ok) ok = RF_WAIT(kv_full[vseq % NS], (vseq / NS) & 1, 24);
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        const int rows = s.kv - u * kBN;
+        const int rows = kv - u * kBN;
         if (ok && rows < kBN) {
           const int vs = __shfl_sync(0xffffffffu, vseq, 0) % NS;
           unsigned char* v = smem + L::kOffKV + vs * L::kTileBytes;
@@ -556,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && (ok = RF_LOCK())) {
           tc_fence_after_sync();
           issue_pv<D>(mm_o, mm_p, v_desc0 + RF_SLOT(vseq), jj > 0);
-          if (fast) issue_qk<D>(mm_s, q_desc, k_desc0 + RF_SLOT(k2));
+          if (fast) issue_s(k2);
           issue_unlock(&bar.issue_lock);
           const int v_done = vseq;
           if (fast) qk_commits(k2);
@@ -565,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&bar.o_done[t]);
           } else if (!fast && next_k(k2) && (ok = RF_LOCK())) {
             tc_fence_after_sync();
-            issue_qk<D>(mm_s, q_desc, k_desc0 + RF_SLOT(k2));
+            issue_s(k2);
             issue_unlock(&bar.issue_lock);
             qk_commits(k2);
           }
@@ -577,19 +704,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       // while the softmax warps write this segment's output: release the steps
-      // after this group's last, and start the next segment
+      // after this group's last, and start this group's next segment (the one
+      // after the next, when the next is the other group's alone)
       if (lane == 0 && n > 0) {
         int k2;
         advance(k2);
-        if (ok) start_segment(item + 1);
+        if (ok) start_segment(k + 1);
+        if (ok && n_seg == 0 && bar.seg[(k + 1) % kSegs].seq >= 0) start_segment(k + 2);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (group_sync_or(t, !ok)) {  // after the segment's epilogue
-        ok = false;
-        break;
-      }
     }
-#undef RF_WAIT
 #undef RF_SLOT
 #undef RF_LOCK
     // never leave with MMAs in flight (their operands live in this CTA)
@@ -606,26 +730,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_s = tmem + L::kTmemS + t * kBN + lane_off;
     const uint32_t tm_o = tmem + L::kTmemO + t * D + lane_off;
     const uint32_t tm_p = tmem + L::tmem_p(t) + lane_off;
-    const int row_tok = r / p.G;
+    const int row_tok = r / p.G, row_head = r - row_tok * p.G;
+    const int causal = p.plan->causal;
     int j = 0;                           // S tiles consumed (all segments)
     int o_segs = 0;                      // segments whose final P.V was waited for
     int n_split = 0;                     // split segments so far
     bool ok = true;
-    Seg s;
-    while (span.next(s)) {
-      const int tile = s.split ? 0 : t;              // the group's query tile
+    for (int k = 0;; ++k) {
+      if (ok) ok = RF_WAIT_WARP(seg_full[k % kSegs], (k / kSegs) & 1, 31);
+      if (group_sync_or(t, !ok)) {
+        ok = false;
+        break;
+      }
+      const Seg s = bar.seg[k % kSegs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.seg_empty[k % kSegs]);
+      if (s.seq < 0) break;
+      if (s.mode >= kSolo0 && s.mode != kSolo0 + t) continue;  // the other group's
+      const int tile = s.mode == kPair ? t : 0;      // the group's query tile
       const int tok = tile * p.tt + row_tok;         // token within the item
       const bool row_ok = row_tok < p.tt && tok < s.ntok;
       // a warp without live rows leaves the softmax to the others
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
-      const int n = span.group_steps(s, t);
+      const int n = t == 0 ? s.n[0] : s.n[1];
       // keys this row sees, and the fewest any row of the tile sees; a row that
       // holds no token computes on whatever is there and is not written
-      const int row_lim = row_ok ? plan_visible(s.tok0 + tok, s.n, s.kv, span.causal) : s.kv;
-      const int first_lim = plan_visible(s.tok0 + tile * p.tt, s.n, s.kv, span.causal);
+      const int row_lim = !row_ok || !causal ? s.kv : max(0, s.lim0 + tok);
+      const int first_lim = causal ? max(0, s.lim0 + tile * p.tt) : s.kv;
       float m_run = kNegInf, l_run = 0.f;
       for (int jj = 0; jj < n; ++jj, ++j) {
-        const int u = s.kb + (s.split ? 2 * jj + t : jj);
+        const int u = s.kb + (s.mode == kSplit ? 2 * jj + t : jj);
         if (ok && warp_ok)
           ok = mbar_wait_warp(&bar.s_full[t], j & 1, p.status,
                               dev_code(kDevTimeout, kKerPaged, 30), abort_flag);
@@ -714,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dev_code(kDevTimeout, kKerPaged, 32), abort_flag);
         ++o_segs;
       }
-      if (s.split) {
+      if (s.mode == kSplit) {
         // Group 1's state over the odd steps goes to group 0 (m and l through
         // shared memory, O_1 read from tensor memory in the same lanes), which
         // joins it with its own and writes the rows. Group 1 then waits until
@@ -746,12 +880,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float a0 = m_run == kNegInf ? 0.f : ex2_approx(m_run - m);
               const float a1 = m1 == kNegInf ? 0.f : ex2_approx(m1 - m);
               const float l = a0 * l_run + a1 * l1;
-              const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+              const float inv = l == 0.f ? 0.f : __frcp_rn(l);  // NaN stays NaN
               // a group without steps leaves its O columns unwritten: its
               // weight is 0 and its values are never used
               const float w0 = a0 * inv, w1 = a1 * inv;
               const uint32_t tm_o1 = tmem + L::kTmemO + D + lane_off;
-              const RowOut out = row_out<D>(p, s, 0, r);
+              const RowOut out = row_out<D>(p, s, 0, r, row_tok, row_head);
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o0[32], o1[32];
@@ -767,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               if (row_ok && out.lse != nullptr)
-                *out.lse = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+                *out.lse = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -775,36 +909,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (ok && warp_ok) {
-        const RowOut out = row_out<D>(p, s, t, r);
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // NaN stays NaN
+        const RowOut out = row_out<D>(p, s, tile, r, row_tok, row_head);
+        const float inv = l_run == 0.f ? 0.f : __frcp_rn(l_run);  // NaN stays NaN
         tc_fence_after_sync();
+        if (n > 0) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t ov[32];
-          if (n > 0) tmem_ld32_wait(tm_o + c, ov);
-          if (row_ok) {
-            float v[32];
+          for (int c = 0; c < D; c += 64) {
+            uint32_t ov[64];
+            tmem_ld64_wait(tm_o + c, ov);
+            if (row_ok) {
+              // a row without keys has P = 0 in every step: O is 0 as it stands
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              v[e] = inv != 0.f && n > 0 ? __uint_as_float(ov[e]) * inv : 0.f;
-            put32(out, c, v, p.o_wide);
+              for (int h = 0; h < 64; h += 32) {
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(ov[h + e]) * inv;
+                put32(out, c + h, v, p.o_wide);
+              }
+            }
           }
+          tc_fence_before_sync();
+        } else if (row_ok) {
+          const float v[32] = {};
+          for (int c = 0; c < D; c += 32) put32(out, c, v, p.o_wide);
         }
-        tc_fence_before_sync();
         if (row_ok && out.lse != nullptr)
-          *out.lse = l_run == 0.f ? kNegInf : (m_run + log2f(l_run)) * kLn2;
-      }
-      if (group_sync_or(t, !ok)) {
-        ok = false;
-        break;
+          *out.lse = l_run == 0.f ? kNegInf : (m_run + __log2f(l_run)) * kLn2;
       }
     }
   }
+#undef RF_WAIT
+#undef RF_WAIT_WARP
 
   // ------------------------------------------------------------ teardown
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kWarpLoad) {
+  if (warp == kWarpK) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }

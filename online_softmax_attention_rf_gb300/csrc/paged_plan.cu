@@ -11,34 +11,37 @@ namespace rf {
 namespace {
 
 constexpr int kThreads = 1024;
-// Cost of an item: kItemCost, plus per step kPairCost when it has two tiles
-// and kSingleCost when it has one.
-constexpr int kItemCost = 2;
+// Cost of an item: a fixed part (filling the pipeline and writing the output),
+// plus per step kPairCost when it has two tiles and kSingleCost when it has
+// one. Measured at d = 128: 5 us, 1.7 us and 1.2 us. With fewer items than
+// CTAs every CTA pays the fixed part about once whatever the cuts are, and only
+// the steps are shared out.
+constexpr int kItemCost = 8;
+constexpr int kItemCostFew = 1;
 constexpr int kPairCost = 3;
 constexpr int kSingleCost = 2;
-// A span is worth at least this much, so that a short step is not cut into
-// more parts than merging them pays for. Two cuts of one item are then more
-// than a step apart: no CTA inside an item is left without steps.
-constexpr int kMinSpan = 8;
-static_assert(kMinSpan / 2 >= kPairCost && kPairCost >= kSingleCost, "cuts may coincide");
+// A span is worth at least this much. Two cuts of one item are then more than
+// a step apart: no CTA inside an item is left without steps.
+constexpr int kMinSpan = 4;
+static_assert(kMinSpan - 1 >= kPairCost && kPairCost >= kSingleCost, "cuts may coincide");
 
 struct Item {
   int rows, steps, cost;
 };
 
 // Item `pair` of a sequence with n new and kv cached tokens.
-__device__ __forceinline__ Item item_of(int pair, int n, int kv, int causal, int G) {
+__device__ __forceinline__ Item item_of(int pair, int n, int kv, int causal, int G, int fixed) {
   const int tt = plan_tile_tokens(G);
   const int i0 = pair * 2 * tt, i1 = min(n, i0 + 2 * tt);
   Item it;
   it.rows = (i1 - i0) * G;
   it.steps = (plan_visible(i1 - 1, n, kv, causal) + kPlanTile - 1) / kPlanTile;
-  it.cost = kItemCost + it.steps * (i1 - i0 > tt ? kPairCost : kSingleCost);
+  it.cost = fixed + it.steps * (i1 - i0 > tt ? kPairCost : kSingleCost);
   return it;
 }
 
 __device__ PlanStart locate(int64_t x, const int64_t* cost, const int32_t* cu, const int32_t* kvl,
-                            const PagedPlanArgs& a) {
+                            const PagedPlanArgs& a, int fixed) {
   int lo = 0, hi = a.B;  // the first b with cost[b + 1] > x
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -54,10 +57,10 @@ __device__ PlanStart locate(int64_t x, const int64_t* cost, const int32_t* cu, c
   st.head = static_cast<int>(rem / per_head);
   rem -= st.head * per_head;
   for (; st.pair < pairs; ++st.pair) {
-    const Item it = item_of(st.pair, n, kv, a.causal, G);
+    const Item it = item_of(st.pair, n, kv, a.causal, G, fixed);
     if (rem < it.cost) {
       const int w = it.rows > tt * G ? kPairCost : kSingleCost;
-      const int step = rem <= kItemCost ? 0 : static_cast<int>((rem - kItemCost + w - 1) / w);
+      const int step = rem <= fixed ? 0 : static_cast<int>((rem - fixed + w - 1) / w);
       if (step < it.steps || step == 0) {
         st.step = step;
         return st;
@@ -117,13 +120,24 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
     }
     return;
   }
-  // costs of the sequences, a warp each
   const int G = a.H / a.Hkv, tt = plan_tile_tokens(G);
+  // the number of items
+  int64_t items = 0;
+  for (int b = tid; b < a.B; b += kThreads) items += (cu[b + 1] - cu[b] + 2 * tt - 1) / (2 * tt);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+  if (lane == 0) wsum[warp] = items;
+  __syncthreads();
+  items = 0;
+  for (int w = 0; w < kThreads / 32; ++w) items += wsum[w];
+  const int fixed = items * a.Hkv > kPlanCtas ? kItemCost : kItemCostFew;
+  __syncthreads();
+  // costs of the sequences, a warp each
   for (int b = warp; b < a.B; b += kThreads / 32) {
     const int n = cu[b + 1] - cu[b], kv = kvl[b];
     const int pairs = (n + 2 * tt - 1) / (2 * tt);
     int64_t sum = 0;
-    for (int p = lane; p < pairs; p += 32) sum += item_of(p, n, kv, a.causal, G).cost;
+    for (int p = lane; p < pairs; p += 32) sum += item_of(p, n, kv, a.causal, G, fixed).cost;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) cost[b + 1] = sum * a.Hkv;
@@ -157,8 +171,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
     __syncthreads();
   }
   const int64_t total = cost[a.B];
-  const int ctas = static_cast<int>(min64(kPlanCtas, (total + kMinSpan - 1) / kMinSpan));
-  if (tid <= ctas) start[tid] = locate(ctas > 0 ? total * tid / ctas : 0, cost, cu, kvl, a);
+  const int ctas = total == 0 ? 0 : static_cast<int>(min64(kPlanCtas, max64(1, total / kMinSpan)));
+  if (tid <= ctas) start[tid] = locate(ctas > 0 ? total * tid / ctas : 0, cost, cu, kvl, a, fixed);
   __syncthreads();
   // items that a cut falls into: found by the first cut inside each
   PlanMerge m{};
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
         while (tid + parts <= ctas && start[tid + parts - 1].step > 0 &&
                same_item(start[tid + parts - 1], s))
           ++parts;
-        const int rows = item_of(s.pair, cu[s.seq + 1] - cu[s.seq], kvl[s.seq], a.causal, G).rows;
+        const int rows = item_of(s.pair, cu[s.seq + 1] - cu[s.seq], kvl[s.seq], a.causal, G, fixed).rows;
         m = PlanMerge{s.seq, s.head, s.pair, tid - 1, parts, rows, 0, 0};
       }
     }
