@@ -9,6 +9,8 @@ the library is missing, every call raises.
 """
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
@@ -564,22 +566,35 @@ def splitk_merge(o_part, lse_part, out_dtype=torch.bfloat16):
 
 
 # The paged serving calls run once a layer or once a token, where the host's
-# share of a call shows: each checks what it is given in one expression and
-# leaves naming the fault to a function of its own.
+# share of a call shows: their arguments are marshalled by a native module
+# (csrc/serving_binding.cpp, over the same C entry points), which answers None
+# for tensors that do not fit and the status of a refused call.
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_SERVING = None
+
+
+def _serving():
+    """The native binding of the paged serving calls; raises if it has not been
+    built."""
+    global _SERVING
+    if _SERVING is None:
+        lib()
+        path = _build.BINDING_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(
+                "_rf_serving.so is not built (%s); run `python -m "
+                "online_softmax_attention_rf_gb300.build`" % path)
+        loader = importlib.machinery.ExtensionFileLoader("_rf_serving", path)
+        spec = importlib.util.spec_from_file_location("_rf_serving", path, loader=loader)
+        _SERVING = importlib.util.module_from_spec(spec)
+        loader.exec_module(_SERVING)
+    return _SERVING
 
 
 def _launch(index, fn, *args):
     """fn(*args, the current stream of device `index`), with that device current."""
-    if index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index))
-    if status != RF_OK:
-        _check(status)
+    with torch.cuda.device(index):
+        _check(fn(*args, _stream()))
 
 
 def _same_device(*ts):
@@ -604,10 +619,6 @@ def _expect(t, name, dtype, shape, optional=False):
     if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s"
                          % (name, dtype, tuple(shape)))
-
-
-def _fits(t, dtype, shape, index):
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
 
 
 def _expect_pool(cache, name, Hkv, d, dtype):
@@ -684,45 +695,13 @@ def kv_append_paged(q, k, v, k_cache, v_cache, slots, pos=None, cos_sin=None, q_
     k_cache, v_cache [pages, page, Hkv, d] (any strides with d contiguous),
     slots int64 [T] (negative: skipped) -> q_out [T, H, d], or None without q.
     q_out may be q itself when q is contiguous."""
-    index, dtype, shape = k.get_device(), k.dtype, k.shape
-    kst, vst, kc, vc = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
-    pool = k_cache.shape
-    ok = (index >= 0 and len(shape) == 3 and v.shape == shape and v.dtype is dtype
-          and v.get_device() == index and kst[2] == 1 == vst[2]
-          and (shape[1] == 1 or kst[1] == shape[2] == vst[1])
-          and len(pool) == 4 and pool[2:] == shape[1:] and v_cache.shape == pool
-          and kc[3] == 1 == vc[3] and k_cache.dtype is dtype and v_cache.dtype is dtype
-          and k_cache.get_device() == index and v_cache.get_device() == index
-          and _fits(slots, torch.int64, shape[:1], index)
-          and (q_weight is None or _fits(q_weight, dtype, shape[2:], index))
-          and (k_weight is None or _fits(k_weight, dtype, shape[2:], index))
-          and (cos_sin is None or (cos_sin.dim() == 2 and cos_sin.is_contiguous()
-                                   and cos_sin.dtype is torch.float32
-                                   and cos_sin.get_device() == index and pos is not None
-                                   and _fits(pos, torch.int32, shape[:1], index))))
-    H = qs = 0
-    if ok and q is not None:
-        qshape, qst = q.shape, q.stride()
-        ok = (len(qshape) == 3 and qshape[0] == shape[0] and qshape[2] == shape[2]
-              and q.dtype is dtype and q.get_device() == index and qst[2] == 1
-              and (qshape[1] == 1 or qst[1] == shape[2])
-              and (q_out is None or _fits(q_out, dtype, qshape, index)))
-        H = qshape[1]
-        qs = qst[0] if qshape[0] > 1 else H * shape[2]
-    if not ok:
+    r = _serving().kv_append_paged(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight,
+                                   k_weight, eps, interleaved, q_out)
+    if r.__class__ is tuple:
+        return r[0]
+    if r is None:
         _refuse_append(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight, k_weight, q_out)
-    T, Hkv, d = shape
-    if q is not None and q_out is None:
-        q_out = torch.empty(qshape, dtype=dtype, device=q.device)
-    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    _launch(index, lib().rf_kv_append_paged, None if q is None else q.data_ptr(), qs, k.data_ptr(),
-            kst[0] if T > 1 else Hkv * d, v.data_ptr(), vst[0] if T > 1 else Hkv * d, None if q is None else q_out.data_ptr(),
-            k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2], T, H,
-            Hkv, d, pool[1], pool[0], slots.data_ptr(), None if pos is None else pos.data_ptr(),
-            None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot, 1 if interleaved else 0,
-            None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps, _dt(k))
-    return None if q is None else q_out
+    _check(r)
 
 
 class PagedPlan:
@@ -785,35 +764,16 @@ def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse
     fits), k_cache, v_cache [pages, page, Hkv, d] (any strides with d
     contiguous), block_table int32 [B, max_pages], plan a ``PagedPlan`` of the
     step -> (o [T, H, d], lse float32 [T, H] or None)."""
-    index, dtype, shape, pool = q.get_device(), q.dtype, q.shape, k_cache.shape
-    qs, kc, vc, tb = q.stride(), k_cache.stride(), v_cache.stride(), block_table.stride()
-    d = shape[-1]
-    ok = (index >= 0 and shape == (plan.T, plan.H, d) and qs[-1] == 1
-          and (plan.H == 1 or qs[1] == d)
-          and pool[1:] == (plan.page, plan.Hkv, d) and v_cache.shape == pool
-          and kc[-1] == 1 == vc[-1] and k_cache.dtype is dtype and v_cache.dtype is dtype
-          and block_table.dtype is torch.int32 and tb[-1] == 1
-          and block_table.shape == (plan.B, plan.max_pages)
-          and k_cache.get_device() == index and v_cache.get_device() == index
-          and block_table.get_device() == index and plan.buf.get_device() == index
-          and (out is None or _fits(out, dtype, shape, index))
-          and (lse is None or _fits(lse, torch.float32, shape[:2], index))
-          and (workspace is None or (workspace.is_contiguous()
-                                     and workspace.get_device() == index)))
-    if not ok:
-        _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace)
-    dev = q.device
-    o = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
-    if lse is None and with_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = attn_paged_workspace(d, dev)
-    _launch(index, lib().rf_attn_paged, q.data_ptr(), qs[0] if plan.T > 1 else plan.H * d, k_cache.data_ptr(), kc[0], kc[1],
-            kc[2], v_cache.data_ptr(), vc[0], vc[1], vc[2], plan.page, pool[0],
-            block_table.data_ptr(), tb[0], plan.max_pages, plan.buf.data_ptr(), plan.B, plan.T,
-            plan.H, plan.Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, o.data_ptr(),
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _dt(q))
-    return o, lse
+        workspace = attn_paged_workspace(q.shape[-1], q.device)
+    r = _serving().attn_paged(q, k_cache, v_cache, block_table, plan.buf, plan.B, plan.T, plan.H,
+                              plan.Hkv, plan.page, plan.max_pages, scale, out, lse, with_lse,
+                              workspace)
+    if r.__class__ is tuple:
+        return r
+    if r is None:
+        _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace)
+    _check(r)
 
 
 def draft_verify_workspace(B, S, device="cuda"):
@@ -845,31 +805,14 @@ def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None,
     [0, 1), expo float32 [B, V] exponential variates, n_draft int32 [B],
     temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1], n_accepted
     int32 [B])."""
-    index, dtype, shape = target.get_device(), target.dtype, target.shape
-    ok = index >= 0 and len(shape) == 3 and shape[1] > 1 and target.is_contiguous()
-    if ok:
-        B, S, V = shape[0], shape[1] - 1, shape[2]
-        ok = ((draft is None or _fits(draft, dtype, (B, S, V), index))
-              and _fits(tokens, torch.int32, (B, S), index)
-              and _fits(u, torch.float32, (B, S), index)
-              and _fits(expo, torch.float32, (B, V), index)
-              and (n_draft is None or _fits(n_draft, torch.int32, (B,), index))
-              and (temperature is None or _fits(temperature, torch.float32, (B,), index))
-              and (workspace is None or (workspace.is_contiguous()
-                                         and workspace.get_device() == index)))
-    if not ok:
-        _refuse_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
-    dev = target.device
-    out = torch.empty((B, S + 1), dtype=torch.int32, device=dev)
-    n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = draft_verify_workspace(B, S, dev)
-    _launch(index, lib().rf_draft_verify, target.data_ptr(),
-            None if draft is None else draft.data_ptr(), tokens.data_ptr(), u.data_ptr(),
-            expo.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
-            None if temperature is None else temperature.data_ptr(), B, S, V, out.data_ptr(),
-            n_accepted.data_ptr(), workspace.data_ptr(), workspace.nbytes, _dt(target))
-    return out, n_accepted
+        workspace = draft_verify_workspace(tokens.shape[0], tokens.shape[-1], target.device)
+    r = _serving().draft_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
+    if r.__class__ is tuple:
+        return r
+    if r is None:
+        _refuse_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
+    _check(r)
 
 
 def set_debug_visited(buf):

@@ -5,7 +5,9 @@ Every translation unit in ``csrc/`` is compiled for sm_103a only
 at the repository root; the shared library lands in ``lib/librf.so`` next to
 this file. The CUDA runtime is linked statically, and the driver's tensor-map
 encoder is looked up at run time, so the library loads on a machine without a
-GPU driver (only the kernels need one).
+GPU driver (only the kernels need one). The paged serving calls have a native
+binding (csrc/serving_binding.cpp, compiled against the installed torch's
+headers), ``lib/_rf_serving.so``, which calls librf.so next to it.
 
 Usage:  python -m online_softmax_attention_rf_gb300.build [--force] [-v]
 """
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(HERE, "lib")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(LIBDIR, "librf.so")
+BINDING_SRC = os.path.join(CSRC, "serving_binding.cpp")
+BINDING_PATH = os.path.join(LIBDIR, "_rf_serving.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE,
@@ -63,6 +68,36 @@ def _compile(src, verbose, extra):
     return obj
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, " ".join(cmd), r.stderr))
+
+
+def _torch_dir():
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_binding(obj):
+    t = _torch_dir()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    dirs = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+          *[f for d in dirs for f in ("-isystem", d)], "-c", BINDING_SRC, "-o", obj],
+         "g++ for %s" % BINDING_SRC)
+
+
+def _link_binding(obj):
+    tlib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-l:librf.so",
+          "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + tlib], "link of %s" % BINDING_PATH)
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force=False, verbose=False, extra_flags=()):
     """Compile what changed and link lib/librf.so; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -75,9 +110,15 @@ def build(force=False, verbose=False, extra_flags=()):
         objs.append(obj)
         if force or _stale(obj, [src, *hdrs]):
             todo.append(src)
-    if todo:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(todo))) as ex:
-            list(ex.map(lambda s: _compile(s, verbose, list(extra_flags)), todo))
+    binding_obj = os.path.join(BUILD_DIR, "serving_binding.o")
+    binding = force or _stale(binding_obj, [BINDING_SRC, os.path.join(INCLUDE, "rf.h")])
+    if todo or binding:
+        with concurrent.futures.ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
+            jobs = [ex.submit(_compile, s, verbose, list(extra_flags)) for s in todo]
+            if binding:
+                jobs.append(ex.submit(_compile_binding, binding_obj))
+            for j in jobs:
+                j.result()
     if force or todo or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp"
         cmd = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
@@ -85,6 +126,8 @@ def build(force=False, verbose=False, extra_flags=()):
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
         os.replace(tmp, LIB_PATH)
+    if force or binding or _stale(BINDING_PATH, [binding_obj]):
+        _link_binding(binding_obj)
     return LIB_PATH
 
 

@@ -27,8 +27,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kStatThreads = 256;
 constexpr int kStatWarps = kStatThreads / 32;
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSplits = 32;
 constexpr int kCluster = 8;
 constexpr int kNone = 0x7fffffff;
@@ -71,6 +69,7 @@ struct Vec16;
 template <>
 struct Vec16<float> {
   static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
   static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
     x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
@@ -79,6 +78,7 @@ struct Vec16<float> {
 template <>
 struct Vec16<__nv_bfloat16> {
   static constexpr int N = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;  // two -inf
   static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -163,20 +163,25 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(const VerifyArgs a,
   const uint4* xv = reinterpret_cast<const uint4*>(x + h);
   Running st;
   if (!greedy) {
-    int k = tid;
-    for (; k + (U - 1) * kStatThreads < nv; k += U * kStatThreads) {
-      uint4 w[U];
+    // batches of U groups a thread, the next one on its way while one is
+    // worked on; groups past the end count as -inf
+    auto load = [&](uint4 (&w)[U], int k) {
 #pragma unroll
-      for (int j = 0; j < U; ++j) w[j] = xv[k + j * kStatThreads];
+      for (int j = 0; j < U; ++j) {
+        w[j] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+        if (k + j * kStatThreads < nv) w[j] = xv[k + j * kStatThreads];
+      }
+    };
+    uint4 w[U], ahead[U];
+    load(w, tid);
+    for (int k = tid; k < nv; k += U * kStatThreads) {
+      load(ahead, k + U * kStatThreads);
       float y[U * N];
 #pragma unroll
       for (int j = 0; j < U; ++j) V::unpack(w[j], y + j * N);
       take_batch<U * N>(st, y, c);
-    }
-    for (; k < nv; k += kStatThreads) {
-      float y[N];
-      V::unpack(xv[k], y);
-      take_batch<N>(st, y, c);
+#pragma unroll
+      for (int j = 0; j < U; ++j) w[j] = ahead[j];
     }
     for (int v = v0 + tid; v < h; v += kStatThreads) {
       const float y = to_f32(x[v]);
@@ -240,9 +245,10 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
 // One cluster per sequence. kVec: every row starts on a boundary of four
 // numbers (V a multiple of 4 and aligned tensors): loads of four numbers,
 // otherwise of one.
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kThreads>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     choose_kernel(const VerifyArgs a, const Stat* __restrict__ stats, int nsplit) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ float rm[2 * kMaxDrafts + 1], rl[2 * kMaxDrafts + 1];
   __shared__ int rarg[2 * kMaxDrafts + 1];
   __shared__ uint8_t accept[kMaxDrafts];
@@ -346,7 +352,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
         if (w > 0.f && v != skip) take(best, __fdividef(w, ev), v);
       };
       if constexpr (kVec) {
-#pragma unroll 2
+#pragma unroll 4
         for (int v = (rank * kThreads + tid) * 4; v < a.V; v += kCluster * kThreads * 4) {
           float xp[4], xq[4] = {0.f, 0.f, 0.f, 0.f}, ev[4];
           load4(pt + v, xp);
@@ -396,6 +402,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
         i < at ? a.tokens[int64_t(b) * a.S + i] : i == at ? chosen : -1;
 }
 
+template <typename T, int kThreads>
+cudaError_t launch_choose(const VerifyArgs& a, const Stat* stats, int nsplit, bool vec,
+                          cudaStream_t s) {
+  return launch_pdl(vec ? choose_kernel<T, true, kThreads> : choose_kernel<T, false, kThreads>,
+                    dim3(static_cast<unsigned>(a.B) * kCluster), dim3(kThreads), 0, s, a, stats,
+                    nsplit);
+}
+
 template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
   Stat* stats = static_cast<Stat*>(ws);
@@ -415,9 +429,14 @@ cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
   const bool vec = a.V % 4 == 0 && at(a.target) % (4 * sizeof(T)) == 0 &&
                    at(a.draft) % (4 * sizeof(T)) == 0 && at(a.expo) % 16 == 0;
-  const dim3 grid(static_cast<unsigned>(a.B) * kCluster);
-  return launch_pdl(vec ? choose_kernel<T, true> : choose_kernel<T, false>, grid, dim3(kThreads), 0,
-                    s, a, static_cast<const Stat*>(stats), ns);
+  // as many threads a CTA as keep all clusters resident at once: with few
+  // sequences a sweep over the vocabulary then takes few rounds of loads
+  // (one sequence, V = 32000: 8.3 us at 512 threads, 11.4 at 256), with many
+  // there is no second wave (64 sequences, V = 131072: 30 us and 24)
+  const int ctas = a.B * kCluster;
+  if (ctas <= 152) return launch_choose<T, 1024>(a, stats, ns, vec, s);
+  if (ctas <= 2 * 152) return launch_choose<T, 512>(a, stats, ns, vec, s);
+  return launch_choose<T, 256>(a, stats, ns, vec, s);
 }
 
 }  // namespace
