@@ -805,8 +805,6 @@ def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None,
     [0, 1), expo float32 [B, V] exponential variates, n_draft int32 [B],
     temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1], n_accepted
     int32 [B])."""
-    if workspace is None:
-        workspace = draft_verify_workspace(tokens.shape[0], tokens.shape[-1], target.device)
     r = _serving().draft_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
     if r.__class__ is tuple:
         return r

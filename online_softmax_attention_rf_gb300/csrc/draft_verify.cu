@@ -25,7 +25,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kStatThreads = 256;
+constexpr int kStatThreads = 128;
 constexpr int kStatWarps = kStatThreads / 32;
 constexpr int kMaxSplits = 32;
 constexpr int kCluster = 8;
@@ -40,6 +40,12 @@ struct Stat {
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // exp((x - m) / T) with c = log2(e) / T. The difference is taken before the
 // scaling, so that it is exact or nearly so for the entries that matter.
@@ -138,7 +144,7 @@ template <typename T>
 __global__ void __launch_bounds__(kStatThreads) stats_kernel(const VerifyArgs a, Stat* stats,
                                                              int nsplit, int piece) {
   using V = Vec16<T>;
-  constexpr int N = V::N, U = 4;
+  constexpr int N = V::N, U = 2;
   const int per = a.draft != nullptr ? 2 * a.S + 1 : a.S + 1;
   const int row = blockIdx.x / nsplit, split = blockIdx.x % nsplit;
   const int b = row / per, r = row % per;
@@ -163,26 +169,38 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(const VerifyArgs a,
   const uint4* xv = reinterpret_cast<const uint4*>(x + h);
   Running st;
   if (!greedy) {
-    // batches of U groups a thread, the next one on its way while one is
-    // worked on; groups past the end count as -inf
-    auto load = [&](uint4 (&w)[U], int k) {
+    // Whole batches of U groups a thread, two register sets in turn, each
+    // loaded while the other is worked on; then one batch with what is left,
+    // whose missing groups count as -inf.
+    const uint4* at = xv + tid;
+    auto load = [&](uint4 (&w)[U], int batch) {
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        w[j] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
-        if (k + j * kStatThreads < nv) w[j] = xv[k + j * kStatThreads];
-      }
+      for (int j = 0; j < U; ++j) w[j] = at[(batch * U + j) * kStatThreads];
     };
-    uint4 w[U], ahead[U];
-    load(w, tid);
-    for (int k = tid; k < nv; k += U * kStatThreads) {
-      load(ahead, k + U * kStatThreads);
+    auto work = [&](const uint4 (&w)[U]) {
       float y[U * N];
 #pragma unroll
       for (int j = 0; j < U; ++j) V::unpack(w[j], y + j * N);
       take_batch<U * N>(st, y, c);
+    };
+    const int whole = nv / (U * kStatThreads);
+    uint4 wa[U], wb[U], rest[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) w[j] = ahead[j];
+    for (int j = 0; j < U; ++j) {
+      const int k = (whole * U + j) * kStatThreads;
+      rest[j] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+      if (k + tid < nv) rest[j] = at[k];
     }
+    if (whole > 0) load(wa, 0);
+    int i = 0;
+    for (; i + 2 <= whole; i += 2) {
+      load(wb, i + 1);
+      work(wa);
+      if (i + 2 < whole) load(wa, i + 2);
+      work(wb);
+    }
+    if (i < whole) work(wa);
+    work(rest);
     for (int v = v0 + tid; v < h; v += kStatThreads) {
       const float y = to_f32(x[v]);
       take_batch<1>(st, &y, c);
@@ -335,36 +353,57 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const T* qt = draft + int64_t(at) * a.V;
     const bool has_q = refused && a.draft != nullptr;
     const float* e = a.expo + int64_t(b) * a.V;
-    const float pm = rm[at], pl = 1.f / rl[at];
-    const float qm = has_q ? rm[a.S + 1 + at] : 0.f, ql = has_q ? 1.f / rl[a.S + 1 + at] : 0.f;
+    // p = exp2((x - m) c - log2 l): the sum's logarithm rides in the exponent
+    const float pm = rm[at], pk = -log2f(rl[at]);
+    const float qm = has_q ? rm[a.S + 1 + at] : 0.f, qk = has_q ? -log2f(rl[a.S + 1 + at]) : 0.f;
     const int out_of_race = refused && !has_q ? a.tokens[int64_t(b) * a.S + at] : -1;
     chosen = -1;
     // pass 0: the remainder max(p - q, 0) (p itself when everything was
     // accepted); pass 1, only when rounding leaves nothing of the remainder: p
     for (int pass = 0; pass < (refused ? 2 : 1); ++pass) {
       Best best{0.f, kNone};
-      const bool minus_q = has_q && pass == 0;
       const int skip = pass == 0 ? out_of_race : -1;
-      auto one = [&](float xp, float xq, float ev, int v) {
-        float w = weight(xp, pm, c) * pl;
-        if (minus_q) w -= weight(xq, qm, c) * ql;
-        // the quotient's error is two steps: below what the weights carry
-        if (w > 0.f && v != skip) take(best, __fdividef(w, ev), v);
+      // w / e as w * (1 / e): two steps of error, below what the weights carry.
+      // A thread's indices ascend, so the first of equal scores stays.
+      auto one = [&](float w, float ev, int v) {
+        const float score = w * rcp_approx(ev);
+        if (score > best.score) best = Best{score, v};
       };
-      if constexpr (kVec) {
+      auto p_of = [&](float x) { return ex2_approx(fmaf(x - pm, c, pk)); };
+      auto q_of = [&](float x) { return ex2_approx(fmaf(x - qm, c, qk)); };
+      constexpr int kStep = kCluster * kThreads * (kVec ? 4 : 1);
+      const int first = (rank * kThreads + tid) * (kVec ? 4 : 1);
+      if (has_q && pass == 0) {
+        if constexpr (kVec) {
 #pragma unroll 4
-        for (int v = (rank * kThreads + tid) * 4; v < a.V; v += kCluster * kThreads * 4) {
-          float xp[4], xq[4] = {0.f, 0.f, 0.f, 0.f}, ev[4];
-          load4(pt + v, xp);
-          load4(e + v, ev);
-          if (minus_q) load4(qt + v, xq);
+          for (int v = first; v < a.V; v += kStep) {
+            float xp[4], xq[4], ev[4];
+            load4(pt + v, xp);
+            load4(qt + v, xq);
+            load4(e + v, ev);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) one(xp[i], xq[i], ev[i], v + i);
+            for (int i = 0; i < 4; ++i) one(p_of(xp[i]) - q_of(xq[i]), ev[i], v + i);
+          }
+        } else {
+#pragma unroll 4
+          for (int v = first; v < a.V; v += kStep)
+            one(p_of(to_f32(pt[v])) - q_of(to_f32(qt[v])), e[v], v);
         }
       } else {
+        if constexpr (kVec) {
 #pragma unroll 4
-        for (int v = rank * kThreads + tid; v < a.V; v += kCluster * kThreads)
-          one(to_f32(pt[v]), minus_q ? to_f32(qt[v]) : 0.f, e[v], v);
+          for (int v = first; v < a.V; v += kStep) {
+            float xp[4], ev[4];
+            load4(pt + v, xp);
+            load4(e + v, ev);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) one(v + i == skip ? 0.f : p_of(xp[i]), ev[i], v + i);
+          }
+        } else {
+#pragma unroll 4
+          for (int v = first; v < a.V; v += kStep)
+            one(v == skip ? 0.f : p_of(to_f32(pt[v])), e[v], v);
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
@@ -414,9 +453,10 @@ template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
   Stat* stats = static_cast<Stat*>(ws);
   const int64_t rows = int64_t(a.B) * (a.draft != nullptr ? 2 * a.S + 1 : a.S + 1);
-  // enough pieces that the rows fill the SMs a few times over, but pieces of
-  // at least 2048 logits
-  int64_t nsplit = (152 * 8 + rows - 1) / rows;
+  // enough pieces that the rows fill the SMs a few times over (more, smaller
+  // pieces pay their start more often: 16 times over, 49.5 us for 64 sequences
+  // at V = 131072, 5 times 47.1, 3 times 52), but pieces of at least 2048 logits
+  int64_t nsplit = (152 * 6 + rows - 1) / rows;
   nsplit = min64(min64(nsplit, kMaxSplits), (int64_t(a.V) + 2047) / 2048);
   // pieces of whole 16-byte groups
   const int piece = static_cast<int>(((a.V + nsplit - 1) / nsplit + 7) / 8 * 8);
@@ -434,7 +474,6 @@ cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
   // (one sequence, V = 32000: 8.3 us at 512 threads, 11.4 at 256), with many
   // there is no second wave (64 sequences, V = 131072: 30 us and 24)
   const int ctas = a.B * kCluster;
-  if (ctas <= 152) return launch_choose<T, 1024>(a, stats, ns, vec, s);
   if (ctas <= 2 * 152) return launch_choose<T, 512>(a, stats, ns, vec, s);
   return launch_choose<T, 256>(a, stats, ns, vec, s);
 }

@@ -229,14 +229,16 @@ PyObject* kv_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// target, draft or None, tokens, u, expo, n_draft or None, temperature or None, workspace
+// target, draft or None, tokens, u, expo, n_draft or None, temperature or None,
+// workspace or None
 PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   try {
     need(n == 8);
     const Tensor &target = tensor(a[0]), &tokens = tensor(a[2]), &u = tensor(a[3]),
-                 &expo = tensor(a[4]), &ws = tensor(a[7]);
-    const Tensor *draft = maybe(a[1]), *n_draft = maybe(a[5]), *temperature = maybe(a[6]);
+                 &expo = tensor(a[4]);
+    const Tensor *draft = maybe(a[1]), *n_draft = maybe(a[5]), *temperature = maybe(a[6]),
+                 *ws = maybe(a[7]);
     const at::Device dev = target.device();
     const at::ScalarType dt = target.scalar_type();
     need(dev.is_cuda() && target.dim() == 3 && target.size(1) > 1 && target.is_contiguous());
@@ -247,14 +249,19 @@ PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(expo, at::kFloat, {B, V}, dev);
     fits(n_draft, at::kInt, {B}, dev);
     fits(temperature, at::kFloat, {B}, dev);
-    need(ws.device() == dev && ws.is_contiguous());
+    need(ws == nullptr || (ws->device() == dev && ws->is_contiguous()));
     const rf_dtype rdt = dtype_of(target);
     const Tensor out = fresh({B, S + 1}, at::kInt, dev), n_accepted = fresh({B}, at::kInt, dev);
+    Tensor new_ws;
+    if (ws == nullptr) {
+      new_ws = fresh({static_cast<int64_t>(rf_draft_verify_workspace_bytes(B, S))}, at::kByte, dev);
+      ws = &new_ws;
+    }
     c10::cuda::CUDAGuard guard(dev);
     const rf_status st = rf_draft_verify(
         target.data_ptr(), ptr<>(draft), ptr<int32_t>(&tokens), ptr<float>(&u), ptr<float>(&expo),
         ptr<int32_t>(n_draft), ptr<float>(temperature), B, S, V, ptr<int32_t>(&out),
-        ptr<int32_t>(&n_accepted), ws.data_ptr(), ws.nbytes(), rdt, stream_of(dev));
+        ptr<int32_t>(&n_accepted), ws->data_ptr(), ws->nbytes(), rdt, stream_of(dev));
     return result(st, THPVariable_Wrap(out), THPVariable_Wrap(n_accepted));
   } catch (const Misfit&) {
     return misfit();
