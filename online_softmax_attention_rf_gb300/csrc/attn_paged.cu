@@ -160,9 +160,10 @@ struct Span {
     t2 = cu[min(cur.seq + 2, B)];
     kv1 = kvl[min(cur.seq + 1, B - 1)];
   }
-  __device__ __forceinline__ void init(const Params& p) {
-    cur = p.plan->start[blockIdx.x];
-    end = p.plan->start[blockIdx.x + 1];
+  __device__ __forceinline__ void init(const Params& p, const PlanStart& first,
+                                       const PlanStart& last) {
+    cur = first;
+    end = last;
     cu = plan_cu_q(p.plan);
     kvl = plan_kv_len(p.plan, p.B);
     B = p.B;
@@ -171,9 +172,9 @@ struct Span {
     causal = p.plan->causal;
     q = solo = 0;
     if (cur.seq < B) {
-      t0 = cu[cur.seq];
-      t1 = cu[cur.seq + 1];
-      kv = kvl[cur.seq];
+      t0 = cur.row0;
+      t1 = cur.row1;
+      kv = cur.kv;
       fetch();
     }
   }
@@ -361,15 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t s_base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_wait();
-  pdl_trigger();
-  if (!plan_matches(p.plan, p)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-      record_status(p.status, dev_code(kDevBadList, kKerPaged, 2));
-    return;
-  }
-  if (static_cast<int>(blockIdx.x) >= p.plan->ctas) return;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bar.seg_full[i], 1);
@@ -396,17 +388,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bar.tmem_base, 512);
     tmem_relinquish();
   }
+  if (warp == kWarpK && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bar.tmem_base;
+  // Up to here nothing of the call's memory was read or written. The plan's
+  // header and this CTA's starts are read together.
+  pdl_wait();
+  pdl_trigger();
+  const PlanStart first = p.plan->start[blockIdx.x], last = p.plan->start[blockIdx.x + 1];
+  const bool matches = plan_matches(p.plan, p);
+  if (!matches && blockIdx.x == 0 && threadIdx.x == 0)
+    record_status(p.status, dev_code(kDevBadList, kKerPaged, 2));
+  const bool busy = matches && static_cast<int>(blockIdx.x) < p.plan->ctas;
   volatile int* abort_flag = &bar.abort_flag;
 #define RF_WAIT(b, par, site)                                                         \
   mbar_wait(&bar.b, (par), p.status, dev_code(kDevTimeout, kKerPaged, site), abort_flag)
 #define RF_WAIT_WARP(b, par, site)                                                    \
   mbar_wait_warp(&bar.b, (par), p.status, dev_code(kDevTimeout, kKerPaged, site), abort_flag)
 
-  if (warp == kWarpK || warp == kWarpV) {
+  if (!busy) {
+    // no span
+  } else if (warp == kWarpK || warp == kWarpV) {
     // ------------------------------------------------------------ producers
     // K producer, per segment: the first K tile, then Q (once the Q ring has
     // room: after the second K tile at the latest), then the other K tiles. It
@@ -415,10 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_k = warp == kWarpK;
     const CUtensorMap* map = is_k ? &tm_k : &tm_v;
     const bool token_first = is_k ? p.k_token_first : p.v_token_first;
-    if (lane == 0) {
-      prefetch_tensormap(map);
-      if (is_k) prefetch_tensormap(&tm_q);
-    }
     const int boxes = kBN / p.box;
     const int my_key = lane % boxes * p.box, my_chunk = lane / boxes;
     const bool has_box = my_chunk < D / 64;
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
     };
     if (is_k) {
-      span.init(p);
+      span.init(p, first, last);
       span.next(s);
       publish(0, s);
       if (s.seq >= 0) id = page_of(s, s.kb, in_page);
@@ -950,121 +954,102 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Running softmax state of a row over parts: m, l and 16 columns.
+// Running softmax state of one row over parts: m, l and 16 columns.
 struct MergeState {
-  float m, l, acc[16];
+  float m = kNegInf, l = 0.f;
+  float acc[16] = {};
+  // joined with another state; one without keys (m = -inf) adds nothing, NaN
+  // passes through
+  __device__ __forceinline__ void add(float m2, float l2, const float (&v)[16]) {
+    const float mn = fmaxf(m, m2);
+    const float a = m == kNegInf ? 0.f : __expf(m - mn);
+    const float b = m2 == kNegInf ? 0.f : __expf(m2 - mn);
+    l = l * a + l2 * b;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = acc[e] * a + (b != 0.f ? b * v[e] : 0.f);
+    m = mn;
+  }
 };
 
-__device__ __forceinline__ void merge_add(MergeState& st, float ls, float weight,
-                                          const float (&v)[16]) {
-  // a part without keys (-inf) adds nothing; NaN passes through
-  const float mn = fmaxf(st.m, ls);
-  const float a = st.m == kNegInf ? 0.f : expf(st.m - mn);
-  const float b = ls == kNegInf ? 0.f : weight * expf(ls - mn);
-  st.l = st.l * a + b;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) st.acc[e] = st.acc[e] * a + (b != 0.f ? b * v[e] : 0.f);
-  st.m = mn;
-}
-
 // Joins the parts of the items that several CTAs share: LSE = log sum_s
-// exp(lse_s), O = sum_s exp(lse_s - LSE) O_s, parts in a fixed order. A block
-// takes 32 rows (a lane each) and 64 columns of an item: with few parts a warp
-// joins all of them for 16 columns, with many the four warps take every fourth
-// part and join their states through shared memory.
-constexpr int kMergeShare = 8;  // parts from which the warps share them
+// exp(lse_s), O = sum_s exp(lse_s - LSE) O_s, in a fixed order. A warp takes 32
+// rows of an item and 16 columns, a lane a row; where the rows are few the lanes
+// share the parts too and join their states by shuffles. Two blocks an SM, each
+// of which reads the plan once: with more, smaller blocks their reads of the
+// same few lines of it queue up in L2 (1216 blocks whose warps read it each:
+// 21 us for 8 items of 3 parts).
+constexpr int kMergeThreads = 512;
+constexpr int kMergeBlocks = 2 * kPlanCtas;
 
 template <int D>
-__global__ void __launch_bounds__(128) attn_paged_merge(const Params p) {
-  __shared__ float xs[4][18][32];
+__global__ void __launch_bounds__(kMergeThreads, 2) attn_paged_merge(const Params p) {
+  constexpr int kGroups = D / 16;
+  __shared__ alignas(16) int4 table[kPlanCtas * 2];
+  __shared__ int head[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const PlanHeader* h = p.plan;
+  // The plan was complete before the attention kernel let this one start, so it
+  // is read (past L1, which may hold an older one) while that kernel runs; the
+  // partial states have to be waited for. Every block waits, tasks or not: what
+  // follows in the stream may rely on this kernel's end alone.
+  if (threadIdx.x < 16) head[threadIdx.x] = __ldcg(reinterpret_cast<const int*>(p.plan) + threadIdx.x);
+  for (int i = threadIdx.x; i < 2 * kPlanCtas; i += kMergeThreads)
+    table[i] = __ldcg(reinterpret_cast<const int4*>(p.plan->merge) + i);
+  __syncthreads();
+  const PlanMerge* merge = reinterpret_cast<const PlanMerge*>(table);
+  const bool matches = head[0] == kPlanMagic && head[1] == p.B && head[2] == p.T && head[3] == p.H &&
+                       head[4] == p.Hkv && head[5] == p.page && head[6] == p.max_pages;
+  const int n_merge = matches ? head[9] : 0;
+  const int tasks = matches ? head[10] * kGroups : 0;
   pdl_wait();
-  if (!plan_matches(h, p)) return;
-  const int n_merge = h->n_merge;
-  const int tasks = h->merge_units * (D / 64);
-  const int32_t* cu = plan_cu_q(h);
-  for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int unit = task / (D / 64), c64 = task % (D / 64) * 64;
+  // neighbouring warps take the column groups of one unit: a row's sectors are
+  // written by one block
+  for (int task = blockIdx.x * (kMergeThreads / 32) + warp; task < tasks;
+       task += kMergeBlocks * (kMergeThreads / 32)) {
+    const int unit = task / kGroups, c = task % kGroups * 16;
     int e = -1;  // the item: the last one with unit0 <= unit
-    for (int i = lane; i < n_merge; i += 32)
-      if (h->merge[i].unit0 <= unit) e = i;
-    e = __reduce_max_sync(0xffffffffu, e);
-    const PlanMerge g = h->merge[e];
+    for (int k = lane; k - lane < n_merge; k += 32)
+      e += __popc(__ballot_sync(0xffffffffu, k < n_merge && merge[k].unit0 <= unit));
+    const PlanMerge g = merge[e];
     const int ntok = g.rows / p.G;
     const int u0 = plan_units(ntok, 0, p.G);
     const int tile = unit - g.unit0 >= u0 ? 1 : 0;
-    const int r = (unit - g.unit0 - tile * u0) * 32 + lane;
-    const int tok = tile * p.tt + r / p.G;
-    const bool row_ok = r < p.G * p.tt && tok < ntok;
-    const bool share = g.parts >= kMergeShare;
-    const int64_t row =
-        int64_t(cu[g.seq] + g.pair * 2 * p.tt + tok) * p.H + g.head * p.G + r % p.G;
+    const int r0 = (unit - g.unit0 - tile * u0) * 32;
+    const int live = min(32, min(p.tt, ntok - tile * p.tt) * p.G - r0);  // rows of the 32
+    const int pad = live > 16 ? 32 : live > 8 ? 16 : 8;
+    const int row = lane & (pad - 1);
+    const int r = r0 + row;
     MergeState st;
-    for (int k = 0; k < (share ? 4 : 1); ++k) {
-      const int c = c64 + (share ? k : warp) * 16;
-      st.m = kNegInf;
-      st.l = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) st.acc[i] = 0.f;
-#pragma unroll 4
-      for (int i = share ? warp : 0; i < g.parts; i += share ? 4 : 1) {
+    if (row < live) {
+#pragma unroll 2
+      for (int i = lane / pad; i < g.parts; i += 32 / pad) {
         const int cta = g.cta + i;
         const int64_t at = int64_t(i == 0 ? 2 * cta + 1 : 2 * cta) * 2 + tile;
-        if (row_ok) {
-          const float ls = p.lse_part[at * kBM + r];
-          const float* from = p.o_part + (at * (D / 4) * kBM + r) * 4 + c * kBM;
-          float v[16];
+        const float ls = __ldcg(p.lse_part + at * kBM + r);
+        const float* from = p.o_part + (at * (D / 4) * kBM + r) * 4 + c * kBM;
+        float v[16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 x = *reinterpret_cast<const float4*>(from + q * 4 * kBM);
-            v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
-          }
-          merge_add(st, ls, 1.f, v);
+        for (int q = 0; q < 4; ++q) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(from + q * 4 * kBM));
+          v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
         }
-      }
-      if (share) {
-        // the four warps' states of these columns; warp k joins them
-        __syncthreads();
-        xs[warp][0][lane] = st.m;
-        xs[warp][1][lane] = st.l;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) xs[warp][2 + i][lane] = st.acc[i];
-        __syncthreads();
-        if (warp == k) {
-          st.m = kNegInf;
-          st.l = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) st.acc[i] = 0.f;
-          for (int w = 0; w < 4; ++w) {
-            // a warp's state is (m, l, acc): its mean acc / l, with weight l
-            const float m2 = xs[w][0][lane], l2 = xs[w][1][lane];
-            const float mn = fmaxf(st.m, m2);
-            const float a = st.m == kNegInf ? 0.f : expf(st.m - mn);
-            const float b = m2 == kNegInf ? 0.f : expf(m2 - mn);
-            st.l = st.l * a + (l2 == 0.f ? 0.f : l2 * b);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              st.acc[i] = st.acc[i] * a + (l2 == 0.f ? 0.f : xs[w][2 + i][lane] * b);
-            st.m = mn;
-          }
-          if (row_ok) {
-            const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) st.acc[i] *= inv;
-            put_bf16x16(p.o + row * D + c, st.acc, p.o_wide);
-            if (c == 0 && p.lse != nullptr) p.lse[row] = st.l == 0.f ? kNegInf : st.m + logf(st.l);
-          }
-        }
+        st.add(ls, 1.f, v);
       }
     }
-    if (!share && row_ok) {
-      const int c = c64 + warp * 16;
-      const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+    for (int o = pad; o < 32; o <<= 1) {
+      float v[16];
+      const float m2 = __shfl_xor_sync(0xffffffffu, st.m, o);
+      const float l2 = __shfl_xor_sync(0xffffffffu, st.l, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __shfl_xor_sync(0xffffffffu, st.acc[i], o);
+      st.add(m2, l2, v);
+    }
+    if (lane < pad && row < live) {
+      const int64_t to = int64_t(g.row0 + tile * p.tt + r / p.G) * p.H + g.head * p.G + r % p.G;
+      const float inv = st.l == 0.f ? 0.f : __fdividef(1.f, st.l);
 #pragma unroll
       for (int i = 0; i < 16; ++i) st.acc[i] *= inv;
-      put_bf16x16(p.o + row * D + c, st.acc, p.o_wide);
-      if (c == 0 && p.lse != nullptr) p.lse[row] = st.l == 0.f ? kNegInf : st.m + logf(st.l);
+      put_bf16x16(p.o + to * D + c, st.acc, p.o_wide);
+      if (c == 0 && p.lse != nullptr) p.lse[to] = st.l == 0.f ? kNegInf : st.m + __logf(st.l);
     }
   }
 }
@@ -1154,7 +1139,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
   }
   e = launch_pdl(attn_paged_kernel<D>, dim3(kPlanCtas), dim3(kThreads), smem, s, mq, mk, mv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_paged_merge<D>, dim3(kPlanCtas * 6), dim3(128), 0, s, p);
+  return launch_pdl(attn_paged_merge<D>, dim3(kMergeBlocks), dim3(kMergeThreads), 0, s, p);
 }
 
 }  // namespace

@@ -11,43 +11,51 @@ namespace rf {
 namespace {
 
 constexpr int kThreads = 1024;
-// Cost of an item: a fixed part (filling the pipeline and writing the output),
-// plus per step kPairCost when it has two tiles and kSingleCost when it has
-// one. Measured at d = 128: 5 us, 1.7 us and 1.2 us. With fewer items than
-// CTAs every CTA pays the fixed part about once whatever the cuts are, and only
-// the steps are shared out.
-constexpr int kItemCost = 8;
-constexpr int kItemCostFew = 1;
-constexpr int kPairCost = 3;
-constexpr int kSingleCost = 2;
+// Cost of an item, in units of 0.28 us: a fixed part (filling the pipeline and
+// writing the output) and a part per step, of items with two tiles (measured at
+// d = 128: 5 us, 1.7 us) and with one (3.4 us, 1.45 us: memory bounds the step
+// of a decode item).
+constexpr int kPairFixed = 18;
+constexpr int kPairCost = 6;
+constexpr int kSingleFixed = 12;
+constexpr int kSingleCost = 5;
 // A span is worth at least this much. Two cuts of one item are then more than
 // a step apart: no CTA inside an item is left without steps.
-constexpr int kMinSpan = 4;
+constexpr int kMinSpan = 8;
 static_assert(kMinSpan - 1 >= kPairCost && kPairCost >= kSingleCost, "cuts may coincide");
+// With no more items than CTAs an item is cut by itself, into equal parts of at
+// least this cost (both softmax groups have a step of a one-tile item then): a
+// span that held the end of one item and the start of the next would pay two
+// fixed parts one after the other (8 items of 5 steps: 10.6 us, against 7.5).
+constexpr int kMinPart = 10;
 
 struct Item {
   int rows, steps, cost;
+  int fixed, per_step;
 };
 
 // Item `pair` of a sequence with n new and kv cached tokens.
-__device__ __forceinline__ Item item_of(int pair, int n, int kv, int causal, int G, int fixed) {
+__device__ __forceinline__ Item item_of(int pair, int n, int kv, int causal, int G) {
   const int tt = plan_tile_tokens(G);
   const int i0 = pair * 2 * tt, i1 = min(n, i0 + 2 * tt);
   Item it;
   it.rows = (i1 - i0) * G;
   it.steps = (plan_visible(i1 - 1, n, kv, causal) + kPlanTile - 1) / kPlanTile;
-  it.cost = fixed + it.steps * (i1 - i0 > tt ? kPairCost : kSingleCost);
+  const bool two = i1 - i0 > tt;
+  it.per_step = two ? kPairCost : kSingleCost;
+  it.fixed = two ? kPairFixed : kSingleFixed;
+  it.cost = it.fixed + it.steps * it.per_step;
   return it;
 }
 
-__device__ PlanStart locate(int64_t x, const int64_t* cost, const int32_t* cu, const int32_t* kvl,
-                            const PagedPlanArgs& a, int fixed) {
+__device__ PlanStart locate_item(int64_t x, const int64_t* cost, const int32_t* cu, const int32_t* kvl,
+                            const PagedPlanArgs& a) {
   int lo = 0, hi = a.B;  // the first b with cost[b + 1] > x
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (cost[mid + 1] <= x) lo = mid + 1; else hi = mid;
   }
-  PlanStart st{lo, 0, 0, 0};
+  PlanStart st{lo, 0, 0, 0, 0, 0, 0, 0};
   if (lo == a.B) return st;
   const int G = a.H / a.Hkv, tt = plan_tile_tokens(G);
   const int n = cu[lo + 1] - cu[lo], kv = kvl[lo];
@@ -57,10 +65,10 @@ __device__ PlanStart locate(int64_t x, const int64_t* cost, const int32_t* cu, c
   st.head = static_cast<int>(rem / per_head);
   rem -= st.head * per_head;
   for (; st.pair < pairs; ++st.pair) {
-    const Item it = item_of(st.pair, n, kv, a.causal, G, fixed);
+    const Item it = item_of(st.pair, n, kv, a.causal, G);
     if (rem < it.cost) {
-      const int w = it.rows > tt * G ? kPairCost : kSingleCost;
-      const int step = rem <= fixed ? 0 : static_cast<int>((rem - fixed + w - 1) / w);
+      const int step =
+          rem <= it.fixed ? 0 : static_cast<int>((rem - it.fixed + it.per_step - 1) / it.per_step);
       if (step < it.steps || step == 0) {
         st.step = step;
         return st;
@@ -76,6 +84,18 @@ __device__ PlanStart locate(int64_t x, const int64_t* cost, const int32_t* cu, c
   st.head = 0;
   do ++st.seq;
   while (st.seq < a.B && cu[st.seq + 1] == cu[st.seq]);
+  return st;
+}
+
+// The start at cost x, with its sequence's lengths.
+__device__ PlanStart locate(int64_t x, const int64_t* cost, const int32_t* cu, const int32_t* kvl,
+                            const PagedPlanArgs& a) {
+  PlanStart st = locate_item(x, cost, cu, kvl, a);
+  if (st.seq < a.B) {
+    st.row0 = cu[st.seq];
+    st.row1 = cu[st.seq + 1];
+    st.kv = kvl[st.seq];
+  }
   return st;
 }
 
@@ -130,49 +150,120 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
   __syncthreads();
   items = 0;
   for (int w = 0; w < kThreads / 32; ++w) items += wsum[w];
-  const int fixed = items * a.Hkv > kPlanCtas ? kItemCost : kItemCostFew;
+  const bool few = items * a.Hkv <= kPlanCtas;
   __syncthreads();
-  // costs of the sequences, a warp each
-  for (int b = warp; b < a.B; b += kThreads / 32) {
-    const int n = cu[b + 1] - cu[b], kv = kvl[b];
-    const int pairs = (n + 2 * tt - 1) / (2 * tt);
-    int64_t sum = 0;
-    for (int p = lane; p < pairs; p += 32) sum += item_of(p, n, kv, a.causal, G, fixed).cost;
+  // prefix sums over the sequences of their costs, or of their items
+  auto scan = [&](bool count) {
+    for (int b = warp; b < a.B; b += kThreads / 32) {
+      const int n = cu[b + 1] - cu[b], kv = kvl[b];
+      const int pairs = (n + 2 * tt - 1) / (2 * tt);
+      int64_t sum = count ? (lane == 0 ? pairs : 0) : 0;
+      if (!count)
+        for (int p = lane; p < pairs; p += 32) sum += item_of(p, n, kv, a.causal, G).cost;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) cost[b + 1] = sum * a.Hkv;
-  }
-  __syncthreads();
-  // inclusive prefix sums
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int64_t v = b < a.B ? cost[b + 1] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) cost[b + 1] = sum * a.Hkv;
     }
-    if (lane == 31) wsum[warp] = v;
+    if (tid == 0) carry = 0;
     __syncthreads();
-    if (warp == 0) {
-      int64_t s = wsum[lane];
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      int64_t v = b < a.B ? cost[b + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
       }
-      wsum[lane] = s;
+      if (lane == 31) wsum[warp] = v;
+      __syncthreads();
+      if (warp == 0) {
+        int64_t s = wsum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += u;
+        }
+        wsum[lane] = s;
+      }
+      __syncthreads();
+      v += carry + (warp > 0 ? wsum[warp - 1] : 0);
+      if (b < a.B) cost[b + 1] = v;
+      __syncthreads();
+      if (tid == kThreads - 1) carry = v;
+      __syncthreads();
+    }
+    return cost[a.B];
+  };
+  const int64_t total = scan(few);
+  int ctas = 0;
+  bool by_item = few;
+  if (few) {
+    // thread i has item i
+    PlanStart st{};
+    Item it{};
+    int worth = 0;
+    if (tid < total) {
+      int lo = 0, hi = a.B;  // the first b with cost[b + 1] > tid
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cost[mid + 1] <= tid) lo = mid + 1; else hi = mid;
+      }
+      const int per_head = static_cast<int>(cost[lo + 1] - cost[lo]) / a.Hkv;
+      const int rem = tid - static_cast<int>(cost[lo]);
+      st = PlanStart{lo, rem / per_head, rem % per_head, 0, cu[lo], cu[lo + 1], kvl[lo], 0};
+      it = item_of(st.pair, st.row1 - st.row0, st.kv, a.causal, G);
+      worth = it.steps * it.per_step;
+    }
+    if (tid < kPlanCtas) units[tid] = worth;
+    __syncthreads();
+    // the least part worth (a warp, by bisection) with which all parts fit
+    if (warp == 0) {
+      auto parts_at = [&](int part) {
+        int sum = 0;
+        for (int i = lane; i < total; i += 32) sum += max(1, (units[i] + part - 1) / part);
+        return __reduce_add_sync(0xffffffffu, sum);
+      };
+      int lo = kMinPart, hi = kMinPart;
+      for (int i = lane; i < total; i += 32) hi = max(hi, units[i]);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (parts_at(mid) <= kPlanCtas) hi = mid; else lo = mid + 1;
+      }
+      int64_t sum = 0;
+      for (int i = lane; i < total; i += 32) sum += units[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // unless the largest part is longer than an even span and its second
+      // fixed part: items of unequal length, about as many as CTAs
+      if (lane == 0) carry = lo <= sum / kPlanCtas + kSingleFixed || lo == kMinPart ? lo : -1;
     }
     __syncthreads();
-    v += carry + (warp > 0 ? wsum[warp - 1] : 0);
-    if (b < a.B) cost[b + 1] = v;
+    const int part = static_cast<int>(carry);
+    by_item = part > 0;
     __syncthreads();
-    if (tid == kThreads - 1) carry = v;
-    __syncthreads();
+    if (by_item) {
+      const int parts = tid < total ? max(1, min(it.steps, (worth + part - 1) / part)) : 0;
+      if (tid < kPlanCtas) flag[tid] = parts;
+      __syncthreads();
+      int cta0 = 0;
+      ctas = 0;
+      for (int i = 0; i < total; ++i) {
+        if (i < tid) cta0 += flag[i];
+        ctas += flag[i];
+      }
+      for (int j = 0; j < parts; ++j) {
+        st.step = static_cast<int>(int64_t(it.steps) * j / parts);
+        start[cta0 + j] = st;
+      }
+      if (tid == 0) start[ctas] = PlanStart{a.B, 0, 0, 0, 0, 0, 0, 0};
+    }
   }
-  const int64_t total = cost[a.B];
-  const int ctas = total == 0 ? 0 : static_cast<int>(min64(kPlanCtas, max64(1, total / kMinSpan)));
-  if (tid <= ctas) start[tid] = locate(ctas > 0 ? total * tid / ctas : 0, cost, cu, kvl, a, fixed);
+  if (!by_item) {
+    const int64_t sum = few ? scan(false) : total;
+    ctas = static_cast<int>(min64(kPlanCtas, max64(1, sum / kMinSpan)));
+    if (tid <= ctas) start[tid] = locate(sum * tid / ctas, cost, cu, kvl, a);
+  }
   __syncthreads();
   // items that a cut falls into: found by the first cut inside each
   PlanMerge m{};
@@ -187,8 +278,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
         while (tid + parts <= ctas && start[tid + parts - 1].step > 0 &&
                same_item(start[tid + parts - 1], s))
           ++parts;
-        const int rows = item_of(s.pair, cu[s.seq + 1] - cu[s.seq], kvl[s.seq], a.causal, G, fixed).rows;
-        m = PlanMerge{s.seq, s.head, s.pair, tid - 1, parts, rows, 0, 0};
+        const int rows = item_of(s.pair, cu[s.seq + 1] - cu[s.seq], kvl[s.seq], a.causal, G).rows;
+        m = PlanMerge{s.seq, s.head, s.pair, tid - 1, parts, rows, 0, s.row0 + s.pair * 2 * tt};
       }
     }
     flag[tid] = first;

@@ -28,15 +28,17 @@ constexpr int kPlanRows = 2 * kPlanTile;  // packed rows per item
 // [pair * 2 * (128 / G), ...) of (seq, head). seq == B: the end.
 struct PlanStart {
   int seq, head, pair, step;
+  int row0, row1, kv, pad;  // the sequence's packed rows and cached tokens
 };
 
 // An item computed by the CTAs [cta, cta + parts), with `rows` packed rows. The
 // merge takes each of its tiles in units of 32 rows, numbered from unit0 on.
 struct PlanMerge {
-  int seq, head, pair, cta, parts, rows, unit0, pad;
+  int seq, head, pair, cta, parts, rows, unit0;
+  int row0;  // its first token among the packed tokens
 };
 
-struct PlanHeader {
+struct alignas(16) PlanHeader {
   int magic, B, T, H, Hkv, page, max_pages, causal;
   int ctas;         // spans in use
   int n_merge;      // items in parts
@@ -47,7 +49,8 @@ struct PlanHeader {
   // followed by int32 cu_q[B + 1], kv_len[B] and one word of padding, then
   // int64 cost[B + 1] (prefix sums)
 };
-static_assert(sizeof(PlanHeader) % 8 == 0, "the prefix sums need 8-byte alignment");
+static_assert(sizeof(PlanHeader) % 16 == 0 && sizeof(PlanStart) == 32 && sizeof(PlanMerge) == 32,
+              "entries are read by 16 bytes; the prefix sums need 8-byte alignment");
 
 __host__ __device__ inline const int32_t* plan_cu_q(const void* plan) {
   return reinterpret_cast<const int32_t*>(static_cast<const PlanHeader*>(plan) + 1);

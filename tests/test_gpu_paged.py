@@ -173,8 +173,11 @@ def _spans(plan, cu, kv, H, Hkv, causal):
     and its merge entries, decoded from device memory."""
     w = plan.buf.cpu().numpy().view(np.int32)
     ctas, n_merge, units = w[8], w[9], w[10]
-    start = w[16:16 + 153 * 4].reshape(153, 4)
-    merge = w[16 + 153 * 4:16 + 153 * 4 + 152 * 8].reshape(152, 8)[:n_merge]
+    start = w[16:16 + 153 * 8].reshape(153, 8)
+    merge = w[16 + 153 * 8:16 + 305 * 8].reshape(152, 8)[:n_merge]
+    for s in start[:ctas]:
+        assert (s[4], s[5], s[6]) == (cu[s[0]], cu[s[0] + 1], kv[s[0]])
+    start = start[:, :4]
     tt = 128 // (H // Hkv)
     items = []
     for b in range(len(kv)):
@@ -209,6 +212,7 @@ def _spans(plan, cu, kv, H, Hkv, causal):
     ([(0, 5), (3, 1), (0, 0), (700, 900), (1, 4000), (0, 9)], 28, 4),
     ([(1 + i % 5, 40 * i + 6) for i in range(1100)], 8, 2), ([(130, 130)] * 7, 128, 1),
     ([(0, 3)], 4, 4), ([(9000, 9000), (1, 60000)], 4, 4),
+    ([(1, 100), (1, 9000)] * 9, 64, 8), ([(1, 40000)], 4, 4), ([(130, 9000)], 8, 1),
 ])
 def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal):
     cu = [0]
@@ -240,11 +244,17 @@ def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal)
         first = min(m[5], 128 // G * G)        # rows of the first tile, in units of 32
         unit0 += -(-first // 32) + -(-(m[5] - first) // 32)
     assert unit0 == units
-    if len(spans) > 1:     # and the spans are even, up to a step and an item's fixed cost
-        fixed = 8 if len(items) > 152 else 1
-        cost = [sum(fixed + (k1 - k0) * (3 if items[i][4] > 128 // (H // Hkv) * (H // Hkv) else 2)
+    pair = [it[4] > 128 // G * G for it in items]
+    by_item = len(items) <= 152 and all(len(span) == 1 for span in spans)
+    worth = sum(it[3] * (6 if p else 5) for it, p in zip(items, pair))
+    if by_item:   # each CTA has a part of one item, none much larger than an even span
+        assert all((k1 - k0) * (6 if pair[i] else 5) <= max(10, worth / 152 + 12) + 6
+                   for span in spans for i, k0, k1 in span)
+    else:         # the spans are even: a cut moves by up to a step, or by the fixed
+        # part of the item that it falls into
+        cost = [sum((18 if pair[i] else 12) * (k0 == 0) + (k1 - k0) * (6 if pair[i] else 5)
                     for i, k0, k1 in span) for span in spans]
-        assert max(cost) <= sum(cost) / len(cost) + 22
+        assert max(cost) <= sum(cost) / len(cost) + 24
 
 
 # ---------------------------------------------------------------- attention
