@@ -140,6 +140,43 @@ def test_kv_append_paged(cuda_device, dtype, T, H, Hkv, d, rot, page, norm, inte
     assert np.array_equal(k_old, k_new) and np.array_equal(v_old, v_new)   # nothing else moved
 
 
+@pytest.mark.parametrize("T,H,Hkv,d,dtype,skip", [
+    (1500, 4, 2, 64, torch.bfloat16, 7),       # several tokens a block, some skipped
+    (2000, 1, 1, 16, torch.float32, 0),
+    (457, 40, 8, 256, torch.float32, 3),       # a token's heads take several stages
+    (5000, 0, 1, 128, torch.bfloat16, 2),
+])
+def test_kv_append_paged_many_tokens(cuda_device, T, H, Hkv, d, dtype, skip):
+    gen = torch.Generator().manual_seed(T)
+    qkv = torch.randn(T, H + 2 * Hkv, d, generator=gen).to(dtype).cuda()
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    pages = -(-T // 16) + 1
+    kc, vc = torch.zeros(2, pages, 16, Hkv, d, dtype=dtype, device="cuda")
+    slots = torch.randperm(pages * 16, generator=gen)[:T].cuda()
+    if skip:
+        slots[::skip] = -1
+    pos = torch.randint(0, 300, (T,), generator=gen, dtype=torch.int32).cuda()
+    ang = torch.rand(300, d // 2, generator=gen).cuda() * 6.3
+    cs = torch.cat([ang.cos(), ang.sin()], 1)
+    got = api.kv_append_paged(q if H else None, k, v, kc, vc, slots, pos, cs)
+    assert api.device_status() == 0
+    live = slots >= 0
+    c, s = cs[pos.long()].double().chunk(2, 1)
+
+    def turned(x):
+        a, b = x.double().chunk(2, -1)
+        return torch.cat([a * c[:, None] - b * s[:, None], b * c[:, None] + a * s[:, None]], -1)
+
+    last = BF16_STEP if dtype == torch.bfloat16 else F32_STEP
+    at = slots[live] // 16, slots[live] % 16
+    for have, x in [(kc[at], k)] + ([(got[live], q)] if H else []):
+        want = turned(x)[live]
+        size = x[live].double().abs().unfold(-1, d // 2, d // 2).sum(-2).repeat(1, 1, 2)
+        assert ((have.double() - want).abs() <= 3 * F32_STEP * size + 1.01 * last * want.abs()).all()
+    assert torch.equal(vc[at], v[live])
+    assert (kc != 0).any(-1).any(-1).sum() == live.sum()       # and nothing else was written
+
+
 def test_kv_append_paged_in_place(cuda_device):
     gen = torch.Generator().manual_seed(5)
     q = torch.randn(20, 4, 128, generator=gen).bfloat16().cuda()
