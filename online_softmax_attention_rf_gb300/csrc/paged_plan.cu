@@ -15,7 +15,7 @@ constexpr int kThreads = 1024;
 // writing the output) and a part per step, of items with two tiles (measured at
 // d = 128: 5 us, 1.7 us) and with one (3.4 us, 1.45 us: memory bounds the step
 // of a decode item).
-constexpr int kPairFixed = 18;
+constexpr int kPairFixed = 22;
 constexpr int kPairCost = 6;
 constexpr int kSingleFixed = 12;
 constexpr int kSingleCost = 5;

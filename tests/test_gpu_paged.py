@@ -289,9 +289,9 @@ def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal)
                    for span in spans for i, k0, k1 in span)
     else:         # the spans are even: a cut moves by up to a step, or by the fixed
         # part of the item that it falls into
-        cost = [sum((18 if pair[i] else 12) * (k0 == 0) + (k1 - k0) * (6 if pair[i] else 5)
+        cost = [sum((22 if pair[i] else 12) * (k0 == 0) + (k1 - k0) * (6 if pair[i] else 5)
                     for i, k0, k1 in span) for span in spans]
-        assert max(cost) <= sum(cost) / len(cost) + 24
+        assert max(cost) <= sum(cost) / len(cost) + 28
 
 
 # ---------------------------------------------------------------- attention
