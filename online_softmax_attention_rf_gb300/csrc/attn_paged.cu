@@ -248,7 +248,11 @@ struct Span {
 };
 
 // Named barrier of one group -- its four softmax warps and its issuer warp --
-// that also ORs a predicate over the group.
+// that also ORs a predicate over the group: after each step's P, and once at the
+// end of the span. A warp that fails calls it once with true and leaves, and the
+// others leave at whichever of their calls it meets. Every warp thus makes its
+// last call together with the four others, and none waits at a barrier that the
+// rest have abandoned.
 __device__ __forceinline__ bool group_sync_or(int t, bool pred) {
   uint32_t r;
   asm volatile(
@@ -640,10 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     for (int k = 0;; ++k) {
-      // the five warps of a group take up a segment together, or unwind together
       if (ok) ok = RF_WAIT_WARP(seg_full[k % kSegs], (k / kSegs) & 1, 26);
-      if (group_sync_or(t, !ok)) {
-        ok = false;
+      if (!ok) {
+        group_sync_or(t, true);
         break;
       }
       const Seg& d = bar.seg[k % kSegs];
@@ -652,8 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && !end && started < k) start_segment(k);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (lane == 0) mbar_arrive(&bar.seg_empty[k % kSegs]);
-      if (end) break;
+      if (end) {
+        group_sync_or(t, false);
+        break;
+      }
       if (mode >= kSolo0 && mode != kSolo0 + t) continue;  // the other group's
+      bool left = false;
       for (int jj = 0; jj < n; ++jj) {
         // While the softmax runs: wait for V_u, zero its rows past the cache's
         // end, and see whether the next step's K tile is there. If it is, its
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         // P_t is in tensor memory
         if (group_sync_or(t, !ok)) {
-          ok = false;
+          left = true;
           break;
         }
         if (lane == 0 && (ok = RF_LOCK())) {
@@ -703,14 +710,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (group_sync_or(t, !ok)) {  // after the segment's steps
-        ok = false;
-        break;
-      }
+      if (left) break;
       // while the softmax warps write this segment's output: release the steps
       // after this group's last, and start this group's next segment (the one
       // after the next, when the next is the other group's alone)
-      if (lane == 0 && n > 0) {
+      if (lane == 0 && ok && n > 0) {
         int k2;
         advance(k2);
         if (ok) start_segment(k + 1);
@@ -742,14 +746,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int k = 0;; ++k) {
       if (ok) ok = RF_WAIT_WARP(seg_full[k % kSegs], (k / kSegs) & 1, 31);
-      if (group_sync_or(t, !ok)) {
-        ok = false;
+      if (!ok) {
+        group_sync_or(t, true);
         break;
       }
       const Seg s = bar.seg[k % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.seg_empty[k % kSegs]);
-      if (s.seq < 0) break;
+      if (s.seq < 0) {
+        group_sync_or(t, false);
+        break;
+      }
+      bool left = false;
       if (s.mode >= kSolo0 && s.mode != kSolo0 + t) continue;  // the other group's
       const int tile = s.mode == kPair ? t : 0;      // the group's query tile
       const int tok = tile * p.tt + row_tok;         // token within the item
@@ -837,15 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before_sync();
         }
         if (group_sync_or(t, !ok)) {
-          ok = false;
+          left = true;
           break;
         }
       }
-      // the issuer has committed the segment's last P.V (or given up)
-      if (group_sync_or(t, !ok)) {
-        ok = false;
-        break;
-      }
+      if (left) break;
       // epilogue: O = acc / l, LSE = (m + log2 l) ln 2
       if (n > 0) {
         ok = mbar_wait_warp(&bar.o_done[t], o_segs & 1, p.status,
