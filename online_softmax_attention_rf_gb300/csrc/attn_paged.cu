@@ -41,7 +41,7 @@
 #include <mutex>
 
 #include "paged_plan.h"
-#include "rf_device.cuh"
+#include "paged_device.cuh"
 
 namespace rf {
 namespace {

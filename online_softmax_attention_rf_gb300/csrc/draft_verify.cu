@@ -18,7 +18,7 @@
 // that row's logits are in L2 by then).
 #include <cooperative_groups.h>
 
-#include "rf_device.cuh"
+#include "paged_device.cuh"
 
 namespace rf {
 namespace {

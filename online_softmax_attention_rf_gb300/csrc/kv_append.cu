@@ -21,7 +21,7 @@
 // members of every rotated pair are in it: pieces p and p + rot/2 for half-split
 // pairs, neighbouring pieces otherwise. The rotation then needs no exchange
 // between lanes, and only the norm's sum does.
-#include "rf_device.cuh"
+#include "paged_device.cuh"
 
 namespace rf {
 namespace {

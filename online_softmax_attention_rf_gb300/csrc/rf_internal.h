@@ -37,7 +37,7 @@ __host__ __device__ constexpr int dev_code(int kind, int kernel, int site) {
   return (kind << 16) | (kernel << 8) | site;
 }
 
-// Launch with programmatic stream serialisation (rf_device.cuh: pdl_wait).
+// Launch with programmatic stream serialisation (paged_device.cuh: pdl_wait).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args... args) {
