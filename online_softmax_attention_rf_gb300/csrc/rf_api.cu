@@ -870,6 +870,7 @@ rf_status rf_draft_verify(const void* target, const void* draft, const int32_t* 
   const char* fn = "rf_draft_verify";
   if (B < 0 || S < 1 || V < 1)
     return fail(RF_ERR_INVALID, "%s: bad sizes B=%d S=%d V=%d", fn, B, S, V);
+  if (V > (1 << 30)) return fail(RF_ERR_INVALID, "%s: V > 2^30", fn);
   if (S > rf::kMaxDrafts) return fail(RF_ERR_UNSUPPORTED, "%s: S > %d", fn, rf::kMaxDrafts);
   if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
   if (B == 0) return ok();

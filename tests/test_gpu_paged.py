@@ -401,6 +401,45 @@ def test_attn_paged_layouts(cuda_device, head_major, fused):
     _check_attention(c, o, lse)
 
 
+def test_attn_paged_other_orders_of_the_pool(cuda_device):
+    # pages between the tokens ([page, pages, Hkv, d]), and keys and values of a
+    # page side by side ([pages, 2, page, Hkv, d]); K and V in different orders
+    c = _attention_case([(40, 300), (1, 150)], 8, 2, 128, 16, seed=17)
+    o, lse = _attend(c)
+    _check_attention(c, o, lse)
+    inner = c["kc"].permute(1, 0, 2, 3).contiguous().permute(1, 0, 2, 3)
+    both = torch.stack([c["kc"], c["vc"]], 1)
+    for kc, vc in [(inner, c["vc"]), (both[:, 0], both[:, 1]),
+                   (c["kc"], c["vc"].transpose(1, 2).contiguous().transpose(1, 2))]:
+        o2, lse2 = _attend(dict(c, kc=kc, vc=vc))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert api.device_status() == 0
+
+
+def test_attn_paged_output_on_a_16_byte_boundary(cuda_device):
+    # O takes 32-byte stores only where they are aligned
+    for lengths in ([(70, 300), (1, 150)], [(1, 9000)]):
+        c = _attention_case(lengths, 8, 2, 64, 16, seed=18)
+        o, lse = _attend(c)
+        room = torch.zeros(o.numel() + 16, dtype=o.dtype, device="cuda")
+        odd = room[8:8 + o.numel()].view(o.shape)
+        assert odd.data_ptr() % 32 == 16
+        _attend(c, out=odd)
+        assert torch.equal(o, odd) and (room[:8] == 0).all() and (room[-8:] == 0).all()
+
+
+def test_attn_paged_rows_before_the_first_sequence(cuda_device):
+    # cu_q may start above 0
+    c = _attention_case([(3, 40), (1, 9)], 4, 2, 64, 8, seed=19, pad=5)
+    shifted = dict(c, cu=[x + 5 for x in c["cu"]],
+                   q=torch.cat([torch.full_like(c["q"][:5], float("nan")), c["q"][:4]]))
+    o, lse = _attend(c)
+    out = torch.full_like(o, 3.0)
+    o2, lse2 = _attend(shifted, out=out)
+    assert torch.equal(o2[5:], o[:4]) and torch.equal(lse2[5:], lse[:4]) and (o2[:5] == 3).all()
+    _check_attention(c, o, lse)
+
+
 def test_attn_paged_leaves_padded_rows(cuda_device):
     c = _attention_case([(3, 40), (1, 9)], 4, 2, 64, 8, seed=7, pad=5)
     o = torch.full((c["T"], 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")

@@ -150,6 +150,7 @@ VERIFY = ["target", "draft", "tokens", "u", "expo", "n_draft", "temperature", "B
 @pytest.mark.parametrize("kw,expect", [
     (dict(B=-1), api.RF_ERR_INVALID), (dict(S=0), api.RF_ERR_INVALID),
     (dict(S=65), api.RF_ERR_UNSUPPORTED), (dict(V=0), api.RF_ERR_INVALID),
+    (dict(V=(1 << 30) + 1), api.RF_ERR_INVALID), (dict(B=(1 << 20) + 1), api.RF_ERR_INVALID),
     (dict(dt=3), api.RF_ERR_INVALID), (dict(target=None), api.RF_ERR_INVALID),
     (dict(tokens=None), api.RF_ERR_INVALID), (dict(u=None), api.RF_ERR_INVALID),
     (dict(expo=None), api.RF_ERR_INVALID), (dict(out=None), api.RF_ERR_INVALID),
