@@ -249,22 +249,22 @@ __device__ __forceinline__ void take(Best& a, float score, int idx) {
   if (score > a.score || (score == a.score && idx < a.idx)) a = Best{score, idx};
 }
 
-// Four consecutive numbers.
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
+// W consecutive numbers, loaded as one or two words.
+template <typename T, int W>
+struct alignas(W * sizeof(T) < 16 ? W * sizeof(T) : 16) Pack {
+  T x[W];
+};
 
-// One cluster per sequence. kVec: every row starts on a boundary of four
-// numbers (V a multiple of 4 and aligned tensors): loads of four numbers,
-// otherwise of one.
-template <typename T, bool kVec, int kThreads>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+// One cluster per sequence. W: the numbers a thread loads at a time from each
+// row; every row starts on a boundary of W numbers. Bound by the latency of its
+// few rounds of loads: 23 us alone on cold caches for 64 sequences at
+// V = 131072, 35 % of the memory's rate; it reads 67 MB, part of it from L2.
+// The exponentials prefetched into L2 under stats_kernel bought nothing (47.9
+// us against 46.7 for both kernels): they take their bandwidth from it. Two
+// register sets against the compiler's unrolled loads: 12.3 us against 13.7 for
+// 16 sequences at an odd V = 50001.
+template <typename T, int W, int kThreads>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1024 / kThreads)
     choose_kernel(const VerifyArgs a, const Stat* __restrict__ stats, int nsplit) {
   constexpr int kWarps = kThreads / 32;
   __shared__ float rm[2 * kMaxDrafts + 1], rl[2 * kMaxDrafts + 1];
@@ -281,7 +281,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   cluster.barrier_arrive();  // waited for before any CTA's memory is written by another
   const T* target = static_cast<const T*>(a.target) + int64_t(b) * (a.S + 1) * a.V;
   const T* draft = static_cast<const T*>(a.draft) + (a.draft != nullptr ? int64_t(b) * a.S * a.V : 0);
-  pdl_wait();
+  // stats_kernel lets this grid start only when all of its CTAs have seen the
+  // work before it complete, so the call's inputs can be read now; what
+  // stats_kernel writes has to be waited for, and this grid writes nothing before.
   bool greedy;
   const float c = log2e_over(a.temperature, b, &greedy);
   const int nd = drafts_of(a, b);
@@ -298,6 +300,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       if (a.draft != nullptr) xd = to_f32(draft[int64_t(tid) * a.V + x]);
     }
   }
+  pdl_wait();
   // the row statistics, joined from their pieces in a fixed order
   for (int r = warp; r < per; r += kWarps) {
     const bool is_draft = r > a.S;
@@ -371,39 +374,44 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       };
       auto p_of = [&](float x) { return ex2_approx(fmaf(x - pm, c, pk)); };
       auto q_of = [&](float x) { return ex2_approx(fmaf(x - qm, c, qk)); };
-      constexpr int kStep = kCluster * kThreads * (kVec ? 4 : 1);
-      const int first = (rank * kThreads + tid) * (kVec ? 4 : 1);
-      if (has_q && pass == 0) {
-        if constexpr (kVec) {
-#pragma unroll 4
-          for (int v = first; v < a.V; v += kStep) {
-            float xp[4], xq[4], ev[4];
-            load4(pt + v, xp);
-            load4(qt + v, xq);
-            load4(e + v, ev);
+      // two register sets in turn: one loads while the other is worked on
+      constexpr int U = W == 1 ? 4 : 1;
+      constexpr int kStep = kCluster * kThreads * W;
+      const bool two = has_q && pass == 0;
+      struct Set {
+        Pack<T, W> p[U], q[U];
+        Pack<float, W> e[U];
+      };
+      auto load = [&](Set& k, int v) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) one(p_of(xp[i]) - q_of(xq[i]), ev[i], v + i);
-          }
-        } else {
-#pragma unroll 4
-          for (int v = first; v < a.V; v += kStep)
-            one(p_of(to_f32(pt[v])) - q_of(to_f32(qt[v])), e[v], v);
+        for (int j = 0; j < U; ++j, v += kStep) {
+          if (v >= a.V) break;
+          k.p[j] = *reinterpret_cast<const Pack<T, W>*>(pt + v);
+          if (two) k.q[j] = *reinterpret_cast<const Pack<T, W>*>(qt + v);
+          k.e[j] = *reinterpret_cast<const Pack<float, W>*>(e + v);
         }
-      } else {
-        if constexpr (kVec) {
-#pragma unroll 4
-          for (int v = first; v < a.V; v += kStep) {
-            float xp[4], ev[4];
-            load4(pt + v, xp);
-            load4(e + v, ev);
+      };
+      auto work = [&](const Set& k, int v) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) one(v + i == skip ? 0.f : p_of(xp[i]), ev[i], v + i);
+        for (int j = 0; j < U; ++j, v += kStep) {
+          if (v >= a.V) break;
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const float w = v + i == skip ? 0.f : p_of(to_f32(k.p[j].x[i]));
+            one(two ? w - q_of(to_f32(k.q[j].x[i])) : w, k.e[j].x[i], v + i);
           }
-        } else {
-#pragma unroll 4
-          for (int v = first; v < a.V; v += kStep)
-            one(v == skip ? 0.f : p_of(to_f32(pt[v])), e[v], v);
         }
+      };
+      Set ka, kb;
+      int v = (rank * kThreads + tid) * W;
+      load(ka, v);
+      while (v < a.V) {
+        load(kb, v + U * kStep);
+        work(ka, v);
+        v += U * kStep;
+        load(ka, v + U * kStep);
+        work(kb, v);
+        v += U * kStep;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
@@ -441,12 +449,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
         i < at ? a.tokens[int64_t(b) * a.S + i] : i == at ? chosen : -1;
 }
 
-template <typename T, int kThreads>
-cudaError_t launch_choose(const VerifyArgs& a, const Stat* stats, int nsplit, bool vec,
-                          cudaStream_t s) {
-  return launch_pdl(vec ? choose_kernel<T, true, kThreads> : choose_kernel<T, false, kThreads>,
-                    dim3(static_cast<unsigned>(a.B) * kCluster), dim3(kThreads), 0, s, a, stats,
-                    nsplit);
+template <typename T, int W>
+cudaError_t launch_choose(const VerifyArgs& a, const Stat* stats, int nsplit, cudaStream_t s) {
+  // as many threads a CTA as keep all clusters resident at once: with few
+  // sequences a sweep over the vocabulary then takes few rounds of loads
+  // (one sequence, V = 32000: 8.3 us at 512 threads, 11.4 at 256), with many
+  // there is no second wave (64 sequences, V = 131072: 30 us and 24)
+  const int ctas = a.B * kCluster;
+  const bool few = ctas <= 2 * 152;
+  return launch_pdl(few ? choose_kernel<T, W, 512> : choose_kernel<T, W, 256>, dim3(ctas),
+                    dim3(few ? 512 : 256), 0, s, a, stats, nsplit);
 }
 
 template <typename T>
@@ -467,15 +479,14 @@ cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
                              dim3(kStatThreads), 0, s, a, stats, ns, piece);
   if (e != cudaSuccess) return e;
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
-  const bool vec = a.V % 4 == 0 && at(a.target) % (4 * sizeof(T)) == 0 &&
-                   at(a.draft) % (4 * sizeof(T)) == 0 && at(a.expo) % 16 == 0;
-  // as many threads a CTA as keep all clusters resident at once: with few
-  // sequences a sweep over the vocabulary then takes few rounds of loads
-  // (one sequence, V = 32000: 8.3 us at 512 threads, 11.4 at 256), with many
-  // there is no second wave (64 sequences, V = 131072: 30 us and 24)
-  const int ctas = a.B * kCluster;
-  if (ctas <= 2 * 152) return launch_choose<T, 512>(a, stats, ns, vec, s);
-  return launch_choose<T, 256>(a, stats, ns, vec, s);
+  const auto fits = [&](int w) {
+    return a.V % w == 0 && at(a.target) % (w * sizeof(T)) == 0 &&
+           at(a.draft) % (w * sizeof(T)) == 0 && at(a.expo) % 16 == 0;
+  };
+  if constexpr (sizeof(T) == 2)
+    if (fits(8)) return launch_choose<T, 8>(a, stats, ns, s);
+  if (fits(4)) return launch_choose<T, 4>(a, stats, ns, s);
+  return launch_choose<T, 1>(a, stats, ns, s);
 }
 
 }  // namespace
