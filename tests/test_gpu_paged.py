@@ -393,6 +393,32 @@ def test_attn_paged_rising_scores(cuda_device):
     _check_attention(c, o, lse)
 
 
+@pytest.mark.parametrize("H,Hkv,nq", [(4, 4, 1), (4, 4, 32), (4, 4, 33), (15, 3, 6), (15, 3, 7),
+                                      (32, 1, 1), (33, 1, 1), (64, 2, 1), (28, 4, 4), (28, 4, 5)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attn_paged_few_rows_of_small_heads(cuda_device, H, Hkv, nq, causal):
+    # on both sides of 32 packed rows; whole items, items in parts, tiles whose
+    # last keys miss some of the quarters
+    for kv in ([nq, 40, 129, 700], [1037, 1, 33, 97, 650], [20011]):
+        lengths = [(min(nq, x), x) for x in kv]
+        c = _attention_case(lengths, H, Hkv, 64, 16, seed=nq + len(kv), causal=causal)
+        o, lse = _attend(c)
+        _check_attention(c, o, lse)
+    assert api.device_status() == 0
+
+
+def test_attn_paged_small_heads_in_mixed_batches(cuda_device):
+    # short single tokens, long ones and chunks in turn on one SM
+    lengths = [(1, 90), (1, 5000), (200, 900), (1, 2000), (3, 2500), (1, 100), (1, 1500), (64, 1000)] * 3
+    for H, Hkv in ((8, 8), (16, 4)):
+        c = _attention_case(lengths, H, Hkv, 64, 16, seed=23)
+        o, lse = _attend(c)
+        _check_attention(c, o, lse)
+        o2, lse2 = _attend(c)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert api.device_status() == 0
+
+
 @pytest.mark.parametrize("head_major,fused", [(True, False), (False, True), (True, True)])
 def test_attn_paged_layouts(cuda_device, head_major, fused):
     c = _attention_case([(65, 200), (1, 333)], 8, 2, 64, 16, seed=6, head_major=head_major,
