@@ -659,16 +659,18 @@ rf_status rf_attn_paged(const void *q, int64_t q_stride, const void *k_cache,
  *           certainty (copied ones): q_i is 1 at x_i;
  *  tokens : int32 [B, S]; u: float [B, S] in [0, 1); expo: float [B, V] > 0;
  *  n_draft: int32 [B] in [0, S], or NULL (all S);
- *  temperature: float [B], or NULL (1); not above 0: greedy (draft i is accepted when it
- *           is the target's largest logit, lowest index first);
+ *  temperature: float [B], finite, or NULL (1); not above 0: greedy (draft i
+ *           is accepted when it is the target's largest logit, lowest index
+ *           first);
  *  out    : int32 [B, S + 1]: the accepted drafts, the drawn token, then -1;
  *  n_accepted: int32 [B].
  *  ws     : device workspace, 16-byte aligned, ws_bytes >=
  *           rf_draft_verify_workspace_bytes(B, S).
- * 0 <= B <= 2^20, 1 <= S <= 64, 1 <= V <= 2^30. A token outside [0, V) is refused, and a row
- * that gives no probabilities (all -inf, or a NaN or +inf in it) refuses its
- * draft and draws -1; both are reported through rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED
- * (S > 64), RF_ERR_CUDA.
+ * 0 <= B <= 2^20, 1 <= S <= 64, 1 <= V <= 2^30. A token outside [0, V) is
+ * refused, and a row that gives no probabilities (all -inf, or a NaN or +inf in
+ * it) refuses its draft and draws -1; both are reported through
+ * rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED (S > 64),
+ * RF_ERR_CUDA.
  */
 size_t rf_draft_verify_workspace_bytes(int B, int S);
 rf_status rf_draft_verify(const void *target, const void *draft, const int32_t *tokens,

@@ -6,6 +6,11 @@ and the current CUDA stream to the C entry point of the same name, and turns
 a non-OK status into ``RFError``. Every step of the computation runs in the
 library's kernels; nothing here computes, and there is no CPU fallback -- if
 the library is missing, every call raises.
+
+The calls of a serving loop (``kv_append_paged``, ``attn_paged``,
+``draft_verify``) go through a native module (csrc/serving_binding.cpp), which
+does the same checks without Python's time for them; arguments that it does not
+accept come back here for the error that names them.
 """
 
 import ctypes
@@ -763,7 +768,8 @@ def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse
     """rf_attn_paged: q [T, H, d] bf16 (a strided view of a fused projection
     fits), k_cache, v_cache [pages, page, Hkv, d] (any strides with d
     contiguous), block_table int32 [B, max_pages], plan a ``PagedPlan`` of the
-    step -> (o [T, H, d], lse float32 [T, H] or None)."""
+    step -> (o [T, H, d], lse float32 [T, H] or None). Rows outside every
+    sequence are left as they are (uninitialised without `out`)."""
     if workspace is None:
         workspace = attn_paged_workspace(q.shape[-1], q.device)
     r = _serving().attn_paged(q, k_cache, v_cache, block_table, plan.buf, plan.B, plan.T, plan.H,

@@ -33,6 +33,13 @@
 // Every wait is bounded; on expiry the kernel records a status code and the CTA
 // unwinds, the five warps of a group together at a reducing named barrier.
 //
+// Measured: decode of 8 sequences x 8 key heads x 65536 keys 6.72 TB/s of cache
+// at d = 128 (pages of 16 to 128) and 5.24 at d = 64, memory and the chain
+// scores -> softmax -> P.V of a one-tile step bounding them; a chunk of 2048
+// tokens at 32768 keys, 64 heads, d = 128, 1.43 to 1.53 ms (1490 to 1396
+// TFLOP/s), bound as attn_tc.cu is; one token over 515 keys 12.7 us, launches
+// and dependent loads.
+//
 // P is rounded to bf16 for the tensor cores (scores, maxima, sums and
 // accumulators stay in float32): half a step, 2^-8, of each weight. The row
 // sum takes the unrounded weights.

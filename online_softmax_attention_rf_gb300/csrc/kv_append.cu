@@ -13,7 +13,7 @@
 // it, if enough reads are in flight and the arithmetic stays out of the way. A
 // producer lane keeps a ring of 16 KB stages filled with bulk copies (the heads
 // of a token lie back to back), and four warps take rows from it with packed
-// float32 arithmetic: 59 us for 8192 tokens of 80 heads of 128, 5.75 TB/s, which
+// float32 arithmetic: 56 us for 8192 tokens of 80 heads of 128, 6.04 TB/s, which
 // is what the same kernel takes to copy the rows. (Rows loaded into registers by
 // a block a token: 80 us, the reads in flight and the issue slots both short;
 // eight consumer warps, whose registers spill at three CTAs an SM: 79 us, and 64

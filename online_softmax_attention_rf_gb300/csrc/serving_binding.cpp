@@ -151,7 +151,9 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       new_out = fresh({T, H, d}, dt, dev);
       out = &new_out;
     }
-    if (lse == nullptr && PyObject_IsTrue(a[14]) == 1) {
+    const int with_lse = PyObject_IsTrue(a[14]);
+    need(with_lse >= 0);
+    if (lse == nullptr && with_lse) {
       new_lse = fresh({T, H}, at::kFloat, dev);
       lse = &new_lse;
     }
