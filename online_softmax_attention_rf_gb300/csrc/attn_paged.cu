@@ -34,9 +34,9 @@
 // unwinds, the five warps of a group together at a reducing named barrier.
 //
 // Measured: decode of 8 sequences x 8 key heads x 65536 keys 6.72 TB/s of cache
-// at d = 128 (pages of 16 to 128) and 5.24 at d = 64, memory and the chain
+// at d = 128 (pages of 16 to 128) and 5.39 at d = 64, memory and the chain
 // scores -> softmax -> P.V of a one-tile step bounding them; a chunk of 2048
-// tokens at 32768 keys, 64 heads, d = 128, 1.43 to 1.53 ms (1490 to 1396
+// tokens at 32768 keys, 64 heads, d = 128, 1.41 to 1.50 ms (1510 to 1420
 // TFLOP/s), bound as attn_tc.cu is; one token over 515 keys 12.7 us, launches
 // and dependent loads.
 //
@@ -67,9 +67,17 @@ constexpr int kChunk = 16384;              // one 128-row x 64-column bf16 swizz
 template <int D>
 struct Layout {
   static constexpr int kTileBytes = kBM * D * 2;
-  // as many as fit (d = 64, 8 x 8 heads of 65536 keys: 4.61 TB/s with 8 slots,
-  // 5.13 with 10, 5.24 with 12)
-  static constexpr int kStages = (D == 128) ? 5 : 12;
+  // Two rings, of K and of V tiles, as many slots as fit. One ring of five for
+  // both (d = 128) was not sound: behind a K producer that is late, a table
+  // entry coming from memory, the V producer would wait for a phase two ahead of
+  // the slot's barrier, and the parity of that wait passes at once
+  // (tests/test_paged_protocol.py). With a wait for the K tile it cost 2 % of a
+  // chunk; 2 + 3 slots: 2048 tokens at 32768 keys 1.41 ms, 3 + 2: 1.45, one ring
+  // of 5: 1.43. d = 64, 8 x 8 heads of 65536 keys: 6 + 6 slots 5.39 TB/s, 4 + 8
+  // 5.22, 5 + 7 5.19, 4 + 4 5.09.
+  static constexpr int kSlotsK = (D == 128) ? 2 : 6;
+  static constexpr int kSlotsV = (D == 128) ? 3 : 6;
+  static constexpr int kStages = kSlotsK + kSlotsV;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kOffQ + 2 * kTileBytes;
   static constexpr int kOffBar = kOffKV + kStages * kTileBytes;
@@ -79,6 +87,11 @@ struct Layout {
   static constexpr int kBytes = kOffXch + kXchBytes + 1024;  // + alignment slack
   static constexpr uint32_t kTmemS = 0;
   static constexpr uint32_t kTmemO = 2 * kBN;
+  // slot and use of a step's K and V tiles (n: the steps before it in the span)
+  __device__ static __forceinline__ int slot_k(int n) { return n % kSlotsK; }
+  __device__ static __forceinline__ int slot_v(int n) { return kSlotsK + n % kSlotsV; }
+  __device__ static __forceinline__ int use_k(int n) { return n / kSlotsK; }
+  __device__ static __forceinline__ int use_v(int n) { return n / kSlotsV; }
   __host__ __device__ static constexpr uint32_t tmem_p(int t) {
     return D == 128 ? kTmemS + t * kBN : kTmemO + 2 * D + t * 64;
   }
@@ -440,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_key = lane % boxes * p.box, my_chunk = lane / boxes;
     const bool has_box = my_chunk < D / 64;
     unsigned char* const my_dst = smem + L::kOffKV + my_chunk * kChunk + my_key * 128;
-    int seq = is_k ? 0 : 1;     // K/V sequence number of the next copy
+    int step = 0;               // steps copied
     int q_loads = 0;
     bool ok = true;
     // this lane's page of step u of a segment and the box's first row in it
@@ -489,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         id = page_of(s, s.kb, in_page);
       }
       bool q_due = is_k && s.ke > s.kb;
-      for (int u = s.kb; ok && u < s.ke; ++u, seq += 2) {
+      for (int u = s.kb; ok && u < s.ke; ++u, ++step) {
         int in_next = 0;
         const int id_next = page_of(s, u + 1, in_next);
         const bool mine = has_box && u * kBN + my_key < s.kv;
@@ -497,10 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           record_status(p.status, dev_code(kDevBadList, kKerPaged, 3));
           id = p.num_pages;  // past the pool: the copy fills with zeros
         }
-        const int slot = seq % NS;
+        const int slot = is_k ? L::slot_k(step) : L::slot_v(step);
         if (lane == 0) {
           const int n_box = min(boxes, (s.kv - u * kBN + p.box - 1) / p.box);
-          ok = RF_WAIT(kv_empty[slot], ((seq / NS) & 1) ^ 1, 10);
+          ok = RF_WAIT(kv_empty[slot], ((is_k ? L::use_k(step) : L::use_v(step)) & 1) ^ 1, 10);
           if (ok) mbar_arrive_expect_tx(&bar.kv_full[slot], n_box * p.box * D * 2);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -539,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // never leave with copies in flight: this warp's last copies, one per slot
     if (lane == 0) {
-      const int end = is_k ? seq : seq - 1;  // the last copy into each slot: from end - NS on
-      for (int sq = seq - 2; sq >= 0 && sq >= end - NS; sq -= 2)
-        mbar_wait(&bar.kv_full[sq % NS], (sq / NS) & 1, p.status,
+      for (int n = step - 1; n >= max(0, step - (is_k ? L::kSlotsK : L::kSlotsV)); --n)
+        mbar_wait(&bar.kv_full[is_k ? L::slot_k(n) : L::slot_v(n)],
+                  (is_k ? L::use_k(n) : L::use_v(n)) & 1, p.status,
                   dev_code(kDevTimeout, kKerPaged, 11), nullptr);
       for (int qs = max(0, q_loads - 2); qs < q_loads; ++qs)
         mbar_wait(&bar.q_full[qs & 1], (qs >> 1) & 1, p.status,
@@ -558,14 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t mm_s = tmem + L::kTmemS + t * kBN;
     const uint32_t mm_o = tmem + L::kTmemO + t * D;
     const uint32_t mm_p = tmem + L::tmem_p(t);
-    int seq = 0;              // K/V sequence number of the next step
-    int vseq = 0;             // V tile of the step whose QK was issued last
+    int step = 0;             // steps of the span passed
+    int vstep = 0;            // the step whose QK was issued last
     int n_iss = 0, n_seg = 0; // steps of the started segment issued so far, and all of them
     int started = -1;         // last segment whose Q was waited for
     bool issued_any = false;
     // the segment being started (lane 0), this group's Q tile in it
     int a_kb = 0, a_ke = 0, a_mode = 0, u_next = 0, q_slot = 0;
-#define RF_SLOT(sq) (static_cast<uint64_t>((((sq) % NS) * L::kTileBytes) >> 4))
+#define RF_SLOT(slot) (static_cast<uint64_t>(((slot) * L::kTileBytes) >> 4))
 #define RF_LOCK() issue_lock(&bar.issue_lock, p.status, dev_code(kDevTimeout, kKerPaged, 23), abort_flag)
     auto needs = [&](int u) {
       if (a_mode == kPair) return u < a_kb + n_seg;
@@ -574,47 +587,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // The next step this group takes; steps that only the other group takes are
     // released (both slots) once they have landed. False at the segment's end.
-    auto advance = [&](int& kseq) -> bool {
+    auto advance = [&](int& k_step) -> bool {
       while (u_next < a_ke) {
         const int u = u_next++;
-        const int ks = seq;
-        seq += 2;
+        const int n = step++;
         if (needs(u)) {
-          kseq = ks;
+          k_step = n;
           return true;
         }
-        for (int e = 0; e < 2; ++e) {
-          if (!(ok = RF_WAIT(kv_full[(ks + e) % NS], ((ks + e) / NS) & 1, 20))) return false;
-          mbar_arrive(&bar.kv_empty[(ks + e) % NS]);
-        }
+        if (!(ok = RF_WAIT(kv_full[L::slot_k(n)], L::use_k(n) & 1, 20))) return false;
+        mbar_arrive(&bar.kv_empty[L::slot_k(n)]);
+        if (!(ok = RF_WAIT(kv_full[L::slot_v(n)], L::use_v(n) & 1, 20))) return false;
+        mbar_arrive(&bar.kv_empty[L::slot_v(n)]);
       }
       return false;
     };
-    auto next_k = [&](int& kseq) -> bool {
-      if (!advance(kseq)) return false;
-      return (ok = RF_WAIT(kv_full[kseq % NS], (kseq / NS) & 1, 21));
+    auto next_k = [&](int& k_step) -> bool {
+      if (!advance(k_step)) return false;
+      return (ok = RF_WAIT(kv_full[L::slot_k(k_step)], L::use_k(k_step) & 1, 21));
     };
     // Whether everything up to the K tile of this group's next step has landed.
     // Between this group's steps lies at most one of the other's (a split
     // item), so each barrier tested is at most one phase behind.
     auto landed = [&]() -> bool {
-      int sq = seq;
-      for (int u = u_next; u < a_ke; ++u, sq += 2) {
-        const bool k_in = mbar_test_wait(&bar.kv_full[sq % NS], (sq / NS) & 1);
+      int n = step;
+      for (int u = u_next; u < a_ke; ++u, ++n) {
+        const bool k_in = mbar_test_wait(&bar.kv_full[L::slot_k(n)], L::use_k(n) & 1);
         if (!k_in || needs(u)) return k_in;
-        if (!mbar_test_wait(&bar.kv_full[(sq + 1) % NS], ((sq + 1) / NS) & 1)) return false;
+        if (!mbar_test_wait(&bar.kv_full[L::slot_v(n)], L::use_v(n) & 1)) return false;
       }
       return false;
     };
-    auto qk_commits = [&](int kseq) {
+    auto qk_commits = [&](int k_step) {
       mma_commit(&bar.s_full[t]);
-      mma_commit(&bar.kv_empty[kseq % NS]);
+      mma_commit(&bar.kv_empty[L::slot_k(k_step)]);
       if (++n_iss == n_seg) mma_commit(&bar.q_empty[q_slot]);  // the segment's last read of Q
-      vseq = kseq + 1;
+      vstep = k_step;
     };
-    auto issue_s = [&](int kseq) {
+    auto issue_s = [&](int k_step) {
       issue_qk<D>(mm_s, q_desc0 + static_cast<uint64_t>((q_slot * L::kTileBytes) >> 4),
-                  k_desc0 + RF_SLOT(kseq));
+                  k_desc0 + RF_SLOT(L::slot_k(k_step)));
     };
     // Segment k (lane 0): wait for its Q tiles, release the ones this group does
     // not read, and issue the first QK; without steps of its own, release all.
@@ -638,17 +650,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive(&bar.q_empty[b]);
       }
-      int kseq;
+      int k_step;
       if (n_seg == 0) {
-        advance(kseq);  // releases every step; returns false
+        advance(k_step);  // releases every step; returns false
         return;
       }
-      if (next_k(kseq) && (ok = RF_LOCK())) {
+      if (next_k(k_step) && (ok = RF_LOCK())) {
         tc_fence_after_sync();
-        issue_s(kseq);
+        issue_s(k_step);
         issue_unlock(&bar.issue_lock);
         issued_any = true;
-        qk_commits(kseq);
+        qk_commits(k_step);
       }
     };
 
@@ -675,16 +687,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // end, and see whether the next step's K tile is there. If it is, its
         // Q K^T goes out in one block with this step's P.V. If it is not (memory
         // bounds a decode step), P.V goes first: it frees V_u's slot, without
-        // which the ring of five slots could not run ahead of the two groups.
+        // which the rings could not run ahead of the two groups.
         const bool last = jj + 1 == n;
         const int u = kb + (mode == kSplit ? 2 * jj + t : jj);
         int k2 = 0;
         bool fast = false;
-        if (lane == 0 && ok) ok = RF_WAIT(kv_full[vseq % NS], (vseq / NS) & 1, 24);
+        if (lane == 0 && ok) ok = RF_WAIT(kv_full[L::slot_v(vstep)], L::use_v(vstep) & 1, 24);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         const int rows = kv - u * kBN;
         if (ok && rows < kBN) {
-          const int vs = __shfl_sync(0xffffffffu, vseq, 0) % NS;
+          const int vs = L::slot_v(__shfl_sync(0xffffffffu, vstep, 0));
           unsigned char* v = smem + L::kOffKV + vs * L::kTileBytes;
           for (int i = rows * 8 + lane; i < kBN * 8; i += 32)
 #pragma unroll
@@ -702,12 +714,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && (ok = RF_LOCK())) {
           tc_fence_after_sync();
-          issue_pv<D>(mm_o, mm_p, v_desc0 + RF_SLOT(vseq), jj > 0);
+          const int v_slot = L::slot_v(vstep);
+          issue_pv<D>(mm_o, mm_p, v_desc0 + RF_SLOT(v_slot), jj > 0);
           if (fast) issue_s(k2);
           issue_unlock(&bar.issue_lock);
-          const int v_done = vseq;
           if (fast) qk_commits(k2);
-          mma_commit(&bar.kv_empty[v_done % NS]);
+          mma_commit(&bar.kv_empty[v_slot]);
           if (last) {
             mma_commit(&bar.o_done[t]);
           } else if (!fast && next_k(k2) && (ok = RF_LOCK())) {
@@ -1084,7 +1096,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // A 4-D bf16 map, 128-byte swizzle; extents, strides and box of dimensions
 // 1..3 in elements (dimension 0: D contiguous elements, boxes of 64). L2 fetches
 // what a row holds: 256 bytes at d = 64 would bring in the neighbouring head,
-// which another CTA reads much later (4.02 TB/s of cache instead of 5.24).
+// which another CTA reads much later (4.02 TB/s of cache instead of 5.24, one ring of 12 slots).
 bool make_map(CUtensorMap* m, const void* base, int D, const int64_t (&ext)[3],
               const int64_t (&stride)[3], const int (&box)[3]) {
   auto fn = encode_fn();
