@@ -606,15 +606,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!advance(k_step)) return false;
       return (ok = RF_WAIT(kv_full[L::slot_k(k_step)], L::use_k(k_step) & 1, 21));
     };
-    // Whether everything up to the K tile of this group's next step has landed.
-    // Between this group's steps lies at most one of the other's (a split
-    // item), so each barrier tested is at most one phase behind.
-    auto landed = [&]() -> bool {
-      int n = step;
-      for (int u = u_next; u < a_ke; ++u, ++n) {
-        const bool k_in = mbar_test_wait(&bar.kv_full[L::slot_k(n)], L::use_k(n) & 1);
-        if (!k_in || needs(u)) return k_in;
-        if (!mbar_test_wait(&bar.kv_full[L::slot_v(n)], L::use_v(n) & 1)) return false;
+    // next_k without waiting: whether everything up to the K tile of this group's
+    // next step has landed. Between this group's steps lies at most one of the
+    // other's (a split item), so each barrier tested is at most one phase behind.
+    auto try_k = [&](int& k_step) -> bool {
+      while (u_next < a_ke) {
+        if (!mbar_test_wait(&bar.kv_full[L::slot_k(step)], L::use_k(step) & 1)) return false;
+        if (!needs(u_next)) {
+          if (!mbar_test_wait(&bar.kv_full[L::slot_v(step)], L::use_v(step) & 1)) return false;
+          mbar_arrive(&bar.kv_empty[L::slot_k(step)]);
+          mbar_arrive(&bar.kv_empty[L::slot_v(step)]);
+        }
+        k_step = step++;
+        if (needs(u_next++)) return true;
       }
       return false;
     };
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0 && ok && !last && landed()) fast = next_k(k2);
+        if (lane == 0 && ok && !last) fast = try_k(k2);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         // P_t is in tensor memory
         if (group_sync_or(t, !ok)) {

@@ -208,18 +208,23 @@ def _run(segs, rings, rng, planted=None, p_resc=0.3):
                 yield wait(("kv_full", slot), use)
             return n
 
-        def landed():
-            a, n = st["seg"], st["n"]
-            for u in range(st["u"], a["ke"]):
-                slot, use = slot_k(n)
-                k_in = B["kv_full", slot].done(use)
-                if not k_in or _needs(a, t, u):
-                    return k_in
-                slot, use = slot_v(n)
-                if not B["kv_full", slot].done(use):
-                    return False
-                n += 1
-            return False
+        def try_k():
+            a = st["seg"]
+            while st["u"] < a["ke"]:
+                n, mine = st["n"], _needs(a, t, st["u"])
+                k, v = slot_k(n), slot_v(n)
+                if not B["kv_full", k[0]].done(k[1]):
+                    return None
+                if not mine:
+                    if not B["kv_full", v[0]].done(v[1]):
+                        return None
+                    B["kv_empty", k[0]].arrive()
+                    B["kv_empty", v[0]].arrive()
+                st["n"] += 1
+                st["u"] += 1
+                if mine:
+                    return n
+            return None
 
         def qk(n):
             k, jj = st["started"], st["n_iss"]
@@ -270,8 +275,8 @@ def _run(segs, rings, rng, planted=None, p_resc=0.3):
                 fast = None
                 v, use = slot_v(st["v"])
                 yield wait(("kv_full", v), use)
-                if not last and landed():
-                    fast = yield from next_k()
+                if not last:
+                    fast = try_k()
                 B["group", t].arrive()
                 yield wait(("group", t), groups)
                 groups += 1
