@@ -87,11 +87,6 @@ struct Layout {
   static constexpr int kBytes = kOffXch + kXchBytes + 1024;  // + alignment slack
   static constexpr uint32_t kTmemS = 0;
   static constexpr uint32_t kTmemO = 2 * kBN;
-  // slot and use of a step's K and V tiles (n: the steps before it in the span)
-  __device__ static __forceinline__ int slot_k(int n) { return n % kSlotsK; }
-  __device__ static __forceinline__ int slot_v(int n) { return kSlotsK + n % kSlotsV; }
-  __device__ static __forceinline__ int use_k(int n) { return n / kSlotsK; }
-  __device__ static __forceinline__ int use_v(int n) { return n / kSlotsV; }
   __host__ __device__ static constexpr uint32_t tmem_p(int t) {
     return D == 128 ? kTmemS + t * kBN : kTmemO + 2 * D + t * 64;
   }
@@ -115,6 +110,25 @@ struct Seg {
   int pad[3];
 };
 static_assert(sizeof(Seg) == 64, "descriptor size");
+
+// The slots of a step's K and V tiles and the parities of their uses, carried
+// from step to step: the division that slot n % kSlotsK asks for is on the
+// issuers' path.
+template <int D>
+struct Slots {
+  int k = 0, v = Layout<D>::kSlotsK;
+  uint32_t kp = 0, vp = 0;
+  __device__ __forceinline__ void next() {
+    if (++k == Layout<D>::kSlotsK) {
+      k = 0;
+      kp ^= 1;
+    }
+    if (++v == Layout<D>::kStages) {
+      v = Layout<D>::kSlotsK;
+      vp ^= 1;
+    }
+  }
+};
 
 struct Bars {
   Seg seg[kSegs];
@@ -454,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool has_box = my_chunk < D / 64;
     unsigned char* const my_dst = smem + L::kOffKV + my_chunk * kChunk + my_key * 128;
     int step = 0;               // steps copied
+    Slots<D> at;
     int q_loads = 0;
     bool ok = true;
     // this lane's page of step u of a segment and the box's first row in it
@@ -502,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         id = page_of(s, s.kb, in_page);
       }
       bool q_due = is_k && s.ke > s.kb;
-      for (int u = s.kb; ok && u < s.ke; ++u, ++step) {
+      for (int u = s.kb; ok && u < s.ke; ++u, ++step, at.next()) {
         int in_next = 0;
         const int id_next = page_of(s, u + 1, in_next);
         const bool mine = has_box && u * kBN + my_key < s.kv;
@@ -510,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           record_status(p.status, dev_code(kDevBadList, kKerPaged, 3));
           id = p.num_pages;  // past the pool: the copy fills with zeros
         }
-        const int slot = is_k ? L::slot_k(step) : L::slot_v(step);
+        const int slot = is_k ? at.k : at.v;
         if (lane == 0) {
           const int n_box = min(boxes, (s.kv - u * kBN + p.box - 1) / p.box);
-          ok = RF_WAIT(kv_empty[slot], ((is_k ? L::use_k(step) : L::use_v(step)) & 1) ^ 1, 10);
+          ok = RF_WAIT(kv_empty[slot], (is_k ? at.kp : at.vp) ^ 1, 10);
           if (ok) mbar_arrive_expect_tx(&bar.kv_full[slot], n_box * p.box * D * 2);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -552,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // never leave with copies in flight: this warp's last copies, one per slot
     if (lane == 0) {
-      for (int n = step - 1; n >= max(0, step - (is_k ? L::kSlotsK : L::kSlotsV)); --n)
-        mbar_wait(&bar.kv_full[is_k ? L::slot_k(n) : L::slot_v(n)],
-                  (is_k ? L::use_k(n) : L::use_v(n)) & 1, p.status,
+      const int ring = is_k ? L::kSlotsK : L::kSlotsV;
+      for (int n = max(0, step - ring); n < step; ++n)
+        mbar_wait(&bar.kv_full[(is_k ? 0 : L::kSlotsK) + n % ring], (n / ring) & 1, p.status,
                   dev_code(kDevTimeout, kKerPaged, 11), nullptr);
       for (int qs = max(0, q_loads - 2); qs < q_loads; ++qs)
         mbar_wait(&bar.q_full[qs & 1], (qs >> 1) & 1, p.status,
@@ -571,8 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t mm_s = tmem + L::kTmemS + t * kBN;
     const uint32_t mm_o = tmem + L::kTmemO + t * D;
     const uint32_t mm_p = tmem + L::tmem_p(t);
-    int step = 0;             // steps of the span passed
-    int vstep = 0;            // the step whose QK was issued last
+    Slots<D> at;              // of the next step
+    Slots<D> cur;             // of the step whose QK was issued last
     int n_iss = 0, n_seg = 0; // steps of the started segment issued so far, and all of them
     int started = -1;         // last segment whose Q was waited for
     bool issued_any = false;
@@ -587,50 +602,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // The next step this group takes; steps that only the other group takes are
     // released (both slots) once they have landed. False at the segment's end.
-    auto advance = [&](int& k_step) -> bool {
+    auto advance = [&](Slots<D>& mine) -> bool {
       while (u_next < a_ke) {
-        const int u = u_next++;
-        const int n = step++;
-        if (needs(u)) {
-          k_step = n;
+        const bool own = needs(u_next++);
+        const Slots<D> w = at;
+        at.next();
+        if (own) {
+          mine = w;
           return true;
         }
-        if (!(ok = RF_WAIT(kv_full[L::slot_k(n)], L::use_k(n) & 1, 20))) return false;
-        mbar_arrive(&bar.kv_empty[L::slot_k(n)]);
-        if (!(ok = RF_WAIT(kv_full[L::slot_v(n)], L::use_v(n) & 1, 20))) return false;
-        mbar_arrive(&bar.kv_empty[L::slot_v(n)]);
+        if (!(ok = RF_WAIT(kv_full[w.k], w.kp, 20))) return false;
+        mbar_arrive(&bar.kv_empty[w.k]);
+        if (!(ok = RF_WAIT(kv_full[w.v], w.vp, 20))) return false;
+        mbar_arrive(&bar.kv_empty[w.v]);
       }
       return false;
     };
-    auto next_k = [&](int& k_step) -> bool {
-      if (!advance(k_step)) return false;
-      return (ok = RF_WAIT(kv_full[L::slot_k(k_step)], L::use_k(k_step) & 1, 21));
+    auto next_k = [&](Slots<D>& mine) -> bool {
+      if (!advance(mine)) return false;
+      return (ok = RF_WAIT(kv_full[mine.k], mine.kp, 21));
     };
     // next_k without waiting: whether everything up to the K tile of this group's
     // next step has landed. Between this group's steps lies at most one of the
     // other's (a split item), so each barrier tested is at most one phase behind.
-    auto try_k = [&](int& k_step) -> bool {
+    auto try_k = [&](Slots<D>& mine) -> bool {
       while (u_next < a_ke) {
-        if (!mbar_test_wait(&bar.kv_full[L::slot_k(step)], L::use_k(step) & 1)) return false;
-        if (!needs(u_next)) {
-          if (!mbar_test_wait(&bar.kv_full[L::slot_v(step)], L::use_v(step) & 1)) return false;
-          mbar_arrive(&bar.kv_empty[L::slot_k(step)]);
-          mbar_arrive(&bar.kv_empty[L::slot_v(step)]);
+        if (!mbar_test_wait(&bar.kv_full[at.k], at.kp)) return false;
+        const bool own = needs(u_next);
+        if (!own) {
+          if (!mbar_test_wait(&bar.kv_full[at.v], at.vp)) return false;
+          mbar_arrive(&bar.kv_empty[at.k]);
+          mbar_arrive(&bar.kv_empty[at.v]);
         }
-        k_step = step++;
-        if (needs(u_next++)) return true;
+        mine = at;
+        at.next();
+        ++u_next;
+        if (own) return true;
       }
       return false;
     };
-    auto qk_commits = [&](int k_step) {
+    auto qk_commits = [&](const Slots<D>& w) {
       mma_commit(&bar.s_full[t]);
-      mma_commit(&bar.kv_empty[L::slot_k(k_step)]);
+      mma_commit(&bar.kv_empty[w.k]);
       if (++n_iss == n_seg) mma_commit(&bar.q_empty[q_slot]);  // the segment's last read of Q
-      vstep = k_step;
+      cur = w;
     };
-    auto issue_s = [&](int k_step) {
+    auto issue_s = [&](const Slots<D>& w) {
       issue_qk<D>(mm_s, q_desc0 + static_cast<uint64_t>((q_slot * L::kTileBytes) >> 4),
-                  k_desc0 + RF_SLOT(L::slot_k(k_step)));
+                  k_desc0 + RF_SLOT(w.k));
     };
     // Segment k (lane 0): wait for its Q tiles, release the ones this group does
     // not read, and issue the first QK; without steps of its own, release all.
@@ -654,17 +673,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive(&bar.q_empty[b]);
       }
-      int k_step;
+      Slots<D> first;
       if (n_seg == 0) {
-        advance(k_step);  // releases every step; returns false
+        advance(first);  // releases every step; returns false
         return;
       }
-      if (next_k(k_step) && (ok = RF_LOCK())) {
+      if (next_k(first) && (ok = RF_LOCK())) {
         tc_fence_after_sync();
-        issue_s(k_step);
+        issue_s(first);
         issue_unlock(&bar.issue_lock);
         issued_any = true;
-        qk_commits(k_step);
+        qk_commits(first);
       }
     };
 
@@ -694,13 +713,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // which the rings could not run ahead of the two groups.
         const bool last = jj + 1 == n;
         const int u = kb + (mode == kSplit ? 2 * jj + t : jj);
-        int k2 = 0;
+        Slots<D> k2;
         bool fast = false;
-        if (lane == 0 && ok) ok = RF_WAIT(kv_full[L::slot_v(vstep)], L::use_v(vstep) & 1, 24);
+        if (lane == 0 && ok) ok = RF_WAIT(kv_full[cur.v], cur.vp, 24);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         const int rows = kv - u * kBN;
         if (ok && rows < kBN) {
-          const int vs = L::slot_v(__shfl_sync(0xffffffffu, vstep, 0));
+          const int vs = __shfl_sync(0xffffffffu, cur.v, 0);
           unsigned char* v = smem + L::kOffKV + vs * L::kTileBytes;
           for (int i = rows * 8 + lane; i < kBN * 8; i += 32)
 #pragma unroll
@@ -718,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && (ok = RF_LOCK())) {
           tc_fence_after_sync();
-          const int v_slot = L::slot_v(vstep);
+          const int v_slot = cur.v;
           issue_pv<D>(mm_o, mm_p, v_desc0 + RF_SLOT(v_slot), jj > 0);
           if (fast) issue_s(k2);
           issue_unlock(&bar.issue_lock);
@@ -740,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // after this group's last, and start this group's next segment (the one
       // after the next, when the next is the other group's alone)
       if (lane == 0 && ok && n > 0) {
-        int k2;
-        advance(k2);
+        Slots<D> none;
+        advance(none);
         if (ok) start_segment(k + 1);
         if (ok && n_seg == 0 && bar.seg[(k + 1) % kSegs].seq >= 0) start_segment(k + 2);
       }
