@@ -33,10 +33,10 @@
 // Every wait is bounded; on expiry the kernel records a status code and the CTA
 // unwinds, the five warps of a group together at a reducing named barrier.
 //
-// Measured: decode of 8 sequences x 8 key heads x 65536 keys 6.72 TB/s of cache
-// at d = 128 (pages of 16 to 128) and 5.39 at d = 64, memory and the chain
+// Measured: decode of 8 sequences x 8 key heads x 65536 keys 6.74 TB/s of cache
+// at d = 128 (pages of 16 to 128) and 5.64 at d = 64, memory and the chain
 // scores -> softmax -> P.V of a one-tile step bounding them; a chunk of 2048
-// tokens at 32768 keys, 64 heads, d = 128, 1.41 to 1.50 ms (1510 to 1420
+// tokens at 32768 keys, 64 heads, d = 128, 1.38 to 1.52 ms (1547 to 1400
 // TFLOP/s), bound as attn_tc.cu is; one token over 515 keys 12.7 us, launches
 // and dependent loads.
 //
