@@ -466,6 +466,66 @@ def test_attn_paged_rows_before_the_first_sequence(cuda_device):
     _check_attention(c, o, lse)
 
 
+def test_paged_calls_of_nothing(cuda_device):
+    # no sequences, no tokens, sequences without new tokens, no drafts to judge
+    pool = torch.full((2, 4, 16, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    for B, T in ((0, 0), (0, 3), (3, 0), (3, 2)):
+        cu, kv = _i32([0] * (B + 1)), _i32([20] * B)
+        table = _i32([[0, 1]] * B).view(B, 2)
+        plan = api.PagedPlan(cu, kv, T, 4, 2, 16, 2)
+        pos, slots = api.paged_slots(cu, kv, table, 16, 4, T)
+        assert pos.tolist() == [0] * T and slots.tolist() == [-1] * T
+        x = torch.full((T, 4, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+        o = torch.full_like(x, 3.0)
+        assert api.attn_paged(x, pool[0], pool[1], table, plan, out=o)[1].shape == (T, 4)
+        assert (o == 3).all()
+        out = torch.full_like(x, 7.0)
+        api.kv_append_paged(x, x[:, :2], x[:, 2:], pool[0], pool[1], slots, q_out=out)
+        assert (out == 7).all() and (pool == 5).all()
+    none = torch.empty(0, 3, 10, device="cuda")
+    tokens, accepted = api.draft_verify(none, None, _i32([]).view(0, 2),
+                                        torch.empty(0, 2, device="cuda"),
+                                        torch.empty(0, 10, device="cuda"))
+    assert tokens.shape == (0, 3) and accepted.shape == (0,)
+    assert api.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_paged_a_whole_tile_of_heads(cuda_device, d):
+    # 128 and 100 query heads of one key head: a tile holds one token
+    for H in (128, 100):
+        c = _attention_case([(1, 700), (3, 40), (2, 1)], H, 1, d, 16, seed=H)
+        o, lse = _attend(c)
+        _check_attention(c, o, lse)
+    assert api.device_status() == 0
+
+
+def test_append_and_verify_on_another_stream(cuda_device):
+    # two streams at once, tensors made on the current one
+    gen = torch.Generator().manual_seed(3)
+    k = torch.randn(50, 2, 64, generator=gen).bfloat16().cuda()
+    slots = torch.randperm(64, generator=gen)[:50].cuda()
+    logits = torch.randn(4, 4, 5000, generator=gen).cuda()
+    drafted = logits[:, :3].argmax(-1).to(torch.int32)
+    u, expo = torch.full((4, 3), 0.5, device="cuda"), torch.ones(4, 5000, device="cuda")
+    draft = logits[:, :3].contiguous()
+    pools = [torch.zeros(2, 4, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    api.kv_append_paged(None, k, k, pools[2][0], pools[2][1], slots)
+    want = api.draft_verify(logits, draft, drafted, u, expo)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                api.kv_append_paged(None, k, k, pools[i][0], pools[i][1], slots)
+                got[i] = api.draft_verify(logits, draft, drafted, u, expo)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(pools[i], pools[2])
+        assert all(torch.equal(x, y) for x, y in zip(got[i], want))
+    assert api.device_status() == 0
+
+
 def test_attn_paged_leaves_padded_rows(cuda_device):
     c = _attention_case([(3, 40), (1, 9)], 4, 2, 64, 8, seed=7, pad=5)
     o = torch.full((c["T"], 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
