@@ -256,6 +256,9 @@ def _prepare_verify(case, st, device, g):
     if case["ragged"]:
         st["n_draft"] = torch.randint(0, S + 1, (B,), generator=g, device=device,
                                       dtype=torch.int32)
+    if own:
+        from online_softmax_attention_rf_gb300 import api
+        st["ws"] = api.draft_verify_workspace(B, S, device)
 
 
 # ------------------------------------------------------------------ one pass
@@ -283,7 +286,7 @@ def _own(op, st):
                                     interleaved=st["case"]["interleaved"])
         return q_out, st["k_cache"], st["v_cache"]
     return api.draft_verify(st["target"], st["draft"], st["tokens"], st["u"], st["expo"],
-                            n_draft=st["n_draft"], temperature=st["temp"])
+                            n_draft=st["n_draft"], temperature=st["temp"], workspace=st["ws"])
 
 
 def _plain_attn(st):
