@@ -32,8 +32,8 @@ constexpr int kCluster = 8;
 constexpr int kNone = 0x7fffffff;
 
 // State of one row piece: maximum, sum of exp((x - max) / T), lowest index of
-// the maximum (filled in greedy rows only).
-struct Stat {
+// the maximum (filled in greedy rows only). Read as one int4.
+struct alignas(16) Stat {
   float m, l;
   int arg, pad;
 };
@@ -265,7 +265,7 @@ struct alignas(W * sizeof(T) < 16 ? W * sizeof(T) : 16) Pack {
 // 16 sequences at an odd V = 50001.
 template <typename T, int W, int kThreads>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1024 / kThreads)
-    choose_kernel(const VerifyArgs a, const Stat* __restrict__ stats, int nsplit) {
+    choose_kernel(const VerifyArgs a, const Stat* stats, int nsplit) {
   constexpr int kWarps = kThreads / 32;
   __shared__ float rm[2 * kMaxDrafts + 1], rl[2 * kMaxDrafts + 1];
   __shared__ int rarg[2 * kMaxDrafts + 1];
@@ -301,7 +301,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
     }
   }
   pdl_wait();
-  // the row statistics, joined from their pieces in a fixed order
+  // The row statistics, joined from their pieces in a fixed order. stats_kernel
+  // may write them while this grid runs, so they are neither __restrict__ (read
+  // as data that never changes) nor taken from L1.
   for (int r = warp; r < per; r += kWarps) {
     const bool is_draft = r > a.S;
     const int i = is_draft ? r - a.S - 1 : r;
@@ -309,10 +311,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
     float m = kNegInf, l = 0.f;
     int arg = kNone;
     if (lane < nsplit) {
-      const Stat s = stats[(int64_t(b) * per + r) * nsplit + lane];
-      m = s.m;
-      l = s.l;
-      arg = s.arg;
+      const int4 s = __ldcg(reinterpret_cast<const int4*>(stats + (int64_t(b) * per + r) * nsplit + lane));
+      m = __int_as_float(s.x);
+      l = __int_as_float(s.y);
+      arg = s.z;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {

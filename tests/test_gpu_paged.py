@@ -909,6 +909,47 @@ def test_draft_verify_captured(cuda_device):
         _check_verify(new, out, n_acc)
 
 
+def _rewritten_in_place(c, sets, names):
+    """Calls one behind the other on one stream, with one workspace: a kernel
+    writes the inputs `names` of the next set into the same tensors directly
+    ahead of each call, and the host waits for nothing in between. Yields the
+    calls' results beside those of calls by themselves."""
+    c = {k: None if v is None else v.cuda() for k, v in c.items()}
+    sets = [{n: s[n].cuda() for n in names} for s in sets]
+    B, S = c["tokens"].shape
+
+    def call(kw, ws):
+        return api.draft_verify(*(kw[n] for n in ("target", "draft", "tokens", "u", "expo",
+                                                  "n_draft", "temperature")), workspace=ws)
+
+    want = []
+    for s in sets:
+        want.append(call(dict(c, **s), api.draft_verify_workspace(B, S)))
+        torch.cuda.synchronize()
+    assert len({str([x.tolist() for x in w]) for w in want}) > 1
+    ws = api.draft_verify_workspace(B, S)
+    for n in names:
+        c[n] = torch.empty_like(sets[0][n])
+    torch.cuda.synchronize()
+    got, order = [], [i % len(sets) for i in range(200)]
+    for i in order:
+        for n in names:
+            torch.add(sets[i][n], 0, out=c[n])
+        got.append(call(c, ws))
+    torch.cuda.synchronize()
+    assert api.device_status() == 0
+    return [(got[k], want[i]) for k, i in enumerate(order)]
+
+
+@pytest.mark.parametrize("B,S,V", [(1, 4, 600), (4, 3, 20000), (40, 6, 1000)])
+def test_draft_verify_statistics_of_this_call(cuda_device, B, S, V):
+    # the draw starts under the statistics of its own call: it must not see the
+    # last call's, which lie at the same place in the workspace
+    cases = [_verify_case(B, S, V, torch.float32, 50 + i) for i in range(5)]
+    for got, want in _rewritten_in_place(cases[0], cases, ("target", "draft")):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ---------------------------------------------------------------- together
 
 def test_speculative_decoding_over_a_paged_cache(cuda_device):
