@@ -51,15 +51,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // scaling, so that it is exact or nearly so for the entries that matter.
 __device__ __forceinline__ float weight(float x, float m, float c) { return ex2_approx((x - m) * c); }
 
-__device__ __forceinline__ float log2e_over(const float* temperature, int b, bool* greedy) {
-  const float t = temperature != nullptr ? temperature[b] : 1.f;
+__device__ __forceinline__ float log2e_over(float t, bool* greedy) {
   *greedy = !(t > 0.f);
   return *greedy ? kLog2e : kLog2e / t;
 }
 
-__device__ __forceinline__ int drafts_of(const VerifyArgs& a, int b) {
-  return a.n_draft != nullptr ? max(0, min(a.S, a.n_draft[b])) : a.S;
-}
+__device__ __forceinline__ int drafts_of(const VerifyArgs& a, int n) { return max(0, min(a.S, n)); }
 
 __device__ __forceinline__ void merge(float& m, float& l, float m2, float l2, float c) {
   const float mn = fmaxf(m, m2);
@@ -153,8 +150,8 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(const VerifyArgs a,
   pdl_wait();
   pdl_trigger();
   bool greedy;
-  const float c = log2e_over(a.temperature, b, &greedy);
-  const int nd = drafts_of(a, b);
+  const float c = log2e_over(a.temperature != nullptr ? a.temperature[b] : 1.f, &greedy);
+  const int nd = drafts_of(a, a.n_draft != nullptr ? a.n_draft[b] : a.S);
   if (is_draft ? (i >= nd || greedy) : i > nd) return;  // never looked at
   const T* x = is_draft ? static_cast<const T*>(a.draft) + (int64_t(b) * a.S + i) * a.V
                         : static_cast<const T*>(a.target) + (int64_t(b) * (a.S + 1) + i) * a.V;
@@ -282,22 +279,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
   const T* target = static_cast<const T*>(a.target) + int64_t(b) * (a.S + 1) * a.V;
   const T* draft = static_cast<const T*>(a.draft) + (a.draft != nullptr ? int64_t(b) * a.S * a.V : 0);
   // stats_kernel lets this grid start only when all of its CTAs have seen the
-  // work before it complete, so the call's inputs can be read now; what
-  // stats_kernel writes has to be waited for, and this grid writes nothing before.
+  // work before it complete, so the call's inputs are complete in L2 by now; only
+  // pdl_wait makes them visible through L1, so what is read before it is read past
+  // L1. What stats_kernel writes has to be waited for, and this grid writes
+  // nothing before.
   bool greedy;
-  const float c = log2e_over(a.temperature, b, &greedy);
-  const int nd = drafts_of(a, b);
+  const float c =
+      log2e_over(a.temperature != nullptr ? __ldcg(a.temperature + b) : 1.f, &greedy);
+  const int nd = drafts_of(a, a.n_draft != nullptr ? __ldcg(a.n_draft + b) : a.S);
   // the drafted tokens' logits, on their way while the statistics are joined
   int x = 0;
   bool in_range = false;
   float xt = 0.f, xd = 0.f, xu = 0.f;
   if (tid < nd) {
-    x = a.tokens[int64_t(b) * a.S + tid];
-    xu = a.u[int64_t(b) * a.S + tid];
+    x = __ldcg(a.tokens + int64_t(b) * a.S + tid);
+    xu = __ldcg(a.u + int64_t(b) * a.S + tid);
     in_range = x >= 0 && x < a.V;
     if (in_range && !greedy) {
-      xt = to_f32(target[int64_t(tid) * a.V + x]);
-      if (a.draft != nullptr) xd = to_f32(draft[int64_t(tid) * a.V + x]);
+      xt = to_f32(__ldcg(target + int64_t(tid) * a.V + x));
+      if (a.draft != nullptr) xd = to_f32(__ldcg(draft + int64_t(tid) * a.V + x));
     }
   }
   pdl_wait();

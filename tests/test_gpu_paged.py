@@ -950,6 +950,21 @@ def test_draft_verify_statistics_of_this_call(cuda_device, B, S, V):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("B,S,V,certain", [(1, 4, 600, False), (4, 3, 20000, False),
+                                           (40, 6, 1000, True), (3, 64, 257, False)])
+def test_draft_verify_inputs_of_this_call(cuda_device, B, S, V, certain):
+    # the draw reads drafts, their logits, random numbers and temperatures before
+    # the statistics are done: they must be this call's too
+    cases = [_verify_case(B, S, V, torch.float32, 60 + i, certain, ragged=True, greedy=True,
+                          agree=0.3) for i in range(7)]
+    for c in cases[::2]:
+        c["temperature"] = c["temperature"].flip(0)      # other sequences are greedy
+    names = ("target", "tokens", "u", "expo", "n_draft", "temperature") + \
+        (() if certain else ("draft",))
+    for got, want in _rewritten_in_place(cases[0], cases, names):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ---------------------------------------------------------------- together
 
 def test_speculative_decoding_over_a_paged_cache(cuda_device):
