@@ -18,6 +18,8 @@
 // that row's logits are in L2 by then).
 #include <cooperative_groups.h>
 
+#include <cfloat>
+
 #include "paged_device.cuh"
 
 namespace rf {
@@ -32,7 +34,8 @@ constexpr int kCluster = 8;
 constexpr int kNone = 0x7fffffff;
 
 // State of one row piece: maximum, sum of exp((x - max) / T), lowest index of
-// the maximum (filled in greedy rows only). Read as one int4.
+// the maximum (filled in greedy rows only, whose sum is 0, or NaN where the row
+// has a NaN). Read as one int4.
 struct alignas(16) Stat {
   float m, l;
   int arg, pad;
@@ -129,6 +132,7 @@ __device__ __forceinline__ void take_greedy(Running& st, float x, int v) {
     st.m = x;
     st.arg = v;
   }
+  if (x != x) st.l = x;  // a NaN shows in the sum
 }
 
 // One CTA: piece `split` of one logit row. Rows of sequence b: its S + 1
@@ -326,7 +330,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
     if (lane == 0) {
       rm[r] = m;
       rl[r] = l;
-      rarg[r] = arg;
+      // the greedy choice, of a row with a finite maximum and without NaN
+      rarg[r] = l == 0.f && fabsf(m) <= FLT_MAX ? arg : -1;
     }
   }
   __syncthreads();
@@ -351,7 +356,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
   int chosen;
   cluster.barrier_wait();
   if (greedy) {
-    chosen = rarg[at] == kNone ? -1 : rarg[at];
+    chosen = rarg[at];
   } else {
     const bool refused = at < nd;
     const T* pt = target + int64_t(at) * a.V;

@@ -909,6 +909,39 @@ def test_draft_verify_captured(cuda_device):
         _check_verify(new, out, n_acc)
 
 
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 101), (torch.bfloat16, 9000)])
+@pytest.mark.parametrize("bad", ["-inf", "nan", "inf", "all nan"])
+def test_draft_verify_greedy_row_without_probabilities(cuda_device, dtype, V, bad):
+    # greedy sequences whose judging row (the first, a middle one, the extra one)
+    # has no finite maximum or a NaN: the row refuses its draft and draws -1
+    c = _verify_case(4, 3, V, dtype, 21)
+    c["temperature"] = torch.tensor([0.0, 0.0, 0.0, 1.0])
+    c["target"][:3, torch.arange(3), torch.arange(3)] = 30.0
+    c["tokens"][:3] = torch.arange(3, dtype=torch.int32)    # what the rows choose
+    good = {k: None if v is None else v.clone() for k, v in c.items()}
+    for b, row in enumerate((0, 2, 3)):
+        if bad in ("-inf", "all nan"):
+            c["target"][b, row] = float(bad.split()[-1])
+        else:
+            c["target"][b, row, V - 7] = float(bad)
+    out, n_acc = _verify(c)
+    with pytest.raises(api.RFError):
+        api.device_status()
+    want, want_acc = _verify(good)
+    assert api.device_status() == 0
+    _check_verify(good, want, want_acc)
+    assert want_acc[:3].cpu().tolist() == [3, 3, 3]
+    # the accepted drafts ahead of the bad row, then -1
+    assert n_acc[:3].cpu().tolist() == [0, 2, 3]
+    assert out[:3].cpu().tolist() == [[-1] * 4, [0, 1, -1, -1], [0, 1, 2, -1]]
+    assert torch.equal(out[3], want[3]) and n_acc[3] == want_acc[3]
+    # a bad row behind the first refusal is not looked at
+    c["tokens"][:, 0] = V - 1
+    c["target"][:, 0] = good["target"][:, 0]
+    out, _ = _verify(c)
+    assert api.device_status() == 0 and (out[:, 0] >= 0).all()
+
+
 def _rewritten_in_place(c, sets, names):
     """Calls one behind the other on one stream, with one workspace: a kernel
     writes the inputs `names` of the next set into the same tensors directly
