@@ -369,8 +369,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
     const int out_of_race = refused && !has_q ? a.tokens[int64_t(b) * a.S + at] : -1;
     chosen = -1;
     // pass 0: the remainder max(p - q, 0) (p itself when everything was
-    // accepted); pass 1, only when rounding leaves nothing of the remainder: p
-    for (int pass = 0; pass < (refused ? 2 : 1); ++pass) {
+    // accepted); pass 1, only when rounding leaves nothing of the remainder: p.
+    // None when the draft row has no probabilities (its sum is 0 or NaN).
+    const bool draws = !has_q || rl[a.S + 1 + at] > 0.f;
+    for (int pass = 0; draws && pass < (refused ? 2 : 1); ++pass) {
       Best best{0.f, kNone};
       const int skip = pass == 0 ? out_of_race : -1;
       // w / e as w * (1 / e): two steps of error, below what the weights carry.

@@ -942,6 +942,34 @@ def test_draft_verify_greedy_row_without_probabilities(cuda_device, dtype, V, ba
     assert api.device_status() == 0 and (out[:, 0] >= 0).all()
 
 
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 101), (torch.bfloat16, 9000)])
+@pytest.mark.parametrize("bad", ["-inf", "nan", "inf", "all nan"])
+def test_draft_verify_draft_row_without_probabilities(cuda_device, dtype, V, bad):
+    # a draft row that is no distribution refuses its draft and draws -1, as a
+    # target row does; one behind the first refusal is not looked at
+    c = _verify_case(3, 3, V, dtype, 22)
+    c["target"][:, torch.arange(3), torch.arange(3)] = 30.0   # accepted with certainty
+    c["tokens"][:] = torch.arange(3, dtype=torch.int32)
+    good = {k: None if v is None else v.clone() for k, v in c.items()}
+    for b, row in enumerate((0, 2)):
+        if bad in ("-inf", "all nan"):
+            c["draft"][b, row] = float(bad.split()[-1])
+        else:
+            c["draft"][b, row, V - 7] = float(bad)
+    out, n_acc = _verify(c)
+    with pytest.raises(api.RFError):
+        api.device_status()
+    want, want_acc = _verify(good)
+    assert api.device_status() == 0
+    _check_verify(good, want, want_acc)
+    assert n_acc.cpu().tolist() == [0, 2, want_acc[2].item()]
+    assert out[:2].cpu().tolist() == [[-1] * 4, [0, 1, -1, -1]] and torch.equal(out[2], want[2])
+    c["tokens"][1, 0] = V - 1
+    c["draft"][0] = good["draft"][0]
+    out, n_acc = _verify(c)
+    assert api.device_status() == 0 and n_acc[1] == 0 and out[1, 0] >= 0
+
+
 def _rewritten_in_place(c, sets, names):
     """Calls one behind the other on one stream, with one workspace: a kernel
     writes the inputs `names` of the next set into the same tensors directly
