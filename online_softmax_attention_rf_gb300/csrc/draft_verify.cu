@@ -54,9 +54,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // scaling, so that it is exact or nearly so for the entries that matter.
 __device__ __forceinline__ float weight(float x, float m, float c) { return ex2_approx((x - m) * c); }
 
+// log2(e) / T. Below a temperature of 4.3e-39 it would be infinite, and the
+// largest logit's 0 * inf a NaN; the largest finite number still leaves nothing
+// of any logit that is 2^-120 below the largest.
 __device__ __forceinline__ float log2e_over(float t, bool* greedy) {
   *greedy = !(t > 0.f);
-  return *greedy ? kLog2e : kLog2e / t;
+  return *greedy ? kLog2e : fminf(kLog2e / t, FLT_MAX);
 }
 
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int n) { return max(0, min(a.S, n)); }

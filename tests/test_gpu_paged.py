@@ -873,6 +873,21 @@ def test_draft_verify_token_out_of_range(cuda_device):
         assert n_acc[0].item() == 0 and 0 <= out[0, 0].item() < 100
 
 
+@pytest.mark.parametrize("temp", [1e-45, 1e-40, 4e-39, 5e-39, 1e-37, 1e37, 3.4e38])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_draft_verify_extreme_temperatures(cuda_device, dtype, temp):
+    # subnormal ones among them: the largest logits share all the probability; at
+    # the other end every entry but -inf weighs the same
+    c = _verify_case(6, 3, 3000, dtype, 23)
+    c["temperature"] = torch.full((6,), temp)
+    c["target"][::2, :, [40, 2999]] = 20.0       # two largest logits
+    c["target"][:, :, 7] = float("-inf")
+    c["draft"][:, :, 8] = float("-inf")
+    out, n_acc = _verify(c)
+    assert api.device_status() == 0
+    _check_verify(c, out, n_acc)
+
+
 def test_draft_verify_ties_go_to_the_lowest_index(cuda_device):
     V = 10000
     target = torch.zeros(2, 2, V)
