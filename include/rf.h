@@ -657,7 +657,9 @@ rf_status rf_attn_paged(const void *q, int64_t q_stride, const void *k_cache,
  *           probability;
  *  draft  : [B, S, V] logits of the same dtype, or NULL: drafts with
  *           certainty (copied ones): q_i is 1 at x_i;
- *  tokens : int32 [B, S]; u: float [B, S] in [0, 1); expo: float [B, V] > 0;
+ *  tokens : int32 [B, S]; u: float [B, S] in [0, 1); expo: float [B, V] in
+ *           [2^-126, 2^32] (the draw multiplies by 1 / expo in float32, which
+ *           takes subnormal numbers for 0; not checked);
  *  n_draft: int32 [B] in [0, S], or NULL (all S);
  *  temperature: float [B], finite, or NULL (1); not above 0: greedy (draft i
  *           is accepted when it is the target's largest logit, lowest index

@@ -808,9 +808,9 @@ def _refuse_verify(target, draft, tokens, u, expo, n_draft, temperature, workspa
 def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None, workspace=None):
     """rf_draft_verify: target logits [B, S + 1, V], draft logits [B, S, V] (or
     None: drafts with certainty), tokens int32 [B, S], u float32 [B, S] in
-    [0, 1), expo float32 [B, V] exponential variates, n_draft int32 [B],
-    temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1], n_accepted
-    int32 [B])."""
+    [0, 1), expo float32 [B, V] exponential variates (2^-126 to 2^32), n_draft
+    int32 [B], temperature float32 [B] (0: greedy) -> (out int32 [B, S + 1],
+    n_accepted int32 [B])."""
     r = _serving().draft_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
     if r.__class__ is tuple:
         return r

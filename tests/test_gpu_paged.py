@@ -888,6 +888,21 @@ def test_draft_verify_extreme_temperatures(cuda_device, dtype, temp):
     _check_verify(c, out, n_acc)
 
 
+def test_draft_verify_smallest_and_largest_exponentials(cuda_device):
+    c = _verify_case(8, 2, 2000, torch.float32, 24, sharp=1.0)
+    c["expo"][0::4] = 2.0 ** 32
+    c["expo"][0::4, 100] = 2.0 ** 31.5
+    c["expo"][1::4, [50, 60]] = torch.tensor([2.0 ** -125, 2.0 ** -126])
+    c["target"][1::4, :, [50, 60]] = 0.0                 # equal weights, the second one wins
+    c["draft"][1::4, :, [50, 60]] = -4.0
+    c["expo"][2::4] = 2.0 ** -126
+    out, n_acc = _verify(c)
+    assert api.device_status() == 0
+    _check_verify(c, out, n_acc)
+    refused = [b for b in (1, 5) if n_acc[b] < 2]
+    assert all(out[b, n_acc[b]].item() == 60 for b in refused)
+
+
 def test_draft_verify_ties_go_to_the_lowest_index(cuda_device):
     V = 10000
     target = torch.zeros(2, 2, V)
