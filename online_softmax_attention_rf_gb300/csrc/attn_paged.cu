@@ -278,8 +278,7 @@ struct Span {
   }
   // Steps that the item's token i needs.
   __device__ __forceinline__ int steps_of(int i, const Seg& s) const {
-    const int lim = causal ? max(0, s.lim0 + i) : s.kv;
-    return (lim + kBN - 1) / kBN;
+    return plan_steps(causal ? max(0, s.lim0 + i) : s.kv);
   }
 };
 
@@ -473,9 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // this lane's page of step u of a segment and the box's first row in it
     auto page_of = [&](const Seg& s, int u, int& in_page) -> int {
-      const int key = u * kBN + my_key;
       in_page = 0;
-      if (u >= s.ke || !has_box || key >= s.kv) return -1;
+      if (u >= s.ke || !has_box) return -1;
+      const int key = u * kBN + my_key;
+      if (key >= s.kv) return -1;
       const int pi = key / p.page;
       in_page = key - pi * p.page;
       return p.table[int64_t(s.seq) * p.table_stride + pi];
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int slot = is_k ? at.k : at.v;
         if (lane == 0) {
-          const int n_box = min(boxes, (s.kv - u * kBN + p.box - 1) / p.box);
+          const int n_box = (min(kBN, s.kv - u * kBN) + p.box - 1) / p.box;
           ok = RF_WAIT(kv_empty[slot], (is_k ? at.kp : at.vp) ^ 1, 10);
           if (ok) mbar_arrive_expect_tx(&bar.kv_full[slot], n_box * p.box * D * 2);
         }
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && warp_ok) {
           tc_fence_after_sync();
           const int k0 = u * kBN;
-          const int lim = (k0 + kBN > first_lim) ? max(0, min(kBN, row_lim - k0)) : kBN;
+          const int lim = (first_lim - k0 < kBN) ? max(0, min(kBN, row_lim - k0)) : kBN;
           float mx;
           {
             uint32_t sr[128];

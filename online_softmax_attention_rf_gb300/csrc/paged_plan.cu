@@ -40,7 +40,7 @@ __device__ __forceinline__ Item item_of(int pair, int n, int kv, int causal, int
   const int i0 = pair * 2 * tt, i1 = min(n, i0 + 2 * tt);
   Item it;
   it.rows = (i1 - i0) * G;
-  it.steps = (plan_visible(i1 - 1, n, kv, causal) + kPlanTile - 1) / kPlanTile;
+  it.steps = plan_steps(plan_visible(i1 - 1, n, kv, causal));
   const bool two = i1 - i0 > tt;
   it.per_step = two ? kPairCost : kSingleCost;
   it.fixed = two ? kPairFixed : kSingleFixed;

@@ -76,6 +76,12 @@ __host__ __device__ inline int plan_units(int ntok, int tile, int G) {
   return tok > 0 ? (tok * G + 31) / 32 : 0;
 }
 
+// Key tiles that hold the first `keys` keys. A cache may have up to 2^31 - 1 of
+// them: rounding up by an addition would wrap.
+__host__ __device__ inline int plan_steps(int keys) {
+  return keys / kPlanTile + (keys % kPlanTile != 0 ? 1 : 0);
+}
+
 // Keys that token i of n new ones sees, of kv cached ones.
 __host__ __device__ inline int plan_visible(int i, int n, int kv, int causal) {
   if (!causal) return kv;

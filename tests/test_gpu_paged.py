@@ -294,6 +294,31 @@ def test_paged_plan_covers_every_step_once(cuda_device, lengths, H, Hkv, causal)
         assert max(cost) <= sum(cost) / len(cost) + 28
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths", [
+    [(1, 2 ** 31 - 8)], [(200, 2 ** 31 - 8)], [(1, 2 ** 31 - 9), (0, 2 ** 31 - 8), (3, 5)],
+    [(1, 2 ** 31 - 128 + i) for i in (-1, 0, 1, 120)] * 50,
+])
+def test_paged_plan_of_the_longest_caches(cuda_device, lengths, causal):
+    H, Hkv, page = 8, 4, 8
+    cu = [0]
+    for n, _ in lengths:
+        cu.append(cu[-1] + n)
+    kv = [m for _, m in lengths]
+    plan = api.PagedPlan(_i32(cu), _i32(kv), cu[-1], H, Hkv, page, (2 ** 31 - 8) // page, causal)
+    assert api.device_status() == 0
+    items, spans, _, _ = _spans(plan, cu, kv, H, Hkv, causal)
+    at = [0] * len(items)
+    for span in spans:
+        for i, k0, k1 in span:
+            assert at[i] == k0
+            at[i] = k1
+    assert at == [it[3] for it in items]
+    steps = [sum(k1 - k0 for _, k0, k1 in span) for span in spans]
+    # an item cut by itself has a whole number of parts, 37 at least here
+    assert len(spans) == 152 and max(steps) <= 38 / 37 * sum(steps) / 152 + 2
+
+
 # ---------------------------------------------------------------- attention
 
 def _attention_case(lengths, H, Hkv, d, page, seed=0, causal=True, head_major=False, pad=0, amp=1.0,
@@ -621,6 +646,33 @@ def test_attn_paged_cache_beyond_32_bits(cuda_device):
     api.kv_append_paged(None, k, k, kc, vc, torch.tensor(at, device="cuda"))
     assert torch.equal(kc[pages - 1, 127], k[0]) and torch.equal(vc[16500, 3], k[1])
     assert api.device_status() == 0
+
+
+def test_attn_paged_the_longest_cache(cuda_device):
+    # one token over 2^31 - 11 keys, most of them in the same five pages. Scores
+    # are 0 and values small whole numbers, so that each part's sums are exact; the
+    # keys behind the last one would outweigh all others.
+    page, d, kv = 8, 64, 2 ** 31 - 11
+    width = (2 ** 31 - 8) // page
+    gen = torch.Generator().manual_seed(12)
+    kc = torch.randn(6, page, 1, d, generator=gen).bfloat16().cuda()
+    vc = torch.randint(-1, 4, (6, page, 1, d), generator=gen).bfloat16().cuda()
+    kc[..., 0] = 0
+    kc[5, 5:, 0, 0], vc[5, 5:] = 100.0, 100.0
+    q = torch.zeros(1, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    table = torch.randint(0, 5, (1, width), dtype=torch.int32, device="cuda")
+    table[0, -1] = 5
+    counts = torch.stack([(table == i).sum() for i in range(5)]).double()
+    total = (counts[:, None, None] * vc[:5, :, 0].double()).sum((0, 1)) + vc[5, :5, 0].double().sum(0)
+    plan = api.PagedPlan(_i32([0, 1]), _i32([kv]), 1, 1, 1, page, width)
+    o, lse = api.attn_paged(q, kc, vc, table, plan, 1.0)
+    assert api.device_status() == 0
+    want = total / kv
+    # parts are exact; joining 152 of them takes a few float32 steps each
+    tol = (1.01 * BF16_STEP + 4 * 152 * F32_STEP) * want.abs()
+    assert ((o[0, 0].double() - want).abs() <= tol).all()
+    assert abs(lse.item() - math.log(kv)) <= 152 * 4 * F32_STEP * math.log(kv)
 
 
 def test_attn_paged_bad_table_entry_is_reported(cuda_device):

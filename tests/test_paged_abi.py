@@ -2,6 +2,7 @@
 types that they refuse on the host, and calls with nothing to do."""
 
 import math
+import subprocess
 
 import pytest
 
@@ -102,6 +103,35 @@ def test_paged_plan_rejects(L):
         assert _call(L.rf_paged_plan, PLAN, ok, kw) == api.RF_ERR_INVALID, kw
         assert L.rf_last_error().startswith(b"rf_paged_plan")
     assert _call(L.rf_paged_plan, PLAN, ok, dict(H=258, Hkv=2)) == api.RF_ERR_UNSUPPORTED
+
+
+def test_plan_steps_up_to_the_longest_cache(tmp_path):
+    # the plan's arithmetic over lengths, compiled for the host: caches of up to
+    # 2^31 - 1 tokens
+    (tmp_path / "steps.cpp").write_text("""
+#include <cstddef>
+#define __host__
+#define __device__
+#include "paged_plan.h"
+#include <cstdio>
+#include <initializer_list>
+int main() {
+  for (long long keys : {0LL, 1LL, 127LL, 128LL, 129LL, 2147483519LL, 2147483520LL, 2147483521LL,
+                         2147483640LL, 2147483647LL}) {
+    const int kv = static_cast<int>(keys);
+    std::printf("%lld %d %d %d\\n", keys, rf::plan_steps(kv), rf::plan_visible(0, 1, kv, 1),
+                rf::plan_visible(2, 3, kv, 0));
+  }
+}
+""")
+    exe = str(tmp_path / "steps")
+    subprocess.run(["g++", "-std=c++17", "-ftrapv", "-I", build.CSRC, str(tmp_path / "steps.cpp"),
+                    "-o", exe], check=True)
+    rows = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split("\n")
+    rows = [[int(x) for x in r.split()] for r in rows if r]
+    assert len(rows) == 10
+    for keys, steps, last, every in rows:
+        assert steps == -(-keys // 128) and last == every == keys
 
 
 ATTN = ["q", "q_stride", "k", "kp", "kt", "kh", "v", "vp", "vt", "vh", "page", "num_pages", "table",
