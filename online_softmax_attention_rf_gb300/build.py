@@ -13,6 +13,8 @@ Usage:  python -m online_softmax_attention_rf_gb300.build [--force] [-v]
 """
 
 import concurrent.futures
+import importlib.util
+import json
 import os
 import shutil
 import subprocess
@@ -75,27 +77,42 @@ def _run(cmd, what):
 
 
 def _torch_dir():
-    import torch
-    return os.path.dirname(torch.__file__)
+    """Directory of the installed torch, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("the binding of the paged serving calls needs torch")
+    return spec.submodule_search_locations[0]
 
 
-def _compile_binding(obj):
+def _binding_commands(obj, tmp):
+    """The binding's compile and link commands."""
     t = _torch_dir()
+    gxx = shutil.which("g++") or "g++"
+    tlib = os.path.join(t, "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     dirs = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
             sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
-          *[f for d in dirs for f in ("-isystem", d)], "-c", BINDING_SRC, "-o", obj],
-         "g++ for %s" % BINDING_SRC)
+    return ([gxx, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+             *[f for d in dirs for f in ("-isystem", d)], "-c", BINDING_SRC, "-o", obj],
+            [gxx, "-shared", "-o", tmp, obj, "-L", LIBDIR, "-l:librf.so", "-L", tlib,
+             "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN",
+             "-Wl,-rpath," + tlib])
 
 
-def _link_binding(obj):
-    tlib = os.path.join(_torch_dir(), "lib")
-    tmp = BINDING_PATH + ".tmp"
-    _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-l:librf.so",
-          "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
-          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + tlib], "link of %s" % BINDING_PATH)
-    os.replace(tmp, BINDING_PATH)
+def _binding_made_with(commands):
+    """What a built binding depends on besides its sources: the commands (they
+    name torch's, Python's and CUDA's directories), torch's version and Python's
+    binary interface. A binding made with something else is built again."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        version = f.read()
+    return json.dumps([commands, version, sysconfig.get_config_var("SOABI")], indent=1)
+
+
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def build(force=False, verbose=False, extra_flags=()):
@@ -111,12 +128,16 @@ def build(force=False, verbose=False, extra_flags=()):
         if force or _stale(obj, [src, *hdrs]):
             todo.append(src)
     binding_obj = os.path.join(BUILD_DIR, "serving_binding.o")
-    binding = force or _stale(binding_obj, [BINDING_SRC, os.path.join(INCLUDE, "rf.h")])
+    binding_tmp, binding_stamp = BINDING_PATH + ".tmp", os.path.join(BUILD_DIR, "serving_binding.json")
+    commands = _binding_commands(binding_obj, binding_tmp)
+    made_with = _binding_made_with(commands)
+    binding = force or made_with != _read(binding_stamp) or \
+        _stale(binding_obj, [BINDING_SRC, os.path.join(INCLUDE, "rf.h")])
     if todo or binding:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
             jobs = [ex.submit(_compile, s, verbose, list(extra_flags)) for s in todo]
             if binding:
-                jobs.append(ex.submit(_compile_binding, binding_obj))
+                jobs.append(ex.submit(_run, commands[0], "g++ for %s" % BINDING_SRC))
             for j in jobs:
                 j.result()
     if force or todo or _stale(LIB_PATH, objs):
@@ -127,7 +148,10 @@ def build(force=False, verbose=False, extra_flags=()):
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
         os.replace(tmp, LIB_PATH)
     if force or binding or _stale(BINDING_PATH, [binding_obj]):
-        _link_binding(binding_obj)
+        _run(commands[1], "link of %s" % BINDING_PATH)
+        os.replace(binding_tmp, BINDING_PATH)
+        with open(binding_stamp, "w") as f:
+            f.write(made_with)
     return LIB_PATH
 
 
