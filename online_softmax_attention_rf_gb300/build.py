@@ -20,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -84,6 +85,20 @@ def _torch_dir():
     return spec.submodule_search_locations[0]
 
 
+def _binding_lacks():
+    """What the binding needs and this machine does not have, or None. Users of the
+    C library need none of it."""
+    try:
+        t = _torch_dir()
+    except RuntimeError:
+        return "torch"
+    for what, path in (("torch's headers", os.path.join(t, "include", "ATen")),
+                       ("Python.h", os.path.join(sysconfig.get_paths()["include"], "Python.h"))):
+        if not os.path.exists(path):
+            return "%s (%s)" % (what, path)
+    return None if shutil.which("g++") else "g++"
+
+
 def _binding_commands(obj, tmp):
     """The binding's compile and link commands."""
     t = _torch_dir()
@@ -116,7 +131,10 @@ def _read(path):
 
 
 def build(force=False, verbose=False, extra_flags=()):
-    """Compile what changed and link lib/librf.so; returns its path."""
+    """Compile what changed and link lib/librf.so, then the binding of the paged
+    serving calls; returns librf.so's path. Where the binding cannot be built
+    (no torch, Python.h or g++) the library is, with a warning; those calls of
+    api.py then raise."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     hdrs = _headers()
@@ -129,17 +147,19 @@ def build(force=False, verbose=False, extra_flags=()):
             todo.append(src)
     binding_obj = os.path.join(BUILD_DIR, "serving_binding.o")
     binding_tmp, binding_stamp = BINDING_PATH + ".tmp", os.path.join(BUILD_DIR, "serving_binding.json")
-    commands = _binding_commands(binding_obj, binding_tmp)
-    made_with = _binding_made_with(commands)
-    binding = force or made_with != _read(binding_stamp) or \
-        _stale(binding_obj, [BINDING_SRC, os.path.join(INCLUDE, "rf.h")])
-    if todo or binding:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
-            jobs = [ex.submit(_compile, s, verbose, list(extra_flags)) for s in todo]
-            if binding:
-                jobs.append(ex.submit(_run, commands[0], "g++ for %s" % BINDING_SRC))
-            for j in jobs:
-                j.result()
+    lacks = _binding_lacks()
+    binding = False
+    if lacks is None:
+        commands = _binding_commands(binding_obj, binding_tmp)
+        made_with = _binding_made_with(commands)
+        binding = force or made_with != _read(binding_stamp) or \
+            _stale(binding_obj, [BINDING_SRC, os.path.join(INCLUDE, "rf.h")])
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
+        jobs = [ex.submit(_compile, s, verbose, list(extra_flags)) for s in todo]
+        if binding:
+            binding_job = ex.submit(_run, commands[0], "g++ for %s" % BINDING_SRC)
+        for j in jobs:
+            j.result()
     if force or todo or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp"
         cmd = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
@@ -147,7 +167,13 @@ def build(force=False, verbose=False, extra_flags=()):
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
         os.replace(tmp, LIB_PATH)
-    if force or binding or _stale(BINDING_PATH, [binding_obj]):
+    if lacks is not None:
+        warnings.warn("_rf_serving.so, the binding of the paged serving calls, is not built: no "
+                      + lacks)
+        return LIB_PATH
+    if binding:
+        binding_job.result()
+    if binding or _stale(BINDING_PATH, [binding_obj]):
         _run(commands[1], "link of %s" % BINDING_PATH)
         os.replace(binding_tmp, BINDING_PATH)
         with open(binding_stamp, "w") as f:

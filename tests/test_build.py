@@ -1,5 +1,6 @@
-"""The build: what makes the serving binding stale. Nothing is compiled here; the
-commands are recorded."""
+"""The build: what makes the serving binding stale, and the C library on a machine
+that cannot build the binding. Nothing is compiled here; the commands are
+recorded."""
 
 import os
 import subprocess
@@ -23,6 +24,7 @@ def tree(tmp_path, monkeypatch):
     torch_dir = tmp_path / "torch"
     torch_dir.mkdir()
     (torch_dir / "version.py").write_text("__version__ = '1'")
+    (torch_dir / "include" / "ATen").mkdir(parents=True)
     monkeypatch.setattr(build, "_torch_dir", lambda: str(torch_dir))
     ran = []
 
@@ -79,3 +81,48 @@ def test_binding_is_rebuilt_for_another_python(tree, monkeypatch):
     monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "another")
     build.build()
     assert len(_binding(ran)) == len(ran) == 2
+
+
+@pytest.mark.parametrize("lacking", ["torch", "torch's headers", "Python.h", "g++"])
+def test_library_builds_where_the_binding_cannot(tree, monkeypatch, lacking):
+    tmp, ran = tree
+    if lacking == "torch":
+        def none():
+            raise RuntimeError("no torch")
+        monkeypatch.setattr(build, "_torch_dir", none)
+    elif lacking == "torch's headers":
+        os.rmdir(tmp / "torch" / "include" / "ATen")
+    elif lacking == "Python.h":
+        monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp / "none")})
+    else:
+        which = build.shutil.which
+        monkeypatch.setattr(build.shutil, "which", lambda n: None if n == "g++" else which(n))
+    with pytest.warns(UserWarning, match="_rf_serving.so.*not built: no " + lacking.replace("+", r"\+")):
+        assert build.build() == build.LIB_PATH
+    assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
+    assert len(ran) == len(build.sources()) + 1 and not _binding(ran)
+
+
+def test_library_is_linked_when_the_binding_fails(tree, monkeypatch):
+    _, ran = tree
+    run = subprocess.run
+
+    def fails(cmd, **kw):
+        done = run(cmd, **kw)
+        if _binding([cmd]):
+            done = type("Failed", (_Done,), {"returncode": 1, "stderr": "an error"})
+        return done
+
+    monkeypatch.setattr(subprocess, "run", fails)
+    with pytest.raises(RuntimeError, match="an error"):
+        build.build()
+    assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
+
+
+def test_serving_calls_raise_without_the_binding(monkeypatch, tmp_path):
+    from online_softmax_attention_rf_gb300 import api
+    build.build()
+    monkeypatch.setattr(api, "_SERVING", None)
+    monkeypatch.setattr(api._build, "BINDING_PATH", str(tmp_path / "none.so"))
+    with pytest.raises(RuntimeError, match="_rf_serving.so is not built"):
+        api.draft_verify(None, None, None, None, None)
