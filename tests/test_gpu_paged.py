@@ -756,6 +756,59 @@ def test_attn_paged_captured_step_follows_its_lengths(cuda_device):
         _check_attention(c, o, lse)
 
 
+def test_paged_steps_one_behind_the_other(cuda_device):
+    # steps enqueued without the host waiting for any of them: the inputs are
+    # rewritten by kernels directly ahead of each, the plan and the workspace are
+    # the same ones, and each step's results are those of the step by itself
+    H, Hkv, d, page, B, width = 8, 2, 64, 16, 6, 200
+    gen = torch.Generator().manual_seed(31)
+    pages = B * width
+    table = torch.randperm(pages, generator=gen).view(B, width).int().cuda()
+    filled = torch.randn(2, pages, page, Hkv, d, generator=gen).bfloat16().cuda()
+    cs = torch.randn(width * page, d, generator=gen).cuda()
+    steps = []
+    for i in range(6):
+        n = torch.randint(0, 4, (B,), generator=gen) if i % 2 else torch.ones(B, dtype=torch.long)
+        kv = torch.randint(4, width * page, (B,), generator=gen)
+        steps.append((_i32([0] + n.cumsum(0).tolist()), _i32(kv), torch.randn(
+            4 * B, H + 2 * Hkv, d, generator=gen).bfloat16().cuda()))
+    cu, kv_len, qkv = (torch.zeros_like(x) for x in steps[0])
+    pool = torch.empty_like(filled)
+
+    def step(cu, kv_len, qkv, plan, ws):
+        pos, slots = api.paged_slots(cu, kv_len, table, page, pages, 4 * B)
+        o = torch.zeros(4 * B, H, d, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(4 * B, H, device="cuda")
+        q = torch.zeros_like(o)
+        api.kv_append_paged(qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:], pool[0], pool[1], slots,
+                            pos, cs, q_out=q)
+        plan.update(cu, kv_len)
+        api.attn_paged(q, pool[0], pool[1], table, plan, out=o, lse=lse, workspace=ws)
+        return q, o, lse
+
+    def plan_of(cu, kv_len):
+        return api.PagedPlan(cu, kv_len, 4 * B, H, Hkv, page, width)
+
+    want = []
+    for s in steps:
+        pool.copy_(filled)
+        torch.cuda.synchronize()
+        want.append(step(*s, plan_of(*s[:2]), api.attn_paged_workspace(d)))
+        torch.cuda.synchronize()
+    plan, ws = plan_of(*steps[0][:2]), api.attn_paged_workspace(d)
+    got, order = [], [(i * i) % 6 for i in range(60)]
+    torch.cuda.synchronize()
+    for i in order:
+        torch.add(filled, 0, out=pool)
+        for x, y in zip((cu, kv_len, qkv), steps[i]):
+            torch.add(y, 0, out=x)
+        got.append(step(cu, kv_len, qkv, plan, ws))
+    torch.cuda.synchronize()
+    assert api.device_status() == 0
+    for i, g in zip(order, got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i]))
+
+
 def test_attn_paged_two_streams(cuda_device):
     # two calls in flight, a workspace each, on streams other than the tensors'
     cases = [_attention_case([(1, 4000), (3, 2500)], 8, 2, 128, 16, seed=20 + i) for i in range(2)]
