@@ -576,6 +576,9 @@ rf_status rf_paged_slots(const int32_t *cu_q, const int32_t *kv_len, const int32
  *      through. rot = 0: no rotation, pos and cos_sin are ignored.
  *  q_weight, k_weight: dtype dt [d], each may be NULL (no norm).
  * d and rot multiples of 16, d <= 256 (RF_ERR_UNSUPPORTED otherwise), rot <= d.
+ * More pools can be written than rf_attn_paged reads: that takes RF_BF16 with d
+ * 64 or 128 and pages of a multiple of 8 tokens. The other pools (float32, other
+ * d, smaller pages) are for a reader of the caller's own.
  * Pointers and strides in bytes 16-byte aligned (slots 8, pos 4). A slot or
  * position out of range skips the token and is reported through
  * rf_device_status. Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED, RF_ERR_CUDA.

@@ -699,7 +699,9 @@ def kv_append_paged(q, k, v, k_cache, v_cache, slots, pos=None, cos_sin=None, q_
     q [T, H, d] (or None), k, v [T, Hkv, d] (views of a fused projection fit),
     k_cache, v_cache [pages, page, Hkv, d] (any strides with d contiguous),
     slots int64 [T] (negative: skipped) -> q_out [T, H, d], or None without q.
-    q_out may be q itself when q is contiguous."""
+    q_out may be q itself when q is contiguous. bf16 or float32, d a multiple of
+    16 up to 256; ``attn_paged`` reads bf16 pools with d 64 or 128 and pages of a
+    multiple of 8 tokens only."""
     r = _serving().kv_append_paged(q, k, v, k_cache, v_cache, slots, pos, cos_sin, q_weight,
                                    k_weight, eps, interleaved, q_out)
     if r.__class__ is tuple:
@@ -768,8 +770,10 @@ def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse
     """rf_attn_paged: q [T, H, d] bf16 (a strided view of a fused projection
     fits), k_cache, v_cache [pages, page, Hkv, d] (any strides with d
     contiguous), block_table int32 [B, max_pages], plan a ``PagedPlan`` of the
-    step -> (o [T, H, d], lse float32 [T, H] or None). Rows outside every
-    sequence are left as they are (uninitialised without `out`)."""
+    step -> (o [T, H, d], lse float32 [T, H] or None). d 64 or 128, pages of a
+    multiple of 8 tokens. Rows outside every sequence are left as they are
+    (uninitialised without `out`). Without `workspace` each call takes a new one
+    from torch's allocator; a loop keeps one (``attn_paged_workspace``)."""
     if workspace is None:
         workspace = attn_paged_workspace(q.shape[-1], q.device)
     r = _serving().attn_paged(q, k_cache, v_cache, block_table, plan.buf, plan.B, plan.T, plan.H,

@@ -72,8 +72,9 @@ struct Layout {
   // entry coming from memory, the V producer would wait for a phase two ahead of
   // the slot's barrier, and the parity of that wait passes at once
   // (tests/test_paged_protocol.py). With a wait for the K tile it cost 2 % of a
-  // chunk; 2 + 3 slots: 2048 tokens at 32768 keys 1.41 ms, 3 + 2: 1.45, one ring
-  // of 5: 1.43. d = 64, 8 x 8 heads of 65536 keys: 6 + 6 slots 5.39 TB/s, 4 + 8
+  // chunk. Measured before the issuers' release and test became one walk: 2 + 3
+  // slots: 2048 tokens at 32768 keys 1.41 ms, 3 + 2: 1.45, one ring of 5: 1.43.
+  // d = 64, 8 x 8 heads of 65536 keys: 6 + 6 slots 5.39 TB/s (5.64 since), 4 + 8
   // 5.22, 5 + 7 5.19, 4 + 4 5.09.
   static constexpr int kSlotsK = (D == 128) ? 2 : 6;
   static constexpr int kSlotsV = (D == 128) ? 3 : 6;

@@ -139,11 +139,12 @@ __device__ __forceinline__ void take_greedy(Running& st, float x, int v) {
 }
 
 // One CTA: piece `split` of one logit row. Rows of sequence b: its S + 1
-// target rows, then its S draft rows. Bound by memory (each logit is read
-// once) with about 70 % of the issue slots: 16-byte loads, four in flight a
-// thread, packed float32 arithmetic; rows of any alignment (a row of an odd
-// vocabulary starts anywhere) by single numbers up to the first 16-byte
-// boundary and after the last.
+// target rows, then its S draft rows. Bound by the loads in flight (16 bytes,
+// four a thread, each logit read once): 29.9 us for the 151 MB of 64 sequences of
+// 4 drafts at V = 131072 in bf16, 5.06 TB/s, with 47 % of the issue slots; packed
+// float32 arithmetic; rows of any alignment (a row of an odd vocabulary starts
+// anywhere) by single numbers up to the first 16-byte boundary and after the
+// last.
 template <typename T>
 __global__ void __launch_bounds__(kStatThreads) stats_kernel(const VerifyArgs a, Stat* stats,
                                                              int nsplit, int piece) {
@@ -261,12 +262,13 @@ struct alignas(W * sizeof(T) < 16 ? W * sizeof(T) : 16) Pack {
 
 // One cluster per sequence. W: the numbers a thread loads at a time from each
 // row; every row starts on a boundary of W numbers. Bound by the latency of its
-// few rounds of loads: 23 us alone on cold caches for 64 sequences at
-// V = 131072, 35 % of the memory's rate; it reads 67 MB, part of it from L2.
-// The exponentials prefetched into L2 under stats_kernel bought nothing (47.9
-// us against 46.7 for both kernels): they take their bandwidth from it. Two
-// register sets against the compiler's unrolled loads: 12.3 us against 13.7 for
-// 16 sequences at an odd V = 50001.
+// few rounds of loads: 21.5 us alone on cold caches for 64 sequences at
+// V = 131072 in bf16, which read 64 MB, 38 % of the memory's rate; behind
+// stats_kernel, with part of that in L2, about 12. Measured when both kernels took
+// 46.7 us there: the exponentials prefetched into L2 under stats_kernel, 47.9 (they
+// take their bandwidth from it). Two register sets against the compiler's
+// unrolled loads, both kernels of 16 sequences at an odd V = 50001 (9.3 us today):
+// 12.3 us against 13.7.
 template <typename T, int W, int kThreads>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1024 / kThreads)
     choose_kernel(const VerifyArgs a, const Stat* stats, int nsplit) {
@@ -464,9 +466,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 102
 template <typename T, int W>
 cudaError_t launch_choose(const VerifyArgs& a, const Stat* stats, int nsplit, cudaStream_t s) {
   // as many threads a CTA as keep all clusters resident at once: with few
-  // sequences a sweep over the vocabulary then takes few rounds of loads
-  // (one sequence, V = 32000: 8.3 us at 512 threads, 11.4 at 256), with many
-  // there is no second wave (64 sequences, V = 131072: 30 us and 24)
+  // sequences a sweep over the vocabulary then takes few rounds of loads, with
+  // many there is no second wave. Both kernels, replayed, at 512 threads and at
+  // 256: one sequence, V = 32000, float32: 5.7 us and 6.5; 64 sequences,
+  // V = 131072, bf16: 46.0 and 42.0.
   const int ctas = a.B * kCluster;
   const bool few = ctas <= 2 * 152;
   return launch_pdl(few ? choose_kernel<T, W, 512> : choose_kernel<T, W, 256>, dim3(ctas),
@@ -477,9 +480,11 @@ template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, void* ws, cudaStream_t s) {
   Stat* stats = static_cast<Stat*>(ws);
   const int64_t rows = int64_t(a.B) * (a.draft != nullptr ? 2 * a.S + 1 : a.S + 1);
-  // enough pieces that the rows fill the SMs a few times over (more, smaller
-  // pieces pay their start more often: 16 times over, 49.5 us for 64 sequences
-  // at V = 131072, 5 times 47.1, 3 times 52), but pieces of at least 2048 logits
+  // enough pieces that the rows fill the SMs a few times over, but pieces of at
+  // least 2048 logits. Both kernels, replayed, at 3, 6, 8 and 16 times over: 64
+  // sequences of 4 drafts, V = 131072, bf16: 48.0, 42.0, 45.1, 44.9 us (4 and 5
+  // times give the same pieces as 6; more pieces pay their start more often); 16
+  // sequences of up to 7 copied drafts, V = 50001, float32: 9.7, 9.3, 8.8, 10.4.
   int64_t nsplit = (152 * 6 + rows - 1) / rows;
   nsplit = min64(min64(nsplit, kMaxSplits), (int64_t(a.V) + 2047) / 2048);
   // pieces of whole 16-byte groups

@@ -12,9 +12,14 @@ namespace {
 
 constexpr int kThreads = 1024;
 // Cost of an item, in units of 0.28 us: a fixed part (filling the pipeline and
-// writing the output) and a part per step, of items with two tiles (measured at
-// d = 128: 5 us, 1.7 us) and with one (3.4 us, 1.45 us: memory bounds the step
-// of a decode item).
+// writing the output) and a part per step. Set at d = 128. Two tiles: a step
+// measured at 1.7 us, the fixed part at 5 us (18 units); 22 units stand between
+// what the spans of six ragged chunks showed, 92 us on average: the longest 106
+// us at 18 units, 98 at 28 with the shortest down to 74. One tile: 3.4 us, and
+// 1.45 a step (memory bounds the step of a decode item). At d = 64, for which the
+// same costs are used, steps take 1.45 and 0.85 us: a one-tile step is charged
+// too much there, and by those times the longest span of a batch that mixes
+// chunks and single tokens is 16 % above the mean.
 constexpr int kPairFixed = 22;
 constexpr int kPairCost = 6;
 constexpr int kSingleFixed = 12;
