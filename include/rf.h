@@ -685,6 +685,192 @@ rf_status rf_draft_verify(const void *target, const void *draft, const int32_t *
                           rf_stream stream);
 
 /*
+ * A step whose new tokens are the nodes of trees (speculative decoding with
+ * several drafts for a place): the packed rows of sequence b are its nodes, in an
+ * order in which a node follows its parent; all of them are in the cache (their
+ * keys are the last n_b of kv_len[b]).
+ *
+ * rf_tree_mask writes each node's mask: bit j (of word j / 64, bit j % 64) tells
+ * whether it sees the sequence's node j: itself and its ancestors. And its
+ * position, kv_len[b] - n_b + depth (a root has depth 0; not below 0): the pos of
+ * rf_kv_append_paged (rf_paged_slots gives the slots).
+ *  parent int32 [T]: number of the parent within the sequence, -1 for a root;
+ *  cu_q int32 [B + 1], kv_len int32 [B] (NULL with pos NULL); all device;
+ *  mask uint64 [T, words], 1 <= words <= 16; pos int32 [T] or NULL.
+ * Rows outside every sequence get 0. A parent that does not come before its child
+ * makes the child a root, and a sequence of more than 64 * words nodes gets masks
+ * and positions of 0; both are reported through rf_device_status. B, T >= 0.
+ * Errors: RF_ERR_INVALID (sizes, NULL or misaligned pointers), RF_ERR_UNSUPPORTED
+ * (words > 16), RF_ERR_CUDA.
+ */
+rf_status rf_tree_mask(const int32_t *parent, const int32_t *cu_q, const int32_t *kv_len, int B,
+                       int T, int words, uint64_t *mask, int32_t *pos, rf_stream stream);
+
+/*
+ * rf_attn_paged with a tree's mask: a new token sees every key before the
+ * sequence's new ones (j < kv_len[b] - n_b), and of the new ones those whose bit
+ * is set in its mask (RedFuser, sections 2 and 3, as rf_attn_paged).
+ *  tree: uint64 [T, tree_words], 8-byte aligned, device; node j's bit is as
+ *        rf_tree_mask writes it; any other set of bits does as well (bits of
+ *        nodes that there are not are ignored, nodes behind the words' bits are
+ *        not seen). A row that sees no key gets O = 0 and lse = -inf.
+ *  plan: made with causal = 0 (a plan with causal = 1 computes nothing and is
+ *        reported through rf_device_status).
+ * 1 <= tree_words <= 2^24. Other arguments and errors as rf_attn_paged.
+ */
+rf_status rf_attn_paged_tree(const void *q, int64_t q_stride, const void *k_cache,
+                             int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             const void *v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                             int64_t v_head_stride, int page, int num_pages, const int32_t *table,
+                             int64_t table_stride, int max_pages, const void *plan, int B, int T,
+                             int H, int Hkv, int d, float scale, void *o, float *lse, float *ws,
+                             size_t ws_bytes, const uint64_t *tree, int tree_words, rf_dtype dt,
+                             rf_stream stream);
+
+/*
+ * The walk down each tree along the tokens that the target drew: from node 0, to
+ * the child that holds the token drawn at the present node, as long as there is
+ * one (the first by number, where several hold it). With the draws taken from the
+ * target's distribution at each node (rf_sample_rows over the nodes' logits) the
+ * emitted tokens follow that distribution.
+ *  parent, tokens, sampled int32 [T]: a node's parent (numbers above the node's
+ *      own are never followed), its drafted token, the token drawn at it (below
+ *      0: none; the walk ends);
+ *  cu_q int32 [B + 1], kv_len int32 [B] (with the nodes);
+ *  path, out int32 [T], written: at row cu_q[b] + i the i'th node of the walk and
+ *      the token drawn at it (the last one is the extra token), -1 behind its end
+ *      and in rows outside every sequence;
+ *  n_path int32 [B]: nodes of the walk (0 for a sequence without nodes);
+ *  base, new_len int32 [B]: kv_len[b] - n_b, and that plus n_path[b]: with path as
+ *      keep and n_path as n_keep the arguments of rf_kv_compact_paged, and the
+ *      cache's length after it.
+ * All device, 4-byte aligned. Offsets that are not ascending within [0, T] make a
+ * sequence empty and are reported through rf_device_status. B, T >= 0.
+ * Errors: RF_ERR_INVALID, RF_ERR_CUDA.
+ */
+rf_status rf_tree_accept(const int32_t *parent, const int32_t *tokens, const int32_t *sampled,
+                         const int32_t *cu_q, const int32_t *kv_len, int B, int T, int32_t *path,
+                         int32_t *out, int32_t *n_path, int32_t *base, int32_t *new_len,
+                         rf_stream stream);
+
+/*
+ * A token drawn from each row of logits, from given random numbers (the cascade
+ * of rf_softmax_rows, a selection, and a third reduction, argmax). Per row, with
+ * p = softmax(logits / temperature) over what is left after each step:
+ *   top_k: the k largest logits; top_p: of those, in descending order, the
+ *   shortest run whose probabilities (renormalised) reach top_p, at least one;
+ *   min_p: of those, the ones of at least min_p times the largest probability
+ *   (the largest always stays). Equal logits: the lower index comes first.
+ * The token is argmax_j p_j / expo[b, j] over what is left (lowest index on a
+ * tie), which with independent exponential variates is j with probability p_j.
+ *  logits : [B, V], dtype dt (RF_F32 or RF_BF16), rows `stride` elements apart;
+ *           -inf entries have no probability;
+ *  expo   : float [B, V], in [2^-126, 2^32] (as rf_draft_verify; not checked);
+ *  temperature: float [B], finite, or NULL (1); not above 0: greedy (the largest
+ *           logit, lowest index first; the limits and expo do not matter);
+ *  top_k  : int32 [B] or NULL; below 1 or at least V: no limit;
+ *  top_p  : float [B] or NULL; at least 1: no limit; not above 0: the largest;
+ *  min_p  : float [B] or NULL; not above 0: no limit; above 1: as 1;
+ *  token  : int32 [B]; logprob: float [B] or NULL: ln p of the token, p the
+ *           distribution that it was drawn from (0 for a greedy row).
+ * A row that gives no probabilities (all -inf, or a NaN or +inf in it) gets the
+ * token -1 and a NaN, and is reported through rf_device_status. 0 <= B <= 2^20,
+ * 1 <= V <= 2^20 (RF_ERR_UNSUPPORTED above), stride >= V where B > 1. Errors:
+ * RF_ERR_INVALID, RF_ERR_UNSUPPORTED, RF_ERR_CUDA.
+ */
+rf_status rf_sample_rows(const void *logits, int64_t stride, const float *expo,
+                         const float *temperature, const int32_t *top_k, const float *top_p,
+                         const float *min_p, int B, int V, int32_t *token, float *logprob,
+                         rf_dtype dt, rf_stream stream);
+
+/*
+ * A cache pool of all layers, as the calls below take it (read on the host during
+ * the call): the d elements of layer l, page P, token row r, key head h are at
+ * k + l * k_layer_stride + P * k_page_stride + r * k_token_stride + h *
+ * k_head_stride (elements), the same for v. Strides in bytes and both pointers
+ * 16-byte aligned, strides >= 0; d * element size a multiple of 16, d <= 1024.
+ * layers in [0, 32767] (0: nothing launched), Hkv, page, num_pages >= 1; page *
+ * num_pages and page * Hkv * d <= 2^31 - 1.
+ */
+typedef struct {
+  void *k, *v;
+  int64_t k_layer_stride, k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_layer_stride, v_page_stride, v_token_stride, v_head_stride;
+  int layers, num_pages, page, Hkv, d;
+  rf_dtype dt;
+} rf_kv_pool;
+
+/*
+ * Kept tokens moved together in the cache, in place, in all layers: row base[b] +
+ * keep[cu_keep[b] + i] of sequence b to row base[b] + i, i < n_keep[b]. For the
+ * accepted nodes of a tree (rf_tree_accept), or a long cache that drops tokens.
+ *  table int32 [B, max_pages], rows table_stride apart;
+ *  keep int32 [N], ascending and >= 0 within each sequence; cu_keep int32 [B + 1];
+ *  n_keep int32 [B] or NULL (cu_keep[b + 1] - cu_keep[b]); base int32 [B] or NULL
+ *  (0). All device.
+ * Rows behind the last kept one stay as they are, and those in place already are
+ * not touched. Offsets out of range, entries that do not ascend and rows without a
+ * page are skipped and reported through rf_device_status. Two sequences must not
+ * share a page that a row is moved to. B, N >= 0; B * Hkv <= 2^31 - 1. Errors:
+ * RF_ERR_INVALID, RF_ERR_UNSUPPORTED (d), RF_ERR_CUDA.
+ */
+rf_status rf_kv_compact_paged(const rf_kv_pool *pool, const int32_t *table, int64_t table_stride,
+                              int B, int max_pages, const int32_t *keep, int N,
+                              const int32_t *cu_keep, const int32_t *n_keep, const int32_t *base,
+                              rf_stream stream);
+
+/*
+ * Pages copied in all layers: page src[i] to page dst[i], i < n; a pair with
+ * either below 0 is skipped. src, dst int32 [n], device. No page may be the dst of
+ * one pair and in another one. Page numbers >= num_pages are skipped and reported
+ * through rf_device_status. 0 <= n <= 2^20. Errors: RF_ERR_INVALID,
+ * RF_ERR_UNSUPPORTED (d), RF_ERR_CUDA.
+ */
+rf_status rf_kv_copy_pages(const rf_kv_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                           rf_stream stream);
+
+/*
+ * The pages of a pool by their owners: refs int32 [num_pages] counts the rows of
+ * block tables that hold a page, 0: free. All pointers device; rows of a table are
+ * table_stride apart, lengths in tokens. Sequences share pages by these calls:
+ *
+ * rf_pages_fork makes row i of `out` a copy of row src[i] of `table` (its pages of
+ * len[src[i]] tokens; entries behind them stay) and gives each of its pages one
+ * owner more. len_out[i] = len[src[i]]. `out` must not overlap `table`. A src
+ * outside [0, B) or a bad length gives an empty row.
+ *
+ * rf_pages_grow gives the n rows of `table` the pages that new_len[i] tokens need
+ * where len[i] are there (a row that does not grow gets none). A partly filled last
+ * page with more than one owner is written to by none of them: the row gets a page
+ * of its own in its place (copy_src[i], copy_dst[i]: the page and its copy, for
+ * rf_kv_copy_pages; else -1, -1), but for the last of the rows that do so when
+ * they are all the owners there are. New pages are the free ones of the lowest
+ * numbers, handed out by ascending row and place. *left: the free pages left. When
+ * there are not enough it is the number that are missing, negative, and nothing
+ * else is changed (copy_src and copy_dst are -1). n <= 16384
+ * (RF_ERR_UNSUPPORTED above), num_pages <= 2^30.
+ *
+ * rf_pages_release takes one owner from each page of a row that lies behind its
+ * new_len[i] tokens (new_len NULL: 0, the whole row) where len[i] are there. The
+ * table is not changed.
+ *
+ * Lengths out of [0, max_pages * page], page numbers out of range and pages without
+ * an owner are skipped and reported through rf_device_status. B, n >= 0.
+ * Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED, RF_ERR_CUDA.
+ */
+rf_status rf_pages_fork(const int32_t *table, int64_t table_stride, const int32_t *len, int B,
+                        const int32_t *src, int n, int32_t *out, int64_t out_stride,
+                        int32_t *len_out, int32_t *refs, int max_pages, int page, int num_pages,
+                        rf_stream stream);
+rf_status rf_pages_grow(int32_t *table, int64_t table_stride, const int32_t *len,
+                        const int32_t *new_len, int n, int32_t *refs, int max_pages, int page,
+                        int num_pages, int32_t *copy_src, int32_t *copy_dst, int32_t *left,
+                        rf_stream stream);
+rf_status rf_pages_release(const int32_t *table, int64_t table_stride, const int32_t *len,
+                           const int32_t *new_len, int n, int32_t *refs, int max_pages, int page,
+                           int num_pages, rf_stream stream);
+
+/*
  * Test aid: when visited is non-NULL, every later rf_attn_fwd on this host
  * thread sets visited[((b*H + h) * nqt + qt) * nkt + kt] = 1 for each
  * 128 x 128 tile (qt, kt) whose scores it computes. The caller zeroes the

@@ -7,8 +7,7 @@ a non-OK status into ``RFError``. Every step of the computation runs in the
 library's kernels; nothing here computes, and there is no CPU fallback -- if
 the library is missing, every call raises.
 
-The calls of a serving loop (``kv_append_paged``, ``attn_paged``,
-``draft_verify``) go through a native module (csrc/serving_binding.cpp), which
+The calls of a serving loop (from ``kv_append_paged`` on) go through a native module (csrc/serving_binding.cpp), which
 does the same checks without Python's time for them; arguments that it does not
 accept come back here for the error that names them.
 """
@@ -42,6 +41,13 @@ class RFBlockMask(ctypes.Structure):
                 ("nkt", ctypes.c_int), ("row_ptr", ctypes.c_void_p), ("col_idx", ctypes.c_void_p),
                 ("per_head", ctypes.c_int), ("tile_bits", ctypes.c_void_p),
                 ("bits", ctypes.c_void_p), ("cta_order", ctypes.c_void_p)]
+
+
+class RFKvPool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + \
+        [("%s_%s_stride" % (c, d), ctypes.c_int64) for c in "kv"
+         for d in ("layer", "page", "token", "head")] + \
+        [(n, ctypes.c_int) for n in ("layers", "num_pages", "page", "Hkv", "d", "dt")]
 
 
 _LIB = None
@@ -95,6 +101,18 @@ SIGNATURES = {
     "rf_attn_paged_workspace_bytes": (_SZ, [_I]),
     "rf_attn_paged": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I, _P, _I64,
                            _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _I, _P]),
+    "rf_attn_paged_tree": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I, _P,
+                                _I64, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _I, _I,
+                                _P]),
+    "rf_tree_mask": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "rf_tree_accept": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "rf_sample_rows": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I, _I, _P, _P, _I, _P]),
+    "rf_kv_compact_paged": (_I, [ctypes.POINTER(RFKvPool), _P, _I64, _I, _I, _P, _I, _P, _P, _P,
+                                 _P]),
+    "rf_kv_copy_pages": (_I, [ctypes.POINTER(RFKvPool), _P, _P, _I, _P]),
+    "rf_pages_fork": (_I, [_P, _I64, _P, _I, _P, _I, _P, _I64, _P, _P, _I, _I, _I, _P]),
+    "rf_pages_grow": (_I, [_P, _I64, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "rf_pages_release": (_I, [_P, _I64, _P, _P, _I, _P, _I, _I, _I, _P]),
     "rf_draft_verify_workspace_bytes": (_SZ, [_I, _I]),
     "rf_draft_verify": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _SZ, _I, _P]),
     "rf_fp8_gemm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
@@ -745,8 +763,8 @@ def attn_paged_workspace(d, device="cuda"):
     return torch.empty(max(1, n // 4), dtype=torch.float32, device=device)
 
 
-def _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace):
-    _same_device(q, k_cache, v_cache, block_table, plan.buf, out, lse, workspace)
+def _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace, tree_mask):
+    _same_device(q, k_cache, v_cache, block_table, plan.buf, out, lse, workspace, tree_mask)
     if q.dim() != 3 or q.shape[:2] != (plan.T, plan.H):
         raise ValueError("q must be [%d, %d, d], as the plan was made for" % (plan.T, plan.H))
     T, H, d = q.shape
@@ -762,12 +780,16 @@ def _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace):
     _expect(lse, "lse", torch.float32, (T, H), optional=True)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    if tree_mask is not None:
+        _expect(tree_mask, "tree_mask", torch.int64, (T,) + tuple(tree_mask.shape[1:2]))
     raise ValueError("attn_paged: unsupported tensors")
 
 
 def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse=None,
-               with_lse=True, workspace=None):
-    """rf_attn_paged: q [T, H, d] bf16 (a strided view of a fused projection
+               with_lse=True, workspace=None, tree_mask=None):
+    """rf_attn_paged, or rf_attn_paged_tree with a tree_mask int64 [T, words] (bit j
+    of a token's words: it sees the sequence's new token j; ``tree_mask`` makes
+    it), which takes a plan made with causal=False: q [T, H, d] bf16 (a strided view of a fused projection
     fits), k_cache, v_cache [pages, page, Hkv, d] (any strides with d
     contiguous), block_table int32 [B, max_pages], plan a ``PagedPlan`` of the
     step -> (o [T, H, d], lse float32 [T, H] or None). d 64 or 128, pages of a
@@ -776,13 +798,15 @@ def attn_paged(q, k_cache, v_cache, block_table, plan, scale=None, out=None, lse
     from torch's allocator; a loop keeps one (``attn_paged_workspace``)."""
     if workspace is None:
         workspace = attn_paged_workspace(q.shape[-1], q.device)
+    if tree_mask is not None and plan.causal:
+        raise ValueError("attn_paged: a tree_mask takes a plan made with causal=False")
     r = _serving().attn_paged(q, k_cache, v_cache, block_table, plan.buf, plan.B, plan.T, plan.H,
                               plan.Hkv, plan.page, plan.max_pages, scale, out, lse, with_lse,
-                              workspace)
+                              workspace, tree_mask)
     if r.__class__ is tuple:
         return r
     if r is None:
-        _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace)
+        _refuse_attn(q, k_cache, v_cache, block_table, plan, out, lse, workspace, tree_mask)
     _check(r)
 
 
@@ -821,6 +845,174 @@ def draft_verify(target, draft, tokens, u, expo, n_draft=None, temperature=None,
     if r is None:
         _refuse_verify(target, draft, tokens, u, expo, n_draft, temperature, workspace)
     _check(r)
+
+
+def _returned(r, refuse, *args):
+    """What a native call returned; refuse(*args) names the fault of tensors that it
+    did not accept."""
+    if r is None:
+        refuse(*args)
+    if r.__class__ is not tuple:
+        _check(r)
+    return r
+
+
+def _refuse_nodes(fn, nodes, cu_q, kv_len):
+    _same_device(*nodes.values(), cu_q, kv_len)
+    if kv_len.dim() != 1 or nodes["parent"].dim() != 1:
+        raise ValueError("parent must be int32 [T] and kv_len int32 [B]")
+    for name, t in nodes.items():
+        _expect(t, name, torch.int32, (nodes["parent"].shape[0],))
+    _expect(kv_len, "kv_len", torch.int32, kv_len.shape)
+    _expect(cu_q, "cu_q", torch.int32, (kv_len.shape[0] + 1,))
+    raise ValueError("%s: unsupported tensors" % fn)
+
+
+def tree_mask(parent, cu_q, kv_len, words=1):
+    """rf_tree_mask: parent int32 [T] (a node's parent within its sequence, before
+    it; -1: a root), cu_q int32 [B + 1], kv_len int32 [B] (with the nodes) -> (mask
+    int64 [T, words] for ``attn_paged``, pos int32 [T] for ``kv_append_paged``).
+    Up to 64 * words nodes a sequence, words up to 16."""
+    return _returned(_serving().tree_mask(parent, cu_q, kv_len, words), _refuse_nodes, "tree_mask",
+                     {"parent": parent}, cu_q, kv_len)
+
+
+def tree_accept(parent, tokens, sampled, cu_q, kv_len):
+    """rf_tree_accept: the walk down each tree from node 0 along the tokens drawn at
+    its nodes. parent, tokens, sampled int32 [T], cu_q int32 [B + 1], kv_len int32
+    [B] (with the nodes) -> (path int32 [T]: the walk's nodes from row cu_q[b] on,
+    then -1; out int32 [T]: the tokens drawn at them; n_path, base, new_len int32
+    [B]). ``kv_compact_paged(k_cache, v_cache, block_table, path, cu_q, n_path,
+    base)`` then leaves new_len tokens in the cache."""
+    return _returned(_serving().tree_accept(parent, tokens, sampled, cu_q, kv_len), _refuse_nodes,
+                     "tree_accept", {"parent": parent, "tokens": tokens, "sampled": sampled}, cu_q,
+                     kv_len)
+
+
+def _refuse_sample(logits, expo, temperature, top_k, top_p, min_p):
+    _same_device(logits, expo, temperature, top_k, top_p, min_p)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [B, V] with contiguous rows")
+    _dt(logits)
+    B, V = logits.shape
+    _expect(expo, "expo", torch.float32, (B, V))
+    _expect(temperature, "temperature", torch.float32, (B,), optional=True)
+    _expect(top_k, "top_k", torch.int32, (B,), optional=True)
+    _expect(top_p, "top_p", torch.float32, (B,), optional=True)
+    _expect(min_p, "min_p", torch.float32, (B,), optional=True)
+    raise ValueError("sample_rows: unsupported tensors")
+
+
+def sample_rows(logits, expo, temperature=None, top_k=None, top_p=None, min_p=None):
+    """rf_sample_rows: a token drawn from each row of logits [B, V] (float32 or bf16;
+    rows may be strided), expo float32 [B, V] exponential variates (2^-126 to
+    2^32), temperature float32 [B] (0: greedy), top_k int32 [B] (0: no limit), top_p
+    float32 [B] (1: no limit), min_p float32 [B] (0: no limit) -> (token int32 [B],
+    logprob float32 [B] under the distribution that is left)."""
+    return _returned(_serving().sample_rows(logits, expo, temperature, top_k, top_p, min_p),
+                     _refuse_sample, logits, expo, temperature, top_k, top_p, min_p)
+
+
+def _refuse_pool(fn, k_cache, v_cache, block_table, ints):
+    _same_device(k_cache, v_cache, block_table, *(t for t, _ in ints.values()))
+    if k_cache.dim() not in (4, 5) or k_cache.shape != v_cache.shape or \
+            k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be pools [pages, page, Hkv, d] or "
+                         "[layers, pages, page, Hkv, d] of one shape and type")
+    _dt(k_cache)
+    if k_cache.stride(-1) != 1 or v_cache.stride(-1) != 1:
+        raise ValueError("the pools' last dimension must be contiguous")
+    if block_table is not None:
+        _expect_table(block_table, block_table.shape[0])
+    for name, (t, shape) in ints.items():
+        _expect(t, name, torch.int32, shape, optional=name in ("n_keep", "base"))
+    raise ValueError("%s: unsupported tensors" % fn)
+
+
+def kv_compact_paged(k_cache, v_cache, block_table, keep, cu_keep, n_keep=None, base=None):
+    """rf_kv_compact_paged: kept tokens of a paged cache moved together, in place:
+    row base[b] + keep[cu_keep[b] + i] to row base[b] + i, i < n_keep[b].
+
+    k_cache, v_cache [pages, page, Hkv, d] or [layers, pages, page, Hkv, d] (any
+    strides with d contiguous, bf16 or float32), block_table int32 [B, max_pages],
+    keep int32 [N] ascending within each sequence, cu_keep int32 [B + 1], n_keep
+    int32 [B] (None: all of the sequence's), base int32 [B] (None: 0)."""
+    r = _serving().kv_compact_paged(k_cache, v_cache, block_table, keep, cu_keep, n_keep, base)
+    if r is None:
+        B = block_table.shape[0]
+        _refuse_pool("kv_compact_paged", k_cache, v_cache, block_table,
+                     {"keep": (keep, (keep.numel(),)), "cu_keep": (cu_keep, (B + 1,)),
+                      "n_keep": (n_keep, (B,)), "base": (base, (B,))})
+    _returned(r, None)
+
+
+def kv_copy_pages(k_cache, v_cache, src, dst):
+    """rf_kv_copy_pages: page src[i] copied to page dst[i] (int32 [n]; a pair with a
+    negative number is skipped) in pools [pages, page, Hkv, d] or [layers, pages,
+    page, Hkv, d] (any strides with d contiguous, bf16 or float32). No page may be
+    the dst of one pair and in another one."""
+    r = _serving().kv_copy_pages(k_cache, v_cache, src, dst)
+    if r is None:
+        n = src.numel()
+        _refuse_pool("kv_copy_pages", k_cache, v_cache, None, {"src": (src, (n,)),
+                                                              "dst": (dst, (n,))})
+    _returned(r, None)
+
+
+def _refuse_pages(fn, tables, refs, ints):
+    _same_device(*(t for t, _ in tables), refs, *(t for t, _ in ints.values()))
+    for t, n in tables:
+        if t.dim() != 2 or t.shape[0] != n:
+            raise ValueError("a block table must be int32 [%d, max_pages]" % n)
+        _expect_table(t, n)
+    if tables[0][0].shape[1] != tables[-1][0].shape[1]:
+        raise ValueError("the block tables must be of one width")
+    _expect(refs, "refs", torch.int32, (refs.numel(),))
+    for name, (t, shape) in ints.items():
+        _expect(t, name, torch.int32, shape,
+                optional=name == "new_len" and fn == "pages_release")
+    raise ValueError("%s: unsupported tensors" % fn)
+
+
+def pages_fork(block_table, kv_len, src, out, refs, page_size):
+    """rf_pages_fork: row i of ``out`` int32 [n, max_pages] becomes a copy of row
+    src[i] of block_table int32 [B, max_pages], and each of its pages gets an owner
+    more in refs int32 [num_pages] -> kv_len[src] int32 [n]. ``pages_grow`` gives
+    the rows pages of their own before they are written to."""
+    r = _serving().pages_fork(block_table, kv_len, src, out, refs, page_size)
+    if r is None:
+        B, n = kv_len.numel(), src.numel()
+        _refuse_pages("pages_fork", [(block_table, B), (out, n)], refs,
+                      {"kv_len": (kv_len, (B,)), "src": (src, (n,))})
+    return _returned(r, None)[0]
+
+
+def pages_grow(block_table, kv_len, new_len, refs, page_size):
+    """rf_pages_grow: the pages that new_len int32 [n] tokens need where kv_len int32
+    [n] are there, written into block_table int32 [n, max_pages] and refs int32
+    [num_pages] -> (copy_src int32 [n], copy_dst int32 [n], left int32 [1]). A
+    partly filled last page that has other owners is replaced: ``kv_copy_pages(
+    k_cache, v_cache, copy_src, copy_dst)`` has to follow before the row is used.
+    left: free pages that remain, or, below 0, that are missing; then nothing was
+    changed."""
+    r = _serving().pages_grow(block_table, kv_len, new_len, refs, page_size)
+    if r is None:
+        n = kv_len.numel()
+        _refuse_pages("pages_grow", [(block_table, n)], refs,
+                      {"kv_len": (kv_len, (n,)), "new_len": (new_len, (n,))})
+    return _returned(r, None)
+
+
+def pages_release(block_table, kv_len, refs, page_size, new_len=None):
+    """rf_pages_release: each page of a row behind its new_len int32 [n] tokens (None:
+    0) of kv_len int32 [n] loses an owner in refs int32 [num_pages]; pages without
+    one are free. The table keeps its entries."""
+    r = _serving().pages_release(block_table, kv_len, refs, page_size, new_len)
+    if r is None:
+        n = kv_len.numel()
+        _refuse_pages("pages_release", [(block_table, n)], refs,
+                      {"kv_len": (kv_len, (n,)), "new_len": (new_len, (n,))})
+    _returned(r, None)
 
 
 def set_debug_visited(buf):

@@ -108,7 +108,8 @@ struct Seg {
   int slot;        // partial slot, -1: the whole item
   int mode;
   int q;           // Q ring number of the first tile
-  int pad[3];
+  int ctx;         // cached tokens before the sequence's new ones (below 0: more new than cached)
+  int pad[2];
 };
 static_assert(sizeof(Seg) == 64, "descriptor size");
 
@@ -171,10 +172,26 @@ struct Params {
   // half-written sectors a store: 8 us a pair of tiles).
   float* o_part;    // [2 * kPlanCtas][2][D / 4][128][4]
   float* lse_part;  // [2 * kPlanCtas][2][128]
+  // A tree's mask: bit j of a packed token's words tells whether it sees the
+  // sequence's new token j (32 bits at a time; nullptr: the plan's mask).
+  const uint32_t* tree;
+  int tree_words;   // of 32 bits, a token
   int* status;
 };
 
+// 32 keys' visibility to a token, the first of them `at` keys behind the
+// context's end (below 0: in the context): one funnel shift of its mask words.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int at) {
+  if (at <= -32) return 0xffffffffu;
+  const int w = at >> 5;  // -1 for a word that begins in the context
+  const uint32_t lo = w < 0 ? 0xffffffffu : w < words ? __ldg(row + w) : 0u;
+  const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, at & 31);
+}
+
 __device__ __forceinline__ bool plan_matches(const PlanHeader* h, const Params& p) {
+  // a tree's mask stands in the place of the causal one
+  if (p.tree != nullptr && h->causal != 0) return false;
   return h->magic == kPlanMagic && h->B == p.B && h->T == p.T && h->H == p.H && h->Hkv == p.Hkv &&
          h->page == p.page && h->max_pages == p.max_pages;
 }
@@ -227,6 +244,7 @@ struct Span {
     s.ntok = min(2 * tt, n - tok0);
     s.row0 = t0 + tok0;
     s.kv = kv;
+    s.ctx = kv - n;
     s.lim0 = causal ? kv - n + tok0 + 1 : kv;
     const int steps = steps_of(s.ntok - 1, s);
     s.kb = cur.step;
@@ -389,7 +407,10 @@ __device__ __forceinline__ void put32(const RowOut& w, int c, const float (&v)[3
   }
 }
 
-template <int D>
+// Tree: the new tokens are the nodes of trees. Only the last key tiles, which
+// hold new tokens, ask for a mask: four words of 32 bits a row, fetched while
+// the scores are computed.
+template <int D, bool Tree>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -813,10 +834,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys this row sees, and the fewest any row of the tile sees; a row that
       // holds no token computes on whatever is there and is not written
       const int row_lim = !row_ok || !causal ? s.kv : max(0, s.lim0 + tok);
-      const int first_lim = causal ? max(0, s.lim0 + tile * p.tt) : s.kv;
+      const int first_lim = Tree ? max(0, s.ctx) : causal ? max(0, s.lim0 + tile * p.tt) : s.kv;
+      const uint32_t* tree = nullptr;
+      if constexpr (Tree) {
+        if (row_ok) tree = p.tree + int64_t(s.row0 + tok) * p.tree_words;
+      }
       float m_run = kNegInf, l_run = 0.f;
       for (int jj = 0; jj < n; ++jj, ++j) {
         const int u = s.kb + (s.mode == kSplit ? 2 * jj + t : jj);
+        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if constexpr (Tree) {
+          if (tree != nullptr && first_lim - u * kBN < kBN) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              seen[i] = tree_bits(tree, p.tree_words, u * kBN + 32 * i - s.ctx);
+          }
+        }
         if (ok && warp_ok)
           ok = mbar_wait_warp(&bar.s_full[t], j & 1, p.status,
                               dev_code(kDevTimeout, kKerPaged, 30), abort_flag);
@@ -824,14 +857,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           const int k0 = u * kBN;
           const int lim = (first_lim - k0 < kBN) ? max(0, min(kBN, row_lim - k0)) : kBN;
+          const bool masked = Tree ? first_lim - k0 < kBN : lim < kBN;
           float mx;
           {
             uint32_t sr[128];
             tmem_ld128_wait(tm_s, sr);
-            if (lim < kBN) {
+            if (masked) {
 #pragma unroll
               for (int c = 0; c < kBN; ++c)
-                if (c >= lim) sr[c] = __float_as_uint(kNegInf);
+                if (c >= lim || (Tree && !(seen[c >> 5] >> (c & 31) & 1))) sr[c] = __float_as_uint(kNegInf);
             }
             float m8[8];
 #pragma unroll
@@ -857,10 +891,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             uint32_t sh1[64];
             tmem_ld64_wait(tm_s + 64 * h, sh1);
-            if (lim < kBN) {
+            if (masked) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
-                if (64 * h + c >= lim) sh1[c] = __float_as_uint(kNegInf);
+                if (64 * h + c >= lim ||
+                    (Tree && !((h == 0 ? seen[c >> 5] : seen[2 + (c >> 5)]) >> (c & 31) & 1)))
+                  sh1[c] = __float_as_uint(kNegInf);
             }
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
@@ -1045,7 +1081,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) attn_paged_merge(const Param
     table[i] = __ldcg(reinterpret_cast<const int4*>(p.plan->merge) + i);
   __syncthreads();
   const PlanMerge* merge = reinterpret_cast<const PlanMerge*>(table);
-  const bool matches = head[0] == kPlanMagic && head[1] == p.B && head[2] == p.T && head[3] == p.H &&
+  const bool matches = (p.tree == nullptr || head[7] == 0) && head[0] == kPlanMagic && head[1] == p.B && head[2] == p.T && head[3] == p.H &&
                        head[4] == p.Hkv && head[5] == p.page && head[6] == p.max_pages;
   const int n_merge = matches ? head[9] : 0;
   const int tasks = matches ? head[10] * kGroups : 0;
@@ -1152,7 +1188,7 @@ bool make_cache_map(CUtensorMap* m, const void* base, const PagedAttnArgs& a, in
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
-template <int D>
+template <int D, bool Tree>
 cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
   Params p{};
   p.plan = static_cast<const PlanHeader*>(a.plan);
@@ -1169,6 +1205,8 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
   p.o_wide = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
   p.o_part = a.ws;
   p.lse_part = a.ws + size_t(2) * kPlanCtas * kPlanRows * D;
+  p.tree = reinterpret_cast<const uint32_t*>(a.tree);
+  p.tree_words = 2 * a.tree_words;
   p.status = a.status;
   CUtensorMap mq, mk, mv;
   // query rows packed (head in group, key head, token): strides ascend
@@ -1182,13 +1220,13 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
     return cudaErrorInvalidValue;
   }
   constexpr int smem = Layout<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<D>,
+  cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<D, Tree>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) {
     *why = "shared memory attribute";
     return e;
   }
-  e = launch_pdl(attn_paged_kernel<D>, dim3(kPlanCtas), dim3(kThreads), smem, s, mq, mk, mv, p);
+  e = launch_pdl(attn_paged_kernel<D, Tree>, dim3(kPlanCtas), dim3(kThreads), smem, s, mq, mk, mv, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_paged_merge<D>, dim3(kMergeBlocks), dim3(kMergeThreads), 0, s, p);
 }
@@ -1196,7 +1234,9 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
 }  // namespace
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t s, const char** why) {
-  return a.d == 128 ? launch_d<128>(a, s, why) : launch_d<64>(a, s, why);
+  if (a.tree != nullptr)
+    return a.d == 128 ? launch_d<128, true>(a, s, why) : launch_d<64, true>(a, s, why);
+  return a.d == 128 ? launch_d<128, false>(a, s, why) : launch_d<64, false>(a, s, why);
 }
 
 }  // namespace rf

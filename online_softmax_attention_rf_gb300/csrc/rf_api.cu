@@ -243,6 +243,108 @@ rf_status check_heads(const char* fn, int H, int Hkv) {
   return RF_OK;
 }
 
+// The shared arguments of the two paged attentions (tree: NULL for rf_attn_paged).
+rf_status attn_paged(const char* fn, const void* q, int64_t q_stride, const void* k_cache,
+                        int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        const void* v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, int page, int num_pages, const int32_t* table,
+                        int64_t table_stride, int max_pages, const void* plan, int B, int T, int H,
+                        int Hkv, int d, float scale, void* o, float* lse, float* ws,
+                        size_t ws_bytes, const uint64_t* tree, int tree_words, rf_dtype dt, rf_stream stream) {
+  rf_status chk = check_pool(fn, B, T, page, num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  chk = check_heads(fn, H, Hkv);
+  if (chk != RF_OK) return chk;
+  if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
+  if (dt != RF_BF16 || (d != 64 && d != 128))
+    return fail(RF_ERR_UNSUPPORTED, "%s: bf16 with d in {64,128} only", fn);
+  if (page % 8 != 0) return fail(RF_ERR_UNSUPPORTED, "%s: page must be a multiple of 8", fn);
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(RF_ERR_INVALID, "%s: scale must be finite and > 0", fn);
+  if (T == 0 || B == 0) return ok();
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || table == nullptr ||
+      plan == nullptr || o == nullptr || ws == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
+    return fail(RF_ERR_INVALID, "%s: q, k_cache, v_cache and o must be 16-byte aligned", fn);
+  if (!aligned(table, 4) || !aligned(lse, 4) || !aligned(plan, 256) || !aligned(ws, 256))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer (plan, ws: 256 bytes)", fn);
+  const int64_t strides[] = {q_stride,      k_page_stride, k_token_stride, k_head_stride,
+                             v_page_stride, v_token_stride, v_head_stride};
+  for (int64_t x : strides)
+    if (x <= 0 || x % 8 != 0 || x >= (int64_t(1) << 38))
+      return fail(RF_ERR_INVALID, "%s: strides must be positive multiples of 8 elements", fn);
+  if (q_stride < int64_t(H) * d && T > 1)
+    return fail(RF_ERR_INVALID, "%s: q_stride < H * d", fn);
+  if (table_stride < max_pages && B > 1)
+    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
+  if (ws_bytes < rf_attn_paged_workspace_bytes(d))
+    return fail(RF_ERR_INVALID, "%s: workspace too small (%zu < %zu)", fn, ws_bytes,
+                rf_attn_paged_workspace_bytes(d));
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::PagedAttnArgs a{};
+  a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.page = page; a.num_pages = num_pages; a.table = table; a.table_stride = table_stride;
+  a.max_pages = max_pages; a.plan = plan;
+  a.B = B; a.T = T; a.H = H; a.Hkv = Hkv; a.d = d; a.scale = scale;
+  a.o = o; a.lse = lse; a.ws = ws; a.tree = tree; a.tree_words = tree_words; a.status = st;
+  const char* why = nullptr;
+  cudaError_t e = rf::launch_attn_paged(a, reinterpret_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why != nullptr)
+    return fail(RF_ERR_CUDA, "%s: %s: %s", fn, why, cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(RF_ERR_CUDA, "%s: launch: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+  return ok();
+}
+
+// A pool's sizes and strides, checked and turned to bytes.
+rf_status read_pool(const char* fn, const rf_kv_pool* p, rf::Pool* out) {
+  if (p == nullptr) return fail(RF_ERR_INVALID, "%s: pool is NULL", fn);
+  if (p->dt != RF_F32 && p->dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
+  const rf_status chk = check_pool(fn, 0, 0, p->page, p->num_pages, 1);
+  if (chk != RF_OK) return chk;
+  if (p->layers < 0 || p->layers > 32767 || p->Hkv < 1 || p->d < 1)
+    return fail(RF_ERR_INVALID, "%s: bad sizes layers=%d Hkv=%d d=%d", fn, p->layers, p->Hkv, p->d);
+  const int64_t es = p->dt == RF_F32 ? 4 : 2;
+  if (p->d * es % 16 != 0 || p->d > 1024)
+    return fail(RF_ERR_UNSUPPORTED, "%s: d must be a multiple of 16 bytes, at most 1024", fn);
+  if (int64_t(p->page) * p->Hkv > INT32_MAX / p->d)
+    return fail(RF_ERR_INVALID, "%s: page * Hkv * d > 2^31-1", fn);
+  const int64_t strides[] = {p->k_layer_stride, p->k_page_stride, p->k_token_stride,
+                             p->k_head_stride,  p->v_layer_stride, p->v_page_stride,
+                             p->v_token_stride, p->v_head_stride};
+  for (int64_t x : strides)
+    if (x < 0 || x * es % 16 != 0 || x >= (int64_t(1) << 40))
+      return fail(RF_ERR_INVALID, "%s: strides must be multiples of 16 bytes", fn);
+  const int64_t row = p->d * es;
+  auto side = [&](void* base, int64_t layer, int64_t page, int64_t token, int64_t head) {
+    rf::PoolSide s{static_cast<char*>(base), layer * es, page * es, token * es, head * es, 0};
+    const bool tokens = (p->Hkv == 1 || s.head == row) && (p->page == 1 || s.token == row * p->Hkv);
+    const bool heads = (p->page == 1 || s.token == row) && (p->Hkv == 1 || s.head == row * p->page);
+    s.dense = tokens || heads;
+    return s;
+  };
+  out->k = side(p->k, p->k_layer_stride, p->k_page_stride, p->k_token_stride, p->k_head_stride);
+  out->v = side(p->v, p->v_layer_stride, p->v_page_stride, p->v_token_stride, p->v_head_stride);
+  out->layers = p->layers;
+  out->num_pages = p->num_pages;
+  out->page = p->page;
+  out->Hkv = p->Hkv;
+  out->row16 = static_cast<int>(row / 16);
+  return RF_OK;
+}
+
+rf_status check_pool_pointers(const char* fn, const rf_kv_pool* p) {
+  if (p->k == nullptr || p->v == nullptr) return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(p->k, 16) || !aligned(p->v, 16))
+    return fail(RF_ERR_INVALID, "%s: the pool's k and v must be 16-byte aligned", fn);
+  return RF_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -806,56 +908,31 @@ rf_status rf_attn_paged(const void* q, int64_t q_stride, const void* k_cache,
                         int64_t table_stride, int max_pages, const void* plan, int B, int T, int H,
                         int Hkv, int d, float scale, void* o, float* lse, float* ws,
                         size_t ws_bytes, rf_dtype dt, rf_stream stream) {
-  const char* fn = "rf_attn_paged";
-  rf_status chk = check_pool(fn, B, T, page, num_pages, max_pages);
-  if (chk != RF_OK) return chk;
-  chk = check_heads(fn, H, Hkv);
-  if (chk != RF_OK) return chk;
-  if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
-  if (dt != RF_BF16 || (d != 64 && d != 128))
-    return fail(RF_ERR_UNSUPPORTED, "%s: bf16 with d in {64,128} only", fn);
-  if (page % 8 != 0) return fail(RF_ERR_UNSUPPORTED, "%s: page must be a multiple of 8", fn);
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return fail(RF_ERR_INVALID, "%s: scale must be finite and > 0", fn);
-  if (T == 0 || B == 0) return ok();
-  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || table == nullptr ||
-      plan == nullptr || o == nullptr || ws == nullptr)
-    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
-    return fail(RF_ERR_INVALID, "%s: q, k_cache, v_cache and o must be 16-byte aligned", fn);
-  if (!aligned(table, 4) || !aligned(lse, 4) || !aligned(plan, 256) || !aligned(ws, 256))
-    return fail(RF_ERR_INVALID, "%s: misaligned pointer (plan, ws: 256 bytes)", fn);
-  const int64_t strides[] = {q_stride,      k_page_stride, k_token_stride, k_head_stride,
-                             v_page_stride, v_token_stride, v_head_stride};
-  for (int64_t x : strides)
-    if (x <= 0 || x % 8 != 0 || x >= (int64_t(1) << 38))
-      return fail(RF_ERR_INVALID, "%s: strides must be positive multiples of 8 elements", fn);
-  if (q_stride < int64_t(H) * d && T > 1)
-    return fail(RF_ERR_INVALID, "%s: q_stride < H * d", fn);
-  if (table_stride < max_pages && B > 1)
-    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
-  if (ws_bytes < rf_attn_paged_workspace_bytes(d))
-    return fail(RF_ERR_INVALID, "%s: workspace too small (%zu < %zu)", fn, ws_bytes,
-                rf_attn_paged_workspace_bytes(d));
-  int* st = rf::status_word();
-  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
-  rf::PagedAttnArgs a{};
-  a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache;
-  a.k_page_stride = k_page_stride; a.k_token_stride = k_token_stride;
-  a.k_head_stride = k_head_stride;
-  a.v_page_stride = v_page_stride; a.v_token_stride = v_token_stride;
-  a.v_head_stride = v_head_stride;
-  a.page = page; a.num_pages = num_pages; a.table = table; a.table_stride = table_stride;
-  a.max_pages = max_pages; a.plan = plan;
-  a.B = B; a.T = T; a.H = H; a.Hkv = Hkv; a.d = d; a.scale = scale;
-  a.o = o; a.lse = lse; a.ws = ws; a.status = st;
-  const char* why = nullptr;
-  cudaError_t e = rf::launch_attn_paged(a, reinterpret_cast<cudaStream_t>(stream), &why);
-  if (e != cudaSuccess && why != nullptr)
-    return fail(RF_ERR_CUDA, "%s: %s: %s", fn, why, cudaGetErrorString(e));
-  if (e != cudaSuccess) return cuda_fail(e, "rf_attn_paged: launch");
-  return ok();
+  return attn_paged("rf_attn_paged", q, q_stride, k_cache, k_page_stride, k_token_stride,
+                    k_head_stride, v_cache, v_page_stride, v_token_stride, v_head_stride, page,
+                    num_pages, table, table_stride, max_pages, plan, B, T, H, Hkv, d, scale, o, lse,
+                    ws, ws_bytes, nullptr, 0, dt, stream);
 }
+
+rf_status rf_attn_paged_tree(const void* q, int64_t q_stride, const void* k_cache,
+                             int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             const void* v_cache, int64_t v_page_stride, int64_t v_token_stride,
+                             int64_t v_head_stride, int page, int num_pages, const int32_t* table,
+                             int64_t table_stride, int max_pages, const void* plan, int B, int T,
+                             int H, int Hkv, int d, float scale, void* o, float* lse, float* ws,
+                             size_t ws_bytes, const uint64_t* tree, int tree_words, rf_dtype dt,
+                             rf_stream stream) {
+  const char* fn = "rf_attn_paged_tree";
+  if (tree_words < 1 || tree_words > (1 << 24))
+    return fail(RF_ERR_INVALID, "%s: need 1 <= tree_words <= 2^24", fn);
+  if (T > 0 && B > 0 && (tree == nullptr || !aligned(tree, 8)))
+    return fail(RF_ERR_INVALID, "%s: tree must be given and 8-byte aligned", fn);
+  return attn_paged(fn, q, q_stride, k_cache, k_page_stride, k_token_stride, k_head_stride, v_cache,
+                    v_page_stride, v_token_stride, v_head_stride, page, num_pages, table,
+                    table_stride, max_pages, plan, B, T, H, Hkv, d, scale, o, lse, ws, ws_bytes,
+                    tree, tree_words, dt, stream);
+}
+
 
 size_t rf_draft_verify_workspace_bytes(int B, int S) {
   if (B < 1 || S < 1 || S > rf::kMaxDrafts) return 0;
@@ -894,6 +971,217 @@ rf_status rf_draft_verify(const void* target, const void* draft, const int32_t* 
   a.B = B; a.S = S; a.V = V; a.out = out; a.n_accepted = n_accepted; a.status = st;
   cudaError_t e = rf::launch_draft_verify(a, dt, ws, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rf_draft_verify: launch");
+  return ok();
+}
+
+rf_status rf_tree_mask(const int32_t* parent, const int32_t* cu_q, const int32_t* kv_len, int B,
+                       int T, int words, uint64_t* mask, int32_t* pos, rf_stream stream) {
+  const char* fn = "rf_tree_mask";
+  if (words < 1) return fail(RF_ERR_INVALID, "%s: words < 1", fn);
+  const rf_status chk = check_pool(fn, B, T, 1, 1, 1);
+  if (chk != RF_OK) return chk;
+  if (words > rf::kMaxTreeWords)
+    return fail(RF_ERR_UNSUPPORTED, "%s: words > %d", fn, rf::kMaxTreeWords);
+  if (B == 0 || T == 0) return ok();
+  if (parent == nullptr || cu_q == nullptr || mask == nullptr || (pos != nullptr && kv_len == nullptr))
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(parent, 4) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(mask, 8) ||
+      !aligned(pos, 4))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::TreeMaskArgs a{};
+  a.parent = parent; a.cu_q = cu_q; a.kv_len = kv_len;
+  a.B = B; a.T = T; a.words = words; a.mask = mask; a.pos = pos; a.status = st;
+  cudaError_t e = rf::launch_tree_mask(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_tree_mask: launch");
+  return ok();
+}
+
+rf_status rf_tree_accept(const int32_t* parent, const int32_t* tokens, const int32_t* sampled,
+                         const int32_t* cu_q, const int32_t* kv_len, int B, int T, int32_t* path,
+                         int32_t* out, int32_t* n_path, int32_t* base, int32_t* new_len,
+                         rf_stream stream) {
+  const char* fn = "rf_tree_accept";
+  const rf_status chk = check_pool(fn, B, T, 1, 1, 1);
+  if (chk != RF_OK) return chk;
+  if (B == 0) return ok();
+  if (cu_q == nullptr || kv_len == nullptr || n_path == nullptr || base == nullptr ||
+      new_len == nullptr ||
+      (T > 0 && (parent == nullptr || tokens == nullptr || sampled == nullptr || path == nullptr ||
+                 out == nullptr)))
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  const void* ptrs[] = {parent, tokens, sampled, cu_q, kv_len, path, out, n_path, base, new_len};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::TreeAcceptArgs a{};
+  a.parent = parent; a.tokens = tokens; a.sampled = sampled; a.cu_q = cu_q; a.kv_len = kv_len;
+  a.B = B; a.T = T; a.path = path; a.out = out; a.n_path = n_path; a.base = base;
+  a.new_len = new_len; a.status = st;
+  cudaError_t e = rf::launch_tree_accept(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_tree_accept: launch");
+  return ok();
+}
+
+rf_status rf_sample_rows(const void* logits, int64_t stride, const float* expo,
+                         const float* temperature, const int32_t* top_k, const float* top_p,
+                         const float* min_p, int B, int V, int32_t* token, float* logprob,
+                         rf_dtype dt, rf_stream stream) {
+  const char* fn = "rf_sample_rows";
+  if (B < 0 || V < 1) return fail(RF_ERR_INVALID, "%s: bad sizes B=%d V=%d", fn, B, V);
+  if (dt != RF_F32 && dt != RF_BF16) return fail(RF_ERR_INVALID, "%s: bad dtype", fn);
+  if (V > rf::kMaxSampleVocab) return fail(RF_ERR_UNSUPPORTED, "%s: V > 2^20", fn);
+  if (B > (1 << 20)) return fail(RF_ERR_INVALID, "%s: B > 2^20", fn);
+  if (B == 0) return ok();
+  if (B > 1 && (stride < V || stride > (int64_t(1) << 38)))
+    return fail(RF_ERR_INVALID, "%s: rows overlap, or lie too far apart", fn);
+  if (logits == nullptr || expo == nullptr || token == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(logits, dt == RF_F32 ? 4 : 2) || !aligned(expo, 4) || !aligned(temperature, 4) ||
+      !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(token, 4) ||
+      !aligned(logprob, 4))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  int* st = rf::status_word();
+  if (st == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  rf::SampleArgs a{};
+  a.logits = logits; a.stride = B > 1 ? stride : V; a.expo = expo; a.temperature = temperature;
+  a.top_k = top_k; a.top_p = top_p; a.min_p = min_p;
+  a.B = B; a.V = V; a.token = token; a.logprob = logprob; a.status = st;
+  cudaError_t e = rf::launch_sample_rows(a, dt, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_sample_rows: launch");
+  return ok();
+}
+
+rf_status rf_kv_compact_paged(const rf_kv_pool* pool, const int32_t* table, int64_t table_stride,
+                              int B, int max_pages, const int32_t* keep, int N,
+                              const int32_t* cu_keep, const int32_t* n_keep, const int32_t* base,
+                              rf_stream stream) {
+  const char* fn = "rf_kv_compact_paged";
+  rf::CompactArgs a{};
+  rf_status chk = read_pool(fn, pool, &a.pool);
+  if (chk != RF_OK) return chk;
+  chk = check_pool(fn, B, N, pool->page, pool->num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  if (int64_t(B) * pool->Hkv > INT32_MAX) return fail(RF_ERR_INVALID, "%s: B * Hkv > 2^31-1", fn);
+  if (B == 0 || N == 0 || pool->layers == 0) return ok();
+  chk = check_pool_pointers(fn, pool);
+  if (chk != RF_OK) return chk;
+  if (table == nullptr || keep == nullptr || cu_keep == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(table, 4) || !aligned(keep, 4) || !aligned(cu_keep, 4) || !aligned(n_keep, 4) ||
+      !aligned(base, 4))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  if (table_stride < max_pages && B > 1)
+    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
+  a.status = rf::status_word();
+  if (a.status == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  a.table = table; a.table_stride = table_stride;
+  a.B = B; a.N = N; a.max_pages = max_pages;
+  a.keep = keep; a.cu_keep = cu_keep; a.n_keep = n_keep; a.base = base;
+  cudaError_t e = rf::launch_kv_compact(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_kv_compact_paged: launch");
+  return ok();
+}
+
+rf_status rf_kv_copy_pages(const rf_kv_pool* pool, const int32_t* src, const int32_t* dst, int n,
+                           rf_stream stream) {
+  const char* fn = "rf_kv_copy_pages";
+  rf::CopyPagesArgs a{};
+  rf_status chk = read_pool(fn, pool, &a.pool);
+  if (chk != RF_OK) return chk;
+  if (n < 0 || n > (1 << 20)) return fail(RF_ERR_INVALID, "%s: need 0 <= n <= 2^20", fn);
+  if (n == 0 || pool->layers == 0) return ok();
+  chk = check_pool_pointers(fn, pool);
+  if (chk != RF_OK) return chk;
+  if (src == nullptr || dst == nullptr) return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(src, 4) || !aligned(dst, 4))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  a.status = rf::status_word();
+  if (a.status == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  a.src = src; a.dst = dst; a.n = n;
+  cudaError_t e = rf::launch_kv_copy_pages(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_kv_copy_pages: launch");
+  return ok();
+}
+
+rf_status rf_pages_fork(const int32_t* table, int64_t table_stride, const int32_t* len, int B,
+                        const int32_t* src, int n, int32_t* out, int64_t out_stride,
+                        int32_t* len_out, int32_t* refs, int max_pages, int page, int num_pages,
+                        rf_stream stream) {
+  const char* fn = "rf_pages_fork";
+  rf_status chk = check_pool(fn, B, n, page, num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  if (n == 0) return ok();
+  if (src == nullptr || out == nullptr || len_out == nullptr || refs == nullptr ||
+      (B > 0 && (table == nullptr || len == nullptr)))
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  const void* ptrs[] = {table, len, src, out, len_out, refs};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  if ((table_stride < max_pages && B > 1) || (out_stride < max_pages && n > 1))
+    return fail(RF_ERR_INVALID, "%s: a table's stride < max_pages", fn);
+  rf::PagesForkArgs a{};
+  a.status = rf::status_word();
+  if (a.status == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  a.table = table; a.table_stride = table_stride; a.len = len; a.src = src;
+  a.out = out; a.out_stride = out_stride; a.len_out = len_out; a.refs = refs;
+  a.B = B; a.n = n; a.max_pages = max_pages; a.page = page; a.num_pages = num_pages;
+  cudaError_t e = rf::launch_pages_fork(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_pages_fork: launch");
+  return ok();
+}
+
+rf_status rf_pages_grow(int32_t* table, int64_t table_stride, const int32_t* len,
+                        const int32_t* new_len, int n, int32_t* refs, int max_pages, int page,
+                        int num_pages, int32_t* copy_src, int32_t* copy_dst, int32_t* left,
+                        rf_stream stream) {
+  const char* fn = "rf_pages_grow";
+  rf_status chk = check_pool(fn, 0, n, page, num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  if (num_pages > (1 << 30)) return fail(RF_ERR_INVALID, "%s: num_pages > 2^30", fn);
+  if (n > rf::kMaxGrowRows) return fail(RF_ERR_UNSUPPORTED, "%s: n > %d", fn, rf::kMaxGrowRows);
+  if (refs == nullptr || left == nullptr ||
+      (n > 0 && (table == nullptr || len == nullptr || new_len == nullptr || copy_src == nullptr ||
+                 copy_dst == nullptr)))
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  const void* ptrs[] = {table, len, new_len, refs, copy_src, copy_dst, left};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  if (table_stride < max_pages && n > 1)
+    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
+  rf::PagesGrowArgs a{};
+  a.status = rf::status_word();
+  if (a.status == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  a.table = table; a.table_stride = table_stride; a.len = len; a.new_len = new_len; a.refs = refs;
+  a.n = n; a.max_pages = max_pages; a.page = page; a.num_pages = num_pages;
+  a.copy_src = copy_src; a.copy_dst = copy_dst; a.left = left;
+  cudaError_t e = rf::launch_pages_grow(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_pages_grow: launch");
+  return ok();
+}
+
+rf_status rf_pages_release(const int32_t* table, int64_t table_stride, const int32_t* len,
+                           const int32_t* new_len, int n, int32_t* refs, int max_pages, int page,
+                           int num_pages, rf_stream stream) {
+  const char* fn = "rf_pages_release";
+  rf_status chk = check_pool(fn, 0, n, page, num_pages, max_pages);
+  if (chk != RF_OK) return chk;
+  if (n == 0) return ok();
+  if (table == nullptr || len == nullptr || refs == nullptr)
+    return fail(RF_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!aligned(table, 4) || !aligned(len, 4) || !aligned(new_len, 4) || !aligned(refs, 4))
+    return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
+  if (table_stride < max_pages && n > 1)
+    return fail(RF_ERR_INVALID, "%s: table_stride < max_pages", fn);
+  rf::PagesReleaseArgs a{};
+  a.status = rf::status_word();
+  if (a.status == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);
+  a.table = table; a.table_stride = table_stride; a.len = len; a.new_len = new_len; a.refs = refs;
+  a.n = n; a.max_pages = max_pages; a.page = page; a.num_pages = num_pages;
+  cudaError_t e = rf::launch_pages_release(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rf_pages_release: launch");
   return ok();
 }
 

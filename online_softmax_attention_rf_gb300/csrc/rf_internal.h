@@ -30,7 +30,10 @@ enum DevKernel : int {
   kKerMla = 8,
   kKerAppend = 9,
   kKerVerify = 10,
-  kKerPaged = 11
+  kKerPaged = 11,
+  kKerSample = 12,
+  kKerTree = 13,
+  kKerPages = 14
 };
 
 __host__ __device__ constexpr int dev_code(int kind, int kernel, int site) {
@@ -179,6 +182,119 @@ struct PagedAttnArgs {
   void* o;
   float* lse;
   float* ws;
+  const uint64_t* tree;  // a row's visible new tokens as bits; nullptr: the plan's mask
+  int tree_words;
+  int* status;
+};
+
+// Trees of drafted tokens (validated on the host).
+constexpr int kMaxTreeWords = 16;
+struct TreeMaskArgs {
+  const int32_t* parent;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int B, T, words;
+  uint64_t* mask;
+  int32_t* pos;
+  int* status;
+};
+struct TreeAcceptArgs {
+  const int32_t* parent;
+  const int32_t* tokens;
+  const int32_t* sampled;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int B, T;
+  int32_t* path;
+  int32_t* out;
+  int32_t* n_path;
+  int32_t* base;
+  int32_t* new_len;
+  int* status;
+};
+
+// Arguments of one drawing of tokens (validated on the host).
+constexpr int kMaxSampleVocab = 1 << 20;
+struct SampleArgs {
+  const void* logits;
+  int64_t stride;
+  const float* expo;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int B, V;
+  int32_t* token;
+  float* logprob;
+  int* status;
+};
+
+// A cache pool as the housekeeping kernels see it: strides in bytes, a (token,
+// head) row of row16 units of 16 bytes. dense: a page is one run of bytes.
+struct PoolSide {
+  char* base;
+  int64_t layer, page, token, head;
+  int dense;
+};
+struct Pool {
+  PoolSide k, v;
+  int layers, num_pages, page, Hkv, row16;
+};
+struct CompactArgs {
+  Pool pool;
+  const int32_t* table;
+  int64_t table_stride;
+  int B, N, max_pages;
+  const int32_t* keep;
+  const int32_t* cu_keep;
+  const int32_t* n_keep;
+  const int32_t* base;
+  int heads, head_splits;  // set by the launcher: heads of a CTA
+  int* status;
+};
+struct CopyPagesArgs {
+  Pool pool;
+  const int32_t* src;
+  const int32_t* dst;
+  int n;
+  int splits, per_split;  // set by the launcher: CTAs of a page, units of a CTA
+  int* status;
+};
+
+// Pages and their owners (validated on the host).
+constexpr int kMaxGrowRows = 16384;
+struct PagesForkArgs {
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* len;
+  const int32_t* src;
+  int32_t* out;
+  int64_t out_stride;
+  int32_t* len_out;
+  int32_t* refs;
+  int B, n, max_pages, page, num_pages;
+  int* status;
+};
+struct PagesGrowArgs {
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t* len;
+  const int32_t* new_len;
+  int32_t* refs;
+  int n, max_pages, page, num_pages;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* left;
+  int wide;  // set by the launcher: refs is 16-byte aligned
+  int* status;
+};
+struct PagesReleaseArgs {
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* len;
+  const int32_t* new_len;
+  int32_t* refs;
+  int n, max_pages, page, num_pages;
   int* status;
 };
 
@@ -228,6 +344,14 @@ cudaError_t launch_paged_slots(const int32_t* cu_q, const int32_t* kv_len, const
                                int* status);
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t s);
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t s, const char** why);
+cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t s);
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s);
+cudaError_t launch_sample_rows(const SampleArgs& a, rf_dtype dt, cudaStream_t s);
+cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s);
+cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t s);
+cudaError_t launch_pages_grow(PagesGrowArgs a, cudaStream_t s);
+cudaError_t launch_pages_release(const PagesReleaseArgs& a, cudaStream_t s);
 int64_t draft_verify_stats(int B, int S);  // bytes of the row statistics
 cudaError_t launch_draft_verify(const VerifyArgs& a, rf_dtype dt, void* ws, cudaStream_t s);
 // order[c] for c < items: the double items whose listed tiles exceed twice

@@ -1,0 +1,581 @@
+// sample.cu -- a token drawn from each row of logits by temperature, top-k,
+// top-p and min-p, from given random numbers.
+//
+// The row softmax cascade (maximum, then sum of exponentials; RedFuser: An
+// Automatic Operator Fusion Framework for Cascaded Reductions on AI
+// Accelerators, section 1) with a selection between the sum and the draw. With
+// m the row's maximum, t_j = (m - x_j) / T * log2 e and w_j = 2^-t_j:
+//   top-k keeps the k largest x_j, top-p of those the shortest run from the
+//   largest down whose weights reach top_p of their sum (equal logits: lower
+//   index first), min-p of those w_j >= min_p; the draw is argmax w_j / e_j.
+// Both cuts fall at one place in the order by (x descending, index ascending),
+// and neither needs the row sorted: a histogram of t in steps of 1/16, of counts
+// for top-k and of weights for top-p, gives the interval that the cut falls
+// into, histograms of the logits' bits inside it narrow it down to one value, and
+// a count of that value's occurrences settles which of them are in.
+// Counts and weights are added as integers (a weight to 28 bits below the power
+// of two of its interval), so that the order of the additions cannot move a cut.
+//
+// A cluster of CTAs holds a row in shared memory, read once from global memory;
+// each pass goes over it there. Histograms are joined through distributed shared
+// memory: each CTA adds up its share of the buckets and hands the sums to all.
+#include <cooperative_groups.h>
+
+#include <cfloat>
+
+#include "paged_device.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace rf {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBuckets = 1024;
+constexpr int kPerUnit = 16;   // buckets of the first histogram per unit of t
+constexpr int kFracBits = 42;  // of the row's sum of weights: up to 2^20 of them, of at most 1
+constexpr int kFineBits = 28;  // of a weight, below the power of two of its interval
+constexpr int kHalf = 14;      // of them in the lower half: 2^17 weights fit 32 bits
+constexpr uint32_t kAll = 0xffffffffu;
+static_assert(kBuckets == 2 * kThreads, "the scan takes two buckets a thread");
+
+template <typename T>
+struct Elem;
+
+template <>
+struct Elem<float> {
+  static constexpr int N = 4;  // in 16 bytes
+  static constexpr uint32_t kLowest = 0x007fffffu;  // key of -inf
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&y)[4]) {
+    y[0] = __uint_as_float(w.x); y[1] = __uint_as_float(w.y);
+    y[2] = __uint_as_float(w.z); y[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  // An order of unsigned numbers that is the logits' (the two zeros are one).
+  static __device__ __forceinline__ uint32_t key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+  }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+  }
+};
+
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kLowest = 0x007fu;
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&y)[8]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = __uint_as_float(r[i] << 16);
+      y[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ uint32_t key(float x) { return Elem<float>::key(x) >> 16; }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return Elem<float>::value(k << 16 | (k & 0x8000u ? 0u : 0xffffu));
+  }
+};
+
+struct Best {
+  float score;
+  int idx;
+  float t;
+};
+constexpr int kNoIdx = 0x7fffffff;
+__device__ __forceinline__ void take(Best& a, const Best& b) {
+  if (b.score > a.score || (b.score == a.score && b.idx < a.idx)) a = b;
+}
+
+struct Shared {
+  // this CTA's histogram: counts, and weights in two halves
+  uint32_t cnt[kBuckets], hi[kBuckets], lo[kBuckets];
+  // the cluster's
+  uint64_t val[kBuckets];
+  uint32_t num[kBuckets];
+  uint64_t wsum[kWarps];
+  uint32_t wcnt[kWarps];
+  // a value of each CTA of the cluster
+  float cmax[kMaxCluster];
+  int cbad[kMaxCluster];
+  uint32_t cties[kMaxCluster];
+  float csum[kMaxCluster];
+  Best cbest[kMaxCluster];
+  // of each warp
+  float wf[kWarps];
+  Best wbest[kWarps];
+  uint64_t found_before;
+  int found;
+  int tie_limit;
+};
+
+// Where a selection ends: every logit above x is in, and of those equal to x
+// the first `ties` (kAll: all).
+struct Cut {
+  float x;
+  uint32_t ties;
+};
+
+// What a selection left of this CTA's logits. -inf has no probability.
+struct Kept {
+  float x = kNegInf;
+  int limit = 0;  // of those equal to x, the ones before this index
+  __device__ __forceinline__ bool has(float y, int v) const { return y > x || (y == x && v < limit); }
+};
+
+// share * total, rounded up, at least 1 (0 <= share < 1).
+__device__ __forceinline__ uint64_t times_up(uint64_t total, float share) {
+  const uint32_t bits = __float_as_uint(share);
+  const int shift = 150 - static_cast<int>(bits >> 23);  // share = m * 2^-shift
+  if (shift >= 128) return 1;  // a total below 2^63 times less than 2^-104
+  const uint64_t m = (bits & 0x7fffffu) | 0x800000u;
+  const uint64_t hi = __umul64hi(total, m), lo = total * m;
+  if (shift >= 64) return (hi >> (shift - 64)) + 1;
+  const uint64_t q = hi << (64 - shift) | lo >> shift;
+  return q + ((lo << (64 - shift)) != 0 || q == 0 ? 1 : 0);
+}
+
+template <typename T, bool kHeld>
+struct Row {
+  using E = Elem<T>;
+  const SampleArgs& a;
+  Shared& sh;
+  cg::cluster_group cluster;
+  int rank, size;
+  int tid, warp, lane;
+  const T* base;     // the row's start rounded down to 16 bytes (groups are read from here)
+  const uint4* held; // this CTA's groups in shared memory
+  int first;         // the row's first element, counted from base
+  int end;           // one past its last
+  int g0, ng;        // this CTA's groups of 16 bytes
+  float max, c;      // maximum, log2(e) / temperature
+
+  __device__ __forceinline__ Row(const SampleArgs& a_, Shared& s)
+      : a(a_), sh(s), cluster(cg::this_cluster()) {}
+
+  // A group's logits; what lies outside the row counts as -inf.
+  __device__ __forceinline__ uint4 load_group(int g) const {
+    const int v = g * E::N;
+    if (v >= first && v + E::N <= end) return __ldg(reinterpret_cast<const uint4*>(base) + g);
+    T y[E::N];
+#pragma unroll
+    for (int i = 0; i < E::N; ++i)
+      y[i] = v + i >= first && v + i < end ? base[v + i] : T(kNegInf);
+    uint4 w;
+    memcpy(&w, y, 16);
+    return w;
+  }
+  // f(x, index counted from base) for each of this thread's logits, in
+  // ascending order of groups: thread i has groups i, i + kThreads, ...
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    for (int g = tid; g < ng; g += kThreads) {
+      float y[E::N];
+      E::unpack(kHeld ? held[g] : load_group(g0 + g), y);
+#pragma unroll
+      for (int i = 0; i < E::N; ++i) f(y[i], (g0 + g) * E::N + i);
+    }
+  }
+  __device__ __forceinline__ float t_of(float x) const { return __fmul_rn(max - x, c); }
+  __device__ __forceinline__ int bucket_of(float x) const {
+    const float t = t_of(x) * kPerUnit;  // not below 0; NaN never (x is not +inf, c is finite)
+    return t < kBuckets - 1 ? static_cast<int>(t) : kBuckets - 1;
+  }
+  // A logit's weight over 2^-e, e the power of its interval, as an integer.
+  __device__ __forceinline__ uint32_t fine(float x) const {
+    const float t = t_of(x);
+    return __float2uint_rn(ex2_approx(floorf(t) - t) * (1u << kFineBits));
+  }
+  __device__ __forceinline__ void add_fine(int b, uint32_t f) const {
+    atomicAdd(&sh.hi[b], f >> kHalf);
+    atomicAdd(&sh.lo[b], f & ((1u << kHalf) - 1));
+  }
+
+  __device__ void clear() const {
+    for (int i = tid; i < kBuckets; i += kThreads) sh.cnt[i] = sh.hi[i] = sh.lo[i] = 0;
+    __syncthreads();
+  }
+
+  // Joins the CTAs' histograms: val (counts, or weights; weights of the first
+  // histogram in units of 2^-kFracBits) and num (counts), the same in each CTA.
+  template <bool kWeights>
+  __device__ void join(bool by_unit) const {
+    cluster.sync();
+    const int share = kBuckets / size;
+    for (int i = tid; i < share; i += kThreads) {
+      const int b = rank * share + i;
+      uint32_t n = 0;
+      uint64_t v = 0;
+      for (int q = 0; q < size; ++q) {
+        n += *cluster.map_shared_rank(&sh.cnt[b], q);
+        if (kWeights)
+          v += (uint64_t(*cluster.map_shared_rank(&sh.hi[b], q)) << kHalf) +
+               *cluster.map_shared_rank(&sh.lo[b], q);
+      }
+      if (!kWeights) v = n;
+      if (kWeights && by_unit) {
+        const int s = kFracBits - kFineBits - b / kPerUnit;
+        v = s >= 0 ? v << s : v >> -s;
+      }
+      for (int q = 0; q < size; ++q) {
+        *cluster.map_shared_rank(&sh.val[b], q) = v;
+        *cluster.map_shared_rank(&sh.num[b], q) = n;
+      }
+    }
+    cluster.sync();
+  }
+
+  // The bucket in which the running sum of val reaches the target (share < 0:
+  // `target`, else that share of the whole), and the sum before it; none: -1.
+  __device__ int find(uint64_t target, float share, uint64_t* rest) const {
+    const uint64_t v0 = sh.val[2 * tid], v1 = sh.val[2 * tid + 1];
+    uint64_t s = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t u = __shfl_up_sync(kAll, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) sh.wsum[warp] = s;
+    if (tid == 0) sh.found = -1;
+    __syncthreads();
+    uint64_t before = 0, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh.wsum[w];
+      total += sh.wsum[w];
+    }
+    if (share >= 0.f) {
+      target = times_up(total, share);
+    }
+    before += s - v0 - v1;
+    if (before < target && target <= before + v0) {
+      sh.found = 2 * tid;
+      sh.found_before = before;
+    }
+    before += v0;
+    if (before < target && target <= before + v1) {
+      sh.found = 2 * tid + 1;
+      sh.found_before = before;
+    }
+    __syncthreads();
+    const int b = sh.found;
+    *rest = target - sh.found_before;
+    __syncthreads();
+    return b;
+  }
+
+  // The least key in [lo, hi] whose bucket is at most b; hi's is.
+  __device__ uint32_t least_key(uint32_t lo, uint32_t hi, int b) const {
+    while (lo < hi) {
+      const uint32_t step = (hi - lo) / 32 + 1;
+      const uint32_t probe = min(hi, lo + lane * step);
+      const uint32_t in = __ballot_sync(kAll, bucket_of(E::value(probe)) <= b);
+      if (in == 0) {
+        lo += 31 * step + 1;
+      } else {
+        const int f = __ffs(in) - 1;
+        hi = min(hi, lo + f * step);
+        if (f > 0) lo += (f - 1) * step + 1; else hi = lo;
+      }
+    }
+    return lo;
+  }
+
+  // The place where the running sum over (x descending, index ascending) of
+  // counts, or of weights, reaches the target; only what `in` keeps is summed.
+  // False: it does not.
+  template <bool kWeights>
+  __device__ bool select(uint64_t target, float share, const Kept& in, Cut* out) const {
+    clear();
+    each([&](float x, int v) {
+      if (!in.has(x, v)) return;
+      const int b = bucket_of(x);
+      if (kWeights) {
+        if (b < kBuckets - 1) add_fine(b, fine(x));
+      } else {
+        atomicAdd(&sh.cnt[b], 1u);
+      }
+    });
+    join<kWeights>(true);
+    uint64_t rest = 0;
+    const int b = find(target, share, &rest);
+    if (b < 0) return false;
+    if (kWeights) {  // in units of the interval's weights
+      const int s = kFracBits - kFineBits - b / kPerUnit;
+      rest = s >= 0 ? (rest + (uint64_t(1) << s) - 1) >> s : rest << -s;
+    }
+    const uint32_t top = E::key(max);
+    uint32_t klo = least_key(E::kLowest, top, b);
+    uint32_t khi = b > 0 ? least_key(klo, top, b - 1) - 1 : top;
+    while (true) {
+      const uint32_t span = khi - klo;
+      if (span == 0) break;
+      int s = 0;
+      while ((span >> s) >= kBuckets) ++s;
+      clear();
+      each([&](float x, int v) {
+        if (!in.has(x, v)) return;
+        const uint32_t k = E::key(x);
+        if (k < klo || k > khi) return;
+        const int i = static_cast<int>((khi - k) >> s);
+        atomicAdd(&sh.cnt[i], 1u);
+        if (kWeights) add_fine(i, fine(x));
+      });
+      join<kWeights>(false);
+      const int i = find(rest, -1.f, &rest);
+      if (i < 0) return false;  // not reached: the interval's sum is at least the rest
+      const uint32_t n = sh.num[i];
+      khi -= static_cast<uint32_t>(i) << s;
+      klo = s > 0 ? max_u32(klo, khi - ((1u << s) - 1)) : khi;
+      if (n == 1) {  // whichever it is, it is in, and nothing below it
+        *out = Cut{E::value(klo), kAll};
+        return true;
+      }
+    }
+    const float x = E::value(klo);
+    if (kWeights) {
+      const uint64_t f = fine(x);
+      rest = (rest + f - 1) / f;
+    }
+    *out = Cut{x, static_cast<uint32_t>(rest < kAll ? rest : kAll)};
+    return true;
+  }
+  static __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+  // What the cut leaves of `in`.
+  __device__ Kept settle(const Cut& cut, const Kept& in) const {
+    const int last = cut.x == in.x ? in.limit : kNoIdx;
+    return Kept{cut.x, cut.ties == kAll ? last : min(last, tie_limit(cut))};
+  }
+  // Of the elements equal to the cut, the first cut.ties are those before the
+  // returned index.
+  __device__ int tie_limit(const Cut& cut) const {
+    uint32_t n = 0;
+    each([&](float x, int) { n += x == cut.x; });
+    n = __reduce_add_sync(kAll, n);
+    if (lane == 0) sh.wcnt[warp] = n;
+    if (tid == 0) sh.tie_limit = kNoIdx;
+    __syncthreads();
+    n = 0;
+    for (int w = 0; w < kWarps; ++w) n += sh.wcnt[w];
+    if (tid < size) *cluster.map_shared_rank(&sh.cties[rank], tid) = n;
+    cluster.sync();
+    uint32_t before = 0;
+    for (int q = 0; q < rank; ++q) before += sh.cties[q];
+    if (cut.ties <= before) return 0;
+    uint32_t left = cut.ties - before;
+    if (left >= n) return kNoIdx;
+    // the left'th of this CTA's, in order
+    for (int g = 0; g < ng; g += kThreads) {
+      uint32_t mine = 0;
+      float y[E::N];
+      if (g + tid < ng) {
+        E::unpack(kHeld ? held[g + tid] : load_group(g0 + g + tid), y);
+#pragma unroll
+        for (int i = 0; i < E::N; ++i) mine += y[i] == cut.x;
+      }
+      uint32_t s = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(kAll, s, o);
+        if (lane >= o) s += u;
+      }
+      __syncthreads();
+      if (lane == 31) sh.wcnt[warp] = s;
+      __syncthreads();
+      uint32_t total = 0, ahead = s - mine;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) ahead += sh.wcnt[w];
+        total += sh.wcnt[w];
+      }
+      if (ahead < left && left <= ahead + mine) {
+#pragma unroll
+        for (int i = 0; i < E::N; ++i)
+          if (y[i] == cut.x && ++ahead == left) sh.tie_limit = (g0 + g + tid) * E::N + i + 1;
+      }
+      if (left <= total) break;
+      left -= total;
+    }
+    __syncthreads();
+    return sh.tie_limit;
+  }
+};
+
+template <typename T, bool kHeld>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+  using E = Elem<T>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ Shared sh;
+  Row<T, kHeld> r(a, sh);
+  r.rank = static_cast<int>(r.cluster.block_rank());
+  r.size = static_cast<int>(r.cluster.num_blocks());
+  r.tid = threadIdx.x;
+  r.warp = r.tid >> 5;
+  r.lane = r.tid & 31;
+  const int b = blockIdx.x / r.size;
+  r.cluster.barrier_arrive();  // waited for before any CTA's memory is written by another
+  pdl_wait();
+  pdl_trigger();
+  const T* x0 = static_cast<const T*>(a.logits) + int64_t(b) * a.stride;
+  r.first = static_cast<int>((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
+  r.end = r.first + a.V;
+  r.base = x0 - r.first;
+  const int groups = (r.end + E::N - 1) / E::N;
+  const int per = (groups + r.size - 1) / r.size;
+  r.g0 = r.rank * per;
+  r.ng = max(0, min(groups - r.g0, per));
+  uint4* held = reinterpret_cast<uint4*>(smem_raw);
+  r.held = held;
+  const float temp = a.temperature != nullptr ? a.temperature[b] : 1.f;
+  const bool greedy = !(temp > 0.f);
+  // 1 / T overflows below 2.9e-39: any finite number in its place leaves the
+  // maximum its weight 1 and takes all others' away
+  r.c = greedy ? 0.f : fminf(kLog2e / temp, FLT_MAX);
+
+  // the row's maximum; a NaN or +inf in it, or nothing finite, refuses it
+  float m = kNegInf;
+  bool bad = false;
+  for (int g = r.tid; g < r.ng; g += kThreads) {
+    const uint4 w = r.load_group(r.g0 + g);
+    if (kHeld) held[g] = w;
+    float y[E::N];
+    E::unpack(w, y);
+#pragma unroll
+    for (int i = 0; i < E::N; ++i) {
+      m = fmaxf(m, y[i]);
+      bad |= !(y[i] <= FLT_MAX);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  if (r.lane == 0) sh.wf[r.warp] = m;
+  bad = __syncthreads_or(bad);
+  m = sh.wf[0];
+  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.wf[w]);
+  r.cluster.barrier_wait();
+  if (r.tid < r.size) {
+    *r.cluster.map_shared_rank(&sh.cmax[r.rank], r.tid) = m;
+    *r.cluster.map_shared_rank(&sh.cbad[r.rank], r.tid) = bad;
+  }
+  r.cluster.sync();
+  m = kNegInf;
+  bad = false;
+  for (int q = 0; q < r.size; ++q) {
+    m = fmaxf(m, sh.cmax[q]);
+    bad |= sh.cbad[q] != 0;
+  }
+  bad |= m == kNegInf;
+  r.max = m;
+
+  Best best{-1.f, kNoIdx, 0.f};
+  float sum = 0.f;
+  if (!bad && greedy) {
+    r.each([&](float x, int v) {
+      if (x == m) take(best, Best{1.f, v, 0.f});
+    });
+    sum = 1.f;
+  } else if (!bad) {
+    Kept kept;
+    Cut cut;
+    const int k = a.top_k != nullptr ? a.top_k[b] : 0;
+    if (k > 0 && k < a.V && r.template select<false>(k, -1.f, kept, &cut)) kept = r.settle(cut, kept);
+    const float p = a.top_p != nullptr ? a.top_p[b] : 1.f;
+    if (!(p >= 1.f) && r.template select<true>(0, p > 0.f ? p : 0.f, kept, &cut))
+      kept = r.settle(cut, kept);
+    const float mp = a.min_p != nullptr ? a.min_p[b] : 0.f;
+    // w >= min_p as t <= -log2(min_p); the maximum always stays
+    const float t_max = mp > 0.f ? fmaxf(0.f, -log2f(mp)) : __int_as_float(0x7f800000);
+    const float* e = a.expo + int64_t(b) * a.V - r.first;
+    r.each([&](float x, int v) {
+      if (!kept.has(x, v)) return;
+      const float t = r.t_of(x);
+      if (t > t_max) return;
+      const float w = ex2_approx(-t);
+      sum += w;
+      take(best, Best{__fdividef(w, e[v]), v, t});
+    });
+  }
+  // the cluster's best and sum, joined in a fixed order
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Best other{__shfl_xor_sync(kAll, best.score, o), __shfl_xor_sync(kAll, best.idx, o),
+                     __shfl_xor_sync(kAll, best.t, o)};
+    take(best, other);
+    sum += __shfl_xor_sync(kAll, sum, o);
+  }
+  __syncthreads();
+  if (r.lane == 0) {
+    sh.wbest[r.warp] = best;
+    sh.wf[r.warp] = sum;
+  }
+  __syncthreads();
+  if (r.tid == 0) {
+    for (int w = 1; w < kWarps; ++w) {
+      take(best, sh.wbest[w]);
+      sum += sh.wf[w];
+    }
+    *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
+    *r.cluster.map_shared_rank(&sh.csum[r.rank], 0) = sum;
+  }
+  r.cluster.sync();
+  if (r.rank == 0 && r.tid == 0) {
+    best = sh.cbest[0];
+    sum = sh.csum[0];
+    for (int q = 1; q < r.size; ++q) {
+      take(best, sh.cbest[q]);
+      sum += sh.csum[q];
+    }
+    const bool none = bad || best.idx == kNoIdx;
+    if (none) record_status(a.status, dev_code(kDevBadList, kKerSample, 1));
+    a.token[b] = none ? -1 : best.idx - r.first;
+    if (a.logprob != nullptr)
+      a.logprob[b] = none ? __int_as_float(0x7fc00000)
+                          : greedy ? 0.f : -(best.t + log2f(sum)) * kLn2;
+  }
+}
+
+template <typename T, bool kHeld>
+cudaError_t launch_k(const SampleArgs& a, int cluster, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T, kHeld>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, kHeld>, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
+  constexpr int kMostHeld = 160 * 1024;
+  // a row goes to as many CTAs as it takes to have few of its logits a thread
+  int cluster = 1;
+  while (cluster < kMaxCluster && a.V > cluster * kThreads * 4) cluster *= 2;
+  const int groups = (a.V + 2 * Elem<T>::N - 2) / Elem<T>::N;  // with any lead
+  const size_t bytes = size_t((groups + cluster - 1) / cluster) * 16;
+  if (bytes <= kMostHeld) return launch_k<T, true>(a, cluster, bytes, s);
+  return launch_k<T, false>(a, cluster, 0, s);
+}
+
+}  // namespace
+
+cudaError_t launch_sample_rows(const SampleArgs& a, rf_dtype dt, cudaStream_t s) {
+  return dt == RF_F32 ? launch_t<float>(a, s) : launch_t<__nv_bfloat16>(a, s);
+}
+
+}  // namespace rf
