@@ -348,6 +348,7 @@ struct Row {
 
   // What the cut leaves of `in`.
   __device__ Kept settle(const Cut& cut, const Kept& in) const {
+    if (cut.x < in.x) return in;  // the lower end of an interval with one logit in it
     const int last = cut.x == in.x ? in.limit : kNoIdx;
     return Kept{cut.x, cut.ties == kAll ? last : min(last, tie_limit(cut))};
   }
