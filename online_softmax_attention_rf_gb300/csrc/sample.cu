@@ -9,12 +9,15 @@
 //   largest down whose weights reach top_p of their sum (equal logits: lower
 //   index first), min-p of those w_j >= min_p; the draw is argmax w_j / e_j.
 // Both cuts fall at one place in the order by (x descending, index ascending),
-// and neither needs the row sorted: a histogram of t in steps of 1/16, of counts
-// for top-k and of weights for top-p, gives the interval that the cut falls
-// into, histograms of the logits' bits inside it narrow it down to one value, and
-// a count of that value's occurrences settles which of them are in.
-// Counts and weights are added as integers (a weight to 28 bits below the power
-// of two of its interval), so that the order of the additions cannot move a cut.
+// and neither needs the row sorted. A histogram of t in steps of 1/16, of counts
+// for top-k and of weights for top-p, gives the interval that the cut falls into.
+// Where no more than 512 logits lie above the interval's lower end, as is usual,
+// these alone go on: one CTA puts them in order and finishes the row. Otherwise
+// histograms of the logits' bits inside the interval narrow it down to one value,
+// and a count of that value's occurrences settles which of them are in.
+// Counts and weights are added as integers (a weight to 22 bits below the power
+// of two of its interval, about what float32 carries), so that the order of the
+// additions cannot move a cut.
 //
 // A cluster of CTAs holds a row in shared memory, read once from global memory;
 // each pass goes over it there. Histograms are joined through distributed shared
@@ -36,10 +39,25 @@ constexpr int kMaxCluster = 8;
 constexpr int kBuckets = 1024;
 constexpr int kPerUnit = 16;   // buckets of the first histogram per unit of t
 constexpr int kFracBits = 42;  // of the row's sum of weights: up to 2^20 of them, of at most 1
-constexpr int kFineBits = 28;  // of a weight, below the power of two of its interval
-constexpr int kHalf = 14;      // of them in the lower half: 2^17 weights fit 32 bits
+constexpr int kFineBits = 22;  // of a weight, below the power of two of its interval
+constexpr int kHalf = 11;      // of them in the lower half: 2^20 weights fit 32 bits
+constexpr int kFew = kThreads; // logits that one CTA finishes, one a thread
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kInf = __builtin_huge_valf();
 static_assert(kBuckets == 2 * kThreads, "the scan takes two buckets a thread");
+static_assert(kFew <= kBuckets, "a histogram's place holds the few logits");
+
+// max(a, b, c), NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 template <typename T>
 struct Elem;
@@ -52,7 +70,11 @@ struct Elem<float> {
     y[0] = __uint_as_float(w.x); y[1] = __uint_as_float(w.y);
     y[2] = __uint_as_float(w.z); y[3] = __uint_as_float(w.w);
   }
-  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  // The group's maximum (NaN if one is) with m.
+  static __device__ __forceinline__ float max_of(const uint4& w, float m) {
+    m = max3_nan(m, __uint_as_float(w.x), __uint_as_float(w.y));
+    return max3_nan(m, __uint_as_float(w.z), __uint_as_float(w.w));
+  }
   // An order of unsigned numbers that is the logits' (the two zeros are one).
   static __device__ __forceinline__ uint32_t key(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -75,7 +97,10 @@ struct Elem<__nv_bfloat16> {
       y[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ float max_of(const uint4& w, float m) {
+    const uint32_t p = max_bf16x2_nan(max_bf16x2_nan(w.x, w.y), max_bf16x2_nan(w.z, w.w));
+    return max3_nan(m, __uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+  }
   static __device__ __forceinline__ uint32_t key(float x) { return Elem<float>::key(x) >> 16; }
   static __device__ __forceinline__ float value(uint32_t k) {
     return Elem<float>::value(k << 16 | (k & 0x8000u ? 0u : 0xffffu));
@@ -93,7 +118,9 @@ __device__ __forceinline__ void take(Best& a, const Best& b) {
 }
 
 struct Shared {
-  // this CTA's histogram: counts, and weights in two halves
+  // this CTA's histogram: counts, and weights in two halves. In the cluster's
+  // first CTA the few logits and their indices take the place of the first two,
+  // sorted ones that of the cluster's sums.
   uint32_t cnt[kBuckets], hi[kBuckets], lo[kBuckets];
   // the cluster's
   uint64_t val[kBuckets];
@@ -102,7 +129,6 @@ struct Shared {
   uint32_t wcnt[kWarps];
   // a value of each CTA of the cluster
   float cmax[kMaxCluster];
-  int cbad[kMaxCluster];
   uint32_t cties[kMaxCluster];
   float csum[kMaxCluster];
   Best cbest[kMaxCluster];
@@ -110,8 +136,11 @@ struct Shared {
   float wf[kWarps];
   Best wbest[kWarps];
   uint64_t found_before;
+  uint64_t total;
   int found;
+  uint32_t found_count;  // logits in the buckets up to the found one
   int tie_limit;
+  uint32_t pushed;       // few logits that arrived
 };
 
 // Where a selection ends: every logit above x is in, and of those equal to x
@@ -149,11 +178,11 @@ struct Row {
   int rank, size;
   int tid, warp, lane;
   const T* base;     // the row's start rounded down to 16 bytes (groups are read from here)
-  const uint4* held; // this CTA's groups in shared memory
+  uint4* held;       // this CTA's groups in shared memory
   int first;         // the row's first element, counted from base
   int end;           // one past its last
   int g0, ng;        // this CTA's groups of 16 bytes
-  float max, c;      // maximum, log2(e) / temperature
+  float max, c16;    // maximum, kPerUnit * log2(e) / temperature
 
   __device__ __forceinline__ Row(const SampleArgs& a_, Shared& s)
       : a(a_), sh(s), cluster(cg::this_cluster()) {}
@@ -170,33 +199,79 @@ struct Row {
     memcpy(&w, y, 16);
     return w;
   }
-  // f(x, index counted from base) for each of this thread's logits, in
-  // ascending order of groups: thread i has groups i, i + kThreads, ...
-  template <typename F>
-  __device__ __forceinline__ void each(F&& f) const {
-    for (int g = tid; g < ng; g += kThreads) {
-      float y[E::N];
-      E::unpack(kHeld ? held[g] : load_group(g0 + g), y);
+
+  // Reads the row; this thread's maximum (NaN if one is).
+  __device__ float read() const {
+    float m = kNegInf;
+    // groups that lie wholly in the row; the first and the last one may not
+    const int f0 = g0 == 0 && first > 0 ? 1 : 0;
+    const int f1 = min(ng, end / E::N - g0);
+    const uint4* from = reinterpret_cast<const uint4*>(base) + g0;
+    constexpr int U = 4;
+    int g = f0 + tid;
+    for (; g + (U - 1) * kThreads < f1; g += U * kThreads) {
+      uint4 w[U];
 #pragma unroll
-      for (int i = 0; i < E::N; ++i) f(y[i], (g0 + g) * E::N + i);
+      for (int j = 0; j < U; ++j) w[j] = __ldg(from + g + j * kThreads);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (kHeld) held[g + j * kThreads] = w[j];
+        m = E::max_of(w[j], m);
+      }
+    }
+    for (; g < f1; g += kThreads) {
+      const uint4 w = __ldg(from + g);
+      if (kHeld) held[g] = w;
+      m = E::max_of(w, m);
+    }
+    // ragged ends: group 0, and those from max(f0, f1) on (one at most)
+    const int e = tid == 0 ? (f0 > 0 && ng > 0 ? 0 : -1) : tid == 1 ? f1 : -1;
+    if (e >= 0 && e < ng && (tid == 0 || e >= f0)) {
+      const uint4 w = load_group(g0 + e);
+      if (kHeld) held[e] = w;
+      m = E::max_of(w, m);
+    }
+    return m;
+  }
+
+  // f(group, index of its first logit from base), over this thread's groups with
+  // a logit of at least `least`, in ascending order.
+  template <typename F>
+  __device__ __forceinline__ void groups_from(float least, F&& f) const {
+#pragma unroll 2
+    for (int g = tid; g < ng; g += kThreads) {
+      const uint4 w = kHeld ? held[g] : load_group(g0 + g);
+      if (E::max_of(w, kNegInf) >= least) f(w, (g0 + g) * E::N);
     }
   }
-  __device__ __forceinline__ float t_of(float x) const { return __fmul_rn(max - x, c); }
-  __device__ __forceinline__ int bucket_of(float x) const {
-    const float t = t_of(x) * kPerUnit;  // not below 0; NaN never (x is not +inf, c is finite)
-    return t < kBuckets - 1 ? static_cast<int>(t) : kBuckets - 1;
+  template <typename F>
+  __device__ __forceinline__ void each_from(float least, F&& f) const {
+    groups_from(least, [&](const uint4& w, int v) {
+      float y[E::N];
+      E::unpack(w, y);
+#pragma unroll
+      for (int i = 0; i < E::N; ++i) f(y[i], v + i);
+    });
   }
-  // A logit's weight over 2^-e, e the power of its interval, as an integer.
-  __device__ __forceinline__ uint32_t fine(float x) const {
-    const float t = t_of(x);
-    return __float2uint_rn(ex2_approx(floorf(t) - t) * (1u << kFineBits));
+
+  // kPerUnit * t: not below 0; +inf for -inf
+  __device__ __forceinline__ float t16_of(float x) const { return __fmul_rn(max - x, c16); }
+  __device__ __forceinline__ int bucket_of(float x) const {
+    const float t = fminf(t16_of(x), kBuckets - 1.f);
+    return __float_as_int(__fadd_rz(t, 8388608.f)) & (kBuckets - 1);
+  }
+  // A weight over 2^-e, e the power of its interval, as an integer.
+  static __device__ __forceinline__ uint32_t fine_of(float t16) {
+    const float e16 = __fadd_rz(t16, 134217728.f) - 134217728.f;  // to a multiple of 16
+    const float f = ex2_approx((e16 - t16) * (1.f / kPerUnit));   // in (0.5, 1]
+    return __float_as_uint(f + 2.f) - 0x40000000u;                // f * 2^22
   }
   __device__ __forceinline__ void add_fine(int b, uint32_t f) const {
     atomicAdd(&sh.hi[b], f >> kHalf);
     atomicAdd(&sh.lo[b], f & ((1u << kHalf) - 1));
   }
 
-  __device__ void clear() const {
+  __device__ __forceinline__ void clear() const {
     for (int i = tid; i < kBuckets; i += kThreads) sh.cnt[i] = sh.hi[i] = sh.lo[i] = 0;
     __syncthreads();
   }
@@ -209,18 +284,22 @@ struct Row {
     const int share = kBuckets / size;
     for (int i = tid; i < share; i += kThreads) {
       const int b = rank * share + i;
-      uint32_t n = 0;
-      uint64_t v = 0;
+      uint32_t n = 0, hi = 0;
+      uint64_t lo = 0;
       for (int q = 0; q < size; ++q) {
         n += *cluster.map_shared_rank(&sh.cnt[b], q);
-        if (kWeights)
-          v += (uint64_t(*cluster.map_shared_rank(&sh.hi[b], q)) << kHalf) +
-               *cluster.map_shared_rank(&sh.lo[b], q);
+        if (kWeights) {
+          hi += *cluster.map_shared_rank(&sh.hi[b], q);
+          lo += *cluster.map_shared_rank(&sh.lo[b], q);
+        }
       }
-      if (!kWeights) v = n;
-      if (kWeights && by_unit) {
-        const int s = kFracBits - kFineBits - b / kPerUnit;
-        v = s >= 0 ? v << s : v >> -s;
+      uint64_t v = n;
+      if (kWeights) {
+        v = (uint64_t(hi) << kHalf) + lo;
+        if (by_unit) {
+          const int s = kFracBits - kFineBits - b / kPerUnit;
+          v = s >= 0 ? v << s : v >> -s;
+        }
       }
       for (int q = 0; q < size; ++q) {
         *cluster.map_shared_rank(&sh.val[b], q) = v;
@@ -231,40 +310,59 @@ struct Row {
   }
 
   // The bucket in which the running sum of val reaches the target (share < 0:
-  // `target`, else that share of the whole), and the sum before it; none: -1.
+  // `target`, else that share of the whole), what the target is behind the sum
+  // before it, and the logits up to it; none: -1.
   __device__ int find(uint64_t target, float share, uint64_t* rest) const {
     const uint64_t v0 = sh.val[2 * tid], v1 = sh.val[2 * tid + 1];
+    const uint32_t n0 = sh.num[2 * tid], n1 = sh.num[2 * tid + 1];
     uint64_t s = v0 + v1;
+    uint32_t n = n0 + n1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t u = __shfl_up_sync(kAll, s, o);
-      if (lane >= o) s += u;
+      const uint32_t m = __shfl_up_sync(kAll, n, o);
+      if (lane >= o) {
+        s += u;
+        n += m;
+      }
     }
-    if (lane == 31) sh.wsum[warp] = s;
+    if (lane == 31) {
+      sh.wsum[warp] = s;
+      sh.wcnt[warp] = n;
+    }
     if (tid == 0) sh.found = -1;
     __syncthreads();
     uint64_t before = 0, total = 0;
+    uint32_t count = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sh.wsum[w];
-      total += sh.wsum[w];
+      const uint64_t u = sh.wsum[w];
+      if (w < warp) {
+        before += u;
+        count += sh.wcnt[w];
+      }
+      total += u;
     }
-    if (share >= 0.f) {
-      target = times_up(total, share);
-    }
+    if (share >= 0.f) target = times_up(total, share);
     before += s - v0 - v1;
+    count += n;
+    int b = -1;
     if (before < target && target <= before + v0) {
-      sh.found = 2 * tid;
-      sh.found_before = before;
+      b = 2 * tid;
+      count -= n1;
+    } else if (before + v0 < target && target <= before + v0 + v1) {
+      b = 2 * tid + 1;
+      before += v0;
     }
-    before += v0;
-    if (before < target && target <= before + v1) {
-      sh.found = 2 * tid + 1;
-      sh.found_before = before;
+    if (b >= 0) {
+      sh.found = b;
+      sh.found_before = target - before;
+      sh.found_count = count;
+      sh.total = total;
     }
     __syncthreads();
-    const int b = sh.found;
-    *rest = target - sh.found_before;
-    __syncthreads();
+    b = sh.found;
+    *rest = sh.found_before;
     return b;
   }
 
@@ -285,25 +383,34 @@ struct Row {
     return lo;
   }
 
-  // The place where the running sum over (x descending, index ascending) of
-  // counts, or of weights, reaches the target; only what `in` keeps is summed.
-  // False: it does not.
-  template <bool kWeights>
-  __device__ bool select(uint64_t target, float share, const Kept& in, Cut* out) const {
+  // The first histogram of what `in` keeps (everything without kPart), and the
+  // bucket that the cut falls into, as find().
+  template <bool kWeights, bool kPart>
+  __device__ int first_histogram(uint64_t target, float share, const Kept& in, uint64_t* rest) const {
     clear();
-    each([&](float x, int v) {
-      if (!in.has(x, v)) return;
-      const int b = bucket_of(x);
+    each_from(kPart ? in.x : kNegInf, [&](float x, int v) {
+      if (kPart && !in.has(x, v)) return;
+      const float t = t16_of(x);
       if (kWeights) {
-        if (b < kBuckets - 1) add_fine(b, fine(x));
-      } else {
+        if (t < kBuckets - 1.f) {  // the weights behind, below 2^-63, count for nothing
+          const int b = __float_as_int(__fadd_rz(t, 8388608.f)) & (kBuckets - 1);
+          atomicAdd(&sh.cnt[b], 1u);
+          add_fine(b, fine_of(t));
+        }
+      } else if (x > kNegInf) {
+        const int b = __float_as_int(__fadd_rz(fminf(t, kBuckets - 1.f), 8388608.f)) & (kBuckets - 1);
         atomicAdd(&sh.cnt[b], 1u);
       }
     });
     join<kWeights>(true);
-    uint64_t rest = 0;
-    const int b = find(target, share, &rest);
-    if (b < 0) return false;
+    return find(target, share, rest);
+  }
+
+  // The place where the running sum over (x descending, index ascending) of
+  // counts, or of weights, goes on from bucket b of the first histogram by
+  // `rest`.
+  template <bool kWeights>
+  __device__ Cut narrow(int b, uint64_t rest, const Kept& in) const {
     if (kWeights) {  // in units of the interval's weights
       const int s = kFracBits - kFineBits - b / kPerUnit;
       rest = s >= 0 ? (rest + (uint64_t(1) << s) - 1) >> s : rest << -s;
@@ -317,34 +424,29 @@ struct Row {
       int s = 0;
       while ((span >> s) >= kBuckets) ++s;
       clear();
-      each([&](float x, int v) {
-        if (!in.has(x, v)) return;
-        const uint32_t k = E::key(x);
-        if (k < klo || k > khi) return;
-        const int i = static_cast<int>((khi - k) >> s);
+      const float xlo = E::value(klo), xhi = E::value(khi);
+      each_from(xlo, [&](float x, int v) {
+        if (!(x >= xlo && x <= xhi) || !in.has(x, v)) return;
+        const int i = static_cast<int>((khi - E::key(x)) >> s);
         atomicAdd(&sh.cnt[i], 1u);
-        if (kWeights) add_fine(i, fine(x));
+        if (kWeights) add_fine(i, fine_of(t16_of(x)));
       });
       join<kWeights>(false);
-      const int i = find(rest, -1.f, &rest);
-      if (i < 0) return false;  // not reached: the interval's sum is at least the rest
+      const int i = find(rest, -1.f, &rest);  // the interval's sum is at least the rest
       const uint32_t n = sh.num[i];
       khi -= static_cast<uint32_t>(i) << s;
-      klo = s > 0 ? max_u32(klo, khi - ((1u << s) - 1)) : khi;
-      if (n == 1) {  // whichever it is, it is in, and nothing below it
-        *out = Cut{E::value(klo), kAll};
-        return true;
-      }
+      klo = s > 0 ? umax(klo, khi - ((1u << s) - 1)) : khi;
+      // a single logit is in, whichever it is, and nothing below it
+      if (n == 1) return Cut{E::value(klo), kAll};
     }
     const float x = E::value(klo);
     if (kWeights) {
-      const uint64_t f = fine(x);
+      const uint64_t f = fine_of(t16_of(x));
       rest = (rest + f - 1) / f;
     }
-    *out = Cut{x, static_cast<uint32_t>(rest < kAll ? rest : kAll)};
-    return true;
+    return Cut{x, static_cast<uint32_t>(rest < kAll ? rest : kAll)};
   }
-  static __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+  static __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
   // What the cut leaves of `in`.
   __device__ Kept settle(const Cut& cut, const Kept& in) const {
@@ -352,12 +454,14 @@ struct Row {
     const int last = cut.x == in.x ? in.limit : kNoIdx;
     return Kept{cut.x, cut.ties == kAll ? last : min(last, tie_limit(cut))};
   }
+
   // Of the elements equal to the cut, the first cut.ties are those before the
   // returned index.
   __device__ int tie_limit(const Cut& cut) const {
     uint32_t n = 0;
-    each([&](float x, int) { n += x == cut.x; });
+    each_from(cut.x, [&](float x, int) { n += x == cut.x; });
     n = __reduce_add_sync(kAll, n);
+    __syncthreads();
     if (lane == 0) sh.wcnt[warp] = n;
     if (tid == 0) sh.tie_limit = kNoIdx;
     __syncthreads();
@@ -404,10 +508,109 @@ struct Row {
     __syncthreads();
     return sh.tie_limit;
   }
+
+  // The best and the sum of the CTA's threads, in a fixed order, in thread 0.
+  __device__ __forceinline__ void reduce(Best& best, float& sum) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Best other{__shfl_xor_sync(kAll, best.score, o), __shfl_xor_sync(kAll, best.idx, o),
+                       __shfl_xor_sync(kAll, best.t, o)};
+      take(best, other);
+      sum += __shfl_xor_sync(kAll, sum, o);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sh.wbest[warp] = best;
+      sh.wf[warp] = sum;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kWarps; ++w) {
+        take(best, sh.wbest[w]);
+        sum += sh.wf[w];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void answer(int b, const Best& best, float sum, bool bad,
+                                         bool greedy) const {
+    const bool none = bad || best.idx == kNoIdx;
+    if (none) record_status(a.status, dev_code(kDevBadList, kKerSample, 1));
+    a.token[b] = none ? -1 : best.idx - first;
+    if (a.logprob != nullptr)
+      a.logprob[b] = none     ? __int_as_float(0x7fc00000)
+                     : greedy ? 0.f
+                              : -(best.t + log2f(sum)) * kLn2;
+  }
+
+  // The few logits from bucket b up go to the cluster's first CTA.
+  __device__ __forceinline__ void push(int b) const {
+    // a bound for the prefilter, a little low; bucket_of decides
+    const float least = fmaxf(kNegInf, max - (b + 2) / c16);
+    each_from(least, [&](float x, int v) {
+      if (!(x > kNegInf) || bucket_of(x) > b) return;
+      const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
+      if (at < kFew) {
+        *cluster.map_shared_rank(&sh.cnt[at], 0) = __float_as_uint(x);
+        *cluster.map_shared_rank(&sh.hi[at], 0) = static_cast<uint32_t>(v);
+      }
+    });
+  }
+
+  // The row from its few logits (one CTA): in order, then both cuts and the draw.
+  // total: the row's sum of weights, where top-k does not cut.
+  __device__ void finish(int b, int k, float p, float t_max, uint64_t total) const {
+    const int n = min(static_cast<int>(sh.pushed), kFew);
+    float* sx = reinterpret_cast<float*>(sh.val);  // sorted
+    int* sv = reinterpret_cast<int*>(sh.val) + kFew;
+    if (tid < n) {
+      const float x = __uint_as_float(sh.cnt[tid]);
+      const int v = static_cast<int>(sh.hi[tid]);
+      int r = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const float y = __uint_as_float(sh.cnt[j]);
+        r += y > x || (y == x && static_cast<int>(sh.hi[j]) < v);
+      }
+      sx[r] = x;
+      sv[r] = v;
+    }
+    __syncthreads();
+    const bool cut_k = k > 0 && k < a.V;
+    bool in = tid < n && (!cut_k || tid < k);
+    const int v = in ? sv[tid] : 0;
+    const float ev = in ? a.expo[int64_t(b) * a.V + (v - first)] : 1.f;
+    const float t = in ? t16_of(sx[tid]) * (1.f / kPerUnit) : kInf;
+    const float w = ex2_approx(-t);
+    if (!(p >= 1.f)) {
+      // weights in units of 2^-kFracBits
+      const uint64_t u = __float2ull_rn(w * 4398046511104.f);
+      uint64_t s = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t q = __shfl_up_sync(kAll, s, o);
+        if (lane >= o) s += q;
+      }
+      if (lane == 31) sh.wsum[warp] = s;
+      __syncthreads();
+      uint64_t before = s - u, all = 0;
+      for (int q = 0; q < kWarps; ++q) {
+        if (q < warp) before += sh.wsum[q];
+        all += sh.wsum[q];
+      }
+      in = in && before < times_up(cut_k ? all : total, p > 0.f ? p : 0.f);
+    }
+    in = in && (t <= t_max || tid == 0);
+    Best best{-1.f, kNoIdx, 0.f};
+    if (in) take(best, Best{__fdividef(w, ev), v, t});
+    float sum = in ? w : 0.f;
+    reduce(best, sum);
+    if (tid == 0) answer(b, best, sum, false, false);
+  }
 };
 
 template <typename T, bool kHeld>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   using E = Elem<T>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ Shared sh;
@@ -418,6 +621,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   r.warp = r.tid >> 5;
   r.lane = r.tid & 31;
   const int b = blockIdx.x / r.size;
+  if (r.tid == 0) sh.pushed = 0;
   r.cluster.barrier_arrive();  // waited for before any CTA's memory is written by another
   pdl_wait();
   pdl_trigger();
@@ -429,96 +633,95 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const int per = (groups + r.size - 1) / r.size;
   r.g0 = r.rank * per;
   r.ng = max(0, min(groups - r.g0, per));
-  uint4* held = reinterpret_cast<uint4*>(smem_raw);
-  r.held = held;
+  r.held = reinterpret_cast<uint4*>(smem_raw);
   const float temp = a.temperature != nullptr ? a.temperature[b] : 1.f;
+  const int k = a.top_k != nullptr ? a.top_k[b] : 0;
+  const float p = a.top_p != nullptr ? a.top_p[b] : 1.f;
+  const float mp = a.min_p != nullptr ? a.min_p[b] : 0.f;
   const bool greedy = !(temp > 0.f);
-  // 1 / T overflows below 2.9e-39: any finite number in its place leaves the
+  // 1 / T overflows for small T: any finite number in its place leaves the
   // maximum its weight 1 and takes all others' away
-  r.c = greedy ? 0.f : fminf(kLog2e / temp, FLT_MAX);
+  r.c16 = greedy ? 0.f : fminf(kPerUnit * kLog2e / temp, FLT_MAX);
 
   // the row's maximum; a NaN or +inf in it, or nothing finite, refuses it
-  float m = kNegInf;
-  bool bad = false;
-  for (int g = r.tid; g < r.ng; g += kThreads) {
-    const uint4 w = r.load_group(r.g0 + g);
-    if (kHeld) held[g] = w;
-    float y[E::N];
-    E::unpack(w, y);
+  float m = r.read();
 #pragma unroll
-    for (int i = 0; i < E::N; ++i) {
-      m = fmaxf(m, y[i]);
-      bad |= !(y[i] <= FLT_MAX);
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    const float q = __shfl_xor_sync(kAll, m, o);
+    m = max3_nan(m, q, q);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
   if (r.lane == 0) sh.wf[r.warp] = m;
-  bad = __syncthreads_or(bad);
+  __syncthreads();
   m = sh.wf[0];
-  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.wf[w]);
+#pragma unroll
+  for (int w = 1; w < kWarps; w += 3)
+    m = max3_nan(m, max3_nan(sh.wf[w], sh.wf[min(w + 1, kWarps - 1)], sh.wf[min(w + 2, kWarps - 1)]),
+                 kNegInf);
   r.cluster.barrier_wait();
-  if (r.tid < r.size) {
-    *r.cluster.map_shared_rank(&sh.cmax[r.rank], r.tid) = m;
-    *r.cluster.map_shared_rank(&sh.cbad[r.rank], r.tid) = bad;
-  }
+  if (r.tid < r.size) *r.cluster.map_shared_rank(&sh.cmax[r.rank], r.tid) = m;
   r.cluster.sync();
   m = kNegInf;
-  bad = false;
-  for (int q = 0; q < r.size; ++q) {
-    m = fmaxf(m, sh.cmax[q]);
-    bad |= sh.cbad[q] != 0;
-  }
-  bad |= m == kNegInf;
+  for (int q = 0; q < r.size; ++q) m = max3_nan(m, sh.cmax[q], kNegInf);
+  const bool bad = !(m <= FLT_MAX) || m == kNegInf;
   r.max = m;
 
   Best best{-1.f, kNoIdx, 0.f};
   float sum = 0.f;
   if (!bad && greedy) {
-    r.each([&](float x, int v) {
+    r.each_from(m, [&](float x, int v) {
       if (x == m) take(best, Best{1.f, v, 0.f});
     });
-    sum = 1.f;
   } else if (!bad) {
-    Kept kept;
-    Cut cut;
-    const int k = a.top_k != nullptr ? a.top_k[b] : 0;
-    if (k > 0 && k < a.V && r.template select<false>(k, -1.f, kept, &cut)) kept = r.settle(cut, kept);
-    const float p = a.top_p != nullptr ? a.top_p[b] : 1.f;
-    if (!(p >= 1.f) && r.template select<true>(0, p > 0.f ? p : 0.f, kept, &cut))
-      kept = r.settle(cut, kept);
-    const float mp = a.min_p != nullptr ? a.min_p[b] : 0.f;
     // w >= min_p as t <= -log2(min_p); the maximum always stays
-    const float t_max = mp > 0.f ? fmaxf(0.f, -log2f(mp)) : __int_as_float(0x7f800000);
+    const float t_max = mp > 0.f ? fmaxf(0.f, -log2f(mp)) : kInf;
+    Kept kept;
+    const bool cut_k = k > 0 && k < a.V, cut_p = !(p >= 1.f);
+    const float share = p > 0.f ? p : 0.f;
+    if (cut_k || cut_p) {
+      uint64_t rest;
+      const int at = cut_k ? r.template first_histogram<false, false>(k, -1.f, kept, &rest)
+                           : r.template first_histogram<true, false>(0, share, kept, &rest);
+      if (at >= 0 && sh.found_count <= kFew) {
+        r.push(at);
+        r.cluster.sync();
+        if (r.rank == 0) r.finish(b, k, p, t_max, sh.total);
+        return;
+      }
+      if (at >= 0)
+        kept = r.settle(cut_k ? r.template narrow<false>(at, rest, kept)
+                              : r.template narrow<true>(at, rest, kept), kept);
+      if (cut_k && cut_p) {
+        const int at_p = r.template first_histogram<true, true>(0, share, kept, &rest);
+        if (at_p >= 0) kept = r.settle(r.template narrow<true>(at_p, rest, kept), kept);
+      }
+    }
     const float* e = a.expo + int64_t(b) * a.V - r.first;
-    r.each([&](float x, int v) {
-      if (!kept.has(x, v)) return;
-      const float t = r.t_of(x);
-      if (t > t_max) return;
-      const float w = ex2_approx(-t);
-      sum += w;
-      take(best, Best{__fdividef(w, e[v]), v, t});
+    // a bound for the prefilter, a little low; t decides
+    const float least = fmaxf(kept.x, m - (t_max * kPerUnit + 1.f) / r.c16);
+    r.groups_from(least, [&](const uint4& w, int v) {
+      float y[E::N], ev[E::N], t[E::N];
+      E::unpack(w, y);
+#pragma unroll
+      for (int i = 0; i < E::N; ++i) {
+        t[i] = r.t16_of(y[i]) * (1.f / kPerUnit);
+        const bool in = y[i] > kNegInf && kept.has(y[i], v + i) && t[i] <= t_max;
+        if (!in) t[i] = -1.f;
+        ev[i] = in ? __ldg(e + v + i) : 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < E::N; ++i) {
+        if (t[i] < 0.f) continue;
+        const float q = ex2_approx(-t[i]);
+        sum += q;
+        // a thread's indices ascend: the first of equal scores stays
+        const float score = __fdividef(q, ev[i]);
+        if (score > best.score) best = Best{score, v + i, t[i]};
+      }
     });
   }
   // the cluster's best and sum, joined in a fixed order
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Best other{__shfl_xor_sync(kAll, best.score, o), __shfl_xor_sync(kAll, best.idx, o),
-                     __shfl_xor_sync(kAll, best.t, o)};
-    take(best, other);
-    sum += __shfl_xor_sync(kAll, sum, o);
-  }
-  __syncthreads();
-  if (r.lane == 0) {
-    sh.wbest[r.warp] = best;
-    sh.wf[r.warp] = sum;
-  }
-  __syncthreads();
+  r.reduce(best, sum);
   if (r.tid == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      take(best, sh.wbest[w]);
-      sum += sh.wf[w];
-    }
     *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
     *r.cluster.map_shared_rank(&sh.csum[r.rank], 0) = sum;
   }
@@ -530,12 +733,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
       take(best, sh.cbest[q]);
       sum += sh.csum[q];
     }
-    const bool none = bad || best.idx == kNoIdx;
-    if (none) record_status(a.status, dev_code(kDevBadList, kKerSample, 1));
-    a.token[b] = none ? -1 : best.idx - r.first;
-    if (a.logprob != nullptr)
-      a.logprob[b] = none ? __int_as_float(0x7fc00000)
-                          : greedy ? 0.f : -(best.t + log2f(sum)) * kLn2;
+    r.answer(b, best, sum, bad, greedy);
   }
 }
 
