@@ -59,6 +59,9 @@ __device__ __forceinline__ uint32_t max_bf16x2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 template <typename T>
 struct Elem;
 
@@ -121,7 +124,8 @@ struct Shared {
   // this CTA's histogram: counts, and weights in two halves. In the cluster's
   // first CTA the few logits and their indices take the place of the first two,
   // sorted ones that of the cluster's sums.
-  uint32_t cnt[kBuckets], hi[kBuckets], lo[kBuckets];
+  alignas(16) uint32_t cnt[kBuckets];
+  uint32_t hi[kBuckets], lo[kBuckets];
   // the cluster's
   uint64_t val[kBuckets];
   uint32_t num[kBuckets];
@@ -135,7 +139,7 @@ struct Shared {
   // of each warp
   float wf[kWarps];
   Best wbest[kWarps];
-  uint64_t found_before;
+  uint64_t found_rest;
   uint64_t total;
   int found;
   uint32_t found_count;  // logits in the buckets up to the found one
@@ -272,7 +276,8 @@ struct Row {
   }
 
   __device__ __forceinline__ void clear() const {
-    for (int i = tid; i < kBuckets; i += kThreads) sh.cnt[i] = sh.hi[i] = sh.lo[i] = 0;
+    uint4* h = reinterpret_cast<uint4*>(sh.cnt);  // cnt, hi, lo
+    for (int i = tid; i < 3 * kBuckets / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
 
@@ -286,7 +291,9 @@ struct Row {
       const int b = rank * share + i;
       uint32_t n = 0, hi = 0;
       uint64_t lo = 0;
-      for (int q = 0; q < size; ++q) {
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q >= size) break;
         n += *cluster.map_shared_rank(&sh.cnt[b], q);
         if (kWeights) {
           hi += *cluster.map_shared_rank(&sh.hi[b], q);
@@ -311,76 +318,55 @@ struct Row {
 
   // The bucket in which the running sum of val reaches the target (share < 0:
   // `target`, else that share of the whole), what the target is behind the sum
-  // before it, and the logits up to it; none: -1.
+  // before it, and the logits up to it; none: -1. Each warp adds up its 64
+  // buckets; the one that the target falls into looks closer.
   __device__ int find(uint64_t target, float share, uint64_t* rest) const {
     const uint64_t v0 = sh.val[2 * tid], v1 = sh.val[2 * tid + 1];
     const uint32_t n0 = sh.num[2 * tid], n1 = sh.num[2 * tid + 1];
     uint64_t s = v0 + v1;
-    uint32_t n = n0 + n1;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t u = __shfl_up_sync(kAll, s, o);
-      const uint32_t m = __shfl_up_sync(kAll, n, o);
-      if (lane >= o) {
-        s += u;
-        n += m;
-      }
-    }
-    if (lane == 31) {
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    const uint32_t n = __reduce_add_sync(kAll, n0 + n1);
+    if (lane == 0) {
       sh.wsum[warp] = s;
       sh.wcnt[warp] = n;
     }
     if (tid == 0) sh.found = -1;
     __syncthreads();
-    uint64_t before = 0, total = 0;
-    uint32_t count = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint64_t u = sh.wsum[w];
-      if (w < warp) {
-        before += u;
-        count += sh.wcnt[w];
-      }
-      total += u;
-    }
+    s = scan(lane < kWarps ? sh.wsum[lane] : 0);
+    const uint64_t total = __shfl_sync(kAll, s, 31);
     if (share >= 0.f) target = times_up(total, share);
-    before += s - v0 - v1;
-    count += n;
-    int b = -1;
-    if (before < target && target <= before + v0) {
-      b = 2 * tid;
-      count -= n1;
-    } else if (before + v0 < target && target <= before + v0 + v1) {
-      b = 2 * tid + 1;
-      before += v0;
-    }
-    if (b >= 0) {
-      sh.found = b;
-      sh.found_before = target - before;
-      sh.found_count = count;
-      sh.total = total;
+    if (warp == __popc(__ballot_sync(kAll, s < target))) {
+      uint64_t before = __shfl_sync(kAll, s, warp > 0 ? warp - 1 : 0);
+      if (warp == 0) before = 0;
+      const uint32_t count = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) +
+                             scan(n0 + n1);
+      before += scan(v0 + v1) - v0 - v1;
+      int b = -1;
+      if (before < target && target <= before + v0)
+        b = 2 * tid;
+      else if (before + v0 < target && target <= before + v0 + v1)
+        b = 2 * tid + 1;
+      if (b >= 0) {
+        sh.found = b;
+        sh.found_rest = target - before - (b & 1 ? v0 : 0);
+        sh.found_count = b & 1 ? count : count - n1;
+        sh.total = total;
+      }
     }
     __syncthreads();
-    b = sh.found;
-    *rest = sh.found_before;
-    return b;
+    *rest = sh.found_rest;
+    return sh.found;
   }
-
-  // The least key in [lo, hi] whose bucket is at most b; hi's is.
-  __device__ uint32_t least_key(uint32_t lo, uint32_t hi, int b) const {
-    while (lo < hi) {
-      const uint32_t step = (hi - lo) / 32 + 1;
-      const uint32_t probe = min(hi, lo + lane * step);
-      const uint32_t in = __ballot_sync(kAll, bucket_of(E::value(probe)) <= b);
-      if (in == 0) {
-        lo += 31 * step + 1;
-      } else {
-        const int f = __ffs(in) - 1;
-        hi = min(hi, lo + f * step);
-        if (f > 0) lo += (f - 1) * step + 1; else hi = lo;
-      }
+  // Inclusive sum over the warp's lanes.
+  template <typename U>
+  __device__ __forceinline__ U scan(U s) const {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const U u = __shfl_up_sync(kAll, s, o);
+      if (lane >= o) s += u;
     }
-    return lo;
+    return s;
   }
 
   // The first histogram of what `in` keeps (everything without kPart), and the
@@ -415,9 +401,17 @@ struct Row {
       const int s = kFracBits - kFineBits - b / kPerUnit;
       rest = s >= 0 ? (rest + (uint64_t(1) << s) - 1) >> s : rest << -s;
     }
-    const uint32_t top = E::key(max);
-    uint32_t klo = least_key(E::kLowest, top, b);
-    uint32_t khi = b > 0 ? least_key(klo, top, b - 1) - 1 : top;
+    // The interval's keys lie in [klo, khi] (max - x is between b and b + 1 over
+    // c16, up to rounding: 2^-21 of it is more than that); from `inside` on they
+    // are in it or above it.
+    const float d_hi = (b + 1) / c16;
+    uint32_t khi = b > 0 ? E::key(max - b / c16 * (1.f - 0x1p-21f)) : E::key(max);
+    uint32_t klo = E::kLowest;
+    float inside = kNegInf;
+    if (b < kBuckets - 1) {
+      klo = umax(klo, E::key(max - d_hi * (1.f + 0x1p-21f)));
+      inside = max - d_hi * (1.f - 0x1p-21f);
+    }
     while (true) {
       const uint32_t span = khi - klo;
       if (span == 0) break;
@@ -426,7 +420,7 @@ struct Row {
       clear();
       const float xlo = E::value(klo), xhi = E::value(khi);
       each_from(xlo, [&](float x, int v) {
-        if (!(x >= xlo && x <= xhi) || !in.has(x, v)) return;
+        if (!(x >= xlo && x <= xhi) || bucket_of(x) != b || !in.has(x, v)) return;
         const int i = static_cast<int>((khi - E::key(x)) >> s);
         atomicAdd(&sh.cnt[i], 1u);
         if (kWeights) add_fine(i, fine_of(t16_of(x)));
@@ -437,7 +431,7 @@ struct Row {
       khi -= static_cast<uint32_t>(i) << s;
       klo = s > 0 ? umax(klo, khi - ((1u << s) - 1)) : khi;
       // a single logit is in, whichever it is, and nothing below it
-      if (n == 1) return Cut{E::value(klo), kAll};
+      if (n == 1 && E::value(klo) > inside) return Cut{E::value(klo), kAll};
     }
     const float x = E::value(klo);
     if (kWeights) {
@@ -524,10 +518,15 @@ struct Row {
       sh.wf[warp] = sum;
     }
     __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) {
-        take(best, sh.wbest[w]);
-        sum += sh.wf[w];
+    if (warp == 0) {
+      best = sh.wbest[lane & (kWarps - 1)];
+      sum = sh.wf[lane & (kWarps - 1)];
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        const Best other{__shfl_xor_sync(kAll, best.score, o), __shfl_xor_sync(kAll, best.idx, o),
+                         __shfl_xor_sync(kAll, best.t, o)};
+        take(best, other);
+        sum += __shfl_xor_sync(kAll, sum, o);
       }
     }
   }
@@ -696,28 +695,66 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
     const float* e = a.expo + int64_t(b) * a.V - r.first;
-    // a bound for the prefilter, a little low; t decides
-    const float least = fmaxf(kept.x, m - (t_max * kPerUnit + 1.f) / r.c16);
-    r.groups_from(least, [&](const uint4& w, int v) {
-      float y[E::N], ev[E::N], t[E::N];
-      E::unpack(w, y);
+    auto draw = [&](float t, int v, float ev) {
+      const float q = ex2_approx(-t);
+      sum += q;
+      // a thread's indices ascend: the first of equal scores stays
+      const float score = __fdividef(q, ev);
+      if (score > best.score) best = Best{score, v, t};
+    };
+    if (kept.x == kNegInf && t_max == kInf) {
+      // nothing is cut off: group by group
+      r.groups_from(kNegInf, [&](const uint4& w, int v) {
+        float y[E::N], ev[E::N];
+        E::unpack(w, y);
 #pragma unroll
-      for (int i = 0; i < E::N; ++i) {
-        t[i] = r.t16_of(y[i]) * (1.f / kPerUnit);
-        const bool in = y[i] > kNegInf && kept.has(y[i], v + i) && t[i] <= t_max;
-        if (!in) t[i] = -1.f;
-        ev[i] = in ? __ldg(e + v + i) : 1.f;
-      }
+        for (int i = 0; i < E::N; ++i) ev[i] = y[i] > kNegInf ? __ldg(e + v + i) : 1.f;
 #pragma unroll
-      for (int i = 0; i < E::N; ++i) {
-        if (t[i] < 0.f) continue;
-        const float q = ex2_approx(-t[i]);
-        sum += q;
-        // a thread's indices ascend: the first of equal scores stays
-        const float score = __fdividef(q, ev[i]);
-        if (score > best.score) best = Best{score, v + i, t[i]};
+        for (int i = 0; i < E::N; ++i)
+          if (y[i] > kNegInf) draw(r.t16_of(y[i]) * (1.f / kPerUnit), v + i, ev[i]);
+      });
+    } else {
+      // Mostly few are left: a bit for each of a thread's next 32 logits that is,
+      // then those, four at a time. The bound is a little low; t decides.
+      const float least = fmaxf(fmaxf(kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
+      constexpr int kGroups = 32 / E::N;
+      for (int g = r.tid; g < r.ng; g += kGroups * kThreads) {
+        uint32_t left = 0;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          if (g + j * kThreads >= r.ng) break;
+          float y[E::N];
+          E::unpack(kHeld ? r.held[g + j * kThreads] : r.load_group(r.g0 + g + j * kThreads), y);
+#pragma unroll
+          for (int i = 0; i < E::N; ++i) left |= (y[i] >= least ? 1u : 0u) << (j * E::N + i);
+        }
+        while (left != 0) {
+          constexpr int U = 4;
+          float t[U], ev[U];
+          int at[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            t[u] = -1.f;
+            ev[u] = 1.f;
+            at[u] = 0;
+            if (left == 0) continue;
+            const int k = __ffs(left) - 1, gk = g + k / E::N * kThreads;
+            left &= left - 1;
+            at[u] = (r.g0 + gk) * E::N + k % E::N;
+            const float y = kHeld ? to_f32(reinterpret_cast<const T*>(r.held + gk)[k % E::N])
+                                  : to_f32(r.base[at[u]]);
+            const float ty = r.t16_of(y) * (1.f / kPerUnit);
+            if (kept.has(y, at[u]) && ty <= t_max) {
+              t[u] = ty;
+              ev[u] = __ldg(e + at[u]);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (t[u] >= 0.f) draw(t[u], at[u], ev[u]);
+        }
       }
-    });
+    }
   }
   // the cluster's best and sum, joined in a fixed order
   r.reduce(best, sum);
