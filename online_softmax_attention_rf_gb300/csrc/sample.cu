@@ -13,15 +13,16 @@
 // for top-k and of weights for top-p, gives the interval that the cut falls into.
 // Where no more than 512 logits lie above the interval's lower end, as is usual,
 // these alone go on: one CTA puts them in order and finishes the row. Otherwise
-// histograms of the logits' bits inside the interval narrow it down to one value,
-// and a count of that value's occurrences settles which of them are in.
-// Counts and weights are added as integers (a weight to 22 bits below the power
-// of two of its interval, about what float32 carries), so that the order of the
-// additions cannot move a cut.
+// histograms of the logits' bits narrow the interval down until few lie in it, and
+// one CTA finds the cut among those.
+// Counts and weights are added as integers (a weight to 20 bits below the power
+// of two of its interval, which is off by 2^-20 of it at most), so that the order
+// of the additions cannot move a cut.
 //
-// A cluster of CTAs holds a row in shared memory, read once from global memory;
-// each pass goes over it there. Histograms are joined through distributed shared
-// memory: each CTA adds up its share of the buckets and hands the sums to all.
+// A cluster of CTAs takes a row: as many as leave all rows' CTAs resident, so
+// that one row has many and many rows have one each. A CTA reads its share once if
+// that fits shared memory beside another CTA's, else in each pass, out of L2.
+// Histograms and few logits are joined through distributed shared memory.
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -39,8 +40,14 @@ constexpr int kMaxCluster = 8;
 constexpr int kBuckets = 1024;
 constexpr int kPerUnit = 16;   // buckets of the first histogram per unit of t
 constexpr int kFracBits = 42;  // of the row's sum of weights: up to 2^20 of them, of at most 1
-constexpr int kFineBits = 22;  // of a weight, below the power of two of its interval
-constexpr int kHalf = 11;      // of them in the lower half: 2^20 weights fit 32 bits
+constexpr int kFineBits = 20;  // of a weight, below the power of two of its interval
+constexpr int kHalf = 17;      // of them in the lower half
+// Logits that a CTA adds to its histogram before the sums are taken out of it: a
+// count and the upper three bits of its weights then share a word, and the lower
+// bits fit another.
+constexpr int kWindow = 32 * kThreads;
+static_assert((uint64_t(kWindow) << kHalf) < (1ull << 32) && kWindow * 7ull < (1ull << kHalf),
+              "a window's sums fit their places");
 constexpr int kFew = kThreads; // logits that one CTA finishes, one a thread
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf();
@@ -69,6 +76,9 @@ template <>
 struct Elem<float> {
   static constexpr int N = 4;  // in 16 bytes
   static constexpr uint32_t kLowest = 0x007fffffu;  // key of -inf
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
   static __device__ __forceinline__ void unpack(const uint4& w, float (&y)[4]) {
     y[0] = __uint_as_float(w.x); y[1] = __uint_as_float(w.y);
     y[2] = __uint_as_float(w.z); y[3] = __uint_as_float(w.w);
@@ -92,6 +102,9 @@ template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
   static constexpr uint32_t kLowest = 0x007fu;
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
   static __device__ __forceinline__ void unpack(const uint4& w, float (&y)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -121,14 +134,14 @@ __device__ __forceinline__ void take(Best& a, const Best& b) {
 }
 
 struct Shared {
-  // this CTA's histogram: counts, and weights in two halves. In the cluster's
-  // first CTA the few logits and their indices take the place of the first two,
-  // sorted ones that of the cluster's sums.
-  alignas(16) uint32_t cnt[kBuckets];
-  uint32_t hi[kBuckets], lo[kBuckets];
-  // the cluster's
-  uint64_t val[kBuckets];
-  uint32_t num[kBuckets];
+  // This CTA's histogram: counts above the upper halves of the weights, and the
+  // lower halves. In the cluster's first CTA few logits and their indices take
+  // its place as they come.
+  alignas(16) uint32_t upper[kBuckets];
+  uint32_t lower[kBuckets];
+  // What the others see of it, of two histograms in turn; few logits in order.
+  uint64_t val[2][kBuckets];
+  uint32_t num[2][kBuckets];
   uint64_t wsum[kWarps];
   uint32_t wcnt[kWarps];
   // a value of each CTA of the cluster
@@ -139,26 +152,28 @@ struct Shared {
   // of each warp
   float wf[kWarps];
   Best wbest[kWarps];
-  uint64_t found_rest;
-  uint64_t total;
+  // the bucket that a sum falls into
   int found;
-  uint32_t found_count;  // logits in the buckets up to the found one
+  uint32_t found_num, found_count;  // logits in it, and up to its end
+  uint64_t found_rest, total;
   int tie_limit;
-  uint32_t pushed;       // few logits that arrived
+  uint32_t pushed;  // few logits that arrived
+  float cut_x;      // the cut among them
+  int cut_limit;
 };
 
-// Where a selection ends: every logit above x is in, and of those equal to x
-// the first `ties` (kAll: all).
-struct Cut {
-  float x;
-  uint32_t ties;
-};
-
-// What a selection left of this CTA's logits. -inf has no probability.
+// What a selection left: the logits above x, and of those equal to x the ones
+// before an index. -inf has no probability.
 struct Kept {
   float x = kNegInf;
-  int limit = 0;  // of those equal to x, the ones before this index
+  int limit = 0;
   __device__ __forceinline__ bool has(float y, int v) const { return y > x || (y == x && v < limit); }
+};
+
+// A thread's two buckets of the cluster's histogram.
+struct Sums {
+  uint64_t v[2];
+  uint32_t n[2];
 };
 
 // share * total, rounded up, at least 1 (0 <= share < 1).
@@ -187,6 +202,7 @@ struct Row {
   int end;           // one past its last
   int g0, ng;        // this CTA's groups of 16 bytes
   float max, c16;    // maximum, kPerUnit * log2(e) / temperature
+  int turn = 0;      // of the two places that others read
 
   __device__ __forceinline__ Row(const SampleArgs& a_, Shared& s)
       : a(a_), sh(s), cluster(cg::this_cluster()) {}
@@ -204,129 +220,168 @@ struct Row {
     return w;
   }
 
-  // Reads the row; this thread's maximum (NaN if one is).
-  __device__ float read() const {
-    float m = kNegInf;
-    // groups that lie wholly in the row; the first and the last one may not
-    const int f0 = g0 == 0 && first > 0 ? 1 : 0;
-    const int f1 = min(ng, end / E::N - g0);
-    const uint4* from = reinterpret_cast<const uint4*>(base) + g0;
-    constexpr int U = 4;
-    int g = f0 + tid;
-    for (; g + (U - 1) * kThreads < f1; g += U * kThreads) {
-      uint4 w[U];
+  // U of this thread's groups, g and those kThreads behind each other, from where
+  // the row is; groups that there are not count as -inf.
+  template <int U, bool kFromShared>
+  __device__ __forceinline__ void fetch(uint4 (&w)[U], int g) const {
+    const uint4* from = kFromShared ? held : reinterpret_cast<const uint4*>(base) + g0;
+    // the first and the last group may not lie wholly in the row
+    const int f0 = !kFromShared && g0 == 0 && first > 0 ? 1 : 0;
+    const int f1 = kFromShared ? ng : min(ng, end / E::N - g0);
+    if (g >= f0 && g + (U - 1) * kThreads < f1) {
 #pragma unroll
-      for (int j = 0; j < U; ++j) w[j] = __ldg(from + g + j * kThreads);
+      for (int j = 0; j < U; ++j)
+        w[j] = kFromShared ? from[g + j * kThreads] : __ldg(from + g + j * kThreads);
+    } else {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        if (kHeld) held[g + j * kThreads] = w[j];
-        m = E::max_of(w[j], m);
+        const int h = g + j * kThreads;
+        w[j] = E::none();
+        if (h < ng) w[j] = kFromShared ? from[h] : load_group(g0 + h);
       }
     }
-    for (; g < f1; g += kThreads) {
-      const uint4 w = __ldg(from + g);
-      if (kHeld) held[g] = w;
-      m = E::max_of(w, m);
-    }
-    // ragged ends: group 0, and those from max(f0, f1) on (one at most)
-    const int e = tid == 0 ? (f0 > 0 && ng > 0 ? 0 : -1) : tid == 1 ? f1 : -1;
-    if (e >= 0 && e < ng && (tid == 0 || e >= f0)) {
-      const uint4 w = load_group(g0 + e);
-      if (kHeld) held[e] = w;
-      m = E::max_of(w, m);
+  }
+
+  // Reads the row; this thread's maximum (NaN if one is).
+  __device__ __forceinline__ float read() const {
+    constexpr int U = 6;
+    float m = kNegInf;
+    for (int g = tid; g < ng; g += U * kThreads) {
+      uint4 w[U];
+      fetch<U, false>(w, g);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (kHeld && g + j * kThreads < ng) held[g + j * kThreads] = w[j];
+        m = E::max_of(w[j], m);
+      }
     }
     return m;
   }
 
-  // f(group, index of its first logit from base), over this thread's groups with
-  // a logit of at least `least`, in ascending order.
-  template <typename F>
-  __device__ __forceinline__ void groups_from(float least, F&& f) const {
-#pragma unroll 2
-    for (int g = tid; g < ng; g += kThreads) {
-      const uint4 w = kHeld ? held[g] : load_group(g0 + g);
-      if (E::max_of(w, kNegInf) >= least) f(w, (g0 + g) * E::N);
-    }
-  }
+  // f(x, index from base) for this thread's logits of at least `least` and some
+  // others, in ascending order.
   template <typename F>
   __device__ __forceinline__ void each_from(float least, F&& f) const {
-    groups_from(least, [&](const uint4& w, int v) {
-      float y[E::N];
-      E::unpack(w, y);
+    constexpr int U = 4;
+    for (int g = tid; g < ng; g += U * kThreads) {
+      uint4 w[U];
+      fetch<U, kHeld>(w, g);
 #pragma unroll
-      for (int i = 0; i < E::N; ++i) f(y[i], v + i);
-    });
+      for (int j = 0; j < U; ++j) {
+        if (E::max_of(w[j], kNegInf) < least) continue;
+        float y[E::N];
+        E::unpack(w[j], y);
+#pragma unroll
+        for (int i = 0; i < E::N; ++i) f(y[i], (g0 + g + j * kThreads) * E::N + i);
+      }
+    }
   }
 
   // kPerUnit * t: not below 0; +inf for -inf
   __device__ __forceinline__ float t16_of(float x) const { return __fmul_rn(max - x, c16); }
-  __device__ __forceinline__ int bucket_of(float x) const {
-    const float t = fminf(t16_of(x), kBuckets - 1.f);
-    return __float_as_int(__fadd_rz(t, 8388608.f)) & (kBuckets - 1);
+  static __device__ __forceinline__ int bucket_at(float t16) {  // t16 in [0, kBuckets)
+    return __float_as_int(__fadd_rz(t16, 8388608.f)) & (kBuckets - 1);
   }
-  // A weight over 2^-e, e the power of its interval, as an integer.
+  __device__ __forceinline__ int bucket_of(float x) const {
+    return bucket_at(fminf(t16_of(x), kBuckets - 1.f));
+  }
+  // A weight over 2^-e, e the power of its interval, as an integer: less than 2^20
+  // (the weight is taken 2^-20 of it smaller).
   static __device__ __forceinline__ uint32_t fine_of(float t16) {
     const float e16 = __fadd_rz(t16, 134217728.f) - 134217728.f;  // to a multiple of 16
-    const float f = ex2_approx((e16 - t16) * (1.f / kPerUnit));   // in (0.5, 1]
-    return __float_as_uint(f + 2.f) - 0x40000000u;                // f * 2^22
-  }
-  __device__ __forceinline__ void add_fine(int b, uint32_t f) const {
-    atomicAdd(&sh.hi[b], f >> kHalf);
-    atomicAdd(&sh.lo[b], f & ((1u << kHalf) - 1));
+    const float f = ex2_approx(fmaf(e16 - t16, 1.f / kPerUnit, -1.3758e-6f));
+    return __float_as_uint(f + 8.f) - 0x41000000u;
   }
 
-  __device__ __forceinline__ void clear() const {
-    uint4* h = reinterpret_cast<uint4*>(sh.cnt);  // cnt, hi, lo
-    for (int i = tid; i < 3 * kBuckets / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
+  // The CTA's histogram of its logits that place(x, index) gives a bucket (not -1),
+  // of those from `least` on, in this thread's two buckets.
+  template <bool kWeights, typename F>
+  __device__ Sums histogram(float least, F&& place) const {
+    uint2* upper = reinterpret_cast<uint2*>(sh.upper);
+    uint2* lower = reinterpret_cast<uint2*>(sh.lower);
+    upper[tid] = lower[tid] = make_uint2(0, 0);
     __syncthreads();
-  }
-
-  // Joins the CTAs' histograms: val (counts, or weights; weights of the first
-  // histogram in units of 2^-kFracBits) and num (counts), the same in each CTA.
-  template <bool kWeights>
-  __device__ void join(bool by_unit) const {
-    cluster.sync();
-    const int share = kBuckets / size;
-    for (int i = tid; i < share; i += kThreads) {
-      const int b = rank * share + i;
-      uint32_t n = 0, hi = 0;
-      uint64_t lo = 0;
+    Sums s{};
+    constexpr int U = 4, kBatches = kWindow / kThreads / (U * E::N);
+    for (int g = tid; g - tid < ng;) {
+#pragma unroll 1
+      for (int k = 0; k < kBatches; ++k, g += U * kThreads) {
+        uint4 w[U];
+        fetch<U, kHeld>(w, g);
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {
-        if (q >= size) break;
-        n += *cluster.map_shared_rank(&sh.cnt[b], q);
-        if (kWeights) {
-          hi += *cluster.map_shared_rank(&sh.hi[b], q);
-          lo += *cluster.map_shared_rank(&sh.lo[b], q);
+        for (int j = 0; j < U; ++j) {
+          if (E::max_of(w[j], kNegInf) < least) continue;
+          float y[E::N];
+          E::unpack(w[j], y);
+#pragma unroll
+          for (int i = 0; i < E::N; ++i) {
+            const int b = place(y[i], (g0 + g + j * kThreads) * E::N + i);
+            if (b < 0) continue;
+            const uint32_t f = kWeights ? fine_of(t16_of(y[i])) : 0u;
+            atomicAdd(&sh.upper[b], (1u << kHalf) + (f >> kHalf));
+            if (kWeights) atomicAdd(&sh.lower[b], f & ((1u << kHalf) - 1));
+          }
         }
       }
-      uint64_t v = n;
-      if (kWeights) {
-        v = (uint64_t(hi) << kHalf) + lo;
-        if (by_unit) {
-          const int s = kFracBits - kFineBits - b / kPerUnit;
-          v = s >= 0 ? v << s : v >> -s;
-        }
+      __syncthreads();
+      const uint2 u = upper[tid], l = lower[tid];
+      upper[tid] = lower[tid] = make_uint2(0, 0);
+      const uint32_t us[2] = {u.x, u.y}, ls[2] = {l.x, l.y};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s.n[i] += us[i] >> kHalf;
+        s.v[i] += (uint64_t(us[i] & ((1u << kHalf) - 1)) << kHalf) + ls[i];
       }
-      for (int q = 0; q < size; ++q) {
-        *cluster.map_shared_rank(&sh.val[b], q) = v;
-        *cluster.map_shared_rank(&sh.num[b], q) = n;
-      }
+      __syncthreads();
     }
-    cluster.sync();
+    if (!kWeights) {
+      s.v[0] = s.n[0];
+      s.v[1] = s.n[1];
+    }
+    return s;
   }
 
-  // The bucket in which the running sum of val reaches the target (share < 0:
-  // `target`, else that share of the whole), what the target is behind the sum
-  // before it, and the logits up to it; none: -1. Each warp adds up its 64
-  // buckets; the one that the target falls into looks closer.
-  __device__ int find(uint64_t target, float share, uint64_t* rest) const {
-    const uint64_t v0 = sh.val[2 * tid], v1 = sh.val[2 * tid + 1];
-    const uint32_t n0 = sh.num[2 * tid], n1 = sh.num[2 * tid + 1];
-    uint64_t s = v0 + v1;
+  // The cluster's histogram from its CTAs'.
+  __device__ void join(Sums& s) {
+    if (size == 1) return;
+    *reinterpret_cast<ulonglong2*>(&sh.val[turn][2 * tid]) = make_ulonglong2(s.v[0], s.v[1]);
+    *reinterpret_cast<uint2*>(&sh.num[turn][2 * tid]) = make_uint2(s.n[0], s.n[1]);
+    cluster.sync();
+#pragma unroll
+    for (int q = 1; q < kMaxCluster; ++q) {
+      if (q >= size) break;
+      const int other = (rank + q) & (size - 1);
+      const ulonglong2 v =
+          *reinterpret_cast<ulonglong2*>(cluster.map_shared_rank(&sh.val[turn][2 * tid], other));
+      const uint2 n = *reinterpret_cast<uint2*>(cluster.map_shared_rank(&sh.num[turn][2 * tid], other));
+      s.v[0] += v.x;
+      s.v[1] += v.y;
+      s.n[0] += n.x;
+      s.n[1] += n.y;
+    }
+    turn ^= 1;  // this place is written again only behind the next histogram's barrier
+  }
+
+  // Inclusive sum over the warp's lanes.
+  template <typename U>
+  __device__ __forceinline__ U scan(U s) const {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const U u = __shfl_up_sync(kAll, s, o);
+      if (lane >= o) s += u;
+    }
+    return s;
+  }
+
+  // The bucket in which the running sum reaches the target (share < 0: `target`,
+  // else that share of the whole) and what the target is behind the sum before it;
+  // none: -1. Each warp adds up its 64 buckets; the one that the target falls into
+  // looks closer.
+  __device__ int find(const Sums& h, uint64_t target, float share, uint64_t* rest) const {
+    uint64_t s = h.v[0] + h.v[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    const uint32_t n = __reduce_add_sync(kAll, n0 + n1);
+    const uint32_t n = __reduce_add_sync(kAll, h.n[0] + h.n[1]);
     if (lane == 0) {
       sh.wsum[warp] = s;
       sh.wcnt[warp] = n;
@@ -340,17 +395,14 @@ struct Row {
       uint64_t before = __shfl_sync(kAll, s, warp > 0 ? warp - 1 : 0);
       if (warp == 0) before = 0;
       const uint32_t count = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) +
-                             scan(n0 + n1);
-      before += scan(v0 + v1) - v0 - v1;
-      int b = -1;
-      if (before < target && target <= before + v0)
-        b = 2 * tid;
-      else if (before + v0 < target && target <= before + v0 + v1)
-        b = 2 * tid + 1;
-      if (b >= 0) {
-        sh.found = b;
-        sh.found_rest = target - before - (b & 1 ? v0 : 0);
-        sh.found_count = b & 1 ? count : count - n1;
+                             scan(h.n[0] + h.n[1]);
+      before += scan(h.v[0] + h.v[1]) - h.v[0] - h.v[1];
+      const bool odd = target > before + h.v[0];
+      if (before < target && target <= before + h.v[0] + h.v[1]) {
+        sh.found = 2 * tid + odd;
+        sh.found_num = odd ? h.n[1] : h.n[0];
+        sh.found_count = odd ? count : count - h.n[1];
+        sh.found_rest = target - before - (odd ? h.v[0] : 0);
         sh.total = total;
       }
     }
@@ -358,143 +410,169 @@ struct Row {
     *rest = sh.found_rest;
     return sh.found;
   }
-  // Inclusive sum over the warp's lanes.
-  template <typename U>
-  __device__ __forceinline__ U scan(U s) const {
+
+  // The bucket of the first histogram of what `in` keeps (everything without
+  // kPart) that the cut falls into, as find(). Weights in units of 2^-kFracBits.
+  template <bool kWeights, bool kPart>
+  __device__ int first_bucket(uint64_t target, float share, const Kept& in, uint64_t* rest) {
+    Sums s = histogram<kWeights>(kPart ? in.x : kNegInf, [&](float x, int v) {
+      const float t = t16_of(x);
+      // the weights of the last bucket, below 2^-63, count for nothing
+      const bool is = kPart ? in.has(x, v) : x > kNegInf;
+      return is && (!kWeights || t < kBuckets - 1.f) ? bucket_at(fminf(t, kBuckets - 1.f)) : -1;
+    });
+    join(s);
+    if (kWeights) {
+      const int e = kFracBits - kFineBits - 2 * tid / kPerUnit;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const U u = __shfl_up_sync(kAll, s, o);
-      if (lane >= o) s += u;
+      for (int i = 0; i < 2; ++i) s.v[i] = e >= 0 ? s.v[i] << e : s.v[i] >> -e;
     }
-    return s;
+    return find(s, target, share, rest);
   }
 
-  // The first histogram of what `in` keeps (everything without kPart), and the
-  // bucket that the cut falls into, as find().
-  template <bool kWeights, bool kPart>
-  __device__ int first_histogram(uint64_t target, float share, const Kept& in, uint64_t* rest) const {
-    clear();
-    each_from(kPart ? in.x : kNegInf, [&](float x, int v) {
-      if (kPart && !in.has(x, v)) return;
-      const float t = t16_of(x);
-      if (kWeights) {
-        if (t < kBuckets - 1.f) {  // the weights behind, below 2^-63, count for nothing
-          const int b = __float_as_int(__fadd_rz(t, 8388608.f)) & (kBuckets - 1);
-          atomicAdd(&sh.cnt[b], 1u);
-          add_fine(b, fine_of(t));
-        }
-      } else if (x > kNegInf) {
-        const int b = __float_as_int(__fadd_rz(fminf(t, kBuckets - 1.f), 8388608.f)) & (kBuckets - 1);
-        atomicAdd(&sh.cnt[b], 1u);
+  // Few logits, those that is(x, index), go to the cluster's first CTA.
+  template <typename F>
+  __device__ __forceinline__ void push(float least, F&& is) const {
+    each_from(least, [&](float x, int v) {
+      if (!is(x, v)) return;
+      const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
+      if (at < kFew) {
+        *cluster.map_shared_rank(&sh.upper[at], 0) = __float_as_uint(x);
+        *cluster.map_shared_rank(&sh.lower[at], 0) = static_cast<uint32_t>(v);
       }
     });
-    join<kWeights>(true);
-    return find(target, share, rest);
+    cluster.sync();
   }
 
-  // The place where the running sum over (x descending, index ascending) of
-  // counts, or of weights, goes on from bucket b of the first histogram by
-  // `rest`.
-  template <bool kWeights>
-  __device__ Cut narrow(int b, uint64_t rest, const Kept& in) const {
-    if (kWeights) {  // in units of the interval's weights
-      const int s = kFracBits - kFineBits - b / kPerUnit;
-      rest = s >= 0 ? (rest + (uint64_t(1) << s) - 1) >> s : rest << -s;
+  // This thread's logit and index of the few, in order (one CTA); how many.
+  __device__ int in_order(float* x, int* v) const {
+    const int n = min(static_cast<int>(sh.pushed), kFew);
+    float* sx = reinterpret_cast<float*>(sh.val);
+    int* sv = reinterpret_cast<int*>(sh.val) + kFew;
+    if (tid < n) {
+      const float mine = __uint_as_float(sh.upper[tid]);
+      const int at = static_cast<int>(sh.lower[tid]);
+      int r = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const float y = __uint_as_float(sh.upper[j]);
+        r += y > mine || (y == mine && static_cast<int>(sh.lower[j]) < at);
+      }
+      sx[r] = mine;
+      sv[r] = at;
     }
-    // The interval's keys lie in [klo, khi] (max - x is between b and b + 1 over
-    // c16, up to rounding: 2^-21 of it is more than that); from `inside` on they
-    // are in it or above it.
-    const float d_hi = (b + 1) / c16;
+    __syncthreads();
+    *x = tid < n ? sx[tid] : kNegInf;
+    *v = tid < n ? sv[tid] : kNoIdx;
+    return n;
+  }
+
+  // Sum over the threads before this one, and over all.
+  __device__ uint64_t sum_before(uint64_t u, uint64_t* all) const {
+    const uint64_t s = scan(u);
+    if (lane == 31) sh.wsum[warp] = s;
+    __syncthreads();
+    const uint64_t w = scan(lane < kWarps ? sh.wsum[lane] : 0);
+    *all = __shfl_sync(kAll, w, 31);
+    const uint64_t before = __shfl_sync(kAll, w, warp > 0 ? warp - 1 : 0);
+    __syncthreads();
+    return (warp > 0 ? before : 0) + s - u;
+  }
+
+  // What is left of `in` when the running sum of counts, or of weights, in the
+  // order of the logits, is cut where it goes on from bucket b of the first
+  // histogram, which holds n logits, by `rest`.
+  template <bool kWeights>
+  __device__ Kept narrow(int b, uint32_t n, uint64_t rest, const Kept& in) {
+    if (kWeights) {  // in units of the interval's weights
+      const int e = kFracBits - kFineBits - b / kPerUnit;
+      rest = e >= 0 ? (rest + (uint64_t(1) << e) - 1) >> e : rest << -e;
+    }
+    // The bucket's keys lie in [klo, khi]: max - x is between b and b + 1 over c16,
+    // up to rounding; 2^-21 of it is more than that.
     uint32_t khi = b > 0 ? E::key(max - b / c16 * (1.f - 0x1p-21f)) : E::key(max);
     uint32_t klo = E::kLowest;
-    float inside = kNegInf;
-    if (b < kBuckets - 1) {
-      klo = umax(klo, E::key(max - d_hi * (1.f + 0x1p-21f)));
-      inside = max - d_hi * (1.f - 0x1p-21f);
-    }
-    while (true) {
-      const uint32_t span = khi - klo;
-      if (span == 0) break;
+    if (b < kBuckets - 1) klo = umax(klo, E::key(max - (b + 1) / c16 * (1.f + 0x1p-21f)));
+    auto is = [&](float x, int v) {
+      return x >= E::value(klo) && x <= E::value(khi) && bucket_of(x) == b && in.has(x, v);
+    };
+    while (n > kFew && khi > klo) {
       int s = 0;
-      while ((span >> s) >= kBuckets) ++s;
-      clear();
-      const float xlo = E::value(klo), xhi = E::value(khi);
-      each_from(xlo, [&](float x, int v) {
-        if (!(x >= xlo && x <= xhi) || bucket_of(x) != b || !in.has(x, v)) return;
-        const int i = static_cast<int>((khi - E::key(x)) >> s);
-        atomicAdd(&sh.cnt[i], 1u);
-        if (kWeights) add_fine(i, fine_of(t16_of(x)));
+      while (((khi - klo) >> s) >= kBuckets) ++s;
+      Sums h = histogram<kWeights>(E::value(klo), [&](float x, int v) {
+        return is(x, v) ? static_cast<int>((khi - E::key(x)) >> s) : -1;
       });
-      join<kWeights>(false);
-      const int i = find(rest, -1.f, &rest);  // the interval's sum is at least the rest
-      const uint32_t n = sh.num[i];
+      join(h);
+      const int i = find(h, rest, -1.f, &rest);  // the interval's sum is at least the rest
+      n = sh.found_num;
       khi -= static_cast<uint32_t>(i) << s;
       klo = s > 0 ? umax(klo, khi - ((1u << s) - 1)) : khi;
-      // a single logit is in, whichever it is, and nothing below it
-      if (n == 1 && E::value(klo) > inside) return Cut{E::value(klo), kAll};
     }
-    const float x = E::value(klo);
-    if (kWeights) {
-      const uint64_t f = fine_of(t16_of(x));
-      rest = (rest + f - 1) / f;
+    if (n > kFew) {  // one value
+      const float x = E::value(klo);
+      if (kWeights) {
+        const uint64_t f = fine_of(t16_of(x));
+        rest = (rest + f - 1) / f;
+      }
+      const int limit = tie_limit(x, static_cast<uint32_t>(rest < kAll ? rest : kAll));
+      return Kept{x, x == in.x ? min(limit, in.limit) : limit};
     }
-    return Cut{x, static_cast<uint32_t>(rest < kAll ? rest : kAll)};
+    push(E::value(klo), is);
+    if (rank == 0) {
+      float x;
+      int v;
+      const int m = in_order(&x, &v);
+      uint64_t all;
+      const uint64_t u = tid < m ? (kWeights ? fine_of(t16_of(x)) : 1) : 0;
+      const uint64_t before = sum_before(u, &all);
+      // the last one that is in; all of them if rounding leaves the sum short
+      if (tid < m && before < rest && (before + u >= rest || tid == m - 1))
+        for (int q = 0; q < size; ++q) {
+          *cluster.map_shared_rank(&sh.cut_x, q) = x;
+          *cluster.map_shared_rank(&sh.cut_limit, q) = v + 1;
+        }
+      if (tid == 0) sh.pushed = 0;
+    }
+    cluster.sync();
+    return Kept{sh.cut_x, sh.cut_limit};
   }
   static __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-  // What the cut leaves of `in`.
-  __device__ Kept settle(const Cut& cut, const Kept& in) const {
-    if (cut.x < in.x) return in;  // the lower end of an interval with one logit in it
-    const int last = cut.x == in.x ? in.limit : kNoIdx;
-    return Kept{cut.x, cut.ties == kAll ? last : min(last, tie_limit(cut))};
-  }
-
-  // Of the elements equal to the cut, the first cut.ties are those before the
-  // returned index.
-  __device__ int tie_limit(const Cut& cut) const {
+  // Of the logits equal to x the first `ties` are those before the returned index.
+  __device__ int tie_limit(float x, uint32_t ties) const {
     uint32_t n = 0;
-    each_from(cut.x, [&](float x, int) { n += x == cut.x; });
+    each_from(x, [&](float y, int) { n += y == x; });
     n = __reduce_add_sync(kAll, n);
-    __syncthreads();
     if (lane == 0) sh.wcnt[warp] = n;
     if (tid == 0) sh.tie_limit = kNoIdx;
     __syncthreads();
-    n = 0;
-    for (int w = 0; w < kWarps; ++w) n += sh.wcnt[w];
+    n = __reduce_add_sync(kAll, lane < kWarps ? sh.wcnt[lane] : 0u);
     if (tid < size) *cluster.map_shared_rank(&sh.cties[rank], tid) = n;
     cluster.sync();
     uint32_t before = 0;
     for (int q = 0; q < rank; ++q) before += sh.cties[q];
-    if (cut.ties <= before) return 0;
-    uint32_t left = cut.ties - before;
+    if (ties <= before) return 0;
+    uint32_t left = ties - before;
     if (left >= n) return kNoIdx;
     // the left'th of this CTA's, in order
     for (int g = 0; g < ng; g += kThreads) {
-      uint32_t mine = 0;
+      uint4 w[1];
+      fetch<1, kHeld>(w, g + tid);
       float y[E::N];
-      if (g + tid < ng) {
-        E::unpack(kHeld ? held[g + tid] : load_group(g0 + g + tid), y);
+      E::unpack(w[0], y);
+      uint32_t mine = 0;
 #pragma unroll
-        for (int i = 0; i < E::N; ++i) mine += y[i] == cut.x;
-      }
-      uint32_t s = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(kAll, s, o);
-        if (lane >= o) s += u;
-      }
+      for (int i = 0; i < E::N; ++i) mine += y[i] == x;
+      const uint32_t s = scan(mine);
       __syncthreads();
       if (lane == 31) sh.wcnt[warp] = s;
       __syncthreads();
-      uint32_t total = 0, ahead = s - mine;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) ahead += sh.wcnt[w];
-        total += sh.wcnt[w];
-      }
+      uint32_t ahead = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) + s - mine;
+      const uint32_t total = __reduce_add_sync(kAll, lane < kWarps ? sh.wcnt[lane] : 0u);
       if (ahead < left && left <= ahead + mine) {
 #pragma unroll
         for (int i = 0; i < E::N; ++i)
-          if (y[i] == cut.x && ++ahead == left) sh.tie_limit = (g0 + g + tid) * E::N + i + 1;
+          if (y[i] == x && ++ahead == left) sh.tie_limit = (g0 + g + tid) * E::N + i + 1;
       }
       if (left <= total) break;
       left -= total;
@@ -503,15 +581,16 @@ struct Row {
     return sh.tie_limit;
   }
 
-  // The best and the sum of the CTA's threads, in a fixed order, in thread 0.
+  // The best and the sum of the CTA's threads, in a fixed order, in warp 0.
   __device__ __forceinline__ void reduce(Best& best, float& sum) const {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    auto step = [&](int o) {
       const Best other{__shfl_xor_sync(kAll, best.score, o), __shfl_xor_sync(kAll, best.idx, o),
                        __shfl_xor_sync(kAll, best.t, o)};
       take(best, other);
       sum += __shfl_xor_sync(kAll, sum, o);
-    }
+    };
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) step(o);
     __syncthreads();
     if (lane == 0) {
       sh.wbest[warp] = best;
@@ -522,12 +601,7 @@ struct Row {
       best = sh.wbest[lane & (kWarps - 1)];
       sum = sh.wf[lane & (kWarps - 1)];
 #pragma unroll
-      for (int o = kWarps / 2; o > 0; o >>= 1) {
-        const Best other{__shfl_xor_sync(kAll, best.score, o), __shfl_xor_sync(kAll, best.idx, o),
-                         __shfl_xor_sync(kAll, best.t, o)};
-        take(best, other);
-        sum += __shfl_xor_sync(kAll, sum, o);
-      }
+      for (int o = kWarps / 2; o > 0; o >>= 1) step(o);
     }
   }
 
@@ -542,61 +616,20 @@ struct Row {
                               : -(best.t + log2f(sum)) * kLn2;
   }
 
-  // The few logits from bucket b up go to the cluster's first CTA.
-  __device__ __forceinline__ void push(int b) const {
-    // a bound for the prefilter, a little low; bucket_of decides
-    const float least = fmaxf(kNegInf, max - (b + 2) / c16);
-    each_from(least, [&](float x, int v) {
-      if (!(x > kNegInf) || bucket_of(x) > b) return;
-      const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
-      if (at < kFew) {
-        *cluster.map_shared_rank(&sh.cnt[at], 0) = __float_as_uint(x);
-        *cluster.map_shared_rank(&sh.hi[at], 0) = static_cast<uint32_t>(v);
-      }
-    });
-  }
-
-  // The row from its few logits (one CTA): in order, then both cuts and the draw.
-  // total: the row's sum of weights, where top-k does not cut.
-  __device__ void finish(int b, int k, float p, float t_max, uint64_t total) const {
-    const int n = min(static_cast<int>(sh.pushed), kFew);
-    float* sx = reinterpret_cast<float*>(sh.val);  // sorted
-    int* sv = reinterpret_cast<int*>(sh.val) + kFew;
-    if (tid < n) {
-      const float x = __uint_as_float(sh.cnt[tid]);
-      const int v = static_cast<int>(sh.hi[tid]);
-      int r = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
-        const float y = __uint_as_float(sh.cnt[j]);
-        r += y > x || (y == x && static_cast<int>(sh.hi[j]) < v);
-      }
-      sx[r] = x;
-      sv[r] = v;
-    }
-    __syncthreads();
-    const bool cut_k = k > 0 && k < a.V;
+  // The row from its few logits (one CTA): both cuts and the draw. total: the row's
+  // sum of weights, where top-k does not cut.
+  __device__ void finish(int b, bool cut_k, int k, float p, float t_max, uint64_t total) const {
+    float x;
+    int v;
+    const int n = in_order(&x, &v);
     bool in = tid < n && (!cut_k || tid < k);
-    const int v = in ? sv[tid] : 0;
-    const float ev = in ? a.expo[int64_t(b) * a.V + (v - first)] : 1.f;
-    const float t = in ? t16_of(sx[tid]) * (1.f / kPerUnit) : kInf;
+    const float ev = in ? __ldg(a.expo + int64_t(b) * a.V + (v - first)) : 1.f;
+    const float t = in ? t16_of(x) * (1.f / kPerUnit) : kInf;
     const float w = ex2_approx(-t);
     if (!(p >= 1.f)) {
-      // weights in units of 2^-kFracBits
-      const uint64_t u = __float2ull_rn(w * 4398046511104.f);
-      uint64_t s = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t q = __shfl_up_sync(kAll, s, o);
-        if (lane >= o) s += q;
-      }
-      if (lane == 31) sh.wsum[warp] = s;
-      __syncthreads();
-      uint64_t before = s - u, all = 0;
-      for (int q = 0; q < kWarps; ++q) {
-        if (q < warp) before += sh.wsum[q];
-        all += sh.wsum[q];
-      }
+      uint64_t all;
+      // as the histogram's weights: 2^kFracBits, less 2^-20 of it
+      const uint64_t before = sum_before(__float2ull_rn(w * 4398042316800.f), &all);
       in = in && before < times_up(cut_k ? all : total, p > 0.f ? p : 0.f);
     }
     in = in && (t <= t_max || tid == 0);
@@ -643,24 +676,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   r.c16 = greedy ? 0.f : fminf(kPerUnit * kLog2e / temp, FLT_MAX);
 
   // the row's maximum; a NaN or +inf in it, or nothing finite, refuses it
+  auto max2 = [](float x, float y) { return max3_nan(x, y, y); };
   float m = r.read();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float q = __shfl_xor_sync(kAll, m, o);
-    m = max3_nan(m, q, q);
-  }
+  for (int o = 16; o > 0; o >>= 1) m = max2(m, __shfl_xor_sync(kAll, m, o));
   if (r.lane == 0) sh.wf[r.warp] = m;
   __syncthreads();
-  m = sh.wf[0];
+  m = sh.wf[r.lane & (kWarps - 1)];
 #pragma unroll
-  for (int w = 1; w < kWarps; w += 3)
-    m = max3_nan(m, max3_nan(sh.wf[w], sh.wf[min(w + 1, kWarps - 1)], sh.wf[min(w + 2, kWarps - 1)]),
-                 kNegInf);
+  for (int o = kWarps / 2; o > 0; o >>= 1) m = max2(m, __shfl_xor_sync(kAll, m, o));
   r.cluster.barrier_wait();
-  if (r.tid < r.size) *r.cluster.map_shared_rank(&sh.cmax[r.rank], r.tid) = m;
-  r.cluster.sync();
-  m = kNegInf;
-  for (int q = 0; q < r.size; ++q) m = max3_nan(m, sh.cmax[q], kNegInf);
+  if (r.size > 1) {
+    if (r.tid < r.size) *r.cluster.map_shared_rank(&sh.cmax[r.rank], r.tid) = m;
+    r.cluster.sync();
+    m = kNegInf;
+    for (int q = 0; q < r.size; ++q) m = max2(m, sh.cmax[q]);
+  }
   const bool bad = !(m <= FLT_MAX) || m == kNegInf;
   r.max = m;
 
@@ -678,20 +709,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const float share = p > 0.f ? p : 0.f;
     if (cut_k || cut_p) {
       uint64_t rest;
-      const int at = cut_k ? r.template first_histogram<false, false>(k, -1.f, kept, &rest)
-                           : r.template first_histogram<true, false>(0, share, kept, &rest);
+      const int at = cut_k ? r.template first_bucket<false, false>(k, -1.f, kept, &rest)
+                           : r.template first_bucket<true, false>(0, share, kept, &rest);
       if (at >= 0 && sh.found_count <= kFew) {
-        r.push(at);
-        r.cluster.sync();
-        if (r.rank == 0) r.finish(b, k, p, t_max, sh.total);
+        // a bound for what is looked at, a little low
+        r.push(m - (at + 2) / r.c16, [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= at; });
+        if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, sh.total);
         return;
       }
       if (at >= 0)
-        kept = r.settle(cut_k ? r.template narrow<false>(at, rest, kept)
-                              : r.template narrow<true>(at, rest, kept), kept);
+        kept = cut_k ? r.template narrow<false>(at, sh.found_num, rest, kept)
+                     : r.template narrow<true>(at, sh.found_num, rest, kept);
       if (cut_k && cut_p) {
-        const int at_p = r.template first_histogram<true, true>(0, share, kept, &rest);
-        if (at_p >= 0) kept = r.settle(r.template narrow<true>(at_p, rest, kept), kept);
+        const int at_p = r.template first_bucket<true, true>(0, share, kept, &rest);
+        if (at_p >= 0) kept = r.template narrow<true>(at_p, sh.found_num, rest, kept);
       }
     }
     const float* e = a.expo + int64_t(b) * a.V - r.first;
@@ -702,76 +733,82 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const float score = __fdividef(q, ev);
       if (score > best.score) best = Best{score, v, t};
     };
-    if (kept.x == kNegInf && t_max == kInf) {
-      // nothing is cut off: group by group
-      r.groups_from(kNegInf, [&](const uint4& w, int v) {
-        float y[E::N], ev[E::N];
-        E::unpack(w, y);
+    const bool all = kept.x == kNegInf && t_max == kInf;
+    // a bound for what is looked at, a little low; t decides
+    const float least = fmaxf(fmaxf(kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
+    constexpr int U = 4;
+    for (int g = r.tid; g < r.ng; g += U * kThreads) {
+      uint4 w[U];
+      r.template fetch<U, kHeld>(w, g);
+      if (all) {  // nothing is cut off
 #pragma unroll
-        for (int i = 0; i < E::N; ++i) ev[i] = y[i] > kNegInf ? __ldg(e + v + i) : 1.f;
+        for (int j = 0; j < U; ++j) {
+          const int v = (r.g0 + g + j * kThreads) * E::N;
+          float y[E::N], ev[E::N];
+          E::unpack(w[j], y);
 #pragma unroll
-        for (int i = 0; i < E::N; ++i)
-          if (y[i] > kNegInf) draw(r.t16_of(y[i]) * (1.f / kPerUnit), v + i, ev[i]);
-      });
-    } else {
-      // Mostly few are left: a bit for each of a thread's next 32 logits that is,
-      // then those, four at a time. The bound is a little low; t decides.
-      const float least = fmaxf(fmaxf(kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
-      constexpr int kGroups = 32 / E::N;
-      for (int g = r.tid; g < r.ng; g += kGroups * kThreads) {
-        uint32_t left = 0;
+          for (int i = 0; i < E::N; ++i) ev[i] = y[i] > kNegInf ? __ldg(e + v + i) : 1.f;
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-          if (g + j * kThreads >= r.ng) break;
-          float y[E::N];
-          E::unpack(kHeld ? r.held[g + j * kThreads] : r.load_group(r.g0 + g + j * kThreads), y);
-#pragma unroll
-          for (int i = 0; i < E::N; ++i) left |= (y[i] >= least ? 1u : 0u) << (j * E::N + i);
+          for (int i = 0; i < E::N; ++i)
+            if (y[i] > kNegInf) draw(r.t16_of(y[i]) * (1.f / kPerUnit), v + i, ev[i]);
         }
-        while (left != 0) {
-          constexpr int U = 4;
-          float t[U], ev[U];
-          int at[U];
+        continue;
+      }
+      // Mostly few are left: a bit for each of these logits that is, then those, four
+      // at a time.
+      uint32_t left = 0;
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            t[u] = -1.f;
-            ev[u] = 1.f;
-            at[u] = 0;
-            if (left == 0) continue;
-            const int k = __ffs(left) - 1, gk = g + k / E::N * kThreads;
-            left &= left - 1;
-            at[u] = (r.g0 + gk) * E::N + k % E::N;
-            const float y = kHeld ? to_f32(reinterpret_cast<const T*>(r.held + gk)[k % E::N])
-                                  : to_f32(r.base[at[u]]);
-            const float ty = r.t16_of(y) * (1.f / kPerUnit);
-            if (kept.has(y, at[u]) && ty <= t_max) {
-              t[u] = ty;
-              ev[u] = __ldg(e + at[u]);
-            }
+      for (int j = 0; j < U; ++j) {
+        float y[E::N];
+        E::unpack(w[j], y);
+#pragma unroll
+        for (int i = 0; i < E::N; ++i) left |= (y[i] >= least ? 1u : 0u) << (j * E::N + i);
+      }
+      while (left != 0) {
+        constexpr int W = 4;
+        float t[W], ev[W];
+        int at[W];
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+          t[u] = -1.f;
+          ev[u] = 1.f;
+          at[u] = 0;
+          if (left == 0) continue;
+          const int bit = __ffs(left) - 1, gk = g + bit / E::N * kThreads;
+          left &= left - 1;
+          at[u] = (r.g0 + gk) * E::N + bit % E::N;
+          const float y = to_f32(kHeld ? reinterpret_cast<const T*>(r.held + gk)[bit % E::N]
+                                       : r.base[at[u]]);
+          const float ty = r.t16_of(y) * (1.f / kPerUnit);
+          if (kept.has(y, at[u]) && ty <= t_max) {
+            t[u] = ty;
+            ev[u] = __ldg(e + at[u]);
           }
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (t[u] >= 0.f) draw(t[u], at[u], ev[u]);
         }
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+          if (t[u] >= 0.f) draw(t[u], at[u], ev[u]);
       }
     }
   }
   // the cluster's best and sum, joined in a fixed order
   r.reduce(best, sum);
-  if (r.tid == 0) {
-    *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
-    *r.cluster.map_shared_rank(&sh.csum[r.rank], 0) = sum;
-  }
-  r.cluster.sync();
-  if (r.rank == 0 && r.tid == 0) {
-    best = sh.cbest[0];
-    sum = sh.csum[0];
-    for (int q = 1; q < r.size; ++q) {
-      take(best, sh.cbest[q]);
-      sum += sh.csum[q];
+  if (r.size > 1) {
+    if (r.tid == 0) {
+      *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
+      *r.cluster.map_shared_rank(&sh.csum[r.rank], 0) = sum;
     }
-    r.answer(b, best, sum, bad, greedy);
+    r.cluster.sync();
+    if (r.rank == 0 && r.tid == 0) {
+      best = sh.cbest[0];
+      sum = sh.csum[0];
+      for (int q = 1; q < r.size; ++q) {
+        take(best, sh.cbest[q]);
+        sum += sh.csum[q];
+      }
+    }
   }
+  if (r.rank == 0 && r.tid == 0) r.answer(b, best, sum, bad, greedy);
 }
 
 template <typename T, bool kHeld>
@@ -798,13 +835,20 @@ cudaError_t launch_k(const SampleArgs& a, int cluster, size_t smem, cudaStream_t
 
 template <typename T>
 cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
-  constexpr int kMostHeld = 160 * 1024;
-  // a row goes to as many CTAs as it takes to have few of its logits a thread
+  constexpr int kSms = 152, kResident = 2 * kSms;  // CTAs
+  constexpr int kMostHeld = 80 * 1024;             // beside another CTA's and both histograms
+  constexpr int64_t kL2 = 100 << 20;
+  // As many CTAs a row as leave all rows' CTAs resident, with a few logits a thread.
   int cluster = 1;
-  while (cluster < kMaxCluster && a.V > cluster * kThreads * 4) cluster *= 2;
+  while (cluster < kMaxCluster && int64_t(a.B) * cluster * 2 <= kResident &&
+         a.V > cluster * kThreads * 4)
+    cluster *= 2;
   const int groups = (a.V + 2 * Elem<T>::N - 2) / Elem<T>::N;  // with any lead
-  const size_t bytes = size_t((groups + cluster - 1) / cluster) * 16;
-  if (bytes <= kMostHeld) return launch_k<T, true>(a, cluster, bytes, s);
+  auto share = [&] { return size_t((groups + cluster - 1) / cluster) * 16; };
+  // rows that are read again, and resident at one time, fit L2
+  while (cluster < kMaxCluster && share() > kMostHeld && kResident * int64_t(share()) > kL2)
+    cluster *= 2;
+  if (share() <= kMostHeld) return launch_k<T, true>(a, cluster, share(), s);
   return launch_k<T, false>(a, cluster, 0, s);
 }
 
