@@ -9,15 +9,17 @@
 //   largest down whose weights reach top_p of their sum (equal logits: lower
 //   index first), min-p of those w_j >= min_p; the draw is argmax w_j / e_j.
 // Both cuts fall at one place in the order by (x descending, index ascending),
-// and neither needs the row sorted. A histogram of t in steps of 1/16, of counts
-// for top-k and of weights for top-p, gives the interval that the cut falls into.
-// Where no more than 512 logits lie above the interval's lower end, as is usual,
-// these alone go on: one CTA puts them in order and finishes the row. Otherwise
-// histograms of the logits' bits narrow the interval down until few lie in it, and
-// one CTA finds the cut among those.
-// Counts and weights are added as integers (a weight to 20 bits below the power
-// of two of its interval, which is off by 2^-20 of it at most), so that the order
-// of the additions cannot move a cut.
+// and neither needs the row sorted. A histogram of counts by t, in steps of 1/16,
+// gives the step that top-k's cut falls into, and, since it bounds the weights in
+// each step to 2^(1/16), the few steps that top-p's may fall into. Where no more
+// than 512 logits lie above the last of these steps' end, as is usual, these alone
+// go on: one CTA puts them in order and finishes the row. Otherwise a histogram,
+// of weights for top-p, divides those steps finely, histograms of the logits' bits
+// narrow it down where that is not enough (equal logits in great numbers), and
+// one CTA finds the cut among the few logits that are left.
+// Weights are added as integers where atomics do it (to 20 bits below the power of
+// two of their step, which is off by 2^-20 of them at most), and else in a fixed
+// order, so that the order of the additions cannot move a cut.
 //
 // A cluster of CTAs takes a row: as many as leave all rows' CTAs resident, so
 // that one row has many and many rows have one each. A CTA reads its share once if
@@ -50,6 +52,8 @@ static_assert((uint64_t(kWindow) << kHalf) < (1ull << 32) && kWindow * 7ull < (1
               "a window's sums fit their places");
 constexpr int kFew = kThreads; // logits that one CTA finishes, one a thread
 constexpr uint32_t kAll = 0xffffffffu;
+// A weight of 1 in units of 2^-kFracBits, less 2^-20 of it (as fine_of has it).
+constexpr float kWeightOne = 4398042316800.f;
 constexpr float kInf = __builtin_huge_valf();
 static_assert(kBuckets == 2 * kThreads, "the scan takes two buckets a thread");
 static_assert(kFew <= kBuckets, "a histogram's place holds the few logits");
@@ -142,6 +146,7 @@ struct Shared {
   // What the others see of it, of two histograms in turn; few logits in order.
   uint64_t val[2][kBuckets];
   uint32_t num[2][kBuckets];
+  uint64_t part[2];  // and of a sum of weights
   uint64_t wsum[kWarps];
   uint32_t wcnt[kWarps];
   // a value of each CTA of the cluster
@@ -277,6 +282,38 @@ struct Row {
     }
   }
 
+  // The same with the sum, in units of 2^-kFracBits, of the weights of what
+  // weight(x, t16, index) says.
+  template <typename W, typename F>
+  __device__ __forceinline__ uint64_t each_and_sum(float least, W&& weight, F&& f) const {
+    // a few weights at a time in float32 (at most 15 roundings), these as integers
+    constexpr int U = 4, kRun = 16 / E::N;
+    uint64_t sum = 0;
+    for (int g = tid; g < ng; g += U * kThreads) {
+      uint4 w[U];
+      fetch<U, kHeld>(w, g);
+#pragma unroll
+      for (int j = 0; j < U; j += kRun) {
+        float run = 0.f;
+#pragma unroll
+        for (int i = j; i < j + kRun; ++i) {
+          if (E::max_of(w[i], kNegInf) < least) continue;
+          float y[E::N];
+          E::unpack(w[i], y);
+#pragma unroll
+          for (int e = 0; e < E::N; ++e) {
+            const int v = (g0 + g + i * kThreads) * E::N + e;
+            const float t16 = t16_of(y[e]);
+            if (weight(y[e], t16, v)) run += ex2_approx(t16 * (-1.f / kPerUnit));
+            f(y[e], t16, v);
+          }
+        }
+        sum += __float2ull_rn(run * kWeightOne);
+      }
+    }
+    return sum;
+  }
+
   // kPerUnit * t: not below 0; +inf for -inf
   __device__ __forceinline__ float t16_of(float x) const { return __fmul_rn(max - x, c16); }
   static __device__ __forceinline__ int bucket_at(float t16) {  // t16 in [0, kBuckets)
@@ -293,33 +330,48 @@ struct Row {
     return __float_as_uint(f + 8.f) - 0x41000000u;
   }
 
-  // The CTA's histogram of its logits that place(x, index) gives a bucket (not -1),
-  // of those from `least` on, in this thread's two buckets.
-  template <bool kWeights, typename F>
-  __device__ Sums histogram(float least, F&& place) const {
+  // A logit that no logit up to the end of step hi lies below.
+  __device__ __forceinline__ float reach(int hi) const {
+    return hi < kBuckets - 1 ? max - (hi + 2) / c16 : kNegInf;
+  }
+
+  // The CTA's histogram of its logits that place(x, t16, index) gives a bucket (not
+  // -1), of those from `least` on, in this thread's two buckets; kSum: and its sum
+  // of the weights of those that weight(x, t16, index), as each_and_sum().
+  template <bool kWeights, bool kSum, typename F, typename W>
+  __device__ Sums histogram(float least, F&& place, W&& weight, uint64_t* sum) const {
     uint2* upper = reinterpret_cast<uint2*>(sh.upper);
     uint2* lower = reinterpret_cast<uint2*>(sh.lower);
     upper[tid] = lower[tid] = make_uint2(0, 0);
     __syncthreads();
     Sums s{};
-    constexpr int U = 4, kBatches = kWindow / kThreads / (U * E::N);
+    constexpr int U = 4, kBatches = kWindow / kThreads / (U * E::N), kRun = 16 / E::N;
     for (int g = tid; g - tid < ng;) {
 #pragma unroll 1
       for (int k = 0; k < kBatches; ++k, g += U * kThreads) {
         uint4 w[U];
         fetch<U, kHeld>(w, g);
+        float run = 0.f;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          if (E::max_of(w[j], kNegInf) < least) continue;
-          float y[E::N];
-          E::unpack(w[j], y);
+          if (E::max_of(w[j], kNegInf) >= least) {
+            float y[E::N];
+            E::unpack(w[j], y);
 #pragma unroll
-          for (int i = 0; i < E::N; ++i) {
-            const int b = place(y[i], (g0 + g + j * kThreads) * E::N + i);
-            if (b < 0) continue;
-            const uint32_t f = kWeights ? fine_of(t16_of(y[i])) : 0u;
-            atomicAdd(&sh.upper[b], (1u << kHalf) + (f >> kHalf));
-            if (kWeights) atomicAdd(&sh.lower[b], f & ((1u << kHalf) - 1));
+            for (int i = 0; i < E::N; ++i) {
+              const int v = (g0 + g + j * kThreads) * E::N + i;
+              const float t16 = t16_of(y[i]);
+              if (kSum && weight(y[i], t16, v)) run += ex2_approx(t16 * (-1.f / kPerUnit));
+              const int b = place(y[i], t16, v);
+              if (b < 0) continue;
+              const uint32_t f = kWeights ? fine_of(t16) : 0u;
+              atomicAdd(&sh.upper[b], (1u << kHalf) + (f >> kHalf));
+              if (kWeights) atomicAdd(&sh.lower[b], f & ((1u << kHalf) - 1));
+            }
+          }
+          if (kSum && j % kRun == kRun - 1) {
+            *sum += __float2ull_rn(run * kWeightOne);
+            run = 0.f;
           }
         }
       }
@@ -341,25 +393,47 @@ struct Row {
     return s;
   }
 
-  // The cluster's histogram from its CTAs'.
-  __device__ void join(Sums& s) {
-    if (size == 1) return;
-    *reinterpret_cast<ulonglong2*>(&sh.val[turn][2 * tid]) = make_ulonglong2(s.v[0], s.v[1]);
+  // The cluster's histogram from its CTAs', and the sum over all of their threads
+  // of a weight each.
+  template <bool kWeights, bool kPart>
+  __device__ uint64_t join(Sums& s, uint64_t part) {
+    if (kPart) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+      if (lane == 0) sh.wsum[warp] = part;
+      __syncthreads();
+      part = sh.wsum[lane & (kWarps - 1)];
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+      __syncthreads();
+    }
+    if (size == 1) return part;
+    if (kWeights)
+      *reinterpret_cast<ulonglong2*>(&sh.val[turn][2 * tid]) = make_ulonglong2(s.v[0], s.v[1]);
     *reinterpret_cast<uint2*>(&sh.num[turn][2 * tid]) = make_uint2(s.n[0], s.n[1]);
+    if (kPart && tid == 0) sh.part[turn] = part;
     cluster.sync();
 #pragma unroll
     for (int q = 1; q < kMaxCluster; ++q) {
       if (q >= size) break;
       const int other = (rank + q) & (size - 1);
-      const ulonglong2 v =
-          *reinterpret_cast<ulonglong2*>(cluster.map_shared_rank(&sh.val[turn][2 * tid], other));
+      if (kWeights) {
+        const ulonglong2 v =
+            *reinterpret_cast<ulonglong2*>(cluster.map_shared_rank(&sh.val[turn][2 * tid], other));
+        s.v[0] += v.x;
+        s.v[1] += v.y;
+      }
       const uint2 n = *reinterpret_cast<uint2*>(cluster.map_shared_rank(&sh.num[turn][2 * tid], other));
-      s.v[0] += v.x;
-      s.v[1] += v.y;
       s.n[0] += n.x;
       s.n[1] += n.y;
+      if (kPart) part += *cluster.map_shared_rank(&sh.part[turn], other);
+    }
+    if (!kWeights) {
+      s.v[0] = s.n[0];
+      s.v[1] = s.n[1];
     }
     turn ^= 1;  // this place is written again only behind the next histogram's barrier
+    return part;
   }
 
   // Inclusive sum over the warp's lanes.
@@ -373,11 +447,11 @@ struct Row {
     return s;
   }
 
-  // The bucket in which the running sum reaches the target (share < 0: `target`,
-  // else that share of the whole) and what the target is behind the sum before it;
-  // none: -1. Each warp adds up its 64 buckets; the one that the target falls into
+  // The bucket in which the running sum of h.v reaches the target and what the
+  // target is behind the sum before it; none: -1 (clamp: the last one with anything
+  // in it). Each warp adds up its 64 buckets; the one that the target falls into
   // looks closer.
-  __device__ int find(const Sums& h, uint64_t target, float share, uint64_t* rest) const {
+  __device__ int find(const Sums& h, uint64_t target, uint64_t* rest, bool clamp = false) const {
     uint64_t s = h.v[0] + h.v[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
@@ -389,8 +463,7 @@ struct Row {
     if (tid == 0) sh.found = -1;
     __syncthreads();
     s = scan(lane < kWarps ? sh.wsum[lane] : 0);
-    const uint64_t total = __shfl_sync(kAll, s, 31);
-    if (share >= 0.f) target = times_up(total, share);
+    if (clamp) target = min(target, __shfl_sync(kAll, s, 31));
     if (warp == __popc(__ballot_sync(kAll, s < target))) {
       uint64_t before = __shfl_sync(kAll, s, warp > 0 ? warp - 1 : 0);
       if (warp == 0) before = 0;
@@ -403,31 +476,66 @@ struct Row {
         sh.found_num = odd ? h.n[1] : h.n[0];
         sh.found_count = odd ? count : count - h.n[1];
         sh.found_rest = target - before - (odd ? h.v[0] : 0);
-        sh.total = total;
       }
     }
     __syncthreads();
+    const int b = sh.found;
     *rest = sh.found_rest;
-    return sh.found;
+    __syncthreads();
+    return b;
   }
 
-  // The bucket of the first histogram of what `in` keeps (everything without
-  // kPart) that the cut falls into, as find(). Weights in units of 2^-kFracBits.
+  // The steps [*lo, *hi] of 1/16 that a cut of what `in` keeps (everything without
+  // kPart) falls into: that of the target'th logit, or, with kWeights, of the share
+  // of the weights, whose sum is *total. False: there is none. sh.found_count: the
+  // logits up to *hi's end; one step: sh.found_num in it, *rest to go in it.
   template <bool kWeights, bool kPart>
-  __device__ int first_bucket(uint64_t target, float share, const Kept& in, uint64_t* rest) {
-    Sums s = histogram<kWeights>(kPart ? in.x : kNegInf, [&](float x, int v) {
-      const float t = t16_of(x);
-      // the weights of the last bucket, below 2^-63, count for nothing
-      const bool is = kPart ? in.has(x, v) : x > kNegInf;
-      return is && (!kWeights || t < kBuckets - 1.f) ? bucket_at(fminf(t, kBuckets - 1.f)) : -1;
-    });
-    join(s);
-    if (kWeights) {
-      const int e = kFracBits - kFineBits - 2 * tid / kPerUnit;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) s.v[i] = e >= 0 ? s.v[i] << e : s.v[i] >> -e;
+  __device__ bool steps(uint64_t target, float share, const Kept& in, int* lo, int* hi,
+                        uint64_t* total, uint64_t* rest) {
+    *reinterpret_cast<uint2*>(&sh.upper[2 * tid]) = make_uint2(0, 0);
+    __syncthreads();
+    const float least = kPart ? in.x : kNegInf;
+    auto is = [&](float x, int v) { return kPart ? in.has(x, v) : x > kNegInf; };
+    auto add = [&](float x, float t16, int v) {
+      if (is(x, v)) atomicAdd(&sh.upper[bucket_at(fminf(t16, kBuckets - 1.f))], 1u);
+    };
+    uint64_t sum = 0;
+    if (kWeights)
+      sum = each_and_sum(least, [&](float x, float, int v) { return is(x, v); }, add);
+    else
+      each_from(least, [&](float x, int v) { add(x, t16_of(x), v); });
+    __syncthreads();
+    Sums s{};
+    s.n[0] = sh.upper[2 * tid];
+    s.n[1] = sh.upper[2 * tid + 1];
+    *total = join<false, kWeights>(s, sum);
+    if (!kWeights) {
+      s.v[0] = s.n[0];
+      s.v[1] = s.n[1];
+      *lo = *hi = find(s, target, rest);
+      return *lo >= 0;
     }
-    return find(s, target, share, rest);
+    // The weights of a step are between 2^-(b + 1)/16 and 2^-b/16 a logit; 2^-18
+    // covers the roundings of the sums, the weights and t.
+    auto bound = [&](int more, float slack) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float w = ex2_approx((2 * tid + i + more) * (-1.f / kPerUnit));
+        s.v[i] = s.n[i] * __float2ull_rn(w * kWeightOne * slack);
+      }
+    };
+    *rest = times_up(*total, share);
+    uint64_t unused;
+    bound(0, 1.f + 0x1p-18f);
+    *lo = min(find(s, *rest, &unused, true), kBuckets - 2);
+    bound(1, 1.f - 0x1p-18f);
+    *hi = find(s, *rest, &unused);
+    if (*hi < 0) {  // behind the bounds' reach; what is in the last step weighs nothing
+      *hi = kBuckets - 2;
+      if (tid == 0) sh.found_count = kAll;
+      __syncthreads();
+    }
+    return true;
   }
 
   // Few logits, those that is(x, index), go to the cluster's first CTA.
@@ -479,31 +587,69 @@ struct Row {
     return (warp > 0 ? before : 0) + s - u;
   }
 
-  // What is left of `in` when the running sum of counts, or of weights, in the
-  // order of the logits, is cut where it goes on from bucket b of the first
-  // histogram, which holds n logits, by `rest`.
+  // What is left of `in` when the running sum of counts, or of weights (rest: of
+  // them in units of 2^-kFracBits), in the order of the logits, is cut within the
+  // steps [lo, hi] by `rest`: counted from lo on, or, with kWeights, from the first
+  // logit on. n: the logits in these steps, or more.
   template <bool kWeights>
-  __device__ Kept narrow(int b, uint32_t n, uint64_t rest, const Kept& in) {
-    if (kWeights) {  // in units of the interval's weights
-      const int e = kFracBits - kFineBits - b / kPerUnit;
+  __device__ Kept narrow(int lo, int hi, uint32_t n, uint64_t rest, const Kept& in) {
+    // The steps divided by a power of two: a part lies within one unit of t, and
+    // what is subtracted and multiplied here is exact.
+    int parts = 0;  // log2 of the parts of a step
+    while ((hi - lo + 1) << (parts + 1) <= kBuckets) ++parts;
+    const float scale = static_cast<float>(1 << parts);
+    auto part_of = [&](float t16) { return bucket_at(fminf((t16 - lo) * scale, kBuckets - 1.f)); };
+    int part = -1;  // the one that the cut falls into (-1: all)
+    auto within = [&](float t16) {
+      return t16 >= lo && (t16 < hi + 1.f || hi == kBuckets - 1) && (part < 0 || part_of(t16) == part);
+    };
+    if ((kWeights || n > kFew) && hi < kBuckets - 1) {
+      uint64_t above = 0;
+      Sums h = histogram<kWeights, kWeights>(
+          reach(hi),
+          [&](float x, float t16, int v) {
+            return in.has(x, v) && within(t16) ? part_of(t16) : -1;
+          },
+          [&](float x, float t16, int v) { return t16 < lo && in.has(x, v); }, &above);
+      above = join<kWeights, kWeights>(h, above);
+      if (kWeights) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e = kFracBits - kFineBits - (lo + ((2 * tid + i) >> parts)) / kPerUnit;
+          h.v[i] = e >= 0 ? h.v[i] << e : h.v[i] >> -e;
+        }
+        rest = rest > above ? rest - above : 1;
+      }
+      part = find(h, rest, &rest, true);
+      n = sh.found_num;
+    }
+    const int step = lo + (part > 0 ? part >> parts : 0);
+    if (kWeights) {  // in units of the part's weights
+      const int e = kFracBits - kFineBits - step / kPerUnit;
       rest = e >= 0 ? (rest + (uint64_t(1) << e) - 1) >> e : rest << -e;
     }
-    // The bucket's keys lie in [klo, khi]: max - x is between b and b + 1 over c16,
-    // up to rounding; 2^-21 of it is more than that.
-    uint32_t khi = b > 0 ? E::key(max - b / c16 * (1.f - 0x1p-21f)) : E::key(max);
+    // The part's keys lie in [klo, khi]: max - x is between its ends over c16, up to
+    // rounding; 2^-21 of it is more than that.
+    const float width = part < 0 ? hi + 1.f - lo : 1.f / scale;
+    const float from = part < 0 ? lo : lo + part / scale;
+    uint32_t khi = from > 0.f ? E::key(max - from / c16 * (1.f - 0x1p-21f)) : E::key(max);
     uint32_t klo = E::kLowest;
-    if (b < kBuckets - 1) klo = umax(klo, E::key(max - (b + 1) / c16 * (1.f + 0x1p-21f)));
+    if (hi < kBuckets - 1) klo = umax(klo, E::key(max - (from + width) / c16 * (1.f + 0x1p-21f)));
     auto is = [&](float x, int v) {
-      return x >= E::value(klo) && x <= E::value(khi) && bucket_of(x) == b && in.has(x, v);
+      return x >= E::value(klo) && x <= E::value(khi) && within(t16_of(x)) && in.has(x, v);
     };
     while (n > kFew && khi > klo) {
       int s = 0;
       while (((khi - klo) >> s) >= kBuckets) ++s;
-      Sums h = histogram<kWeights>(E::value(klo), [&](float x, int v) {
-        return is(x, v) ? static_cast<int>((khi - E::key(x)) >> s) : -1;
-      });
-      join(h);
-      const int i = find(h, rest, -1.f, &rest);  // the interval's sum is at least the rest
+      uint64_t none = 0;
+      Sums h = histogram<kWeights, false>(
+          E::value(klo),
+          [&](float x, float, int v) {
+            return is(x, v) ? static_cast<int>((khi - E::key(x)) >> s) : -1;
+          },
+          [](float, float, int) { return false; }, &none);
+      join<kWeights, false>(h, 0);
+      const int i = find(h, rest, &rest, true);
       n = sh.found_num;
       khi -= static_cast<uint32_t>(i) << s;
       klo = s > 0 ? umax(klo, khi - ((1u << s) - 1)) : khi;
@@ -628,8 +774,7 @@ struct Row {
     const float w = ex2_approx(-t);
     if (!(p >= 1.f)) {
       uint64_t all;
-      // as the histogram's weights: 2^kFracBits, less 2^-20 of it
-      const uint64_t before = sum_before(__float2ull_rn(w * 4398042316800.f), &all);
+      const uint64_t before = sum_before(__float2ull_rn(w * kWeightOne), &all);
       in = in && before < times_up(cut_k ? all : total, p > 0.f ? p : 0.f);
     }
     in = in && (t <= t_max || tid == 0);
@@ -706,23 +851,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const float t_max = mp > 0.f ? fmaxf(0.f, -log2f(mp)) : kInf;
     Kept kept;
     const bool cut_k = k > 0 && k < a.V, cut_p = !(p >= 1.f);
+    uint32_t left = kAll;  // no more logits than these are kept
     const float share = p > 0.f ? p : 0.f;
     if (cut_k || cut_p) {
-      uint64_t rest;
-      const int at = cut_k ? r.template first_bucket<false, false>(k, -1.f, kept, &rest)
-                           : r.template first_bucket<true, false>(0, share, kept, &rest);
-      if (at >= 0 && sh.found_count <= kFew) {
-        // a bound for what is looked at, a little low
-        r.push(m - (at + 2) / r.c16, [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= at; });
-        if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, sh.total);
+      int lo, hi;
+      uint64_t total, rest;
+      const bool is = cut_k ? r.template steps<false, false>(k, 0.f, kept, &lo, &hi, &total, &rest)
+                            : r.template steps<true, false>(0, share, kept, &lo, &hi, &total, &rest);
+      if (is && sh.found_count <= kFew) {
+        r.push(r.reach(hi), [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= hi; });
+        if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, total);
         return;
       }
-      if (at >= 0)
-        kept = cut_k ? r.template narrow<false>(at, sh.found_num, rest, kept)
-                     : r.template narrow<true>(at, sh.found_num, rest, kept);
-      if (cut_k && cut_p) {
-        const int at_p = r.template first_bucket<true, true>(0, share, kept, &rest);
-        if (at_p >= 0) kept = r.template narrow<true>(at_p, sh.found_num, rest, kept);
+      if (is) {
+        left = sh.found_count;
+        kept = cut_k ? r.template narrow<false>(lo, hi, sh.found_num, rest, kept)
+                     : r.template narrow<true>(lo, hi, kAll, rest, kept);
+      }
+      if (cut_k && cut_p &&
+          r.template steps<true, true>(0, share, kept, &lo, &hi, &total, &rest)) {
+        left = min(left, sh.found_count);
+        kept = r.template narrow<true>(lo, hi, kAll, rest, kept);
       }
     }
     const float* e = a.expo + int64_t(b) * a.V - r.first;
@@ -733,61 +882,76 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const float score = __fdividef(q, ev);
       if (score > best.score) best = Best{score, v, t};
     };
-    const bool all = kept.x == kNegInf && t_max == kInf;
     // a bound for what is looked at, a little low; t decides
     const float least = fmaxf(fmaxf(kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
     constexpr int U = 4;
-    for (int g = r.tid; g < r.ng; g += U * kThreads) {
-      uint4 w[U];
-      r.template fetch<U, kHeld>(w, g);
-      if (all) {  // nothing is cut off
+    if (left > static_cast<uint32_t>(a.V) / 8 && t_max == kInf) {
+      // many are left: group by group, the random numbers in 16 bytes where they
+      // lie so
+      const bool wide = reinterpret_cast<uintptr_t>(e) % 16 == 0;
+      for (int g = r.tid; g < r.ng; g += U * kThreads) {
+        uint4 w[U];
+        r.template fetch<U, kHeld>(w, g);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
+          if (E::max_of(w[j], kNegInf) < least) continue;
           const int v = (r.g0 + g + j * kThreads) * E::N;
           float y[E::N], ev[E::N];
           E::unpack(w[j], y);
+          if (wide && v >= r.first && v + E::N <= r.end) {
 #pragma unroll
-          for (int i = 0; i < E::N; ++i) ev[i] = y[i] > kNegInf ? __ldg(e + v + i) : 1.f;
+            for (int i = 0; i < E::N; i += 4) {
+              const float4 q = __ldg(reinterpret_cast<const float4*>(e + v + i));
+              ev[i] = q.x; ev[i + 1] = q.y; ev[i + 2] = q.z; ev[i + 3] = q.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < E::N; ++i) ev[i] = y[i] >= least ? __ldg(e + v + i) : 1.f;
+          }
 #pragma unroll
           for (int i = 0; i < E::N; ++i)
-            if (y[i] > kNegInf) draw(r.t16_of(y[i]) * (1.f / kPerUnit), v + i, ev[i]);
+            if (kept.has(y[i], v + i)) draw(r.t16_of(y[i]) * (1.f / kPerUnit), v + i, ev[i]);
         }
-        continue;
       }
-      // Mostly few are left: a bit for each of these logits that is, then those, four
-      // at a time.
-      uint32_t left = 0;
+    } else {
+      // Few are left: a bit for each of a thread's next logits that is, then those,
+      // four at a time.
+      for (int g = r.tid; g < r.ng; g += U * kThreads) {
+        uint4 w[U];
+        r.template fetch<U, kHeld>(w, g);
+        uint32_t bits = 0;
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        float y[E::N];
-        E::unpack(w[j], y);
+        for (int j = 0; j < U; ++j) {
+          float y[E::N];
+          E::unpack(w[j], y);
 #pragma unroll
-        for (int i = 0; i < E::N; ++i) left |= (y[i] >= least ? 1u : 0u) << (j * E::N + i);
-      }
-      while (left != 0) {
-        constexpr int W = 4;
-        float t[W], ev[W];
-        int at[W];
+          for (int i = 0; i < E::N; ++i) bits |= (y[i] >= least ? 1u : 0u) << (j * E::N + i);
+        }
+        while (bits != 0) {
+          constexpr int W = 4;
+          float t[W], ev[W];
+          int at[W];
 #pragma unroll
-        for (int u = 0; u < W; ++u) {
-          t[u] = -1.f;
-          ev[u] = 1.f;
-          at[u] = 0;
-          if (left == 0) continue;
-          const int bit = __ffs(left) - 1, gk = g + bit / E::N * kThreads;
-          left &= left - 1;
-          at[u] = (r.g0 + gk) * E::N + bit % E::N;
-          const float y = to_f32(kHeld ? reinterpret_cast<const T*>(r.held + gk)[bit % E::N]
-                                       : r.base[at[u]]);
-          const float ty = r.t16_of(y) * (1.f / kPerUnit);
-          if (kept.has(y, at[u]) && ty <= t_max) {
-            t[u] = ty;
-            ev[u] = __ldg(e + at[u]);
+          for (int u = 0; u < W; ++u) {
+            t[u] = -1.f;
+            ev[u] = 1.f;
+            at[u] = 0;
+            if (bits == 0) continue;
+            const int bit = __ffs(bits) - 1, gk = g + bit / E::N * kThreads;
+            bits &= bits - 1;
+            at[u] = (r.g0 + gk) * E::N + bit % E::N;
+            const float y = to_f32(kHeld ? reinterpret_cast<const T*>(r.held + gk)[bit % E::N]
+                                         : r.base[at[u]]);
+            const float ty = r.t16_of(y) * (1.f / kPerUnit);
+            if (kept.has(y, at[u]) && ty <= t_max) {
+              t[u] = ty;
+              ev[u] = __ldg(e + at[u]);
+            }
           }
-        }
 #pragma unroll
-        for (int u = 0; u < W; ++u)
-          if (t[u] >= 0.f) draw(t[u], at[u], ev[u]);
+          for (int u = 0; u < W; ++u)
+            if (t[u] >= 0.f) draw(t[u], at[u], ev[u]);
+        }
       }
     }
   }
