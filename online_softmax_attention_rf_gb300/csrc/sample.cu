@@ -175,6 +175,15 @@ struct Kept {
   __device__ __forceinline__ bool has(float y, int v) const { return y > x || (y == x && v < limit); }
 };
 
+// Where a cut falls: `kept` where that is known, else among the few logits of it up
+// to x whose kPerUnit * t is in [from, to): the row's last step takes them in until
+// their counts or weights reach `rest`.
+struct Cut {
+  Kept kept;
+  float from = kInf, to = kInf, x = kInf;
+  uint64_t rest = 0;  // 0: the cut is known
+};
+
 // A thread's two buckets of the cluster's histogram.
 struct Sums {
   uint64_t v[2];
@@ -211,6 +220,12 @@ struct Row {
 
   __device__ __forceinline__ Row(const SampleArgs& a_, Shared& s)
       : a(a_), sh(s), cluster(cg::this_cluster()) {}
+
+  // What a selection kept: everything without kPart.
+  template <bool kPart>
+  static __device__ __forceinline__ bool in(const Kept& kept, float x, int v) {
+    return kPart ? kept.has(x, v) : x > kNegInf;
+  }
 
   // A group's logits; what lies outside the row counts as -inf.
   __device__ __forceinline__ uint4 load_group(int g) const {
@@ -282,37 +297,32 @@ struct Row {
     }
   }
 
-  // The same with the sum, in units of 2^-kFracBits, of the weights of what
-  // weight(x, t16, index) says.
-  template <typename W, typename F>
-  __device__ __forceinline__ uint64_t each_and_sum(float least, W&& weight, F&& f) const {
-    // a few weights at a time in float32 (at most 15 roundings), these as integers
+  // f(group, index of its first logit from base, sum) for this thread's groups with
+  // a logit of at least `least`; the sum of what f adds to `sum` (weights, a few at
+  // a time in float32, so with 15 roundings at most, and these as integers) in
+  // units of 2^-kFracBits.
+  template <typename F>
+  __device__ __forceinline__ uint64_t groups_sum(float least, int g, int batches, F&& f) const {
     constexpr int U = 4, kRun = 16 / E::N;
     uint64_t sum = 0;
-    for (int g = tid; g < ng; g += U * kThreads) {
+#pragma unroll 1
+    for (int k = 0; k < batches; ++k, g += U * kThreads) {
       uint4 w[U];
       fetch<U, kHeld>(w, g);
 #pragma unroll
       for (int j = 0; j < U; j += kRun) {
         float run = 0.f;
 #pragma unroll
-        for (int i = j; i < j + kRun; ++i) {
-          if (E::max_of(w[i], kNegInf) < least) continue;
-          float y[E::N];
-          E::unpack(w[i], y);
-#pragma unroll
-          for (int e = 0; e < E::N; ++e) {
-            const int v = (g0 + g + i * kThreads) * E::N + e;
-            const float t16 = t16_of(y[e]);
-            if (weight(y[e], t16, v)) run += ex2_approx(t16 * (-1.f / kPerUnit));
-            f(y[e], t16, v);
-          }
-        }
+        for (int i = j; i < j + kRun; ++i)
+          if (E::max_of(w[i], kNegInf) >= least) f(w[i], (g0 + g + i * kThreads) * E::N, run);
         sum += __float2ull_rn(run * kWeightOne);
       }
     }
     return sum;
   }
+  // Batches of groups of a thread: of all, and of a window.
+  __device__ __forceinline__ int batches() const { return (ng + 4 * kThreads - 1) / (4 * kThreads); }
+  static constexpr int kWindowBatches = kWindow / kThreads / (4 * E::N);
 
   // kPerUnit * t: not below 0; +inf for -inf
   __device__ __forceinline__ float t16_of(float x) const { return __fmul_rn(max - x, c16); }
@@ -335,46 +345,23 @@ struct Row {
     return hi < kBuckets - 1 ? max - (hi + 2) / c16 : kNegInf;
   }
 
-  // The CTA's histogram of its logits that place(x, t16, index) gives a bucket (not
-  // -1), of those from `least` on, in this thread's two buckets; kSum: and its sum
-  // of the weights of those that weight(x, t16, index), as each_and_sum().
-  template <bool kWeights, bool kSum, typename F, typename W>
-  __device__ Sums histogram(float least, F&& place, W&& weight, uint64_t* sum) const {
+  // The CTA's histogram in this thread's two buckets, and the sum of groups_sum():
+  // f(group, index, sum, add) adds logits by add(bucket, t16).
+  template <bool kWeights, typename F>
+  __device__ Sums histogram(float least, uint64_t* sum, F&& f) const {
     uint2* upper = reinterpret_cast<uint2*>(sh.upper);
     uint2* lower = reinterpret_cast<uint2*>(sh.lower);
     upper[tid] = lower[tid] = make_uint2(0, 0);
     __syncthreads();
     Sums s{};
-    constexpr int U = 4, kBatches = kWindow / kThreads / (U * E::N), kRun = 16 / E::N;
-    for (int g = tid; g - tid < ng;) {
-#pragma unroll 1
-      for (int k = 0; k < kBatches; ++k, g += U * kThreads) {
-        uint4 w[U];
-        fetch<U, kHeld>(w, g);
-        float run = 0.f;
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          if (E::max_of(w[j], kNegInf) >= least) {
-            float y[E::N];
-            E::unpack(w[j], y);
-#pragma unroll
-            for (int i = 0; i < E::N; ++i) {
-              const int v = (g0 + g + j * kThreads) * E::N + i;
-              const float t16 = t16_of(y[i]);
-              if (kSum && weight(y[i], t16, v)) run += ex2_approx(t16 * (-1.f / kPerUnit));
-              const int b = place(y[i], t16, v);
-              if (b < 0) continue;
-              const uint32_t f = kWeights ? fine_of(t16) : 0u;
-              atomicAdd(&sh.upper[b], (1u << kHalf) + (f >> kHalf));
-              if (kWeights) atomicAdd(&sh.lower[b], f & ((1u << kHalf) - 1));
-            }
-          }
-          if (kSum && j % kRun == kRun - 1) {
-            *sum += __float2ull_rn(run * kWeightOne);
-            run = 0.f;
-          }
-        }
-      }
+    auto add = [&](int b, float t16) {
+      const uint32_t f = kWeights ? fine_of(t16) : 0u;
+      atomicAdd(&sh.upper[b], (1u << kHalf) + (f >> kHalf));
+      if (kWeights) atomicAdd(&sh.lower[b], f & ((1u << kHalf) - 1));
+    };
+    for (int k = 0; k < batches(); k += kWindowBatches) {
+      *sum += groups_sum(least, tid + k * 4 * kThreads, min(kWindowBatches, batches() - k),
+                         [&](const uint4& w, int v, float& run) { f(w, v, run, add); });
       __syncthreads();
       const uint2 u = upper[tid], l = lower[tid];
       upper[tid] = lower[tid] = make_uint2(0, 0);
@@ -485,25 +472,26 @@ struct Row {
     return b;
   }
 
-  // The steps [*lo, *hi] of 1/16 that a cut of what `in` keeps (everything without
-  // kPart) falls into: that of the target'th logit, or, with kWeights, of the share
+  // The steps [*lo, *hi] of 1/16 that a cut of `kept` (everything without kPart) falls into: that of the target'th logit, or, with kWeights, of the share
   // of the weights, whose sum is *total. False: there is none. sh.found_count: the
   // logits up to *hi's end; one step: sh.found_num in it, *rest to go in it.
   template <bool kWeights, bool kPart>
-  __device__ bool steps(uint64_t target, float share, const Kept& in, int* lo, int* hi,
+  __device__ bool steps(uint64_t target, float share, const Kept& kept, int* lo, int* hi,
                         uint64_t* total, uint64_t* rest) {
     *reinterpret_cast<uint2*>(&sh.upper[2 * tid]) = make_uint2(0, 0);
     __syncthreads();
-    const float least = kPart ? in.x : kNegInf;
-    auto is = [&](float x, int v) { return kPart ? in.has(x, v) : x > kNegInf; };
-    auto add = [&](float x, float t16, int v) {
-      if (is(x, v)) atomicAdd(&sh.upper[bucket_at(fminf(t16, kBuckets - 1.f))], 1u);
-    };
-    uint64_t sum = 0;
-    if (kWeights)
-      sum = each_and_sum(least, [&](float x, float, int v) { return is(x, v); }, add);
-    else
-      each_from(least, [&](float x, int v) { add(x, t16_of(x), v); });
+    const uint64_t sum =
+        groups_sum(kPart ? kept.x : kNegInf, tid, batches(), [&](const uint4& w, int v, float& run) {
+          float y[E::N];
+          E::unpack(w, y);
+#pragma unroll
+          for (int i = 0; i < E::N; ++i) {
+            const float t16 = t16_of(y[i]);
+            if (!in<kPart>(kept, y[i], v + i)) continue;
+            if (kWeights) run += ex2_approx(t16 * (-1.f / kPerUnit));
+            atomicAdd(&sh.upper[bucket_at(fminf(t16, kBuckets - 1.f))], 1u);
+          }
+        });
     __syncthreads();
     Sums s{};
     s.n[0] = sh.upper[2 * tid];
@@ -539,15 +527,17 @@ struct Row {
   }
 
   // Few logits, those that is(x, index), go to the cluster's first CTA.
+  __device__ __forceinline__ void push_one(float x, int v) const {
+    const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
+    if (at < kFew) {
+      *cluster.map_shared_rank(&sh.upper[at], 0) = __float_as_uint(x);
+      *cluster.map_shared_rank(&sh.lower[at], 0) = static_cast<uint32_t>(v);
+    }
+  }
   template <typename F>
   __device__ __forceinline__ void push(float least, F&& is) const {
     each_from(least, [&](float x, int v) {
-      if (!is(x, v)) return;
-      const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
-      if (at < kFew) {
-        *cluster.map_shared_rank(&sh.upper[at], 0) = __float_as_uint(x);
-        *cluster.map_shared_rank(&sh.lower[at], 0) = static_cast<uint32_t>(v);
-      }
+      if (is(x, v)) push_one(x, v);
     });
     cluster.sync();
   }
@@ -587,30 +577,40 @@ struct Row {
     return (warp > 0 ? before : 0) + s - u;
   }
 
-  // What is left of `in` when the running sum of counts, or of weights (rest: of
+  // What is left of `kept` when the running sum of counts, or of weights (rest: of
   // them in units of 2^-kFracBits), in the order of the logits, is cut within the
   // steps [lo, hi] by `rest`: counted from lo on, or, with kWeights, from the first
-  // logit on. n: the logits in these steps, or more.
-  template <bool kWeights>
-  __device__ Kept narrow(int lo, int hi, uint32_t n, uint64_t rest, const Kept& in) {
+  // logit on. n: the logits in these steps, or more. last: nothing is cut after it,
+  // so that few logits may be left to the row's last step.
+  template <bool kWeights, bool kPart>
+  __device__ Cut narrow(int lo, int hi, uint32_t n, uint64_t rest, const Kept& kept, bool last) {
     // The steps divided by a power of two: a part lies within one unit of t, and
     // what is subtracted and multiplied here is exact.
     int parts = 0;  // log2 of the parts of a step
     while ((hi - lo + 1) << (parts + 1) <= kBuckets) ++parts;
-    const float scale = static_cast<float>(1 << parts);
-    auto part_of = [&](float t16) { return bucket_at(fminf((t16 - lo) * scale, kBuckets - 1.f)); };
+    const float scale = static_cast<float>(1 << parts), top = lo,
+                bottom = hi < kBuckets - 1 ? hi + 1.f : kInf;
+    auto part_of = [&](float t16) { return bucket_at(fminf((t16 - top) * scale, kBuckets - 1.f)); };
     int part = -1;  // the one that the cut falls into (-1: all)
-    auto within = [&](float t16) {
-      return t16 >= lo && (t16 < hi + 1.f || hi == kBuckets - 1) && (part < 0 || part_of(t16) == part);
-    };
     if ((kWeights || n > kFew) && hi < kBuckets - 1) {
       uint64_t above = 0;
-      Sums h = histogram<kWeights, kWeights>(
-          reach(hi),
-          [&](float x, float t16, int v) {
-            return in.has(x, v) && within(t16) ? part_of(t16) : -1;
-          },
-          [&](float x, float t16, int v) { return t16 < lo && in.has(x, v); }, &above);
+      Sums h = histogram<kWeights>(
+          reach(hi), &above, [&](const uint4& w, int v, float& run, auto&& add) {
+            float y[E::N], t16[E::N];
+            E::unpack(w, y);
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < E::N; ++i) {
+              t16[i] = t16_of(y[i]);
+              if (kPart && !kept.has(y[i], v + i)) t16[i] = kInf;
+              if (kWeights) run += t16[i] < top ? ex2_approx(t16[i] * (-1.f / kPerUnit)) : 0.f;
+              any |= t16[i] >= top && t16[i] < bottom;
+            }
+            if (!any) return;
+#pragma unroll
+            for (int i = 0; i < E::N; ++i)
+              if (t16[i] >= top && t16[i] < bottom) add(part_of(t16[i]), t16[i]);
+          });
       above = join<kWeights, kWeights>(h, above);
       if (kWeights) {
 #pragma unroll
@@ -630,25 +630,32 @@ struct Row {
     }
     // The part's keys lie in [klo, khi]: max - x is between its ends over c16, up to
     // rounding; 2^-21 of it is more than that.
-    const float width = part < 0 ? hi + 1.f - lo : 1.f / scale;
-    const float from = part < 0 ? lo : lo + part / scale;
+    const float from = part < 0 ? top : top + part / scale;
+    const float to = part < 0 ? bottom : top + (part + 1) / scale;
     uint32_t khi = from > 0.f ? E::key(max - from / c16 * (1.f - 0x1p-21f)) : E::key(max);
     uint32_t klo = E::kLowest;
-    if (hi < kBuckets - 1) klo = umax(klo, E::key(max - (from + width) / c16 * (1.f + 0x1p-21f)));
+    if (to < kInf) klo = umax(klo, E::key(max - to / c16 * (1.f + 0x1p-21f)));
+    bool narrowed = false;
     auto is = [&](float x, int v) {
-      return x >= E::value(klo) && x <= E::value(khi) && within(t16_of(x)) && in.has(x, v);
+      const float t16 = t16_of(x);
+      return x >= E::value(klo) && x <= E::value(khi) && t16 >= from && (t16 < to || to == kInf) &&
+             in<kPart>(kept, x, v);
     };
     while (n > kFew && khi > klo) {
       int s = 0;
       while (((khi - klo) >> s) >= kBuckets) ++s;
       uint64_t none = 0;
-      Sums h = histogram<kWeights, false>(
-          E::value(klo),
-          [&](float x, float, int v) {
-            return is(x, v) ? static_cast<int>((khi - E::key(x)) >> s) : -1;
-          },
-          [](float, float, int) { return false; }, &none);
+      Sums h = histogram<kWeights>(E::value(klo), &none,
+                                   [&](const uint4& w, int v, float&, auto&& add) {
+                                     float y[E::N];
+                                     E::unpack(w, y);
+#pragma unroll
+                                     for (int e = 0; e < E::N; ++e)
+                                       if (is(y[e], v + e))
+                                         add((khi - E::key(y[e])) >> s, t16_of(y[e]));
+                                   });
       join<kWeights, false>(h, 0);
+      narrowed = true;
       const int i = find(h, rest, &rest, true);
       n = sh.found_num;
       khi -= static_cast<uint32_t>(i) << s;
@@ -661,8 +668,11 @@ struct Row {
         rest = (rest + f - 1) / f;
       }
       const int limit = tie_limit(x, static_cast<uint32_t>(rest < kAll ? rest : kAll));
-      return Kept{x, x == in.x ? min(limit, in.limit) : limit};
+      return Cut{Kept{x, x == kept.x ? min(limit, kept.limit) : limit}};
     }
+    if (last)  // (nothing below the lowest key is left; of kept what it was)
+      return Cut{kPart && kept.x >= E::value(klo) ? kept : Kept{E::value(klo), kNoIdx}, from, to,
+                 narrowed ? E::value(khi) : kInf, rest};
     push(E::value(klo), is);
     if (rank == 0) {
       float x;
@@ -680,7 +690,7 @@ struct Row {
       if (tid == 0) sh.pushed = 0;
     }
     cluster.sync();
-    return Kept{sh.cut_x, sh.cut_limit};
+    return Cut{Kept{sh.cut_x, sh.cut_limit}};
   }
   static __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
@@ -760,6 +770,25 @@ struct Row {
       a.logprob[b] = none     ? __int_as_float(0x7fc00000)
                      : greedy ? 0.f
                               : -(best.t + log2f(sum)) * kLn2;
+  }
+
+  // The few logits that the last cut falls into (one CTA): those that are in join
+  // the others' best and sum, which thread 0 has.
+  __device__ __forceinline__ void last_few(int b, uint64_t rest, bool weights, Best& best,
+                                           float& sum) const {
+    float x;
+    int v;
+    const int n = in_order(&x, &v);
+    const float t16 = t16_of(x);
+    uint64_t all;
+    const uint64_t u = tid < n ? (weights ? fine_of(t16) : 1) : 0;
+    if (sum_before(u, &all) < rest && tid < n) {
+      const float w = ex2_approx(t16 * (-1.f / kPerUnit));
+      take(best, Best{__fdividef(w, __ldg(a.expo + int64_t(b) * a.V + (v - first))), v,
+                      t16 * (1.f / kPerUnit)});
+      sum += w;
+    }
+    reduce(best, sum);
   }
 
   // The row from its few logits (one CTA): both cuts and the draw. total: the row's
@@ -842,22 +871,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   Best best{-1.f, kNoIdx, 0.f};
   float sum = 0.f;
+  Cut cut;
+  // w >= min_p as t <= -log2(min_p); the maximum always stays
+  const float t_max = mp > 0.f ? fmaxf(0.f, -log2f(mp)) : kInf;
+  const bool cut_k = k > 0 && k < a.V, cut_p = !(p >= 1.f);
   if (!bad && greedy) {
     r.each_from(m, [&](float x, int v) {
       if (x == m) take(best, Best{1.f, v, 0.f});
     });
   } else if (!bad) {
-    // w >= min_p as t <= -log2(min_p); the maximum always stays
-    const float t_max = mp > 0.f ? fmaxf(0.f, -log2f(mp)) : kInf;
-    Kept kept;
-    const bool cut_k = k > 0 && k < a.V, cut_p = !(p >= 1.f);
     uint32_t left = kAll;  // no more logits than these are kept
     const float share = p > 0.f ? p : 0.f;
     if (cut_k || cut_p) {
       int lo, hi;
       uint64_t total, rest;
-      const bool is = cut_k ? r.template steps<false, false>(k, 0.f, kept, &lo, &hi, &total, &rest)
-                            : r.template steps<true, false>(0, share, kept, &lo, &hi, &total, &rest);
+      const bool is = cut_k ? r.template steps<false, false>(k, 0.f, cut.kept, &lo, &hi, &total, &rest)
+                            : r.template steps<true, false>(0, share, cut.kept, &lo, &hi, &total, &rest);
       if (is && sh.found_count <= kFew) {
         r.push(r.reach(hi), [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= hi; });
         if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, total);
@@ -865,13 +894,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       if (is) {
         left = sh.found_count;
-        kept = cut_k ? r.template narrow<false>(lo, hi, sh.found_num, rest, kept)
-                     : r.template narrow<true>(lo, hi, kAll, rest, kept);
+        cut = cut_k ? r.template narrow<false, false>(lo, hi, sh.found_num, rest, cut.kept, !cut_p)
+                    : r.template narrow<true, false>(lo, hi, kAll, rest, cut.kept, true);
       }
       if (cut_k && cut_p &&
-          r.template steps<true, true>(0, share, kept, &lo, &hi, &total, &rest)) {
+          r.template steps<true, true>(0, share, cut.kept, &lo, &hi, &total, &rest)) {
         left = min(left, sh.found_count);
-        kept = r.template narrow<true>(lo, hi, kAll, rest, kept);
+        cut = r.template narrow<true, true>(lo, hi, kAll, rest, cut.kept, true);
       }
     }
     const float* e = a.expo + int64_t(b) * a.V - r.first;
@@ -882,8 +911,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const float score = __fdividef(q, ev);
       if (score > best.score) best = Best{score, v, t};
     };
+    // what is in: 1; what the last step looks at: it goes to the first CTA
+    auto taken = [&](float y, float t16, int v) {
+      if (!cut.kept.has(y, v)) return false;
+      if (t16 < cut.from || y > cut.x) return true;
+      if (t16 < cut.to) r.push_one(y, v);  // (t = inf has no weight)
+      return false;
+    };
     // a bound for what is looked at, a little low; t decides
-    const float least = fmaxf(fmaxf(kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
+    const float least = fmaxf(fmaxf(cut.kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
     constexpr int U = 4;
     if (left > static_cast<uint32_t>(a.V) / 8 && t_max == kInf) {
       // many are left: group by group, the random numbers in 16 bytes where they
@@ -910,7 +946,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           }
 #pragma unroll
           for (int i = 0; i < E::N; ++i)
-            if (kept.has(y[i], v + i)) draw(r.t16_of(y[i]) * (1.f / kPerUnit), v + i, ev[i]);
+          {
+            const float t16 = r.t16_of(y[i]);
+            if (taken(y[i], t16, v + i)) draw(t16 * (1.f / kPerUnit), v + i, ev[i]);
+          }
         }
       }
     } else {
@@ -942,9 +981,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             at[u] = (r.g0 + gk) * E::N + bit % E::N;
             const float y = to_f32(kHeld ? reinterpret_cast<const T*>(r.held + gk)[bit % E::N]
                                          : r.base[at[u]]);
-            const float ty = r.t16_of(y) * (1.f / kPerUnit);
-            if (kept.has(y, at[u]) && ty <= t_max) {
-              t[u] = ty;
+            const float t16 = r.t16_of(y);
+            if (t16 * (1.f / kPerUnit) <= t_max && taken(y, t16, at[u])) {
+              t[u] = t16 * (1.f / kPerUnit);
               ev[u] = __ldg(e + at[u]);
             }
           }
@@ -957,22 +996,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   // the cluster's best and sum, joined in a fixed order
   r.reduce(best, sum);
-  if (r.size > 1) {
-    if (r.tid == 0) {
-      *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
-      *r.cluster.map_shared_rank(&sh.csum[r.rank], 0) = sum;
-    }
-    r.cluster.sync();
-    if (r.rank == 0 && r.tid == 0) {
-      best = sh.cbest[0];
-      sum = sh.csum[0];
-      for (int q = 1; q < r.size; ++q) {
-        take(best, sh.cbest[q]);
-        sum += sh.csum[q];
-      }
+  if (r.tid == 0) {
+    *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
+    *r.cluster.map_shared_rank(&sh.csum[r.rank], 0) = sum;
+  }
+  r.cluster.sync();
+  if (r.rank != 0) return;
+  best = Best{-1.f, kNoIdx, 0.f};
+  sum = 0.f;
+  if (r.tid == 0) {
+    for (int q = 0; q < r.size; ++q) {
+      take(best, sh.cbest[q]);
+      sum += sh.csum[q];
     }
   }
-  if (r.rank == 0 && r.tid == 0) r.answer(b, best, sum, bad, greedy);
+  if (cut.rest > 0) r.last_few(b, cut.rest, cut_p, best, sum);
+  if (r.tid == 0) r.answer(b, best, sum, bad, greedy);
 }
 
 template <typename T, bool kHeld>
