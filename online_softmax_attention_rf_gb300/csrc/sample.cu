@@ -314,7 +314,8 @@ struct Row {
         float run = 0.f;
 #pragma unroll
         for (int i = j; i < j + kRun; ++i)
-          if (E::max_of(w[i], kNegInf) >= least) f(w[i], (g0 + g + i * kThreads) * E::N, run);
+          if (g + i * kThreads < ng && (least == kNegInf || E::max_of(w[i], kNegInf) >= least))
+            f(w[i], (g0 + g + i * kThreads) * E::N, run);
         sum += __float2ull_rn(run * kWeightOne);
       }
     }
@@ -338,6 +339,19 @@ struct Row {
     const float e16 = __fadd_rz(t16, 134217728.f) - 134217728.f;  // to a multiple of 16
     const float f = ex2_approx(fmaf(e16 - t16, 1.f / kPerUnit, -1.3758e-6f));
     return __float_as_uint(f + 8.f) - 0x41000000u;
+  }
+
+  // The least of the logits' type whose t16 is below `from` (all of the warp).
+  __device__ float least_below(float from) const {
+    uint32_t lo = E::kLowest + 1, hi = E::key(max);
+    while (lo < hi) {
+      const uint32_t step = (hi - lo) / 32 + 1;
+      const uint32_t is = __ballot_sync(kAll, t16_of(E::value(min(hi, lo + lane * step))) < from);
+      const int f = is != 0 ? __ffs(is) - 1 : 32;
+      if (f < 32) hi = min(hi, lo + f * step);
+      lo = f > 0 ? lo + (f - 1) * step + 1 : hi;
+    }
+    return E::value(hi);
   }
 
   // A logit that no logit up to the end of step hi lies below.
@@ -487,9 +501,16 @@ struct Row {
 #pragma unroll
           for (int i = 0; i < E::N; ++i) {
             const float t16 = t16_of(y[i]);
-            if (!in<kPart>(kept, y[i], v + i)) continue;
-            if (kWeights) run += ex2_approx(t16 * (-1.f / kPerUnit));
-            atomicAdd(&sh.upper[bucket_at(fminf(t16, kBuckets - 1.f))], 1u);
+            const bool is = in<kPart>(kept, y[i], v + i);
+            if (kWeights) {
+              const float q = ex2_approx(t16 * (-1.f / kPerUnit));
+              run += kPart && !is ? 0.f : q;  // -inf weighs nothing
+            }
+            // the step in the bits from 2 on: a byte offset
+            const uint32_t at = __float_as_uint(__fadd_rz(fminf(t16, kBuckets - 1.f), 2097152.f)) &
+                                (4 * kBuckets - 4);
+            if (is)
+              atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(sh.upper) + at), 1u);
           }
         });
     __syncthreads();
@@ -922,8 +943,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const float least = fmaxf(fmaxf(cut.kept.x, -FLT_MAX), m - (t_max * kPerUnit + 1.f) / r.c16);
     constexpr int U = 4;
     if (left > static_cast<uint32_t>(a.V) / 8 && t_max == kInf) {
-      // many are left: group by group, the random numbers in 16 bytes where they
-      // lie so
+      // Many are left: group by group, the random numbers in 16 bytes where they lie
+      // so. From `sure` on a logit is in; what little lies between is looked at.
+      const float sure =
+          cut.rest > 0 ? (cut.x < kInf ? E::value(E::key(cut.x) + 1) : r.least_below(cut.from))
+          : cut.kept.limit == kNoIdx ? least
+                                     : fmaxf(least, E::value(E::key(cut.kept.x) + 1));
+      const float c = r.c16 * (1.f / kPerUnit);
       const bool wide = reinterpret_cast<uintptr_t>(e) % 16 == 0;
       for (int g = r.tid; g < r.ng; g += U * kThreads) {
         uint4 w[U];
@@ -944,14 +970,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
             for (int i = 0; i < E::N; ++i) ev[i] = y[i] >= least ? __ldg(e + v + i) : 1.f;
           }
+          bool look = false;
 #pragma unroll
-          for (int i = 0; i < E::N; ++i)
-          {
-            const float t16 = r.t16_of(y[i]);
-            if (taken(y[i], t16, v + i)) draw(t16 * (1.f / kPerUnit), v + i, ev[i]);
+          for (int i = 0; i < E::N; ++i) {
+            const float q = ex2_approx((y[i] - m) * c);
+            const bool is = y[i] >= sure;
+            sum += is ? q : 0.f;
+            const float score = __fdividef(q, ev[i]);
+            if (is && score > best.score) {
+              best.score = score;
+              best.idx = v + i;
+            }
+            look |= !is && y[i] >= least;
+          }
+          if (look) {
+#pragma unroll
+            for (int i = 0; i < E::N; ++i) {
+              const float t16 = r.t16_of(y[i]);
+              if (y[i] >= least && y[i] < sure && taken(y[i], t16, v + i)) {
+                const float q = ex2_approx(t16 * (-1.f / kPerUnit));
+                sum += q;
+                take(best, Best{__fdividef(q, ev[i]), v + i, 0.f});
+              }
+            }
           }
         }
       }
+      if (best.idx != kNoIdx)
+        best.t = r.t16_of(to_f32(r.base[best.idx])) * (1.f / kPerUnit);
     } else {
       // Few are left: a bit for each of a thread's next logits that is, then those,
       // four at a time.
