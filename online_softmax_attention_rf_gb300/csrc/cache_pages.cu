@@ -18,16 +18,18 @@ namespace {
 
 // Rows move towards the front: row i of a sequence's list comes from a place at
 // or behind i, and the list ascends. A CTA takes one (sequence, layer, cache,
-// share of the heads) and goes through the list in chunks. A chunk is read whole
-// before any of it is written, and its rows' new places lie before the next
-// chunk's old ones: so the next chunk can be read while this one is written, and
-// nothing is overwritten unread.
+// share of the heads) and goes through the list in chunks: a chunk is read whole
+// before any of it is written, and what it overwrites lies before every later
+// chunk's rows. Loads and stores of one CTA take turns; the four CTAs of an SM
+// overlap (with the next chunk's loads under this one's stores in a CTA there were
+// two, and not all of a batch's CTAs were resident: 512 of unequal length took 166
+// us, 4.5 TB/s).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnits = 8;  // 16-byte units of a chunk a thread
-constexpr int kMoveRows = 128; // rows of a chunk at most
+constexpr int kMoveUnits = 8;  // rows of a chunk a thread has 16 bytes of
+constexpr int kMoveRows = kMoveThreads;  // rows of a chunk at most: a thread looks one up
 
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactArgs a) {
-  __shared__ int64_t from[2][kMoveRows], to[2][kMoveRows];  // -1: stays
+__global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const CompactArgs a) {
+  __shared__ int64_t from[kMoveRows], to[kMoveRows];  // -1: stays
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / a.head_splits, split = blockIdx.x % a.head_splits;
@@ -44,8 +46,9 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactA
   const int32_t* keep = a.keep + c0;
   const int32_t* table = a.table + int64_t(b) * a.table_stride;
   const int h0 = split * a.heads, heads = min(a.heads, a.pool.Hkv - h0);
-  const int ru = heads * a.pool.row16;  // units of a row
-  const int rows = max(1, min(kMoveRows, kMoveThreads * kMoveUnits / ru));
+  const int ru = heads * a.pool.row16;  // units of 16 bytes of a row, at most the threads
+  const int pass = kMoveThreads / ru;   // rows that the threads have at a time
+  const int rows = min(pass * kMoveUnits, kMoveRows);
   char* cache = side.base + layer * side.layer;
 
   auto slot = [&](int64_t pos) -> int64_t {  // bytes, -1: nowhere
@@ -55,7 +58,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactA
     if (id < 0 || id >= a.pool.num_pages) return -1;
     return id * side.page + (pos - int64_t(pi) * a.pool.page) * side.token;
   };
-  auto locate = [&](int chunk, int buf) {
+  auto locate = [&](int chunk) {
     const int i = chunk * rows + threadIdx.x;
     if (threadIdx.x < static_cast<unsigned>(rows)) {
       int64_t f = -1, t = -1;
@@ -73,45 +76,30 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactA
           }
         }
       }
-      from[buf][threadIdx.x] = f;
-      to[buf][threadIdx.x] = t;
+      from[threadIdx.x] = f;
+      to[threadIdx.x] = t;
     }
   };
-  // this thread's units of a chunk: a row of it and bytes within the row
-  int row[kMoveUnits];
-  int64_t off[kMoveUnits];
-#pragma unroll
-  for (int i = 0; i < kMoveUnits; ++i) {
-    const int u = threadIdx.x + i * kMoveThreads;
-    row[i] = u / ru;
-    const int rem = u - row[i] * ru, h = rem / a.pool.row16;
-    off[i] = (h0 + h) * side.head + (rem - h * a.pool.row16) * 16;
-    if (row[i] >= rows) row[i] = -1;
-  }
-  uint4 cur[kMoveUnits], nxt[kMoveUnits];
-  auto load = [&](uint4 (&w)[kMoveUnits], int buf) {
-#pragma unroll
-    for (int i = 0; i < kMoveUnits; ++i)
-      if (row[i] >= 0 && from[buf][row[i]] >= 0)
-        w[i] = *reinterpret_cast<const uint4*>(cache + from[buf][row[i]] + off[i]);
-  };
+  // this thread's rows of a chunk, r0 + j * pass, and its place in them
+  const int r0 = threadIdx.x / ru, u = threadIdx.x - r0 * ru, h = u / a.pool.row16;
+  char* const mine = cache + (h0 + h) * side.head + (u - h * a.pool.row16) * 16;
   const int chunks = (n + rows - 1) / rows;
-  if (chunks == 0) return;
-  locate(0, 0);
-  __syncthreads();
-  load(cur, 0);
   for (int c = 0; c < chunks; ++c) {
-    const int buf = c & 1;
-    if (c + 1 < chunks) locate(c + 1, buf ^ 1);
-    __syncthreads();  // chunk c is read by all
-    if (c + 1 < chunks) load(nxt, buf ^ 1);
+    locate(c);
+    __syncthreads();
+    uint4 w[kMoveUnits];
 #pragma unroll
-    for (int i = 0; i < kMoveUnits; ++i)
-      if (row[i] >= 0 && to[buf][row[i]] >= 0)
-        *reinterpret_cast<uint4*>(cache + to[buf][row[i]] + off[i]) = cur[i];
+    for (int j = 0; j < kMoveUnits; ++j) {
+      const int r = r0 + j * pass;
+      if (r0 < pass && r < rows && from[r] >= 0) w[j] = *reinterpret_cast<const uint4*>(mine + from[r]);
+    }
+    __syncthreads();  // the chunk is read by all
 #pragma unroll
-    for (int i = 0; i < kMoveUnits; ++i) cur[i] = nxt[i];
-    __syncthreads();  // before the places of chunk c are replaced
+    for (int j = 0; j < kMoveUnits; ++j) {
+      const int r = r0 + j * pass;
+      if (r0 < pass && r < rows && to[r] >= 0) *reinterpret_cast<uint4*>(mine + to[r]) = w[j];
+    }
+    __syncthreads();  // before the chunk's places are replaced, and the next one is read
   }
 }
 
@@ -390,9 +378,9 @@ cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s) {
   // a CTA a (sequence, layer, cache); with few of them the heads are shared out
   const int64_t ctas = int64_t(a.B) * a.pool.layers * 2;
   int splits = 1;
-  while (splits < a.pool.Hkv && ctas * splits < 8 * 152) splits *= 2;
+  while (splits < a.pool.Hkv && ctas * splits < 4 * 152) splits *= 2;
   a.heads = (a.pool.Hkv + splits - 1) / splits;
-  const int most = kMoveThreads * kMoveUnits / a.pool.row16;  // a chunk holds a row at least
+  const int most = kMoveThreads / a.pool.row16;  // the threads hold a row
   a.heads = a.heads < most ? a.heads : most;
   a.head_splits = (a.pool.Hkv + a.heads - 1) / a.heads;
   return launch_pdl(kv_compact_kernel, dim3(a.B * a.head_splits, 2 * a.pool.layers),
@@ -425,9 +413,11 @@ cudaError_t launch_pages_release(const PagesReleaseArgs& a, cudaStream_t s) {
 
 cudaError_t launch_pages_grow(PagesGrowArgs a, cudaStream_t s) {
   const size_t smem = size_t(a.n) * sizeof(GrowRow);
-  const cudaError_t e = cudaFuncSetAttribute(
-      pages_grow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  if (smem > 40 * 1024) {  // more than a kernel has by itself
+    const cudaError_t e = cudaFuncSetAttribute(
+        pages_grow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   a.wide = reinterpret_cast<uintptr_t>(a.refs) % 16 == 0;
   return launch_pdl(pages_grow_kernel, dim3(kGrowCluster), dim3(kGrowThreads), smem, s, a);
 }
