@@ -29,7 +29,8 @@ constexpr int kMoveUnits = 8;  // rows of a chunk a thread has 16 bytes of
 constexpr int kMoveRows = kMoveThreads;  // rows of a chunk at most: a thread looks one up
 
 __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const CompactArgs a) {
-  __shared__ int64_t from[kMoveRows], to[kMoveRows];  // -1: stays
+  // places of three chunks in turn, -1: stays
+  __shared__ int64_t from[3][kMoveRows], to[3][kMoveRows];
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / a.head_splits, split = blockIdx.x % a.head_splits;
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
     if (id < 0 || id >= a.pool.num_pages) return -1;
     return id * side.page + (pos - int64_t(pi) * a.pool.page) * side.token;
   };
-  auto locate = [&](int chunk) {
+  auto locate = [&](int chunk, int buf) {
     const int i = chunk * rows + threadIdx.x;
     if (threadIdx.x < static_cast<unsigned>(rows)) {
       int64_t f = -1, t = -1;
@@ -76,30 +77,36 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
           }
         }
       }
-      from[threadIdx.x] = f;
-      to[threadIdx.x] = t;
+      from[buf][threadIdx.x] = f;
+      to[buf][threadIdx.x] = t;
     }
   };
   // this thread's rows of a chunk, r0 + j * pass, and its place in them
   const int r0 = threadIdx.x / ru, u = threadIdx.x - r0 * ru, h = u / a.pool.row16;
   char* const mine = cache + (h0 + h) * side.head + (u - h * a.pool.row16) * 16;
   const int chunks = (n + rows - 1) / rows;
-  for (int c = 0; c < chunks; ++c) {
-    locate(c);
-    __syncthreads();
+  locate(0, 0);
+  __syncthreads();
+  for (int c = 0, buf = 0; c < chunks; ++c) {
+    const int next = buf < 2 ? buf + 1 : 0;
     uint4 w[kMoveUnits];
 #pragma unroll
     for (int j = 0; j < kMoveUnits; ++j) {
       const int r = r0 + j * pass;
-      if (r0 < pass && r < rows && from[r] >= 0) w[j] = *reinterpret_cast<const uint4*>(mine + from[r]);
+      if (r0 < pass && r < rows && from[buf][r] >= 0)
+        w[j] = *reinterpret_cast<const uint4*>(mine + from[buf][r]);
     }
+    // a warp that is behind may still have to write the chunk before this one: the
+    // next one's places go to the third buffer
+    if (c + 1 < chunks) locate(c + 1, next);
     __syncthreads();  // the chunk is read by all
 #pragma unroll
     for (int j = 0; j < kMoveUnits; ++j) {
       const int r = r0 + j * pass;
-      if (r0 < pass && r < rows && to[r] >= 0) *reinterpret_cast<uint4*>(mine + to[r]) = w[j];
+      if (r0 < pass && r < rows && to[buf][r] >= 0)
+        *reinterpret_cast<uint4*>(mine + to[buf][r]) = w[j];
     }
-    __syncthreads();  // before the chunk's places are replaced, and the next one is read
+    buf = next;
   }
 }
 
