@@ -17,25 +17,25 @@ namespace {
 // ------------------------------------------------------------------ rows
 
 // Rows move towards the front: row i of a sequence's list comes from a place at
-// or behind i, and the list ascends. A CTA takes one (sequence, layer, cache,
-// share of the heads) and goes through the list in chunks: a chunk is read whole
-// before any of it is written, and what it overwrites lies before every later
-// chunk's rows. Loads and stores of one CTA take turns; the four CTAs of an SM
-// overlap (with the next chunk's loads under this one's stores in a CTA there were
-// two, and not all of a batch's CTAs were resident: 512 of unequal length took 166
-// us, 4.5 TB/s).
+// or behind i, and the list ascends. A CTA takes a share of one sequence's heads
+// in some of the planes (K and V of the layers) and goes through the list in chunks:
+// in each plane a chunk is read whole before any of it is written, and what it
+// overwrites lies before every later chunk's rows. Loads and stores of one CTA take
+// turns; the four CTAs of an SM overlap. Half of 8 caches of up to 8000 tokens, 8
+// heads, d = 128, 4 layers dropped: 136 us, 5.5 TB/s, bound by memory and by the
+// longest cache's CTAs, which end last (with the next chunk's loads under this one's
+// stores in a CTA there were two CTAs an SM, and not all resident: 166 us).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnits = 8;  // rows of a chunk a thread has 16 bytes of
 constexpr int kMoveRows = kMoveThreads;  // rows of a chunk at most: a thread looks one up
 
 __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const CompactArgs a) {
-  // places of three chunks in turn, -1: stays
-  __shared__ int64_t from[3][kMoveRows], to[3][kMoveRows];
+  // places (page, row in it) of three chunks in turn, -1: stays
+  __shared__ int2 from[3][kMoveRows], to[3][kMoveRows];
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / a.head_splits, split = blockIdx.x % a.head_splits;
-  const int layer = blockIdx.y >> 1;
-  const PoolSide& side = (blockIdx.y & 1) ? a.pool.v : a.pool.k;
+  const int plane0 = blockIdx.y * a.planes, plane1 = min(plane0 + a.planes, 2 * a.pool.layers);
   const int c0 = a.cu_keep[b], room = a.cu_keep[b + 1] - c0;
   const int n = a.n_keep != nullptr ? a.n_keep[b] : room;
   const bool head = split == 0 && blockIdx.y == 0;  // the CTA that reports
@@ -50,19 +50,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
   const int ru = heads * a.pool.row16;  // units of 16 bytes of a row, at most the threads
   const int pass = kMoveThreads / ru;   // rows that the threads have at a time
   const int rows = min(pass * kMoveUnits, kMoveRows);
-  char* cache = side.base + layer * side.layer;
 
-  auto slot = [&](int64_t pos) -> int64_t {  // bytes, -1: nowhere
+  auto slot = [&](int64_t pos) -> int {  // page * tokens of a page + row, -1: nowhere
     if (pos < 0 || pos >= int64_t(a.max_pages) * a.pool.page) return -1;
     const int pi = static_cast<int>(pos / a.pool.page);
     const int id = table[pi];
     if (id < 0 || id >= a.pool.num_pages) return -1;
-    return id * side.page + (pos - int64_t(pi) * a.pool.page) * side.token;
+    return id * a.pool.page + static_cast<int>(pos - int64_t(pi) * a.pool.page);
   };
   auto locate = [&](int chunk, int buf) {
     const int i = chunk * rows + threadIdx.x;
     if (threadIdx.x < static_cast<unsigned>(rows)) {
-      int64_t f = -1, t = -1;
+      int f = -1, t = -1;
       if (i < n) {
         const int k = keep[i];
         const int prev = i > 0 ? keep[i - 1] : -1;
@@ -77,34 +76,39 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
           }
         }
       }
-      from[buf][threadIdx.x] = f;
-      to[buf][threadIdx.x] = t;
+      from[buf][threadIdx.x] = make_int2(f < 0 ? -1 : f / a.pool.page, f % a.pool.page);
+      to[buf][threadIdx.x] = make_int2(t < 0 ? -1 : t / a.pool.page, t % a.pool.page);
     }
   };
   // this thread's rows of a chunk, r0 + j * pass, and its place in them
   const int r0 = threadIdx.x / ru, u = threadIdx.x - r0 * ru, h = u / a.pool.row16;
-  char* const mine = cache + (h0 + h) * side.head + (u - h * a.pool.row16) * 16;
   const int chunks = (n + rows - 1) / rows;
   locate(0, 0);
   __syncthreads();
   for (int c = 0, buf = 0; c < chunks; ++c) {
     const int next = buf < 2 ? buf + 1 : 0;
-    uint4 w[kMoveUnits];
+    for (int plane = plane0; plane < plane1; ++plane) {
+      const PoolSide& side = (plane & 1) ? a.pool.v : a.pool.k;
+      char* const mine = side.base + (plane >> 1) * side.layer + (h0 + h) * side.head +
+                         (u - h * a.pool.row16) * 16;
+      auto at = [&](const int2& p) {
+        return reinterpret_cast<uint4*>(mine + p.x * side.page + p.y * side.token);
+      };
+      uint4 w[kMoveUnits];
 #pragma unroll
-    for (int j = 0; j < kMoveUnits; ++j) {
-      const int r = r0 + j * pass;
-      if (r0 < pass && r < rows && from[buf][r] >= 0)
-        w[j] = *reinterpret_cast<const uint4*>(mine + from[buf][r]);
-    }
-    // a warp that is behind may still have to write the chunk before this one: the
-    // next one's places go to the third buffer
-    if (c + 1 < chunks) locate(c + 1, next);
-    __syncthreads();  // the chunk is read by all
+      for (int j = 0; j < kMoveUnits; ++j) {
+        const int r = r0 + j * pass;
+        if (r0 < pass && r < rows && from[buf][r].x >= 0) w[j] = *at(from[buf][r]);
+      }
+      // a warp that is behind may still have to write the chunk before this one: the
+      // next one's places go to the third buffer
+      if (plane == plane0 && c + 1 < chunks) locate(c + 1, next);
+      __syncthreads();  // the chunk is read by all
 #pragma unroll
-    for (int j = 0; j < kMoveUnits; ++j) {
-      const int r = r0 + j * pass;
-      if (r0 < pass && r < rows && to[buf][r] >= 0)
-        *reinterpret_cast<uint4*>(mine + to[buf][r]) = w[j];
+      for (int j = 0; j < kMoveUnits; ++j) {
+        const int r = r0 + j * pass;
+        if (r0 < pass && r < rows && to[buf][r].x >= 0) *at(to[buf][r]) = w[j];
+      }
     }
     buf = next;
   }
@@ -382,15 +386,18 @@ __global__ void __cluster_dims__(kGrowCluster, 1, 1) __launch_bounds__(kGrowThre
 }  // namespace
 
 cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s) {
-  // a CTA a (sequence, layer, cache); with few of them the heads are shared out
-  const int64_t ctas = int64_t(a.B) * a.pool.layers * 2;
+  // As many CTAs as are resident: with few planes the heads are shared out, with
+  // many a CTA has several (64 sequences, 16 layers: 14.9 us with one each).
+  constexpr int kResident = 4 * 152;
+  const int64_t planes = int64_t(a.B) * a.pool.layers * 2;
   int splits = 1;
-  while (splits < a.pool.Hkv && ctas * splits < 4 * 152) splits *= 2;
+  while (splits < a.pool.Hkv && planes * splits < kResident) splits *= 2;
+  a.planes = static_cast<int>(min64(2 * a.pool.layers, (planes + kResident - 1) / kResident));
   a.heads = (a.pool.Hkv + splits - 1) / splits;
   const int most = kMoveThreads / a.pool.row16;  // the threads hold a row
   a.heads = a.heads < most ? a.heads : most;
   a.head_splits = (a.pool.Hkv + a.heads - 1) / a.heads;
-  return launch_pdl(kv_compact_kernel, dim3(a.B * a.head_splits, 2 * a.pool.layers),
+  return launch_pdl(kv_compact_kernel, dim3(a.B * a.head_splits, (2 * a.pool.layers + a.planes - 1) / a.planes),
                     dim3(kMoveThreads), 0, s, a);
 }
 

@@ -249,7 +249,7 @@ struct CompactArgs {
   const int32_t* cu_keep;
   const int32_t* n_keep;
   const int32_t* base;
-  int heads, head_splits;  // set by the launcher: heads of a CTA
+  int heads, head_splits, planes;  // set by the launcher: heads and planes of a CTA
   int* status;
 };
 struct CopyPagesArgs {
