@@ -158,7 +158,7 @@ struct Shared {
   float wf[kWarps];
   Best wbest[kWarps];
   // the bucket that a sum falls into
-  int found;
+  int found, found2;
   uint32_t found_num, found_count;  // logits in it, and up to its end
   uint64_t found_rest, total;
   int tie_limit;
@@ -298,10 +298,11 @@ struct Row {
   }
 
   // f(group, index of its first logit from base, sum) for this thread's groups with
-  // a logit of at least `least`; the sum of what f adds to `sum` (weights, a few at
+  // a logit of at least `least` (kAllGroups: for all of them, and for groups of -inf
+  // behind them); the sum of what f adds to `sum` (weights, a few at
   // a time in float32, so with 15 roundings at most, and these as integers) in
   // units of 2^-kFracBits.
-  template <typename F>
+  template <bool kAllGroups, typename F>
   __device__ __forceinline__ uint64_t groups_sum(float least, int g, int batches, F&& f) const {
     constexpr int U = 4, kRun = 16 / E::N;
     uint64_t sum = 0;
@@ -314,7 +315,7 @@ struct Row {
         float run = 0.f;
 #pragma unroll
         for (int i = j; i < j + kRun; ++i)
-          if (g + i * kThreads < ng && (least == kNegInf || E::max_of(w[i], kNegInf) >= least))
+          if (kAllGroups || E::max_of(w[i], kNegInf) >= least)
             f(w[i], (g0 + g + i * kThreads) * E::N, run);
         sum += __float2ull_rn(run * kWeightOne);
       }
@@ -374,7 +375,7 @@ struct Row {
       if (kWeights) atomicAdd(&sh.lower[b], f & ((1u << kHalf) - 1));
     };
     for (int k = 0; k < batches(); k += kWindowBatches) {
-      *sum += groups_sum(least, tid + k * 4 * kThreads, min(kWindowBatches, batches() - k),
+      *sum += groups_sum<false>(least, tid + k * 4 * kThreads, min(kWindowBatches, batches() - k),
                          [&](const uint4& w, int v, float& run) { f(w, v, run, add); });
       __syncthreads();
       const uint2 u = upper[tid], l = lower[tid];
@@ -450,9 +451,10 @@ struct Row {
 
   // The bucket in which the running sum of h.v reaches the target and what the
   // target is behind the sum before it; none: -1 (clamp: the last one with anything
-  // in it). Each warp adds up its 64 buckets; the one that the target falls into
-  // looks closer.
-  __device__ int find(const Sums& h, uint64_t target, uint64_t* rest, bool clamp = false) const {
+  // in it). sh.found2: the bucket that a second, larger target falls into. Each warp
+  // adds up its 64 buckets; the one that the target falls into looks closer.
+  __device__ int find(const Sums& h, uint64_t target, uint64_t* rest, bool clamp = false,
+                      uint64_t second = 0) const {
     uint64_t s = h.v[0] + h.v[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
@@ -464,8 +466,11 @@ struct Row {
     if (tid == 0) sh.found = -1;
     __syncthreads();
     s = scan(lane < kWarps ? sh.wsum[lane] : 0);
-    if (clamp) target = min(target, __shfl_sync(kAll, s, 31));
-    if (warp == __popc(__ballot_sync(kAll, s < target))) {
+    const uint64_t all = __shfl_sync(kAll, s, 31);
+    if (clamp) target = min(target, all);
+    second = min(second, all);
+    if (warp == __popc(__ballot_sync(kAll, s < target)) ||
+        (second > target && warp == __popc(__ballot_sync(kAll, s < second)))) {
       uint64_t before = __shfl_sync(kAll, s, warp > 0 ? warp - 1 : 0);
       if (warp == 0) before = 0;
       const uint32_t count = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) +
@@ -477,7 +482,10 @@ struct Row {
         sh.found_num = odd ? h.n[1] : h.n[0];
         sh.found_count = odd ? count : count - h.n[1];
         sh.found_rest = target - before - (odd ? h.v[0] : 0);
+        if (second <= target) sh.found2 = 2 * tid + odd;
       }
+      if (second > target && before < second && second <= before + h.v[0] + h.v[1])
+        sh.found2 = 2 * tid + (second > before + h.v[0]);
     }
     __syncthreads();
     const int b = sh.found;
@@ -486,16 +494,32 @@ struct Row {
     return b;
   }
 
-  // The steps [*lo, *hi] of 1/16 that a cut of `kept` (everything without kPart) falls into: that of the target'th logit, or, with kWeights, of the share
-  // of the weights, whose sum is *total. False: there is none. sh.found_count: the
-  // logits up to *hi's end; one step: sh.found_num in it, *rest to go in it.
+  // The CTA's sum of a number of each thread.
+  __device__ float block_sum(float x) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    if (lane == 0) sh.wf[warp] = x;
+    __syncthreads();
+    x = sh.wf[lane & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    __syncthreads();
+    return x;
+  }
+
+  // The steps [*lo, *hi] of 1/16 that a cut of `kept` (everything without kPart) falls
+  // into: the one with the target'th logit, and *rest to go in it; or, with
+  // kWeights, those that in all likelihood have the place where the weights reach
+  // *rest, which is the share of their sum *total. *enough: the step whose end is
+  // certainly behind the cut. False: there is no cut. sh.found_num, sh.found_count:
+  // the logits in step *enough, and up to its end.
   template <bool kWeights, bool kPart>
   __device__ bool steps(uint64_t target, float share, const Kept& kept, int* lo, int* hi,
-                        uint64_t* total, uint64_t* rest) {
+                        uint64_t* total, uint64_t* rest, int* enough) {
     *reinterpret_cast<uint2*>(&sh.upper[2 * tid]) = make_uint2(0, 0);
     __syncthreads();
     const uint64_t sum =
-        groups_sum(kPart ? kept.x : kNegInf, tid, batches(), [&](const uint4& w, int v, float& run) {
+        groups_sum<!kPart>(kPart ? kept.x : kNegInf, tid, batches(), [&](const uint4& w, int v, float& run) {
           float y[E::N];
           E::unpack(w, y);
 #pragma unroll
@@ -521,26 +545,35 @@ struct Row {
     if (!kWeights) {
       s.v[0] = s.n[0];
       s.v[1] = s.n[1];
-      *lo = *hi = find(s, target, rest);
+      *lo = *hi = *enough = find(s, target, rest);
       return *lo >= 0;
     }
-    // The weights of a step are between 2^-(b + 1)/16 and 2^-b/16 a logit; 2^-18
-    // covers the roundings of the sums, the weights and t.
-    auto bound = [&](int more, float slack) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float w = ex2_approx((2 * tid + i + more) * (-1.f / kPerUnit));
-        s.v[i] = s.n[i] * __float2ull_rn(w * kWeightOne * slack);
-      }
-    };
     *rest = times_up(*total, share);
     uint64_t unused;
-    bound(0, 1.f + 0x1p-18f);
-    *lo = min(find(s, *rest, &unused, true), kBuckets - 2);
-    bound(1, 1.f - 0x1p-18f);
-    *hi = find(s, *rest, &unused);
-    if (*hi < 0) {  // behind the bounds' reach; what is in the last step weighs nothing
-      *hi = kBuckets - 2;
+    // Where it is to be expected: a logit's weight is the step's middle one, give or
+    // take 1.3 % (the spread of a number within 4.4 %), so that the sum is off by 1.3
+    // % of the root of the sum of the weights' squares; five times that, and some.
+    float squares = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float w = ex2_approx((2 * tid + i + 0.5f) * (-1.f / kPerUnit));
+      squares += s.n[i] * w * w;
+      s.v[i] = s.n[i] * __float2ull_rn(w * kWeightOne);
+    }
+    squares = block_sum(squares);
+    const uint64_t off = __float2ull_rn(kWeightOne * 0.065f * sqrtf(squares)) + (*total >> 11);
+    *lo = min(find(s, *rest > off ? *rest - off : 1, &unused, true, *rest + off), kBuckets - 2);
+    *hi = min(sh.found2, kBuckets - 2);
+    __syncthreads();
+    // The logits that are certainly enough: the least that a step's weights can be
+    // reaches the sum with them. 2^-18 covers the roundings of the sums, the weights
+    // and t.
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      s.v[i] = s.n[i] * __float2ull_rn(ex2_approx((2 * tid + i + 1) * (-1.f / kPerUnit)) *
+                                       (kWeightOne * (1.f - 0x1p-18f)));
+    *enough = find(s, *rest, &unused);
+    if (*enough < 0) {
       if (tid == 0) sh.found_count = kAll;
       __syncthreads();
     }
@@ -607,13 +640,17 @@ struct Row {
   __device__ Cut narrow(int lo, int hi, uint32_t n, uint64_t rest, const Kept& kept, bool last) {
     // The steps divided by a power of two: a part lies within one unit of t, and
     // what is subtracted and multiplied here is exact.
-    int parts = 0;  // log2 of the parts of a step
-    while ((hi - lo + 1) << (parts + 1) <= kBuckets) ++parts;
-    const float scale = static_cast<float>(1 << parts), top = lo,
-                bottom = hi < kBuckets - 1 ? hi + 1.f : kInf;
+    int parts, part;  // log2 of the parts of a step; the one with the cut (-1: all)
+    float scale, top, bottom;
     auto part_of = [&](float t16) { return bucket_at(fminf((t16 - top) * scale, kBuckets - 1.f)); };
-    int part = -1;  // the one that the cut falls into (-1: all)
-    if ((kWeights || n > kFew) && hi < kBuckets - 1) {
+    for (const uint64_t whole = rest;; lo = 0, hi = kBuckets - 2) {
+      parts = 0;
+      part = -1;
+      while ((hi - lo + 1) << (parts + 1) <= kBuckets) ++parts;
+      scale = static_cast<float>(1 << parts);
+      top = lo;
+      bottom = hi < kBuckets - 1 ? hi + 1.f : kInf;
+      if (!kWeights && (n <= kFew || hi == kBuckets - 1)) break;
       uint64_t above = 0;
       Sums h = histogram<kWeights>(
           reach(hi), &above, [&](const uint4& w, int v, float& run, auto&& add) {
@@ -639,10 +676,16 @@ struct Row {
           const int e = kFracBits - kFineBits - (lo + ((2 * tid + i) >> parts)) / kPerUnit;
           h.v[i] = e >= 0 ? h.v[i] << e : h.v[i] >> -e;
         }
-        rest = rest > above ? rest - above : 1;
+        // not in these steps, against all likelihood: in any of them
+        const bool all = lo == 0 && hi == kBuckets - 2;
+        if (whole <= above && !all) continue;
+        part = find(h, whole > above ? whole - above : 1, &rest, all);
+        if (part < 0 && !all) continue;
+      } else {
+        part = find(h, whole, &rest, true);
       }
-      part = find(h, rest, &rest, true);
       n = sh.found_num;
+      break;
     }
     const int step = lo + (part > 0 ? part >> parts : 0);
     if (kWeights) {  // in units of the part's weights
@@ -904,12 +947,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     uint32_t left = kAll;  // no more logits than these are kept
     const float share = p > 0.f ? p : 0.f;
     if (cut_k || cut_p) {
-      int lo, hi;
+      int lo, hi, enough;
       uint64_t total, rest;
-      const bool is = cut_k ? r.template steps<false, false>(k, 0.f, cut.kept, &lo, &hi, &total, &rest)
-                            : r.template steps<true, false>(0, share, cut.kept, &lo, &hi, &total, &rest);
+      const bool is = cut_k ? r.template steps<false, false>(k, 0.f, cut.kept, &lo, &hi, &total, &rest, &enough)
+                            : r.template steps<true, false>(0, share, cut.kept, &lo, &hi, &total, &rest, &enough);
       if (is && sh.found_count <= kFew) {
-        r.push(r.reach(hi), [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= hi; });
+        r.push(r.reach(enough),
+               [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= enough; });
         if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, total);
         return;
       }
@@ -919,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     : r.template narrow<true, false>(lo, hi, kAll, rest, cut.kept, true);
       }
       if (cut_k && cut_p &&
-          r.template steps<true, true>(0, share, cut.kept, &lo, &hi, &total, &rest)) {
+          r.template steps<true, true>(0, share, cut.kept, &lo, &hi, &total, &rest, &enough)) {
         left = min(left, sh.found_count);
         cut = r.template narrow<true, true>(lo, hi, kAll, rest, cut.kept, true);
       }
