@@ -790,7 +790,7 @@ rf_status rf_sample_rows(const void *logits, int64_t stride, const float *expo,
  * k_head_stride (elements), the same for v. Strides in bytes and both pointers
  * 16-byte aligned, strides >= 0; d * element size a multiple of 16, d <= 1024.
  * layers in [0, 32767] (0: nothing launched), Hkv, page, num_pages >= 1; page *
- * num_pages and page * Hkv * d <= 2^31 - 1.
+ * num_pages and page * Hkv * d <= 2^31 - 1. k's and v's bytes must not overlap.
  */
 typedef struct {
   void *k, *v;
@@ -836,7 +836,7 @@ rf_status rf_kv_copy_pages(const rf_kv_pool *pool, const int32_t *src, const int
  *
  * rf_pages_fork makes row i of `out` a copy of row src[i] of `table` (its pages of
  * len[src[i]] tokens; entries behind them stay) and gives each of its pages one
- * owner more. len_out[i] = len[src[i]]. `out` must not overlap `table`. A src
+ * owner more. len_out[i] = len[src[i]]. `out` must not overlap `table` (refused). A src
  * outside [0, B) or a bad length gives an empty row.
  *
  * rf_pages_grow gives the n rows of `table` the pages that new_len[i] tokens need

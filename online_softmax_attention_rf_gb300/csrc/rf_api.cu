@@ -1122,6 +1122,10 @@ rf_status rf_pages_fork(const int32_t* table, int64_t table_stride, const int32_
     if (!aligned(p, 4)) return fail(RF_ERR_INVALID, "%s: misaligned pointer", fn);
   if ((table_stride < max_pages && B > 1) || (out_stride < max_pages && n > 1))
     return fail(RF_ERR_INVALID, "%s: a table's stride < max_pages", fn);
+  const int32_t* table_end = table + (B > 1 ? (B - 1) * table_stride : 0) + (B > 0 ? max_pages : 0);
+  const int32_t* out_end = out + (n > 1 ? (n - 1) * out_stride : 0) + max_pages;
+  if (B > 0 && out < table_end && table < out_end)
+    return fail(RF_ERR_INVALID, "%s: out overlaps table", fn);
   rf::PagesForkArgs a{};
   a.status = rf::status_word();
   if (a.status == nullptr) return fail(RF_ERR_CUDA, "%s: no CUDA device", fn);

@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 2;  // of an SM
 constexpr int kMaxCluster = 8;
 constexpr int kBuckets = 1024;
 constexpr int kPerUnit = 16;   // buckets of the first histogram per unit of t
@@ -880,7 +881,7 @@ struct Row {
 };
 
 template <typename T, bool kHeld>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArgs a) {
   using E = Elem<T>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ Shared sh;
@@ -1128,8 +1129,9 @@ cudaError_t launch_k(const SampleArgs& a, int cluster, size_t smem, cudaStream_t
 
 template <typename T>
 cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
-  constexpr int kSms = 152, kResident = 2 * kSms;  // CTAs
-  constexpr int kMostHeld = 80 * 1024;             // beside another CTA's and both histograms
+  constexpr int kResident = kCtas * 152;
+  // beside the SM's other CTA's, and both histograms
+  constexpr size_t kMostHeld = (227 * 1024 / kCtas - sizeof(Shared) - 1024) / 16 * 16;
   constexpr int64_t kL2 = 100 << 20;
   // As many CTAs a row as leave all rows' CTAs resident, with a few logits a thread.
   int cluster = 1;

@@ -125,7 +125,7 @@ def test_kv_compact_paged_offsets_beyond_32_bits(cuda_device):
     # a pool of 9 GB: rows that move lie behind 2^31 and 2^32 bytes, in both layers
     layers, pages, page, Hkv, d = 2, 4500, 64, 8, 1024
     kc = torch.zeros(layers, pages, page, Hkv, d, dtype=torch.bfloat16, device="cuda")
-    vc = kc[:, :, :, :, :]
+    vc = torch.zeros_like(kc)
     rows = [[4499, 3, 4100]]
     for l in range(2):
         for i, p in enumerate(rows[0]):
@@ -408,6 +408,7 @@ def test_housekeeping_refusals(cuda_device):
             bad()
     odd = torch.zeros(2, 4, 8, 2, 6, device="cuda")
     for bad in [lambda: api.kv_copy_pages(odd[0], odd[1], one, one),
+                lambda: api.pages_fork(t, one, one, t, refs, 8),
                 lambda: api.kv_copy_pages(k.flatten()[1:4 * 8 * 2 * 60 + 1].view(4, 8, 2, 60),
                                           v.flatten()[1:4 * 8 * 2 * 60 + 1].view(4, 8, 2, 60), one, one),
                 lambda: api.pages_grow(t, one, one, refs, 0),

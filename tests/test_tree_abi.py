@@ -131,7 +131,7 @@ def test_kv_copy_pages_rejects(L, kw):
     assert _call(L, "rf_kv_copy_pages", COPY, dict(kw, pool=_pool())) == INV
 
 
-FORK = dict(table=A, table_stride=4, len=A, B=2, src=A, n=3, out=A, out_stride=4, len_out=A, refs=A,
+FORK = dict(table=A, table_stride=4, len=A, B=2, src=A, n=3, out=2 * A, out_stride=4, len_out=A, refs=A,
             max_pages=4, page=16, num_pages=9, stream=None)
 GROW = dict(table=A, table_stride=4, len=A, new_len=A, n=3, refs=A, max_pages=4, page=16,
             num_pages=9, copy_src=A, copy_dst=A, left=A, stream=None)
@@ -153,7 +153,8 @@ def test_pages_calls_reject(L, name, ok, kw):
 @pytest.mark.parametrize("name,ok,kw,expect", [
     ("rf_pages_fork", FORK, dict(B=-1), INV), ("rf_pages_fork", FORK, dict(src=None), INV),
     ("rf_pages_fork", FORK, dict(out=None), INV), ("rf_pages_fork", FORK, dict(out_stride=3), INV),
-    ("rf_pages_fork", FORK, dict(len_out=None), INV),
+    ("rf_pages_fork", FORK, dict(len_out=None), INV), ("rf_pages_fork", FORK, dict(out=A), INV),
+    ("rf_pages_fork", FORK, dict(out=A + 4 * 7), INV), ("rf_pages_fork", FORK, dict(out=A - 4), INV),
     ("rf_pages_grow", GROW, dict(new_len=None), INV), ("rf_pages_grow", GROW, dict(left=None), INV),
     ("rf_pages_grow", GROW, dict(copy_src=None), INV), ("rf_pages_grow", GROW, dict(n=16385), UNS),
     ("rf_pages_grow", GROW, dict(page=1, num_pages=(1 << 30) + 1), INV),
