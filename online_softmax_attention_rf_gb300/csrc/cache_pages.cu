@@ -17,24 +17,30 @@ namespace {
 // ------------------------------------------------------------------ rows
 
 // Rows move towards the front: row i of a sequence's list comes from a place at
-// or behind i, and the list ascends. A CTA takes a share of one sequence's heads
-// in some of the planes (K and V of the layers) and goes through the list in chunks:
-// in each plane a chunk is read whole before any of it is written, and what it
-// overwrites lies before every later chunk's rows. Loads and stores of one CTA take
-// turns; the four CTAs of an SM overlap. Half of 8 caches of up to 8000 tokens, 8
-// heads, d = 128, 4 layers dropped: 136 us, 5.5 TB/s, bound by memory and by the
-// longest cache's CTAs, which end last (with the next chunk's loads under this one's
-// stores in a CTA there were two CTAs an SM, and not all resident: 166 us).
+// or behind i, and the list ascends. A cluster of CTAs takes a share of one
+// sequence's heads in some of the planes (K and V of the layers) and goes through
+// the list in rounds of a chunk a CTA: in each plane a round is read whole before
+// any of it is written, and what it overwrites lies before every later round's
+// rows. Loads and stores of one CTA take turns; the four CTAs of an SM overlap. Half
+// of 8 caches of up to 8000 tokens, 8 heads, d = 128, 4 layers dropped: 137 us, 5.4
+// TB/s, bound by memory and by the longest cache's CTAs, which end last (with the
+// next chunk's loads under this one's stores in a CTA there were two CTAs an SM, and
+// not all resident: 166 us).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnits = 8;  // rows of a chunk a thread has 16 bytes of
 constexpr int kMoveRows = kMoveThreads;  // rows of a chunk at most: a thread looks one up
 
+// kCluster: more than one CTA a cluster.
+template <bool kCluster>
 __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const CompactArgs a) {
-  // places (page, row in it) of three chunks in turn, -1: stays
+  // places (page, row in it) of a CTA's three chunks in turn, -1: stays
   __shared__ int2 from[3][kMoveRows], to[3][kMoveRows];
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x / a.head_splits, split = blockIdx.x % a.head_splits;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = kCluster ? static_cast<int>(cluster.num_blocks()) : 1;
+  const int rank = kCluster ? static_cast<int>(cluster.block_rank()) : 0;
+  const int b = blockIdx.x / size / a.head_splits, split = blockIdx.x / size % a.head_splits;
   const int plane0 = blockIdx.y * a.planes, plane1 = min(plane0 + a.planes, 2 * a.pool.layers);
   const int c0 = a.cu_keep[b], room = a.cu_keep[b + 1] - c0;
   const int n = a.n_keep != nullptr ? a.n_keep[b] : room;
@@ -83,9 +89,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
   // this thread's rows of a chunk, r0 + j * pass, and its place in them
   const int r0 = threadIdx.x / ru, u = threadIdx.x - r0 * ru, h = u / a.pool.row16;
   const int chunks = (n + rows - 1) / rows;
-  locate(0, 0);
+  locate(rank, 0);
   __syncthreads();
-  for (int c = 0, buf = 0; c < chunks; ++c) {
+  for (int c = rank, buf = 0; c - rank < chunks; c += size) {
     const int next = buf < 2 ? buf + 1 : 0;
     for (int plane = plane0; plane < plane1; ++plane) {
       const PoolSide& side = (plane & 1) ? a.pool.v : a.pool.k;
@@ -102,8 +108,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
       }
       // a warp that is behind may still have to write the chunk before this one: the
       // next one's places go to the third buffer
-      if (plane == plane0 && c + 1 < chunks) locate(c + 1, next);
-      __syncthreads();  // the chunk is read by all
+      if (plane == plane0 && c - rank + size < chunks) locate(c + size, next);
+      // the round is read by all
+      if (kCluster) cluster.sync(); else __syncthreads();
 #pragma unroll
       for (int j = 0; j < kMoveUnits; ++j) {
         const int r = r0 + j * pass;
@@ -386,19 +393,38 @@ __global__ void __cluster_dims__(kGrowCluster, 1, 1) __launch_bounds__(kGrowThre
 }  // namespace
 
 cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s) {
-  // As many CTAs as are resident: with few planes the heads are shared out, with
-  // many a CTA has several (64 sequences, 16 layers: 14.9 us with one each).
-  constexpr int kResident = 4 * 152;
+  // As many CTAs as are resident: with many planes a CTA has several (64 sequences,
+  // 16 layers: 14.9 us with one each), with few the heads are shared out, then the
+  // list. (One sequence of 8000 tokens, 8 heads, 8 layers, half kept: 103 us without
+  // clusters, 54 with. Lists before heads: the eight sequences above 151 us.)
+  constexpr int kResident = 4 * 152, kMaxCluster = 8;
   const int64_t planes = int64_t(a.B) * a.pool.layers * 2;
-  int splits = 1;
+  int cluster = 1, splits = 1;
   while (splits < a.pool.Hkv && planes * splits < kResident) splits *= 2;
   a.planes = static_cast<int>(min64(2 * a.pool.layers, (planes + kResident - 1) / kResident));
   a.heads = (a.pool.Hkv + splits - 1) / splits;
   const int most = kMoveThreads / a.pool.row16;  // the threads hold a row
   a.heads = a.heads < most ? a.heads : most;
   a.head_splits = (a.pool.Hkv + a.heads - 1) / a.heads;
-  return launch_pdl(kv_compact_kernel, dim3(a.B * a.head_splits, (2 * a.pool.layers + a.planes - 1) / a.planes),
-                    dim3(kMoveThreads), 0, s, a);
+  // (a list of a few rows is one chunk)
+  while (cluster < kMaxCluster && planes * a.head_splits * cluster * 2 <= kResident &&
+         a.N / a.B > 64 * cluster)
+    cluster *= 2;
+  const dim3 grid(a.B * a.head_splits * cluster, (2 * a.pool.layers + a.planes - 1) / a.planes);
+  if (cluster == 1) return launch_pdl(kv_compact_kernel<false>, grid, dim3(kMoveThreads), 0, s, a);
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv_compact_kernel<true>, a);
 }
 
 cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s) {
