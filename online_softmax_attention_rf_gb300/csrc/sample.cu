@@ -183,6 +183,7 @@ struct Cut {
   Kept kept;
   float from = kInf, to = kInf, x = kInf;
   uint64_t rest = 0;  // 0: the cut is known
+  bool weights = false;
 };
 
 // A thread's two buckets of the cluster's histogram.
@@ -581,6 +582,81 @@ struct Row {
     return true;
   }
 
+  // A cut of `kept` (everything without kPart) at the target'th logit, or, with
+  // kWeights, where the weights reach a share of their sum *total, by a histogram of
+  // the largest logit's 1023 next values: with 8 bits of a value (bf16) they span far
+  // enough for most rows, a value's logits weigh the same, and nothing has to be
+  // divided further. False: the cut lies below these values, or there is none.
+  // sh.found_count: the logits down to the cut's value.
+  template <bool kWeights, bool kPart>
+  __device__ bool by_value(uint64_t target, float share, const Kept& kept, bool last, Cut* cut,
+                           uint64_t* total) {
+    *reinterpret_cast<uint2*>(&sh.upper[2 * tid]) = make_uint2(0, 0);
+    __syncthreads();
+    const uint32_t top = E::key(max);
+    uint64_t sum =
+        groups_sum<!kPart>(kPart ? kept.x : kNegInf, tid, batches(), [&](const uint4& w, int v, float& run) {
+          float y[E::N];
+          E::unpack(w, y);
+          uint32_t below[E::N];
+          bool rest = false;  // of the weights: each by itself
+#pragma unroll
+          for (int i = 0; i < E::N; ++i) {
+            below[i] = in<kPart>(kept, y[i], v + i) ? top - E::key(y[i]) : kAll;
+            rest |= below[i] >= kBuckets - 1;
+            if (below[i] < kBuckets - 1) atomicAdd(&sh.upper[below[i]], 1u);
+          }
+          if (kWeights && rest) {
+#pragma unroll
+            for (int i = 0; i < E::N; ++i)
+              if (below[i] >= kBuckets - 1 && below[i] != kAll)
+                run += ex2_approx(t16_of(y[i]) * (-1.f / kPerUnit));
+          }
+        });
+    __syncthreads();
+    Sums s{};
+    s.n[0] = sh.upper[2 * tid];
+    s.n[1] = sh.upper[2 * tid + 1];
+    sum = join<false, kWeights>(s, sum);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s.v[i] = s.n[i] == 0 ? 0 : kWeights ? s.n[i] * weight_of(E::value(top - (2 * tid + i))) : s.n[i];
+    if (kWeights) {
+      sum_before(s.v[0] + s.v[1], total);
+      *total += sum;
+      target = times_up(*total, share);
+    }
+    uint64_t rest;
+    const int b = find(s, target, &rest);
+    if (b < 0) return false;
+    *cut = at_value<kWeights, kPart>(E::value(top - b), rest, kept, last);
+    return true;
+  }
+  // Whether by_value() reaches weights of 2^-16, below which a top-p's cut seldom lies.
+  __device__ __forceinline__ bool values_suffice() const {
+    const uint32_t top = E::key(max);
+    return top - E::kLowest < kBuckets || t16_of(E::value(top - (kBuckets - 2))) >= 16.f * kPerUnit;
+  }
+  // A value's weight in units of 2^-kFracBits.
+  __device__ __forceinline__ uint64_t weight_of(float x) const {
+    return __float2ull_rn(ex2_approx(t16_of(x) * (-1.f / kPerUnit)) * kWeightOne);
+  }
+  // The cut of `kept` that takes the logits above x, and of the sh.found_num equal to
+  // it the first whose counts, or weights in units of 2^-kFracBits, reach rest. last:
+  // as for narrow().
+  template <bool kWeights, bool kPart>
+  __device__ Cut at_value(float x, uint64_t rest, const Kept& kept, bool last) const {
+    if (kWeights) {
+      const uint64_t w = weight_of(x);
+      rest = w > 0 ? (rest + w - 1) / w : kAll;
+    }
+    const uint32_t n = sh.found_num;
+    const int limit = kPart && x == kept.x ? kept.limit : kNoIdx;
+    if (rest >= n) return Cut{Kept{x, limit}};
+    // the row's last step takes the first `rest` of few
+    if (n <= kFew && last) return Cut{Kept{x, limit}, 0.f, kInf, x, rest, false};
+    return Cut{Kept{x, min(limit, tie_limit(x, static_cast<uint32_t>(rest)))}};
+  }
+
   // Few logits, those that is(x, index), go to the cluster's first CTA.
   __device__ __forceinline__ void push_one(float x, int v) const {
     const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
@@ -600,23 +676,28 @@ struct Row {
   // This thread's logit and index of the few, in order (one CTA); how many.
   __device__ int in_order(float* x, int* v) const {
     const int n = min(static_cast<int>(sh.pushed), kFew);
-    float* sx = reinterpret_cast<float*>(sh.val);
-    int* sv = reinterpret_cast<int*>(sh.val) + kFew;
+    // (x descending, index ascending) as one number; its rank by counting
+    uint64_t* all = sh.val[0];
+    uint64_t* sorted = sh.val[1];
+    const uint64_t mine =
+        tid < n ? uint64_t(Elem<float>::key(__uint_as_float(sh.upper[tid]))) << 32 | ~sh.lower[tid] : 0;
+    if (tid < (n + 7) / 8 * 8) all[tid] = mine;
+    __syncthreads();
     if (tid < n) {
-      const float mine = __uint_as_float(sh.upper[tid]);
-      const int at = static_cast<int>(sh.lower[tid]);
       int r = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
-        const float y = __uint_as_float(sh.upper[j]);
-        r += y > mine || (y == mine && static_cast<int>(sh.lower[j]) < at);
+      for (int j = 0; j < n; j += 8) {
+        ulonglong2 o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const ulonglong2*>(all + j + 2 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r += (o[i].x > mine) + (o[i].y > mine);
       }
-      sx[r] = mine;
-      sv[r] = at;
+      sorted[r] = mine;
     }
     __syncthreads();
-    *x = tid < n ? sx[tid] : kNegInf;
-    *v = tid < n ? sv[tid] : kNoIdx;
+    const uint64_t got = tid < n ? sorted[tid] : 0;
+    *x = tid < n ? Elem<float>::value(static_cast<uint32_t>(got >> 32)) : kNegInf;
+    *v = tid < n ? static_cast<int>(~static_cast<uint32_t>(got)) : kNoIdx;
     return n;
   }
 
@@ -652,6 +733,37 @@ struct Row {
       top = lo;
       bottom = hi < kBuckets - 1 ? hi + 1.f : kInf;
       if (!kWeights && (n <= kFew || hi == kBuckets - 1)) break;
+      if constexpr (sizeof(T) == 2) {  // no more values than buckets: by value
+        const uint32_t upto = lo > 0 ? E::key(max - top / c16 * (1.f - 0x1p-21f)) : E::key(max);
+        if (upto - E::key(max - bottom / c16 * (1.f + 0x1p-21f)) < kBuckets) {
+          uint64_t above = 0;
+          Sums h = histogram<false>(
+              reach(hi), &above, [&](const uint4& w, int v, float& run, auto&& add) {
+                float y[E::N];
+                E::unpack(w, y);
+#pragma unroll
+                for (int i = 0; i < E::N; ++i) {
+                  const float t16 = t16_of(y[i]);
+                  if (!in<kPart>(kept, y[i], v + i)) continue;
+                  if (kWeights && t16 < top) run += ex2_approx(t16 * (-1.f / kPerUnit));
+                  if (t16 >= top && t16 < bottom) add(upto - E::key(y[i]), t16);
+                }
+              });
+          above = join<false, kWeights>(h, above);
+          if (kWeights) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              h.v[i] = h.n[i] == 0 ? 0 : h.n[i] * weight_of(E::value(upto - (2 * tid + i)));
+          }
+          const bool all = !kWeights || (lo == 0 && hi == kBuckets - 2);
+          if (kWeights && whole <= above && !all) continue;
+          const uint64_t target = !kWeights ? whole : whole > above ? whole - above : 1;
+          part = find(h, target, &rest, all);
+          if (part < 0 && !all) continue;  // not in these steps, against all likelihood
+          if (part < 0) return Cut{kept};  // what is left weighs nothing
+          return at_value<kWeights, kPart>(E::value(upto - part), rest, kept, last);
+        }
+      }
       uint64_t above = 0;
       Sums h = histogram<kWeights>(
           reach(hi), &above, [&](const uint4& w, int v, float& run, auto&& add) {
@@ -737,7 +849,7 @@ struct Row {
     }
     if (last)  // (nothing below the lowest key is left; of kept what it was)
       return Cut{kPart && kept.x >= E::value(klo) ? kept : Kept{E::value(klo), kNoIdx}, from, to,
-                 narrowed ? E::value(khi) : kInf, rest};
+                 narrowed ? E::value(khi) : kInf, rest, kWeights};
     push(E::value(klo), is);
     if (rank == 0) {
       float x;
@@ -950,23 +1062,49 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
     if (cut_k || cut_p) {
       int lo, hi, enough;
       uint64_t total, rest;
-      const bool is = cut_k ? r.template steps<false, false>(k, 0.f, cut.kept, &lo, &hi, &total, &rest, &enough)
-                            : r.template steps<true, false>(0, share, cut.kept, &lo, &hi, &total, &rest, &enough);
-      if (is && sh.found_count <= kFew) {
-        r.push(r.reach(enough),
-               [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= enough; });
-        if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, total);
-        return;
+      // by values where they are few, else, or below them, by steps of t
+      bool is = false, steps = true;
+      if constexpr (sizeof(T) == 2) {
+        const Kept all;
+        if (cut_k)
+          is = r.template by_value<false, false>(k, 0.f, all, !cut_p, &cut, &total);
+        else if (r.values_suffice())
+          is = r.template by_value<true, false>(0, share, all, true, &cut, &total);
+        steps = !is;
+        if (is && sh.found_count <= kFew) {
+          r.push(cut.kept.x, [&](float x, int) { return x >= cut.kept.x; });
+          if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, total);
+          return;
+        }
+        if (is) left = sh.found_count;
       }
-      if (is) {
-        left = sh.found_count;
-        cut = cut_k ? r.template narrow<false, false>(lo, hi, sh.found_num, rest, cut.kept, !cut_p)
-                    : r.template narrow<true, false>(lo, hi, kAll, rest, cut.kept, true);
+      if (steps) {
+        cut = Cut{};
+        is = cut_k ? r.template steps<false, false>(k, 0.f, cut.kept, &lo, &hi, &total, &rest, &enough)
+                   : r.template steps<true, false>(0, share, cut.kept, &lo, &hi, &total, &rest, &enough);
+        if (is && sh.found_count <= kFew) {
+          r.push(r.reach(enough),
+                 [&](float x, int) { return x > kNegInf && r.bucket_of(x) <= enough; });
+          if (r.rank == 0) r.finish(b, cut_k, k, p, t_max, total);
+          return;
+        }
+        if (is) {
+          left = sh.found_count;
+          cut = cut_k ? r.template narrow<false, false>(lo, hi, sh.found_num, rest, cut.kept, !cut_p)
+                      : r.template narrow<true, false>(lo, hi, kAll, rest, cut.kept, true);
+        }
       }
-      if (cut_k && cut_p &&
-          r.template steps<true, true>(0, share, cut.kept, &lo, &hi, &total, &rest, &enough)) {
-        left = min(left, sh.found_count);
-        cut = r.template narrow<true, true>(lo, hi, kAll, rest, cut.kept, true);
+      if (cut_k && cut_p) {
+        const Kept first = cut.kept;
+        bool found = false;
+        if constexpr (sizeof(T) == 2)
+          found = r.values_suffice() && r.template by_value<true, true>(0, share, first, true, &cut, &total);
+        if (found) {
+          left = min(left, sh.found_count);
+        } else if (r.template steps<true, true>(0, share, first, &lo, &hi, &total, &rest, &enough)) {
+          left = min(left, sh.found_count);
+          cut = r.template narrow<true, true>(lo, hi, kAll, rest, first, true);
+        }
       }
     }
     const float* e = a.expo + int64_t(b) * a.V - r.first;
@@ -1101,7 +1239,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       sum += sh.csum[q];
     }
   }
-  if (cut.rest > 0) r.last_few(b, cut.rest, cut_p, best, sum);
+  if (cut.rest > 0) r.last_few(b, cut.rest, cut.weights, best, sum);
   if (r.tid == 0) r.answer(b, best, sum, bad, greedy);
 }
 
