@@ -1134,46 +1134,61 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
                                      : fmaxf(least, E::value(E::key(cut.kept.x) + 1));
       const float c = r.c16 * (1.f / kPerUnit);
       const bool wide = reinterpret_cast<uintptr_t>(e) % 16 == 0;
+      constexpr int kPair = 8 / E::N;
       for (int g = r.tid; g < r.ng; g += U * kThreads) {
         uint4 w[U];
         r.template fetch<U, kHeld>(w, g);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          if (E::max_of(w[j], kNegInf) < least) continue;
-          const int v = (r.g0 + g + j * kThreads) * E::N;
-          float y[E::N], ev[E::N];
-          E::unpack(w[j], y);
-          if (wide && v >= r.first && v + E::N <= r.end) {
+        for (int j0 = 0; j0 < U; j0 += kPair) {
+          if (g + j0 * kThreads >= r.ng) break;
+          // the random numbers of a few groups are on their way together
+          float ev[kPair][E::N];
 #pragma unroll
-            for (int i = 0; i < E::N; i += 4) {
-              const float4 q = __ldg(reinterpret_cast<const float4*>(e + v + i));
-              ev[i] = q.x; ev[i + 1] = q.y; ev[i + 2] = q.z; ev[i + 3] = q.w;
+          for (int j = 0; j < kPair; ++j) {
+            const int v = (r.g0 + g + (j0 + j) * kThreads) * E::N;
+            if (wide && v >= r.first && v + E::N <= r.end) {
+#pragma unroll
+              for (int i = 0; i < E::N; i += 4) {
+                const float4 q = __ldg(reinterpret_cast<const float4*>(e + v + i));
+                ev[j][i] = q.x; ev[j][i + 1] = q.y; ev[j][i + 2] = q.z; ev[j][i + 3] = q.w;
+              }
+            } else {
+              float y[E::N];
+              E::unpack(w[j0 + j], y);
+#pragma unroll
+              for (int i = 0; i < E::N; ++i) {
+                ev[j][i] = 1.f;
+                if (y[i] >= least) ev[j][i] = __ldg(e + v + i);
+              }
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < E::N; ++i) ev[i] = y[i] >= least ? __ldg(e + v + i) : 1.f;
           }
-          bool look = false;
 #pragma unroll
-          for (int i = 0; i < E::N; ++i) {
-            const float q = ex2_approx((y[i] - m) * c);
-            const bool is = y[i] >= sure;
-            sum += is ? q : 0.f;
-            const float score = __fdividef(q, ev[i]);
-            if (is && score > best.score) {
-              best.score = score;
-              best.idx = v + i;
-            }
-            look |= !is && y[i] >= least;
-          }
-          if (look) {
+          for (int j = 0; j < kPair; ++j) {
+            const int v = (r.g0 + g + (j0 + j) * kThreads) * E::N;
+            float y[E::N];
+            E::unpack(w[j0 + j], y);
+            bool look = false;
 #pragma unroll
             for (int i = 0; i < E::N; ++i) {
-              const float t16 = r.t16_of(y[i]);
-              if (y[i] >= least && y[i] < sure && taken(y[i], t16, v + i)) {
-                const float q = ex2_approx(t16 * (-1.f / kPerUnit));
-                sum += q;
-                take(best, Best{__fdividef(q, ev[i]), v + i, 0.f});
+              const float q = ex2_approx((y[i] - m) * c);
+              const bool is = y[i] >= sure;
+              sum += is ? q : 0.f;
+              const float score = __fdividef(q, ev[j][i]);
+              if (is && score > best.score) {
+                best.score = score;
+                best.idx = v + i;
+              }
+              look |= !is && y[i] >= least;
+            }
+            if (look) {
+#pragma unroll
+              for (int i = 0; i < E::N; ++i) {
+                const float t16 = r.t16_of(y[i]);
+                if (y[i] >= least && y[i] < sure && taken(y[i], t16, v + i)) {
+                  const float q = ex2_approx(t16 * (-1.f / kPerUnit));
+                  sum += q;
+                  take(best, Best{__fdividef(q, ev[j][i]), v + i, 0.f});
+                }
               }
             }
           }
