@@ -407,9 +407,14 @@ __device__ __forceinline__ void put32(const RowOut& w, int c, const float (&v)[3
   }
 }
 
-// Tree: the new tokens are the nodes of trees. Only the last key tiles, which
-// hold new tokens, ask for a mask: four words of 32 bits a row, fetched while
-// the scores are computed.
+// Tree: the new tokens are the nodes of trees. Only the last key tiles, which hold
+// new tokens, ask for a mask: four words of 32 bits a row, fetched while the scores
+// are computed; all others run as without a tree. One tree of 25 nodes over 1030
+// tokens, 32 heads of 8 key heads, d = 128: 18 us, latency. 16 trees of 64 nodes over
+// 16384 to 32768 tokens, 64 heads: 594 us alone, 665 in a long run: its two items a
+// key head run at different times and read the keys twice (1.03 GB for 0.44 of four
+// such trees, 61 % of the memory's rate, 52 % of the tensor cores'). 24 trees of up to
+// 200 nodes, d = 64: 148 us, bound by the pair step (1.45 us).
 template <int D, bool Tree>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_compact_kernel(const Compa
 
 // ------------------------------------------------------------------ pages
 
+// A CTA has 32 KB of a page in flight (pages of less: one CTA each). Bound by memory:
+// 186 pages of 64 KB in 8 planes, as a step of forks copies them, in 27 us of its
+// 36, 7.2 TB/s with what L2 holds of the last step.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 8;  // 16-byte units in flight a thread
 
@@ -229,7 +232,8 @@ __global__ void __launch_bounds__(kOwnThreads) pages_release_kernel(const PagesR
 //
 // One cluster: each CTA works out all rows' needs, and has a share of the pages.
 // It counts the free ones of its share, and once all counts are known hands its
-// own out.
+// own out. Bound by latency (lengths, table and owners, two cluster barriers, two
+// reads of the owners): four rows that grow in a pool of 64 pages 3.7 us, replayed.
 constexpr int kGrowThreads = 1024;
 constexpr int kGrowCluster = 8;
 

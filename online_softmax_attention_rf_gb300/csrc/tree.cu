@@ -3,8 +3,9 @@
 //
 // A step's nodes are packed like a step's tokens: sequence b has the rows
 // cu_q[b] .. cu_q[b + 1] - 1, in an order in which a node follows its parent;
-// parents are numbered within the sequence. Both kernels are a few dependent
-// loads long; a CTA takes a sequence.
+// parents are numbered within the sequence. A CTA takes a sequence. Bound by
+// latency, a few dependent loads and the steps of the walk: one tree of 32 nodes,
+// replayed, mask 2.7 us, walk 1.9.
 #include "paged_device.cuh"
 
 namespace rf {
