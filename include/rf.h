@@ -699,7 +699,8 @@ rf_status rf_draft_verify(const void *target, const void *draft, const int32_t *
  *  mask uint64 [T, words], 1 <= words <= 16; pos int32 [T] or NULL.
  * Rows outside every sequence get 0. A parent that does not come before its child
  * makes the child a root, and a sequence of more than 64 * words nodes gets masks
- * and positions of 0; both are reported through rf_device_status. B, T >= 0.
+ * and positions of 0; both are reported through rf_device_status. B, T >= 0 (one
+ * of them 0: nothing is written).
  * Errors: RF_ERR_INVALID (sizes, NULL or misaligned pointers), RF_ERR_UNSUPPORTED
  * (words > 16), RF_ERR_CUDA.
  */
@@ -745,7 +746,8 @@ rf_status rf_attn_paged_tree(const void *q, int64_t q_stride, const void *k_cach
  *      keep and n_path as n_keep the arguments of rf_kv_compact_paged, and the
  *      cache's length after it.
  * All device, 4-byte aligned. Offsets that are not ascending within [0, T] make a
- * sequence empty and are reported through rf_device_status. B, T >= 0.
+ * sequence empty and are reported through rf_device_status. B, T >= 0 (B = 0:
+ * nothing is written).
  * Errors: RF_ERR_INVALID, RF_ERR_CUDA.
  */
 rf_status rf_tree_accept(const int32_t *parent, const int32_t *tokens, const int32_t *sampled,
@@ -811,7 +813,7 @@ typedef struct {
  * Rows behind the last kept one stay as they are, and those in place already are
  * not touched. Offsets out of range, entries that do not ascend and rows without a
  * page are skipped and reported through rf_device_status. Two sequences must not
- * share a page that a row is moved to. B, N >= 0; B * Hkv <= 2^31 - 1. Errors:
+ * share a page that a row is moved to. B >= 0, 0 <= N <= 2^30; B * Hkv <= 2^31 - 1. Errors:
  * RF_ERR_INVALID, RF_ERR_UNSUPPORTED (d), RF_ERR_CUDA.
  */
 rf_status rf_kv_compact_paged(const rf_kv_pool *pool, const int32_t *table, int64_t table_stride,

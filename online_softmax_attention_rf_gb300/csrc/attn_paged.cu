@@ -870,7 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (masked) {
 #pragma unroll
               for (int c = 0; c < kBN; ++c)
-                if (c >= lim || (Tree && !(seen[c >> 5] >> (c & 31) & 1))) sr[c] = __float_as_uint(kNegInf);
+                if (c >= lim || (Tree && !(seen[c >> 5] >> (c & 31) & 1)))
+                  sr[c] = __float_as_uint(kNegInf);
             }
             float m8[8];
 #pragma unroll
@@ -1086,7 +1087,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) attn_paged_merge(const Param
     table[i] = __ldcg(reinterpret_cast<const int4*>(p.plan->merge) + i);
   __syncthreads();
   const PlanMerge* merge = reinterpret_cast<const PlanMerge*>(table);
-  const bool matches = (p.tree == nullptr || head[7] == 0) && head[0] == kPlanMagic && head[1] == p.B && head[2] == p.T && head[3] == p.H &&
+  const bool matches = (p.tree == nullptr || head[7] == 0) && head[0] == kPlanMagic &&
+                       head[1] == p.B && head[2] == p.T && head[3] == p.H &&
                        head[4] == p.Hkv && head[5] == p.page && head[6] == p.max_pages;
   const int n_merge = matches ? head[9] : 0;
   const int tasks = matches ? head[10] * kGroups : 0;

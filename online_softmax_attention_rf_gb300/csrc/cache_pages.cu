@@ -459,7 +459,8 @@ cudaError_t launch_pages_grow(PagesGrowArgs a, cudaStream_t s) {
   const size_t smem = size_t(a.n) * sizeof(GrowRow);
   if (smem > 40 * 1024) {  // more than a kernel has by itself
     const cudaError_t e = cudaFuncSetAttribute(
-        pages_grow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        pages_grow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(kMaxGrowRows * sizeof(GrowRow)));  // all calls set the same
     if (e != cudaSuccess) return e;
   }
   a.wide = reinterpret_cast<uintptr_t>(a.refs) % 16 == 0;

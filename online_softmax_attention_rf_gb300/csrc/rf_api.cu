@@ -250,7 +250,8 @@ rf_status attn_paged(const char* fn, const void* q, int64_t q_stride, const void
                         int64_t v_head_stride, int page, int num_pages, const int32_t* table,
                         int64_t table_stride, int max_pages, const void* plan, int B, int T, int H,
                         int Hkv, int d, float scale, void* o, float* lse, float* ws,
-                        size_t ws_bytes, const uint64_t* tree, int tree_words, rf_dtype dt, rf_stream stream) {
+                        size_t ws_bytes, const uint64_t* tree, int tree_words, rf_dtype dt,
+                        rf_stream stream) {
   rf_status chk = check_pool(fn, B, T, page, num_pages, max_pages);
   if (chk != RF_OK) return chk;
   chk = check_heads(fn, H, Hkv);
@@ -297,7 +298,8 @@ rf_status attn_paged(const char* fn, const void* q, int64_t q_stride, const void
   cudaError_t e = rf::launch_attn_paged(a, reinterpret_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess && why != nullptr)
     return fail(RF_ERR_CUDA, "%s: %s: %s", fn, why, cudaGetErrorString(e));
-  if (e != cudaSuccess) return fail(RF_ERR_CUDA, "%s: launch: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+  if (e != cudaSuccess)
+    return fail(RF_ERR_CUDA, "%s: launch: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
   return ok();
 }
 
@@ -1064,7 +1066,8 @@ rf_status rf_kv_compact_paged(const rf_kv_pool* pool, const int32_t* table, int6
   if (chk != RF_OK) return chk;
   chk = check_pool(fn, B, N, pool->page, pool->num_pages, max_pages);
   if (chk != RF_OK) return chk;
-  if (int64_t(B) * pool->Hkv > INT32_MAX) return fail(RF_ERR_INVALID, "%s: B * Hkv > 2^31-1", fn);
+  if (int64_t(B) * pool->Hkv > INT32_MAX || N > (1 << 30))
+    return fail(RF_ERR_INVALID, "%s: B * Hkv > 2^31-1 or N > 2^30", fn);
   if (B == 0 || N == 0 || pool->layers == 0) return ok();
   chk = check_pool_pointers(fn, pool);
   if (chk != RF_OK) return chk;

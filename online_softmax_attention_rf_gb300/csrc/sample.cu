@@ -1285,12 +1285,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
   if (r.tid == 0) r.answer(b, best, sum, bad, greedy);
 }
 
+// Of a row's share, beside the SM's other CTA's, and both histograms.
+constexpr size_t kMostHeld = (227 * 1024 / kCtas - sizeof(Shared) - 1024) / 16 * 16;
+
 template <typename T, bool kHeld>
 cudaError_t launch_k(const SampleArgs& a, int cluster, size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T, kHeld>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  if (kHeld) {  // the most that any row needs: calls of two threads set the same
+    const cudaError_t e =
+        cudaFuncSetAttribute(sample_kernel<T, kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kMostHeld));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1310,8 +1315,6 @@ cudaError_t launch_k(const SampleArgs& a, int cluster, size_t smem, cudaStream_t
 template <typename T>
 cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
   constexpr int kResident = kCtas * 152;
-  // beside the SM's other CTA's, and both histograms
-  constexpr size_t kMostHeld = (227 * 1024 / kCtas - sizeof(Shared) - 1024) / 16 * 16;
   constexpr int64_t kL2 = 100 << 20;
   // As many CTAs a row as leave all rows' CTAs resident, with a few logits a thread.
   int cluster = 1;

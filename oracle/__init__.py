@@ -31,9 +31,13 @@ Modules
 ``paged``        serving over a paged key/value cache: slots, append with head
                  norm and rotation, attention of new tokens over pages, and
                  the verification of drafted tokens.
+``tree``         serving with drafted trees: ancestors, attention under them,
+                 sampling with limits, the walk along the drawn tokens, kept
+                 rows of the cache moved together, pages shared, given and freed.
 
 Every function here is pinned by the ``-m "not gpu"`` tests in
-``tests/test_oracle_pins.py`` (``paged``: ``test_oracle_paged.py``) against brute force, closed forms, invariants
+``tests/test_oracle_pins.py`` (``paged``: ``test_oracle_paged.py``;
+``tree``: ``test_oracle_tree.py``) against brute force, closed forms, invariants
 and library routines; none is "parity unpinned".
 """
 

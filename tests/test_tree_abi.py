@@ -119,7 +119,7 @@ def test_pools_rejected(L, name, ok, pool, expect):
 @pytest.mark.parametrize("kw", [
     dict(B=-1), dict(N=-1), dict(max_pages=0), dict(table_stride=3), dict(table=None),
     dict(keep=None), dict(cu_keep=None), dict(keep=A + 2), dict(n_keep=A + 1), dict(base=A + 2),
-    dict(max_pages=1 << 28),
+    dict(max_pages=1 << 28), dict(N=(1 << 30) + 1),
 ])
 def test_kv_compact_paged_rejects(L, kw):
     assert _call(L, "rf_kv_compact_paged", COMPACT, dict(kw, pool=_pool())) == INV
