@@ -62,13 +62,14 @@ constexpr int kHalf = 17;      // of them in the lower half
 constexpr int kWindow = 32 * kThreads;
 static_assert((uint64_t(kWindow) << kHalf) < (1ull << 32) && kWindow * 7ull < (1ull << kHalf),
               "a window's sums fit their places");
+constexpr int kMaxBlocks = 128;  // of a CTA's share, a group of 16 bytes a thread each
 constexpr int kFew = kThreads;  // logits that one CTA finishes, one a thread
 constexpr uint32_t kAll = 0xffffffffu;
 // A weight of 1 in units of 2^-kFracBits, less 2^-20 of it (as fine_of has it).
 constexpr float kWeightOne = 4398042316800.f;
 constexpr float kInf = __builtin_huge_valf();
 static_assert(kBuckets == 2 * kThreads, "the scan takes two buckets a thread");
-static_assert(kFew <= kBuckets, "a histogram's place holds the few logits");
+static_assert(2 * kFew <= kBuckets, "a histogram's place holds the few logits");
 
 // max(a, b, c), NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -159,7 +160,7 @@ struct Shared {
   uint64_t val[2][kBuckets];
   uint32_t num[2][kBuckets];
   uint64_t part[2];  // and of a sum of weights
-  uint64_t wsum[kWarps];
+  uint64_t wsum[kWarps], wlow[kWarps];
   uint32_t wcnt[kWarps];
   // a value of each CTA of the cluster
   float cmax[kMaxCluster];
@@ -170,11 +171,13 @@ struct Shared {
   float wf[kWarps];
   Best wbest[kWarps];
   // the bucket that a sum falls into
-  int found, found2;
+  int found, found2, found_low;
   uint32_t found_num, found_count;  // logits in it, and up to its end
   uint64_t found_rest;
   int tie_limit;
-  uint32_t pushed;  // few logits that arrived
+  uint32_t block_ties[kMaxBlocks];
+  // few logits: of this CTA, their first place in the first CTA, and all that arrived there
+  uint32_t mine, place, pushed;
   float cut_x;      // the cut among them
   int cut_limit;
 };
@@ -467,43 +470,32 @@ struct Row {
     return s;
   }
 
-  // The bucket in which the running sum of h.v reaches the target and what the
-  // target is behind the sum before it; none: -1 (clamp: the last one with anything
-  // in it). sh.found2: the bucket that a second, larger target falls into. Each warp
-  // adds up its 64 buckets; the one that the target falls into looks closer.
-  __device__ int find(const Sums& h, uint64_t target, uint64_t* rest, bool clamp = false,
-                      uint64_t second = 0) const {
-    uint64_t s = h.v[0] + h.v[1];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  // The bucket in which the running sum of h.v reaches the target, aim(sum of all), and
+  // what the target is behind the sum before it; none: -1. Each warp adds up its 64
+  // buckets; the one that the target falls into looks closer.
+  template <typename F>
+  __device__ int find_by(const Sums& h, uint64_t* rest, F&& aim) const {
+    const uint64_t v = sum_of_warp(h.v[0] + h.v[1]);
     const uint32_t n = __reduce_add_sync(kAll, h.n[0] + h.n[1]);
     if (lane == 0) {
-      sh.wsum[warp] = s;
+      sh.wsum[warp] = v;
       sh.wcnt[warp] = n;
     }
     if (tid == 0) sh.found = -1;
     __syncthreads();
-    s = scan(lane < kWarps ? sh.wsum[lane] : 0);
-    const uint64_t all = __shfl_sync(kAll, s, 31);
-    if (clamp) target = min(target, all);
-    second = min(second, all);
-    if (warp == __popc(__ballot_sync(kAll, s < target)) ||
-        (second > target && warp == __popc(__ballot_sync(kAll, s < second)))) {
-      uint64_t before = __shfl_sync(kAll, s, warp > 0 ? warp - 1 : 0);
-      if (warp == 0) before = 0;
+    const uint64_t s = scan(lane < kWarps ? sh.wsum[lane] : 0);
+    const uint64_t target = aim(__shfl_sync(kAll, s, 31));
+    if (warp == __popc(__ballot_sync(kAll, s < target))) {
+      const uint64_t before = before_lane(s, h);
       const uint32_t count = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) +
                              scan(h.n[0] + h.n[1]);
-      before += scan(h.v[0] + h.v[1]) - h.v[0] - h.v[1];
       const bool odd = target > before + h.v[0];
       if (before < target && target <= before + h.v[0] + h.v[1]) {
         sh.found = 2 * tid + odd;
         sh.found_num = odd ? h.n[1] : h.n[0];
         sh.found_count = odd ? count : count - h.n[1];
         sh.found_rest = target - before - (odd ? h.v[0] : 0);
-        if (second <= target) sh.found2 = 2 * tid + odd;
       }
-      if (second > target && before < second && second <= before + h.v[0] + h.v[1])
-        sh.found2 = 2 * tid + (second > before + h.v[0]);
     }
     __syncthreads();
     const int b = sh.found;
@@ -511,18 +503,19 @@ struct Row {
     __syncthreads();
     return b;
   }
-
-  // The CTA's sum of a number of each thread.
-  __device__ float block_sum(float x) const {
+  // clamp: the last bucket with anything in it where all of them do not reach it.
+  __device__ int find(const Sums& h, uint64_t target, uint64_t* rest, bool clamp = false) const {
+    return find_by(h, rest, [&](uint64_t all) { return clamp ? min(target, all) : target; });
+  }
+  __device__ __forceinline__ uint64_t sum_of_warp(uint64_t s) const {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
-    if (lane == 0) sh.wf[warp] = x;
-    __syncthreads();
-    x = sh.wf[lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
-    __syncthreads();
-    return x;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    return s;
+  }
+  // Sum before a lane's buckets, s the warps' running sums.
+  __device__ __forceinline__ uint64_t before_lane(uint64_t s, const Sums& h) const {
+    const uint64_t before = __shfl_sync(kAll, s, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + scan(h.v[0] + h.v[1]) - h.v[0] - h.v[1];
   }
 
   // The steps [*lo, *hi] that a cut of `kept` (everything without kPart) falls
@@ -568,34 +561,66 @@ struct Row {
       return *lo >= 0;
     }
     *rest = times_up(*total, share);
-    uint64_t unused;
     // Where it is to be expected: a logit's weight is the step's middle one, give or
     // take 1.3 % (the spread of a number within 4.4 %), so that the sum is off by 1.3
     // % of the root of the sum of the weights' squares; five times that, and some.
+    // The logits that are certainly enough: the least that a step's weights can be
+    // reaches the sum with them. 2^-18 covers the roundings of the sums, the weights
+    // and t. Both searches go together, as in find_by().
     float squares = 0.f;
+    Sums low{};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float w = ex2_approx((2 * tid + i + 0.5f) * (-1.f / kPerUnit));
       squares += s.n[i] * w * w;
       s.v[i] = s.n[i] * __float2ull_rn(w * kWeightOne);
+      low.v[i] = s.n[i] * __float2ull_rn(ex2_approx((2 * tid + i + 1) * (-1.f / kPerUnit)) *
+                                         (kWeightOne * (1.f - 0x1p-18f)));
     }
-    squares = block_sum(squares);
-    const uint64_t off = __float2ull_rn(kWeightOne * 0.065f * sqrtf(squares)) + (*total >> 11);
-    *lo = min(find(s, *rest > off ? *rest - off : 1, &unused, true, *rest + off), kBuckets - 2);
-    *hi = min(sh.found2, kBuckets - 2);
-    __syncthreads();
-    // The logits that are certainly enough: the least that a step's weights can be
-    // reaches the sum with them. 2^-18 covers the roundings of the sums, the weights
-    // and t.
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      s.v[i] = s.n[i] * __float2ull_rn(ex2_approx((2 * tid + i + 1) * (-1.f / kPerUnit)) *
-                                       (kWeightOne * (1.f - 0x1p-18f)));
-    *enough = find(s, *rest, &unused);
-    if (*enough < 0) {
-      if (tid == 0) sh.found_count = kAll;
-      __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(kAll, squares, o);
+    const uint64_t v = sum_of_warp(s.v[0] + s.v[1]), l = sum_of_warp(low.v[0] + low.v[1]);
+    const uint32_t n = __reduce_add_sync(kAll, s.n[0] + s.n[1]);
+    if (lane == 0) {
+      sh.wsum[warp] = v;
+      sh.wlow[warp] = l;
+      sh.wcnt[warp] = n;
+      sh.wf[warp] = squares;
     }
+    if (tid == 0) {
+      sh.found_low = -1;
+      sh.found_count = kAll;
+    }
+    __syncthreads();
+    squares = sh.wf[lane & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) squares += __shfl_xor_sync(kAll, squares, o);
+    const uint64_t off = __float2ull_rn(kWeightOne * 0.065f * sqrtf(squares)) + (*total >> 11);
+    const uint64_t mid = scan(lane < kWarps ? sh.wsum[lane] : 0);
+    const uint64_t least = scan(lane < kWarps ? sh.wlow[lane] : 0);
+    const uint64_t all = __shfl_sync(kAll, mid, 31);
+    const uint64_t one = min(*rest > off ? *rest - off : 1, all), two = min(*rest + off, all);
+    if (warp == __popc(__ballot_sync(kAll, mid < one)) ||
+        warp == __popc(__ballot_sync(kAll, mid < two))) {
+      const uint64_t before = before_lane(mid, s), end = before + s.v[0] + s.v[1];
+      if (before < one && one <= end) sh.found = 2 * tid + (one > before + s.v[0]);
+      if (before < two && two <= end) sh.found2 = 2 * tid + (two > before + s.v[0]);
+    }
+    if (warp == __popc(__ballot_sync(kAll, least < *rest))) {
+      const uint64_t before = before_lane(least, low);
+      const uint32_t count = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) +
+                             scan(s.n[0] + s.n[1]);
+      const bool odd = *rest > before + low.v[0];
+      if (before < *rest && *rest <= before + low.v[0] + low.v[1]) {
+        sh.found_low = 2 * tid + odd;
+        sh.found_count = odd ? count : count - s.n[1];
+      }
+    }
+    __syncthreads();
+    *lo = min(sh.found, kBuckets - 2);
+    *hi = min(sh.found2, kBuckets - 2);
+    *enough = sh.found_low;
+    __syncthreads();
     return true;
   }
 
@@ -639,13 +664,12 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (kWeights) s.v[i] = s.n[i] == 0 ? 0 : s.n[i] * weight_of(E::value(top - (2 * tid + i)));
-    if (kWeights) {
-      sum_before(s.v[0] + s.v[1], total);
-      *total += sum;
-      target = times_up(*total, share);
-    }
     uint64_t rest;
-    const int b = find(s, target, &rest);
+    const int b = find_by(s, &rest, [&](uint64_t all) {
+      if (!kWeights) return target;
+      *total = all + sum;
+      return times_up(*total, share);
+    });
     if (b < 0) return false;
     *cut = at_value<kWeights, kPart>(E::value(top - b), rest, kept, last);
     return true;
@@ -676,12 +700,28 @@ struct Row {
     return Cut{Kept{x, min(limit, tie_limit(x, static_cast<uint32_t>(rest)))}};
   }
 
-  // Few logits, those that is(x, index), go to the cluster's first CTA.
+  // Few logits go to the cluster's first CTA: collected in the CTA (a counter of the
+  // cluster's that all of them add to costs its way there and back each time), then
+  // sent together. What others read of this CTA's last histogram is not touched.
   __device__ __forceinline__ void push_one(float x, int v) const {
-    const uint32_t at = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), 1u);
+    const uint32_t at = atomicAdd(&sh.mine, 1u);
     if (at < kFew) {
-      *cluster.map_shared_rank(&sh.upper[at], 0) = __float_as_uint(x);
-      *cluster.map_shared_rank(&sh.lower[at], 0) = static_cast<uint32_t>(v);
+      sh.num[turn][at] = __float_as_uint(x);
+      sh.num[turn][kFew + at] = static_cast<uint32_t>(v);
+    }
+  }
+  __device__ __forceinline__ void send() const {
+    __syncthreads();
+    const uint32_t n = min(sh.mine, static_cast<uint32_t>(kFew));
+    if (tid == 0 && n > 0) sh.place = atomicAdd(cluster.map_shared_rank(&sh.pushed, 0), n);
+    __syncthreads();
+    if (tid == 0) sh.mine = 0;
+    if (tid < n) {
+      const uint32_t at = sh.place + tid;
+      if (at < kFew) {
+        *cluster.map_shared_rank(&sh.upper[at], 0) = sh.num[turn][tid];
+        *cluster.map_shared_rank(&sh.lower[at], 0) = sh.num[turn][kFew + tid];
+      }
     }
   }
   template <typename F>
@@ -689,6 +729,7 @@ struct Row {
     each_from(least, [&](float x, int v) {
       if (is(x, v)) push_one(x, v);
     });
+    send();
     cluster.sync();
   }
 
@@ -894,42 +935,54 @@ struct Row {
 
   // Of the logits equal to x the first `ties` are those before the returned index.
   __device__ int tie_limit(float x, uint32_t ties) const {
-    uint32_t n = 0;
-    each_from(x, [&](float y, int) { n += y == x; });
-    n = __reduce_add_sync(kAll, n);
-    if (lane == 0) sh.wcnt[warp] = n;
+    if (tid < kMaxBlocks) sh.block_ties[tid] = 0;
     if (tid == 0) sh.tie_limit = kNoIdx;
     __syncthreads();
-    n = __reduce_add_sync(kAll, lane < kWarps ? sh.wcnt[lane] : 0u);
+    each_from(x, [&](float y, int v) {
+      if (y == x) atomicAdd(&sh.block_ties[(v / E::N - g0) / kThreads], 1u);
+    });
+    __syncthreads();
+    uint32_t n = 0;  // of the CTA, and before each of a lane's blocks
+    uint32_t before[kMaxBlocks / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxBlocks / 32; ++i) {
+      const uint32_t s = scan(sh.block_ties[32 * i + lane]);
+      before[i] = n + s;
+      n += __shfl_sync(kAll, s, 31);
+    }
     if (tid < size) *cluster.map_shared_rank(&sh.cties[rank], tid) = n;
     cluster.sync();
-    uint32_t before = 0;
-    for (int q = 0; q < rank; ++q) before += sh.cties[q];
-    if (ties <= before) return 0;
-    uint32_t left = ties - before;
+    uint32_t others = 0;
+    for (int q = 0; q < rank; ++q) others += sh.cties[q];
+    if (ties <= others) return 0;
+    uint32_t left = ties - others;
     if (left >= n) return kNoIdx;
-    // the left'th of this CTA's, in order
-    for (int g = 0; g < ng; g += kThreads) {
-      uint4 w[1];
-      fetch<1, kHeld>(w, g + tid);
-      float y[E::N];
-      E::unpack(w[0], y);
-      uint32_t mine = 0;
+    // the block with the left'th of this CTA's, and in it the one
+    int block = 0;
 #pragma unroll
-      for (int i = 0; i < E::N; ++i) mine += y[i] == x;
-      const uint32_t s = scan(mine);
-      __syncthreads();
-      if (lane == 31) sh.wcnt[warp] = s;
-      __syncthreads();
-      uint32_t ahead = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) + s - mine;
-      const uint32_t total = __reduce_add_sync(kAll, lane < kWarps ? sh.wcnt[lane] : 0u);
-      if (ahead < left && left <= ahead + mine) {
+    for (int i = 0; i < kMaxBlocks / 32; ++i)
+      block += __popc(__ballot_sync(kAll, before[i] < left));
 #pragma unroll
-        for (int i = 0; i < E::N; ++i)
-          if (y[i] == x && ++ahead == left) sh.tie_limit = (g0 + g + tid) * E::N + i + 1;
-      }
-      if (left <= total) break;
-      left -= total;
+    for (int i = 0; i < kMaxBlocks / 32; ++i) {
+      const uint32_t s = __shfl_sync(kAll, before[i], (block - 1) & 31);
+      if (block > 0 && (block - 1) / 32 == i) left -= s;
+    }
+    uint4 w[1];
+    fetch<1, kHeld>(w, block * kThreads + tid);
+    float y[E::N];
+    E::unpack(w[0], y);
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < E::N; ++i) mine += y[i] == x;
+    const uint32_t s = scan(mine);
+    if (lane == 31) sh.wcnt[warp] = s;
+    __syncthreads();
+    uint32_t ahead = __reduce_add_sync(kAll, lane < warp ? sh.wcnt[lane] : 0u) + s - mine;
+    if (ahead < left && left <= ahead + mine) {
+#pragma unroll
+      for (int i = 0; i < E::N; ++i)
+        if (y[i] == x && ++ahead == left)
+          sh.tie_limit = (g0 + block * kThreads + tid) * E::N + i + 1;
     }
     __syncthreads();
     return sh.tie_limit;
@@ -1025,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
   r.warp = r.tid >> 5;
   r.lane = r.tid & 31;
   const int b = blockIdx.x / r.size;
-  if (r.tid == 0) sh.pushed = 0;
+  if (r.tid == 0) sh.pushed = sh.mine = 0;
   r.cluster.barrier_arrive();  // waited for before any CTA's memory is written by another
   pdl_wait();
   pdl_trigger();
@@ -1159,6 +1212,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
           cut.rest > 0 ? (cut.x < kInf ? E::value(E::key(cut.x) + 1) : r.least_below(cut.from))
           : cut.kept.limit == kNoIdx ? least
                                      : fmaxf(least, E::value(E::key(cut.kept.x) + 1));
+      // A known cut's equal logits are all in before its limit, and none behind it: only
+      // one group has to look at them.
+      const bool known = cut.rest == 0;
+      const int all_before = known ? cut.kept.limit : 0;
+      const int none_from = known ? cut.kept.limit : kNoIdx;
       const float c = r.c16 * (1.f / kPerUnit);
       const bool wide = reinterpret_cast<uintptr_t>(e) % 16 == 0;
       constexpr int kPair = 8 / E::N;
@@ -1194,24 +1252,29 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
             const int v = (r.g0 + g + (j0 + j) * kThreads) * E::N;
             float y[E::N];
             E::unpack(w[j0 + j], y);
+            float in_from = sure, look_from = least;
+            if constexpr (sizeof(T) == 2) {
+              if (v + E::N <= all_before) in_from = least;
+              if (v >= none_from) look_from = sure;
+            }
             bool look = false;
 #pragma unroll
             for (int i = 0; i < E::N; ++i) {
               const float q = ex2_approx((y[i] - m) * c);
-              const bool is = y[i] >= sure;
+              const bool is = y[i] >= in_from;
               sum += is ? q : 0.f;
               const float score = __fdividef(q, ev[j][i]);
               if (is && score > best.score) {
                 best.score = score;
                 best.idx = v + i;
               }
-              look |= !is && y[i] >= least;
+              look |= !is && y[i] >= look_from;
             }
             if (look) {
 #pragma unroll
               for (int i = 0; i < E::N; ++i) {
                 const float t16 = r.t16_of(y[i]);
-                if (y[i] >= least && y[i] < sure && taken(y[i], t16, v + i)) {
+                if (y[i] >= look_from && y[i] < in_from && taken(y[i], t16, v + i)) {
                   const float q = ex2_approx(t16 * (-1.f / kPerUnit));
                   sum += q;
                   take(best, Best{__fdividef(q, ev[j][i]), v + i, 0.f});
@@ -1266,6 +1329,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
     }
   }
   // the cluster's best and sum, joined in a fixed order
+  if (cut.rest > 0) r.send();
   r.reduce(best, sum);
   if (r.tid == 0) {
     *r.cluster.map_shared_rank(&sh.cbest[r.rank], 0) = best;
@@ -1322,9 +1386,16 @@ cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
          a.V > cluster * kThreads * 4)
     cluster *= 2;
   const int groups = (a.V + 2 * Elem<T>::N - 2) / Elem<T>::N;  // with any lead
+  static_assert((kMaxSampleVocab / 4 + 2) / kMaxCluster + 1 <= kMaxBlocks * kThreads &&
+                    kL2 / kResident / 16 + 1 <= kMaxBlocks * kThreads,
+                "a share has no more blocks");
   auto share = [&] { return size_t((groups + cluster - 1) / cluster) * 16; };
-  // rows that are read again, and resident at one time, fit L2
-  while (cluster < kMaxCluster && share() > kMostHeld && kResident * int64_t(share()) > kL2)
+  // rows that are read again, and resident at one time, fit L2; a thread has no more
+  // than 200 logits (200 / 512 rows of 131072 in bf16 with one CTA a row and with two:
+  // top-k 61 / 125 and 46 / 93 us, top-p 122 / 226 and 90 / 194, no limit 50 / 108 and
+  // 50 / 108; rows of 70000 want one where there are no cuts: 64 and 75)
+  while (cluster < kMaxCluster && share() > kMostHeld &&
+         (kResident * int64_t(share()) > kL2 || a.V > cluster * kThreads * 200))
     cluster *= 2;
   if (share() <= kMostHeld) return launch_k<T, true>(a, cluster, share(), s);
   return launch_k<T, false>(a, cluster, 0, s);
