@@ -765,6 +765,9 @@ rf_status rf_tree_accept(const int32_t *parent, const int32_t *tokens, const int
  *   (the largest always stays). Equal logits: the lower index comes first.
  * The token is argmax_j p_j / expo[b, j] over what is left (lowest index on a
  * tie), which with independent exponential variates is j with probability p_j.
+ * Weights are float32: a logit at which the run's sum is within 2^-17 of top_p, or
+ * whose probability is within 2^-17 of min_p's limit (of their values), may be left on
+ * either side. The same call on the same inputs gives the same bits.
  *  logits : [B, V], dtype dt (RF_F32 or RF_BF16), rows `stride` elements apart;
  *           -inf entries have no probability;
  *  expo   : float [B, V], in [2^-126, 2^32] (as rf_draft_verify; not checked);

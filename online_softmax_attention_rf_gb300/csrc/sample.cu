@@ -29,13 +29,15 @@
 // that fits shared memory beside another CTA's, else in each pass, out of L2.
 // Histograms and few logits are joined through distributed shared memory.
 //
-// Measured (replayed, float32, top-k and top-p of one row of 32000: 7.4 us; 200 rows
-// of 50001: top-k 21 us, top-p 56, no limit 22; 512 rows of 131072: min-p 73 us, top-k
-// 113, top-p 213, no limit 147; bf16, 64 rows of 131072: top-k 16, top-p 47). One row
+// Measured (replayed, float32, top-k and top-p of one row of 32000: 7.5 us; 200 rows
+// of 50001: top-k 21 us, top-p 55, no limit 23; 512 rows of 131072: min-p 71 us, top-k
+// 111, top-p 207, no limit 142; bf16, 64 rows of 131072: top-k 16, top-p 45). One row
 // is bound by latency: dependent loads, cluster barriers (about 0.6 us each) and the
-// searches of the histograms. Many rows are bound by how few warps an SM has for the
-// passes' chains of dependent instructions: 64 registers a thread, two CTAs an SM, a
-// third of the issue slots used at top-p; memory does 10 to 25 % of its rate.
+// searches of the histograms. Many rows are bound by the passes' chains of dependent
+// instructions, about 17 a logit and pass, with 16 to 32 warps an SM to run them (64
+// registers a thread, two CTAs an SM): a third to a half of the issue slots are used.
+// Memory does 10 to 25 % of its rate, and telling L2 or L1 of what comes next costs time
+// (top-p 55 to 58, no limit 147 to 179).
 #include <cooperative_groups.h>
 
 #include <cfloat>
