@@ -466,3 +466,70 @@ def test_decoding_with_trees_over_a_paged_cache(cuda_device):
         n = min(len(got[b]), sure[b])
         assert got[b][:n] == plain[b][:n]
     assert sum(sure) > 20 and steps < 20       # several tokens a step
+
+
+def test_a_tree_step_captured_and_replayed_with_other_trees(cuda_device):
+    """One graph of a whole step, padded to T nodes, replayed with other trees, lengths
+    and tables, gives what the calls give one by one, to the bit."""
+    B, T, H, Hkv, d, page, width, vocab = 3, 48, 8, 2, 64, 16, 20, 97
+    gen, rng = torch.Generator().manual_seed(50), np.random.default_rng(50)
+    pools = torch.randn(2, 2, B * width + 1, page, Hkv, d, generator=gen).bfloat16().cuda()
+    back = torch.randn(H * d, vocab, generator=gen).cuda()
+    expo = torch.empty(T, vocab).exponential_(generator=gen).clamp_(1e-20).cuda()
+    limits = [torch.full((T,), 0.8, device="cuda"), _i32([20] * T),
+              torch.full((T,), 0.9, device="cuda"), torch.full((T,), 0.02, device="cuda")]
+    ws = api.attn_paged_workspace(d)
+
+    def inputs():
+        sizes = [int(rng.integers(1, 17)) for _ in range(B)]
+        kv = [n + int(rng.integers(0, width * page - n + 1)) for n in sizes]
+        parents = sum((_parents(n, rng) for n in sizes), [])
+        pad = T - len(parents)
+        return (torch.randn(T, H, d, generator=gen).bfloat16().cuda(), _i32(_offsets(sizes)),
+                _i32(kv), _i32(parents + [-1] * pad), _i32(rng.integers(0, vocab, T)),
+                _i32(rng.permutation(B * width).reshape(B, width)))
+
+    def step(state, pool, plan, out):
+        q, cu, kv, parent, tokens, table = state
+        mask, pos = api.tree_mask(parent, cu, kv)
+        plan.update(cu, kv)
+        o, lse = api.attn_paged(q, pool[0][0], pool[1][0], table, plan, out=out, workspace=ws,
+                                tree_mask=mask)
+        drawn, logprob = api.sample_rows(o.float().view(T, -1) @ back, expo, *limits)
+        path, emitted, n_path, base, new_len = api.tree_accept(parent, tokens, drawn, cu, kv)
+        api.kv_compact_paged(pool[0], pool[1], table, path, cu, n_path, base)
+        return o, mask, pos, drawn, logprob, path, emitted, n_path, base, new_len
+
+    static = inputs()
+    out = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda")
+    plan = api.PagedPlan(static[1], static[2], T, H, Hkv, page, width, causal=False)
+    pool = pools.clone()
+    step(static, pool, plan, out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(static, pool, plan, out)
+    walked = 0
+    for turn in range(4):
+        new = inputs()
+        if turn > 1:  # drafts that are drawn: every node's is its parent's draw
+            first = step(new, pools.clone(), plan, torch.zeros_like(out))[3].tolist()
+            cu, parent = new[1].tolist(), new[3].tolist()
+            for c0, c1 in zip(cu, cu[1:]):
+                for i in range(c0 + 1, c1):
+                    new[4][i] = first[c0 + parent[i]]
+        for a, b in zip(static, new):
+            a.copy_(b)
+        pool.copy_(pools)
+        out.zero_()
+        other = pools.clone()
+        want = step(new, other, plan, torch.zeros_like(out))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        assert torch.equal(pool, other)
+        assert api.device_status() == 0
+        walked += want[7].sum().item()
+    assert walked > 4 * B
