@@ -364,7 +364,8 @@ struct Row {
     return __float_as_uint(f + 8.f) - 0x41000000u;
   }
 
-  // The least of the logits' type whose t16 is below `from` (all of the warp).
+  // The least of the logits' type whose t16 is below `from` (all of the warp): there is
+  // none for 0, which is the maximum's own.
   __device__ float least_below(float from) const {
     uint32_t lo = E::kLowest + 1, hi = E::key(max);
     while (lo < hi) {
@@ -374,7 +375,7 @@ struct Row {
       if (f < 32) hi = min(hi, lo + f * step);
       lo = f > 0 ? lo + (f - 1) * step + 1 : hi;
     }
-    return E::value(hi);
+    return from > 0.f ? E::value(hi) : kInf;
   }
 
   // A logit that no logit up to the end of step hi lies below.
