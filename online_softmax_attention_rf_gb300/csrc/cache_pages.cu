@@ -432,9 +432,15 @@ cudaError_t launch_kv_compact(CompactArgs a, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s) {
+  // A long list of large pages: no more than 2^22 CTAs a plane, which take several
+  // batches of a page each then: pairs and parts of a page fit 32 bits, and an empty
+  // list of 2^20 pairs of 134 MB costs 8.4 ms (one such page among them: 9.8).
+  constexpr int64_t kMost = 1 << 22;
   const int64_t units = int64_t(a.pool.page) * a.pool.Hkv * a.pool.row16;
   const int64_t batch = kCopyThreads * kCopyUnits;
-  a.per_split = static_cast<int>(units < batch ? units : batch);
+  const int64_t most = a.n < kMost ? kMost / a.n : 1, batches = (units + batch - 1) / batch;
+  const int64_t per = (batches + most - 1) / most * batch;
+  a.per_split = static_cast<int>(min64(units, per));
   a.splits = static_cast<int>((units + a.per_split - 1) / a.per_split);
   return launch_pdl(kv_copy_pages_kernel, dim3(a.n * a.splits, 2 * a.pool.layers),
                     dim3(kCopyThreads), 0, s, a);

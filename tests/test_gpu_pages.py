@@ -416,3 +416,27 @@ def test_housekeeping_refusals(cuda_device):
                 lambda: api.pages_release(t, one, refs, 1 << 31 - 1)]:
         with pytest.raises(api.RFError):
             bad()
+
+
+def test_kv_copy_pages_of_a_long_list_and_large_pages(cuda_device):
+    # pages of 134 MB and 2^20 pairs, nearly all of them empty: pairs times the parts of
+    # a page pass 2^32
+    n, page, Hkv, d = 1 << 20, 65552, 8, 128
+    pools = []
+    for i in range(2):
+        c = torch.empty(5, page, Hkv, d, dtype=torch.bfloat16, device="cuda")
+        # every 16 bytes of the pool differ, up to a period that no page's length shares
+        bits = torch.arange(c.numel(), dtype=torch.int32, device="cuda") % (30011 + 10 * i)
+        c.copy_(bits.to(torch.int16).view(torch.bfloat16).view_as(c))
+        pools.append(c)
+    want = [p[:2].view(torch.int16).clone() for p in pools]
+    src = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    dst = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    src[300], dst[300] = 0, 2
+    src[n - 1], dst[n - 1] = 1, 4
+    api.kv_copy_pages(*pools, src, dst)
+    assert api.device_status() == 0
+    for p, w in zip(pools, want):
+        p = p.view(torch.int16)
+        assert torch.equal(p[2], w[0]) and torch.equal(p[4], w[1]) and torch.equal(p[:2], w)
+        assert not torch.equal(p[3], w[0])
