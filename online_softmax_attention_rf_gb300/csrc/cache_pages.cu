@@ -278,6 +278,7 @@ __global__ void __cluster_dims__(kGrowCluster, 1, 1) __launch_bounds__(kGrowThre
   pdl_wait();
   pdl_trigger();
   bool bad = false;
+  constexpr int kNothing = -2;  // in the place of a shared page: the row gets nothing
   auto shared_page = [&](int i) -> int {
     const int len = a.len[i], to = a.new_len[i];
     if (len < 0 || to <= len || to > int64_t(a.max_pages) * a.page || len % a.page == 0) return -1;
@@ -286,7 +287,12 @@ __global__ void __cluster_dims__(kGrowCluster, 1, 1) __launch_bounds__(kGrowThre
       bad = true;
       return -1;
     }
-    return a.refs[id] > 1 ? id : -1;
+    const int owners = a.refs[id];
+    if (owners < 1) {  // a free page: it may be handed out, so that nobody can write to it
+      bad = true;
+      return kNothing;
+    }
+    return owners > 1 ? id : -1;
   };
   for (int i = tid; i < a.n; i += kGrowThreads) rows[i].shared = shared_page(i);
   __syncthreads();
@@ -300,7 +306,7 @@ __global__ void __cluster_dims__(kGrowCluster, 1, 1) __launch_bounds__(kGrowThre
       const int len = a.len[i], to = a.new_len[i];
       if (len < 0 || to < 0 || to > int64_t(a.max_pages) * a.page) {
         bad = true;
-      } else {
+      } else if (rows[i].shared != kNothing) {
         const int id = rows[i].shared;
         int ahead = 0;
         if (id >= 0)

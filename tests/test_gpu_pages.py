@@ -440,3 +440,24 @@ def test_kv_copy_pages_of_a_long_list_and_large_pages(cuda_device):
         p = p.view(torch.int16)
         assert torch.equal(p[2], w[0]) and torch.equal(p[4], w[1]) and torch.equal(p[:2], w)
         assert not torch.equal(p[3], w[0])
+
+
+def test_pages_grow_of_a_row_whose_last_page_has_no_owner(cuda_device):
+    # page 0 is free, whatever row 0's entry says: the row gets nothing, the others theirs,
+    # that page among them
+    for owners in (0, -3):
+        refs = _i32([owners, 1, 2, 0, 0])
+        table = _i32([[0, 9, 9], [1, 9, 9], [2, 9, 9], [0, 9, 9]])
+        src, dst, left = api.pages_grow(table, _i32([3, 5, 4, 6]), _i32([20, 9, 5, 6]), refs, 8)
+        with pytest.raises(api.RFError):
+            api.device_status()
+        free = [p for p in (0, 3, 4) if owners == 0 or p > 0]
+        assert table.tolist() == [[0, 9, 9], [1, free[0], 9], [free[1], 9, 9], [0, 9, 9]]
+        assert src.tolist() == [-1, -1, 2, -1] and dst.tolist() == [-1, -1, free[1], -1]
+        want = [owners, 1, 1, 0, 0]
+        want[free[0]] = want[free[1]] = 1
+        assert refs.tolist() == want and left.item() == len(free) - 2
+    # a row that does not write to it is no matter
+    refs, table = _i32([0, 1]), _i32([[0, 0], [0, 0]])
+    api.pages_grow(table, _i32([3, 8]), _i32([3, 8]), refs, 8)
+    assert api.device_status() == 0 and refs.tolist() == [0, 1]
