@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kOwnThreads) pages_release_kernel(const PagesR
   pdl_trigger();
   const int i = blockIdx.x;
   const int old_len = a.len[i], new_len = a.new_len != nullptr ? a.new_len[i] : 0;
-  bool bad = old_len < 0 || new_len < 0 || old_len > int64_t(a.max_pages) * a.page;
+  bool bad = old_len < 0 || new_len < 0 || max(old_len, new_len) > int64_t(a.max_pages) * a.page;
   if (!bad) {
     const int n = pages_of(old_len, a.page);
     for (int j = pages_of(new_len, a.page) + blockIdx.y * kOwnThreads + threadIdx.x; j < n;
@@ -304,7 +304,7 @@ __global__ void __cluster_dims__(kGrowCluster, 1, 1) __launch_bounds__(kGrowThre
     int count = 0, first = 0;
     if (i < a.n) {
       const int len = a.len[i], to = a.new_len[i];
-      if (len < 0 || to < 0 || to > int64_t(a.max_pages) * a.page) {
+      if (len < 0 || to < 0 || max(len, to) > int64_t(a.max_pages) * a.page) {
         bad = true;
       } else if (rows[i].shared != kNothing) {
         const int id = rows[i].shared;

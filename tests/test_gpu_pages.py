@@ -461,3 +461,18 @@ def test_pages_grow_of_a_row_whose_last_page_has_no_owner(cuda_device):
     refs, table = _i32([0, 1]), _i32([[0, 0], [0, 0]])
     api.pages_grow(table, _i32([3, 8]), _i32([3, 8]), refs, 8)
     assert api.device_status() == 0 and refs.tolist() == [0, 1]
+
+
+@pytest.mark.parametrize("length,new", [(17, 5), (17, 17), (1 << 30, 0), (-1, 3), (3, -1), (3, 17)])
+def test_pages_calls_report_lengths_out_of_range(cuda_device, length, new):
+    # tables of two pages of 8 tokens: 17 tokens are too many, there or to be there
+    refs, table = _i32([1, 1, 1, 0]), _i32([[0, 1], [2, 0]])
+    api.pages_release(table, _i32([length, 8]), refs, 8, _i32([new, 0]))
+    with pytest.raises(api.RFError):
+        api.device_status()
+    assert refs.tolist() == [1, 1, 0, 0]
+    src, dst, left = api.pages_grow(table, _i32([length, 0]), _i32([new, 8]), refs, 8)
+    with pytest.raises(api.RFError):
+        api.device_status()
+    assert table.tolist() == [[0, 1], [2, 0]] and refs.tolist() == [1, 1, 1, 0]
+    assert src.tolist() == dst.tolist() == [-1, -1] and left.item() == 1
