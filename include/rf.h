@@ -861,7 +861,8 @@ rf_status rf_kv_copy_pages(const rf_kv_pool *pool, const int32_t *src, const int
  *
  * Lengths out of [0, max_pages * page], page numbers out of range and pages without
  * an owner are skipped and reported through rf_device_status (a row that would write to
- * a partly filled last page without an owner, which is free, gets nothing). B, n >= 0.
+ * a partly filled last page without an owner, which is free, gets nothing; a fork's row
+ * has the entry of such a page, but no owner is added). B, n >= 0.
  * Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED, RF_ERR_CUDA.
  */
 rf_status rf_pages_fork(const int32_t *table, int64_t table_stride, const int32_t *len, int B,

@@ -175,7 +175,11 @@ __device__ __forceinline__ int pages_of(int len, int page) {  // len >= 0
   return len / page + (len % page != 0 ? 1 : 0);
 }
 
-// A row of the new table is a row of the old one; its pages have one owner more.
+// A row of the new table is a row of the old one; its pages have one owner more, but
+// for those without one, which are free and stay so: nothing adds to a count of 0, so
+// that all rows that read it find it as it was. (Four rows of 32 pages 1.7 us replayed, 1.3
+// without the look; 192 of 40 2.3; 16384 rows of one prompt's 16 pages 35 to 42, 25
+// without, 57 where each looks in L2 and not in L1.)
 __global__ void __launch_bounds__(kOwnThreads) pages_fork_kernel(const PagesForkArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kOwnThreads) pages_fork_kernel(const PagesFork
   for (int j = blockIdx.y * kOwnThreads + threadIdx.x; j < n; j += gridDim.y * kOwnThreads) {
     const int id = a.table[int64_t(s) * a.table_stride + j];
     a.out[int64_t(i) * a.out_stride + j] = id;
-    if (id < 0 || id >= a.num_pages)
+    if (id < 0 || id >= a.num_pages || a.refs[id] < 1)
       bad = true;
     else
       atomicAdd(a.refs + id, 1);

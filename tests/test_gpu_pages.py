@@ -476,3 +476,16 @@ def test_pages_calls_report_lengths_out_of_range(cuda_device, length, new):
         api.device_status()
     assert table.tolist() == [[0, 1], [2, 0]] and refs.tolist() == [1, 1, 1, 0]
     assert src.tolist() == dst.tolist() == [-1, -1] and left.item() == 1
+
+
+def test_pages_fork_gives_free_pages_no_owner(cuda_device):
+    # pages 1 and 3 have no owner: many rows share them, none becomes theirs
+    refs = _i32([1, 0, 2, -1])
+    table = _i32([[0, 1, 2, 3], [2, 0, 9, 9]])
+    out = torch.full((600, 4), 7, dtype=torch.int32, device="cuda")
+    got = api.pages_fork(table, _i32([32, 16]), _i32([0] * 300 + [1] * 300), out, refs, 8)
+    with pytest.raises(api.RFError):
+        api.device_status()
+    assert refs.tolist() == [601, 0, 602, -1]
+    assert got.tolist() == [32] * 300 + [16] * 300
+    assert out.tolist() == [[0, 1, 2, 3]] * 300 + [[2, 0, 7, 7]] * 300
