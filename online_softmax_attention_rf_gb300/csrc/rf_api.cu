@@ -1064,10 +1064,10 @@ rf_status rf_kv_compact_paged(const rf_kv_pool* pool, const int32_t* table, int6
   rf::CompactArgs a{};
   rf_status chk = read_pool(fn, pool, &a.pool);
   if (chk != RF_OK) return chk;
-  chk = check_pool(fn, B, N, pool->page, pool->num_pages, max_pages);
+  chk = check_pool(fn, 0, 0, pool->page, pool->num_pages, max_pages);
   if (chk != RF_OK) return chk;
-  if (int64_t(B) * pool->Hkv > INT32_MAX || N > (1 << 30))
-    return fail(RF_ERR_INVALID, "%s: B * Hkv > 2^31-1 or N > 2^30", fn);
+  if (B < 0 || N < 0 || int64_t(B) * pool->Hkv > INT32_MAX || N > (1 << 30))
+    return fail(RF_ERR_INVALID, "%s: need B, N >= 0, B * Hkv <= 2^31-1 and N <= 2^30", fn);
   if (B == 0 || N == 0 || pool->layers == 0) return ok();
   chk = check_pool_pointers(fn, pool);
   if (chk != RF_OK) return chk;

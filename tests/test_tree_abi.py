@@ -191,3 +191,15 @@ def test_python_refuses_host_tensors_and_causal_plans():
                  lambda: api.pages_release(i.view(1, 2), i, i, 8)]:
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("kw,hkv,expect", [
+    (dict(N=1 << 30), 2, api.RF_OK), (dict(N=(1 << 30) + 1), 2, INV),
+    (dict(N=(1 << 28) + 1), 2, api.RF_OK), (dict(B=(1 << 20) + 1), 2, api.RF_OK),
+    (dict(B=(1 << 30) - 1), 2, api.RF_OK), (dict(B=1 << 30), 2, INV),
+    (dict(B=(1 << 31) - 1), 1, api.RF_OK),
+])
+def test_kv_compact_paged_largest_lists(L, kw, hkv, expect):
+    # (without layers nothing is launched)
+    pool = _pool(layers=0, Hkv=hkv)
+    assert _call(L, "rf_kv_compact_paged", COMPACT, dict(kw, pool=pool)) == expect
