@@ -795,7 +795,9 @@ rf_status rf_sample_rows(const void *logits, int64_t stride, const float *expo,
  * k_head_stride (elements), the same for v. Strides in bytes and both pointers
  * 16-byte aligned, strides >= 0; d * element size a multiple of 16, d <= 1024.
  * layers in [0, 32767] (0: nothing launched), Hkv, page, num_pages >= 1; page *
- * num_pages and page * Hkv * d <= 2^31 - 1. k's and v's bytes must not overlap.
+ * num_pages and page * Hkv * d <= 2^31 - 1. Rows must lie apart (sorted by size, each
+ * dimension's stride goes past all within it; RF_ERR_INVALID otherwise, as for an
+ * expanded tensor), and k's and v's bytes must not overlap.
  */
 typedef struct {
   void *k, *v;

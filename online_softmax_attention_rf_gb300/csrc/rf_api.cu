@@ -5,6 +5,7 @@
 // an invalid call launches nothing and returns RF_ERR_INVALID with a
 // thread-local message (rf_last_error). No entry point allocates device
 // memory or synchronises, except rf_device_status which exists to do so.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -303,6 +304,21 @@ rf_status attn_paged(const char* fn, const void* q, int64_t q_stride, const void
   return ok();
 }
 
+// Whether the rows (of `row` elements) of a pool lie apart: each dimension's steps, from
+// the smallest stride up, go past all that lies within it.
+bool rows_apart(int64_t row, const int64_t* strides, const int* sizes) {
+  int order[4] = {0, 1, 2, 3};
+  std::sort(order, order + 4, [&](int a, int b) { return strides[a] < strides[b]; });
+  int64_t extent = row;
+  for (int i : order) {
+    if (sizes[i] < 2) continue;
+    if (strides[i] < extent) return false;
+    if (strides[i] > (INT64_MAX - extent) / (sizes[i] - 1)) return true;  // past all memory
+    extent += strides[i] * (sizes[i] - 1);
+  }
+  return true;
+}
+
 // A pool's sizes and strides, checked and turned to bytes.
 rf_status read_pool(const char* fn, const rf_kv_pool* p, rf::Pool* out) {
   if (p == nullptr) return fail(RF_ERR_INVALID, "%s: pool is NULL", fn);
@@ -322,6 +338,9 @@ rf_status read_pool(const char* fn, const rf_kv_pool* p, rf::Pool* out) {
   for (int64_t x : strides)
     if (x < 0 || x * es % 16 != 0 || x >= (int64_t(1) << 40))
       return fail(RF_ERR_INVALID, "%s: strides must be multiples of 16 bytes", fn);
+  const int sizes[] = {p->layers, p->num_pages, p->page, p->Hkv};
+  if (!rows_apart(p->d, strides, sizes) || !rows_apart(p->d, strides + 4, sizes))
+    return fail(RF_ERR_INVALID, "%s: rows of the pool overlap", fn);
   const int64_t row = p->d * es;
   auto side = [&](void* base, int64_t layer, int64_t page, int64_t token, int64_t head) {
     rf::PoolSide s{static_cast<char*>(base), layer * es, page * es, token * es, head * es, 0};

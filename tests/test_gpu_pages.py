@@ -489,3 +489,16 @@ def test_pages_fork_gives_free_pages_no_owner(cuda_device):
     assert refs.tolist() == [601, 0, 602, -1]
     assert got.tolist() == [32] * 300 + [16] * 300
     assert out.tolist() == [[0, 1, 2, 3]] * 300 + [[2, 0, 7, 7]] * 300
+
+
+def test_expanded_pools_are_refused(cuda_device):
+    # layers or heads that are one memory: a row would be moved once for each of them
+    x = torch.arange(24.0, device="cuda").view(3, 8, 1, 1).expand(3, 8, 1, 64).contiguous()
+    for pool in (x.expand(2, 3, 8, 1, 64), x.expand(3, 8, 4, 64), x[:1].expand(3, 8, 1, 64)):
+        other = pool.contiguous()
+        for k, v in ((pool, other), (other, pool)):
+            with pytest.raises(api.RFError):
+                api.kv_compact_paged(k, v, _i32([[2, 0]]), _i32([1, 3, 5]), _i32([0, 3]))
+            with pytest.raises(api.RFError):
+                api.kv_copy_pages(k, v, _i32([0]), _i32([1]))
+    assert torch.equal(x[:, :, 0, 0].flatten(), torch.arange(24.0, device="cuda"))

@@ -203,3 +203,26 @@ def test_kv_compact_paged_largest_lists(L, kw, hkv, expect):
     # (without layers nothing is launched)
     pool = _pool(layers=0, Hkv=hkv)
     assert _call(L, "rf_kv_compact_paged", COMPACT, dict(kw, pool=pool)) == expect
+
+
+@pytest.mark.parametrize("name,ok,nothing", [("rf_kv_compact_paged", COMPACT, dict(N=0)),
+                                             ("rf_kv_copy_pages", COPY, dict(n=0))])
+@pytest.mark.parametrize("pool,expect", [
+    (dict(k_head_stride=0), INV), (dict(v_token_stride=0), INV), (dict(k_page_stride=0), INV),
+    (dict(v_layer_stride=0), INV),                       # an expanded pool
+    (dict(k_head_stride=56), INV), (dict(v_token_stride=120), INV), (dict(k_page_stride=1024), INV),
+    (dict(v_layer_stride=8 * 2048), INV), (dict(k_layer_stride=128), INV),
+    # a dimension of one has no stride
+    (dict(layers=1, k_layer_stride=0, v_layer_stride=0), api.RF_OK),
+    (dict(Hkv=1, k_head_stride=0, v_head_stride=8), api.RF_OK),
+    # other orders, and room between the rows
+    (dict(k_head_stride=1024, k_token_stride=64), api.RF_OK),
+    (dict(k_layer_stride=64, k_head_stride=128, k_token_stride=256, k_page_stride=4096), api.RF_OK),
+    (dict(k_head_stride=72, k_token_stride=144, k_page_stride=1 << 39, k_layer_stride=1 << 39,
+          num_pages=1), api.RF_OK),
+    (dict(num_pages=1 << 26, k_page_stride=1 << 39, k_layer_stride=(1 << 40) - 8), INV),
+    (dict(num_pages=1 << 26, k_layer_stride=2048, k_page_stride=1 << 39, v_layer_stride=2048,
+          v_page_stride=4096), api.RF_OK),
+])
+def test_pools_whose_rows_overlap(L, name, ok, nothing, pool, expect):
+    assert _call(L, name, ok, dict(nothing, pool=_pool(**pool))) == expect
