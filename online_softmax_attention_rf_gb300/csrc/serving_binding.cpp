@@ -92,26 +92,23 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType dt, at::Device dev) {
   return at::empty(shape, at::TensorOptions().dtype(dt).device(dev));
 }
 
-// Several new outputs out of one allocation (one costs more than all the views of
-// it), each on a boundary of 16 bytes.
-struct Out {
-  int64_t n;  // elements of four bytes
-  at::ScalarType dt;
-};
+// Several new int32 outputs out of one allocation (one costs more than all the views of
+// it), each on a boundary of 16 bytes. Of one type: torch.save refuses tensors of two
+// types that share a storage.
 template <size_t N>
-std::array<Tensor, N> fresh_outs(const Out (&outs)[N], at::Device dev) {
+std::array<Tensor, N> fresh_ints(const int64_t (&outs)[N], at::Device dev) {
   int64_t words = 0;
-  for (const Out& o : outs) words += (o.n + 3) / 4 * 4;
+  for (const int64_t n : outs) words += (n + 3) / 4 * 4;
   const Tensor buf = fresh({words}, at::kInt, dev);
   std::array<Tensor, N> got;
   int64_t at = 0;
   for (size_t i = 0; i < N; ++i) {
     got[i] = at::detail::make_tensor<c10::TensorImpl>(
-        c10::Storage(buf.storage()), buf.key_set(), c10::scalarTypeToTypeMeta(outs[i].dt));
+        c10::Storage(buf.storage()), buf.key_set(), buf.dtype());
     c10::TensorImpl* t = got[i].unsafeGetTensorImpl();
     t->set_storage_offset(at);
-    t->set_sizes_contiguous({outs[i].n});
-    at += (outs[i].n + 3) / 4 * 4;
+    t->set_sizes_contiguous({outs[i]});
+    at += (outs[i] + 3) / 4 * 4;
   }
   return got;
 }
@@ -353,8 +350,7 @@ PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (const Tensor* t : {&parent, &tokens, &sampled}) fits(*t, at::kInt, {T}, dev);
     fits(cu_q, at::kInt, {B + 1}, dev);
     fits(kv_len, at::kInt, {B}, dev);
-    const auto [path, out, n_path, base, new_len] = fresh_outs(
-        {{T, at::kInt}, {T, at::kInt}, {B, at::kInt}, {B, at::kInt}, {B, at::kInt}}, dev);
+    const auto [path, out, n_path, base, new_len] = fresh_ints({T, T, B, B, B}, dev);
     c10::cuda::CUDAGuard guard(dev);
     const rf_status st = rf_tree_accept(
         ptr<int32_t>(&parent), ptr<int32_t>(&tokens), ptr<int32_t>(&sampled), ptr<int32_t>(&cu_q),
@@ -385,7 +381,7 @@ PyObject* sample_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(top_p, at::kFloat, {B}, dev);
     fits(min_p, at::kFloat, {B}, dev);
     const rf_dtype rdt = dtype_of(logits);
-    const auto [token, logprob] = fresh_outs({{B, at::kInt}, {B, at::kFloat}}, dev);
+    const Tensor token = fresh({B}, at::kInt, dev), logprob = fresh({B}, at::kFloat, dev);
     c10::cuda::CUDAGuard guard(dev);
     const rf_status st = rf_sample_rows(
         logits.data_ptr(), logits.stride(0), ptr<float>(&expo), ptr<float>(temperature),
@@ -525,7 +521,7 @@ PyObject* pages_grow(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(len, at::kInt, {m}, dev);
     fits(new_len, at::kInt, {m}, dev);
     fits(refs, at::kInt, {refs.size(0)}, dev);
-    const auto [src, dst, left] = fresh_outs({{m, at::kInt}, {m, at::kInt}, {1, at::kInt}}, dev);
+    const auto [src, dst, left] = fresh_ints({m, m, 1}, dev);
     c10::cuda::CUDAGuard guard(dev);
     const rf_status st = rf_pages_grow(
         ptr<int32_t>(&table), rows, ptr<int32_t>(&len), ptr<int32_t>(&new_len), m,

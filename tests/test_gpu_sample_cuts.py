@@ -67,3 +67,10 @@ def test_small_top_p_at_high_temperatures(cuda_device, dtype):
         _check(x, expo, [temp] * 8, None, SMALL_P, None, least=0.7)
         _check(x, expo, [temp] * 8, [1, 2, 5, 100, 600, 4000, 0, 4999], SMALL_P, None, least=0.6)
     assert api.device_status() == 0
+
+
+def test_tokens_and_probabilities_are_saved_together(cuda_device, tmp_path):
+    x = torch.zeros(3, 40, device="cuda")
+    got = api.sample_rows(x, torch.ones_like(x))
+    torch.save(got, tmp_path / "drawn")
+    assert all(torch.equal(a, b) for a, b in zip(torch.load(tmp_path / "drawn"), got))
