@@ -698,9 +698,10 @@ rf_status rf_draft_verify(const void *target, const void *draft, const int32_t *
  *  cu_q int32 [B + 1], kv_len int32 [B] (NULL with pos NULL); all device;
  *  mask uint64 [T, words], 1 <= words <= 16; pos int32 [T] or NULL.
  * Rows outside every sequence get 0. A parent that does not come before its child
- * makes the child a root, and a sequence of more than 64 * words nodes gets masks
- * and positions of 0; both are reported through rf_device_status. B, T >= 0 (one
- * of them 0: nothing is written).
+ * makes the child a root, a sequence of more than 64 * words nodes gets masks and
+ * positions of 0, and one whose offsets are not ascending within [0, T] has no rows;
+ * all are reported through rf_device_status. 0 <= B <= 2^20, 0 <= T <= 2^28 (one of
+ * them 0: nothing is written).
  * Errors: RF_ERR_INVALID (sizes, NULL or misaligned pointers), RF_ERR_UNSUPPORTED
  * (words > 16), RF_ERR_CUDA.
  */
@@ -746,8 +747,8 @@ rf_status rf_attn_paged_tree(const void *q, int64_t q_stride, const void *k_cach
  *      keep and n_path as n_keep the arguments of rf_kv_compact_paged, and the
  *      cache's length after it.
  * All device, 4-byte aligned. Offsets that are not ascending within [0, T] make a
- * sequence empty and are reported through rf_device_status. B, T >= 0 (B = 0:
- * nothing is written).
+ * sequence empty and are reported through rf_device_status. 0 <= B <= 2^20, 0 <= T <=
+ * 2^28 (B = 0: nothing is written).
  * Errors: RF_ERR_INVALID, RF_ERR_CUDA.
  */
 rf_status rf_tree_accept(const int32_t *parent, const int32_t *tokens, const int32_t *sampled,
@@ -864,7 +865,8 @@ rf_status rf_kv_copy_pages(const rf_kv_pool *pool, const int32_t *src, const int
  * Lengths out of [0, max_pages * page], page numbers out of range and pages without
  * an owner are skipped and reported through rf_device_status (a row that would write to
  * a partly filled last page without an owner, which is free, gets nothing; a fork's row
- * has the entry of such a page, but no owner is added). B, n >= 0.
+ * has the entry of such a page, but no owner is added). 0 <= B <= 2^20,
+ * 0 <= n <= 2^28.
  * Errors: RF_ERR_INVALID, RF_ERR_UNSUPPORTED, RF_ERR_CUDA.
  */
 rf_status rf_pages_fork(const int32_t *table, int64_t table_stride, const int32_t *len, int B,

@@ -19,19 +19,58 @@ constexpr int kStaged = 1024;  // nodes of a sequence kept in shared memory
 __device__ __forceinline__ bool rows_of(const int32_t* cu_q, int b, int T, int* first, int* n) {
   const int c0 = cu_q[b], c1 = cu_q[b + 1];
   *first = c0;
-  *n = c1 - c0;
+  *n = c0 >= 0 && c1 >= c0 ? c1 - c0 : 0;
   return c0 >= 0 && c1 >= c0 && c1 <= T;
 }
 
-// The rows outside every sequence, f(row) for each: those before the first and
-// behind the last, by the CTAs of these two.
+// The rows of [lo, hi) that no sequence with good offsets has, f(row) for each. All
+// threads call. A look at all offsets finds either how far the rows from the present one
+// on are some sequence's, or how far they are none's; sequences behind each other
+// count as one there, so that a few looks do unless most offsets are bad.
 template <typename F>
-__device__ __forceinline__ void outside(const int32_t* cu_q, int b, int B, int T, F&& f) {
+__device__ void unowned(const int32_t* cu_q, int B, int T, int lo, int hi, F&& f) {
+  __shared__ int end, next;
+  const int each = (B + kThreads - 1) / kThreads;
+  const int s0 = min(int64_t(B), int64_t(threadIdx.x) * each), s1 = min(B, s0 + each);
+  for (int at = lo; at < hi;) {
+    if (threadIdx.x == 0) {
+      end = at;
+      next = hi;
+    }
+    __syncthreads();
+    for (int s = s0; s < s1;) {
+      int n, first, last;
+      if (!rows_of(cu_q, s++, T, &first, &n) || n == 0) continue;
+      last = first + n;
+      for (int more; s < s1 && rows_of(cu_q, s, T, &more, &n); ++s) last = more + n;
+      if (first > at)
+        atomicMin(&next, first);
+      else if (last > at)
+        atomicMax(&end, last);
+    }
+    __syncthreads();
+    const int to = end > at ? end : min(next, hi);
+    if (end <= at)
+      for (int r = at + threadIdx.x; r < to; r += kThreads) f(r);
+    __syncthreads();
+    at = to;
+  }
+}
+
+// The rows outside every sequence, f(row) for each: those before the first and
+// behind the last, by the CTAs of these two, and those between a sequence's offsets
+// where these are not good, by its CTA. (From any row a step in the offsets leads past,
+// or it lies before the first or behind the last.)
+template <typename F>
+__device__ __forceinline__ void outside(const int32_t* cu_q, int b, int B, int T, bool good,
+                                        F&& f) {
   if (b == 0)
-    for (int r = threadIdx.x; r < min(cu_q[0], T); r += kThreads) f(r);
+    for (int r = threadIdx.x; r < min(min(cu_q[0], cu_q[1]), T); r += kThreads) f(r);
   if (b == B - 1)
-    for (int64_t r = int64_t(max(0, cu_q[B])) + threadIdx.x; r < T; r += kThreads)
+    for (int64_t r = int64_t(max(0, max(cu_q[B], cu_q[B - 1]))) + threadIdx.x; r < T; r += kThreads)
       f(static_cast<int>(r));
+  if (!good)
+    unowned(cu_q, B, T, max(0, min(cu_q[b], cu_q[b + 1])), min(T, max(cu_q[b], cu_q[b + 1])), f);
 }
 
 // Node i's bits are those of the nodes on its way up, itself among them. Parents
@@ -44,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) tree_mask_kernel(const TreeMaskArgs 
   const int b = blockIdx.x;
   int c0, n;
   const bool good = rows_of(a.cu_q, b, a.T, &c0, &n);
-  outside(a.cu_q, b, a.B, a.T, [&](int r) {
+  outside(a.cu_q, b, a.B, a.T, good, [&](int r) {
     for (int w = 0; w < a.words; ++w) a.mask[int64_t(r) * a.words + w] = 0;
     if (a.pos != nullptr) a.pos[r] = 0;
   });
@@ -106,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptA
     token[i] = a.tokens[c0 + i];
     drawn[i] = a.sampled[c0 + i];
   }
-  outside(a.cu_q, b, a.B, a.T, [&](int r) { a.path[r] = a.out[r] = -1; });
+  outside(a.cu_q, b, a.B, a.T, good, [&](int r) { a.path[r] = a.out[r] = -1; });
   __syncthreads();
   __shared__ int walked;
   if (threadIdx.x < 32) {

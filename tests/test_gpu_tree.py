@@ -533,3 +533,57 @@ def test_a_tree_step_captured_and_replayed_with_other_trees(cuda_device):
         assert api.device_status() == 0
         walked += want[7].sum().item()
     assert walked > 4 * B
+
+
+def _poison(*sizes):
+    """What torch's allocator hands out next for int32 outputs of these sizes holds
+    numbers that no call gives."""
+    held = [torch.full((n,), 0x55555555, dtype=torch.int32, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    del held
+
+
+BAD_OFFSETS = [
+    ([0, 4, 20], 10), ([-1, 1, 2], 3), ([0, 20, 5, 8], 8), ([0, 3, 12, 3, 7], 9), ([5, 1, 3], 6),
+    ([-5, -3, 2, 4], 6), ([9, 9, 9], 6), ([3, -1], 5), ([0, 1 << 30, -(1 << 30), 2], 4),
+    ([600] + list(range(0, 600, 2)), 605),
+    ([1000 if i % 10 == 3 else 2 * i for i in range(301)], 640),
+    ([-7 if i % 50 == 49 else 3 * i + 4 for i in range(400)], 1300),
+]
+
+
+@pytest.mark.parametrize("cu,T", BAD_OFFSETS)
+def test_rows_of_no_sequence_where_offsets_contradict_themselves(cuda_device, cu, T):
+    # rows that no sequence with good offsets has hold 0 in masks and positions, -1 in
+    # paths and tokens; the others' are theirs
+    B = len(cu) - 1
+    rng = np.random.default_rng(T)
+    good = [0 <= a <= b <= T for a, b in zip(cu, cu[1:])]
+    parent, token = np.full(T, -1), rng.integers(0, 2, T)
+    kv = [0] * B
+    m_ref, p_ref = np.zeros((T, 16), np.int64), np.zeros(T, np.int64)
+    path, out, n_path = np.full(T, -1), np.full(T, -1), [0] * B
+    for b in range(B):
+        n, rows = cu[b + 1] - cu[b], slice(cu[b], cu[b + 1])
+        kv[b] = 20 + b
+        if good[b] and n:
+            p = _parents(n, rng)
+            parent[rows] = p
+            m_ref[rows] = tree.words(tree.mask(p), 16)
+            p_ref[rows] = kv[b] - n + tree.depths(p)
+            nodes, drawn = tree.accept(p, token[rows].tolist(), token[rows].tolist())
+            path[cu[b]:cu[b] + len(nodes)], out[cu[b]:cu[b] + len(nodes)] = nodes, drawn
+            n_path[b] = len(nodes)
+    assert not all(good)
+    args = [_i32(x) for x in (parent, token, token, cu, kv)]
+    _poison(32 * T, T)
+    mask, pos = api.tree_mask(args[0], args[3], args[4], 16)
+    with pytest.raises(api.RFError):
+        api.device_status()
+    assert np.array_equal(mask.cpu().numpy(), m_ref) and pos.tolist() == p_ref.tolist()
+    _poison((T + 3) // 4 * 8 + (B + 3) // 4 * 12)
+    got = api.tree_accept(*args)
+    with pytest.raises(api.RFError):
+        api.device_status()
+    assert got[0].tolist() == path.tolist() and got[1].tolist() == out.tolist()
+    assert got[2].tolist() == n_path
