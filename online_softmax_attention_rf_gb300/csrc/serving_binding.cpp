@@ -317,6 +317,10 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(kv_len, at::kInt, {B}, dev);
     const Tensor mask = fresh({T, words > 0 ? words : 0}, at::kLong, dev), pos = fresh({T}, at::kInt, dev);
     c10::cuda::CUDAGuard guard(dev);
+    if (B == 0) {  // all rows lie outside every sequence, and no kernel runs
+      mask.zero_();
+      pos.zero_();
+    }
     const rf_status st =
         rf_tree_mask(ptr<int32_t>(&parent), ptr<int32_t>(&cu_q), ptr<int32_t>(&kv_len), B, T, words,
                      ptr<uint64_t>(&mask), ptr<int32_t>(&pos), stream_of(dev));
@@ -352,6 +356,10 @@ PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(kv_len, at::kInt, {B}, dev);
     const auto [path, out, n_path, base, new_len] = fresh_ints({T, T, B, B, B}, dev);
     c10::cuda::CUDAGuard guard(dev);
+    if (B == 0) {  // all rows lie outside every sequence, and no kernel runs
+      path.fill_(-1);
+      out.fill_(-1);
+    }
     const rf_status st = rf_tree_accept(
         ptr<int32_t>(&parent), ptr<int32_t>(&tokens), ptr<int32_t>(&sampled), ptr<int32_t>(&cu_q),
         ptr<int32_t>(&kv_len), B, T, ptr<int32_t>(&path), ptr<int32_t>(&out), ptr<int32_t>(&n_path),

@@ -587,3 +587,17 @@ def test_rows_of_no_sequence_where_offsets_contradict_themselves(cuda_device, cu
         api.device_status()
     assert got[0].tolist() == path.tolist() and got[1].tolist() == out.tolist()
     assert got[2].tolist() == n_path
+
+
+@pytest.mark.parametrize("T", [0, 1, 37])
+def test_trees_of_no_sequences(cuda_device, T):
+    # a padded step in which no sequence takes part
+    x, cu, none = _i32([0] * T), _i32([0]), _i32([])
+    _poison(4 * T, T)
+    mask, pos = api.tree_mask(x, cu, none, 2)
+    assert mask.shape == (T, 2) and not mask.any() and pos.tolist() == [0] * T
+    _poison((T + 3) // 4 * 8)
+    path, out, n_path, base, new_len = api.tree_accept(x, x, x, cu, none)
+    assert path.tolist() == out.tolist() == [-1] * T
+    assert n_path.shape == base.shape == new_len.shape == (0,)
+    assert api.device_status() == 0
