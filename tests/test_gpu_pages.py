@@ -502,3 +502,30 @@ def test_expanded_pools_are_refused(cuda_device):
             with pytest.raises(api.RFError):
                 api.kv_copy_pages(k, v, _i32([0]), _i32([1]))
     assert torch.equal(x[:, :, 0, 0].flatten(), torch.arange(24.0, device="cuda"))
+
+
+@pytest.mark.parametrize("most", [40, 400])     # lists of one chunk, and of several
+@pytest.mark.parametrize("dtype,Hkv,d,order", [(torch.bfloat16, 8, 64, "lpth"),
+                                               (torch.float32, 3, 80, "lpht")])
+def test_kv_compact_paged_of_many_sequences_in_many_layers(cuda_device, most, dtype, Hkv, d, order):
+    # more planes (k and v of a sequence's layers) than are in flight: a CTA takes several
+    layers, B, page = 12, 64, 16
+    gen, rng = torch.Generator().manual_seed(most), np.random.default_rng(most)
+    lens = [int(rng.integers(1, most + 1)) for _ in range(B)]
+    lens[0], lens[1] = most, 1
+    rows, pages = _tables(lens, page, 5, gen)
+    pools = [_pool(layers, pages, page, Hkv, d, dtype, order, gen) for _ in range(2)]
+    keep = [sorted(rng.choice(n, int(rng.integers(0, n + 1)), replace=False).tolist())
+            for n in lens]
+    keep[0] = list(range(1, most))
+    want = [p.clone() for p in pools]
+    for r, kept in zip(rows, keep):
+        place = lambda js: (_i32([r[j // page] for j in js]).long(),  # noqa: E731
+                            _i32([j % page for j in js]).long())
+        (p0, r0), (p1, r1) = place(kept), place(range(len(kept)))
+        for w, p in zip(want, pools):
+            w[:, p1, r1] = p[:, p0, r0]
+    cu = np.cumsum([0] + [len(x) for x in keep])
+    api.kv_compact_paged(*pools, _i32(rows), _i32(sum(keep, [])), _i32(cu))
+    assert api.device_status() == 0
+    assert all(torch.equal(p, w) for p, w in zip(pools, want))
