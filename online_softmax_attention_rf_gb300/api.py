@@ -977,7 +977,8 @@ def _refuse_pages(fn, tables, refs, ints):
 def pages_fork(block_table, kv_len, src, out, refs, page_size):
     """rf_pages_fork: row i of ``out`` int32 [n, max_pages] becomes a copy of row
     src[i] of block_table int32 [B, max_pages], and each of its pages gets an owner
-    more in refs int32 [num_pages] -> kv_len[src] int32 [n]. ``pages_grow`` gives
+    more in refs int32 [num_pages] (a page without one is free: it stays so, and is
+    reported) -> kv_len[src] int32 [n]. ``pages_grow`` gives
     the rows pages of their own before they are written to."""
     r = _serving().pages_fork(block_table, kv_len, src, out, refs, page_size)
     if r is None:
@@ -994,7 +995,8 @@ def pages_grow(block_table, kv_len, new_len, refs, page_size):
     partly filled last page that has other owners is replaced: ``kv_copy_pages(
     k_cache, v_cache, copy_src, copy_dst)`` has to follow before the row is used.
     left: free pages that remain, or, below 0, that are missing; then nothing was
-    changed."""
+    changed. A row whose partly filled last page has no owner gets nothing and is
+    reported."""
     r = _serving().pages_grow(block_table, kv_len, new_len, refs, page_size)
     if r is None:
         n = kv_len.numel()

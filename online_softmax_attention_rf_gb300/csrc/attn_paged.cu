@@ -413,8 +413,9 @@ __device__ __forceinline__ void put32(const RowOut& w, int c, const float (&v)[3
 // tokens, 32 heads of 8 key heads, d = 128: 18 us, latency. 16 trees of 64 nodes over
 // 16384 to 32768 tokens, 64 heads: 594 us alone, 665 in a long run: its two items a
 // key head run at different times and read the keys twice (1.03 GB for 0.44 of four
-// such trees, 61 % of the memory's rate, 52 % of the tensor cores'). 24 trees of up to
-// 200 nodes, d = 64: 148 us, bound by the pair step (1.45 us).
+// such trees, 61 % of the memory's rate, 52 % of the tensor cores'; an SM's 309 pair
+// steps are 495 us). 24 trees of up to 200 nodes, d = 64: 148 us, of which an SM's 53 pair
+// steps (1.45 us), 12 one-tile steps and 2.2 items are 111.
 template <int D, bool Tree>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

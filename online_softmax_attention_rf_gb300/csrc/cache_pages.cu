@@ -237,7 +237,10 @@ __global__ void __launch_bounds__(kOwnThreads) pages_release_kernel(const PagesR
 // One cluster: each CTA works out all rows' needs, and has a share of the pages.
 // It counts the free ones of its share, and once all counts are known hands its
 // own out. Bound by latency (lengths, table and owners, two cluster barriers, two
-// reads of the owners): four rows that grow in a pool of 64 pages 3.7 us, replayed.
+// reads of the owners) up to a few hundred rows: four rows that grow in a pool of 64
+// pages 3.7 us, replayed. Many rows that write to one page are counted one by one, which
+// goes with their square: in a pool of 20000 pages 5.4 us for four of them, 6.5 for 192,
+// 18 for 1024, 182 for 4096, 2650 for 16384.
 constexpr int kGrowThreads = 1024;
 constexpr int kGrowCluster = 8;
 
