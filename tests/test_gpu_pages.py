@@ -529,3 +529,11 @@ def test_kv_compact_paged_of_many_sequences_in_many_layers(cuda_device, most, dt
     api.kv_compact_paged(*pools, _i32(rows), _i32(sum(keep, [])), _i32(cu))
     assert api.device_status() == 0
     assert all(torch.equal(p, w) for p, w in zip(pools, want))
+
+
+def test_pages_of_the_most_rows_that_grow_at_once(cuda_device):
+    # thousands of rows share each partly filled page
+    test_pages_fork_grow_release(cuda_device, 7, 16384, 16, 120011, 8)
+    with pytest.raises(api.RFError):
+        one = _i32([0] * 16385)
+        api.pages_grow(one.view(-1, 1), one, one, _i32([0] * 8), 8)
