@@ -451,7 +451,7 @@ cudaError_t launch_kv_copy_pages(CopyPagesArgs a, cudaStream_t s) {
   constexpr int64_t kMost = 1 << 22;
   const int64_t units = int64_t(a.pool.page) * a.pool.Hkv * a.pool.row16;
   const int64_t batch = kCopyThreads * kCopyUnits;
-  const int64_t most = a.n < kMost ? kMost / a.n : 1, batches = (units + batch - 1) / batch;
+  const int64_t most = kMost / a.n, batches = (units + batch - 1) / batch;  // n <= 2^20
   const int64_t per = (batches + most - 1) / most * batch;
   a.per_split = static_cast<int>(min64(units, per));
   a.splits = static_cast<int>((units + a.per_split - 1) / a.per_split);

@@ -1396,9 +1396,10 @@ cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
                 "a share has no more blocks");
   auto share = [&] { return size_t((groups + cluster - 1) / cluster) * 16; };
   // rows that are read again, and resident at one time, fit L2; a thread has no more
-  // than 200 logits as far as eight CTAs go, V = 819200 (200 / 512 rows of 131072 in bf16 with one CTA a row and with two:
-  // top-k 61 / 125 and 46 / 93 us, top-p 122 / 226 and 90 / 194, no limit 50 / 108 and
-  // 50 / 108; rows of 70000 want one where there are no cuts: 64 and 75)
+  // than 200 logits as far as eight CTAs go, V = 819200 (200 / 512 rows of 131072 in bf16
+  // with one CTA a row and with two: top-k 61 / 125 and 46 / 93 us, top-p 122 / 226 and
+  // 90 / 194, no limit 50 / 108 and 50 / 108; rows of 70000 want one where there are no
+  // cuts: 64 and 75)
   while (cluster < kMaxCluster && share() > kMostHeld &&
          (kResident * int64_t(share()) > kL2 || a.V > cluster * kThreads * 200))
     cluster *= 2;
